@@ -47,6 +47,15 @@ class MoeRouting(ctypes.Structure):
         "block_expert", "block_row", "n_blocks")]
 
 
+class MoeI8Mat(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("layout", ctypes.c_int32)]
+
+
+class MoeScoreRule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_groups", "topk_groups", "group_score",
+                                              "renormalise")] + [("scale", ctypes.c_float)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -91,6 +100,20 @@ _SIGNATURES = {
     "moe_layer_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I, _I]),
     "moe_layer_chunked": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I]
                           + [ctypes.POINTER(MoeQ4Mat)] * 6 + [_P, _P, _S, _P]),
+    "moe_norm_i8": (_I, [_P, _P, _P, ctypes.c_float, _I, _I, _P, _P, _P, _P, _P]),
+    "moe_quant_i8": (_I, [_P, _I, _I, _P, _P, _P]),
+    "moe_dequant_i8_bf16": (_I, [_P, _P, _I, _I, _P, _P]),
+    "moe_i8_prepack": (_I, [_P, _I, _I, _I, _P, _P]),
+    "moe_linear_i8_workspace_bytes": (_S, [_I, _I, _I]),
+    "moe_linear_i8": (_I, [_P, _P, _I, _I, ctypes.POINTER(MoeI8Mat), _I, _P, _P, _S, _P]),
+    "moe_route_scored": (_I, [_P, _P, ctypes.POINTER(MoeScoreRule), _I, _I, _I, _I,
+                              ctypes.POINTER(MoeRouting), _P, _S, _P]),
+    "moe_gemm_i8_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I, _I]),
+    "moe_grouped_gemm_i8": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(MoeRouting)]
+                            + [ctypes.POINTER(MoeI8Mat)] * 6 + [_P, _P, _P, _S, _P]),
+    "moe_layer_i8": (_I, [_P, _P, _P, _P, ctypes.POINTER(MoeScoreRule), _I, _I, _I, _I, _I, _I, _I]
+                     + [ctypes.POINTER(MoeI8Mat)] * 6
+                     + [ctypes.POINTER(MoeRouting), _P, _S, _P, _P, _P, _S, _P, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -644,6 +667,283 @@ def moe_layer_chunked(x: torch.Tensor, logits: torch.Tensor, I: int, I_sh: int, 
 
 
 # ---------------------------------------------------------------------------
+# 8-bit operators: norm with 8-bit output, scored routing, products of codes
+# ---------------------------------------------------------------------------
+
+I8 = torch.int8
+
+
+class _On:
+    """Makes the device of a call's tensors the current one, and refuses tensors of another."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, first, *others):
+        d = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != d:
+                raise ValueError(f"arguments on different devices: {first.device} and {t.device}")
+        self.guard = (None if d < 0 or d == torch.cuda.current_device()
+                      else torch.cuda.device(d))
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class DeviceI8Mat:
+    """One set of 8-bit matrices [n_exp, N, K] resident on the device."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, layout: int = LAYOUT_ROWS):
+        """codes int8 [n_exp, N, K] (LAYOUT_TILES: the bytes moe_i8_prepack writes, in the same
+        shape), scales fp32 [n_exp, N]."""
+        _tensor(codes, "codes", I8)
+        if codes.dim() != 3:
+            raise ValueError("codes: expected [n_exp, N, K]")
+        _tensor(scales, "scales", F32, codes.shape[:2])
+        if layout not in (LAYOUT_ROWS, LAYOUT_TILES):
+            raise ValueError("layout: expected LAYOUT_ROWS or LAYOUT_TILES")
+        if codes.get_device() != scales.get_device():
+            raise ValueError("codes and scales: on different devices")
+        self.codes, self.scales, self.layout = codes, scales, layout
+        self.shape = tuple(codes.shape)
+        self.struct = MoeI8Mat(codes.data_ptr(), scales.data_ptr(), layout)
+
+    @classmethod
+    def from_bf16(cls, w: torch.Tensor, prepack: bool = True, stream=None) -> "DeviceI8Mat":
+        """Load time: bf16 weights [n_exp, N, K] quantised by rows (one scale per output
+        channel), in tiles where N allows them and prepack is not False."""
+        _tensor(w, "w", BF16)
+        if w.dim() != 3:
+            raise ValueError("w: expected [n_exp, N, K]")
+        n_exp, N, K = w.shape
+        codes = torch.empty((n_exp, N, K), dtype=I8, device=w.device)
+        scales = torch.empty((n_exp, N), dtype=F32, device=w.device)
+        moe_quant_i8(w.view(n_exp * N, K), codes.view(n_exp * N, K), scales.view(-1), stream)
+        m = cls(codes, scales)
+        return m.prepacked(stream) if prepack and N % 16 == 0 else m
+
+    def prepacked(self, stream=None) -> "DeviceI8Mat":
+        """The same matrices in 16 x 64 tiles; the scales are shared with this object."""
+        if self.layout != LAYOUT_ROWS:
+            raise ValueError("prepacked: the codes are in tiles already")
+        dst = torch.empty_like(self.codes)
+        moe_i8_prepack(self.codes, dst, stream)
+        return DeviceI8Mat(dst, self.scales, LAYOUT_TILES)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+class ScoreRule:
+    """Selection rule of moe_route_scored: score "softmax" or "sigmoid", groups of experts with
+    their worth "top2" or "max", weights renormalised or not, and a factor on them."""
+
+    def __init__(self, score: str = "softmax", n_groups: int = 1, topk_groups: int | None = None,
+                 group_score: str = "top2", renormalise: bool = True, scale: float = 1.0):
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError('score: expected "softmax" or "sigmoid"')
+        if group_score not in ("top2", "max"):
+            raise ValueError('group_score: expected "top2" or "max"')
+        self.score, self.n_groups, self.group_score = score, n_groups, group_score
+        self.topk_groups = n_groups if topk_groups is None else topk_groups
+        self.renormalise, self.scale = bool(renormalise), float(scale)
+        self.struct = MoeScoreRule(int(score == "sigmoid"), n_groups, self.topk_groups,
+                                   int(group_score == "top2"), int(self.renormalise), self.scale)
+
+
+def _i8mat_for(m, name, n_exp, N, K, present=True):
+    if not present:
+        if m is not None:
+            raise ValueError(f"{name}: must be None here")
+        return None
+    if not isinstance(m, DeviceI8Mat):
+        raise TypeError(f"{name}: expected a DeviceI8Mat")
+    if m.shape != (n_exp, N, K):
+        raise ValueError(f"{name}: codes {m.shape} are not a [{n_exp}, {N}, {K}] set")
+    return m
+
+
+def _i8mat(m):
+    if m is None:
+        return None
+    _ptr(m.codes)
+    return ctypes.byref(m.struct)
+
+
+def _codes_of(x, x_scale, name="x"):
+    _tensor(x, name, I8)
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions")
+    _tensor(x_scale, f"{name}_scale", F32, (x.shape[0],))
+    return x.shape
+
+
+def moe_norm_i8(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, sum=None, y=None,
+                q=None, q_scale=None, stream=None):
+    """x, residual bf16 [T, H], weight bf16 [H]; writes those of sum, y (bf16 [T, H]), q (int8)
+    and q_scale (fp32 [T]) that are given.  sum may be x or residual."""
+    T, H = _x_of(x)
+    _tensor(weight, "weight", BF16, (H,))
+    for name, t in (("residual", residual), ("sum", sum), ("y", y)):
+        if t is not None:
+            _tensor(t, name, BF16, (T, H))
+    if (q is None) != (q_scale is None):
+        raise ValueError("q and q_scale: both or neither")
+    if q is not None:
+        _tensor(q, "q", I8, (T, H))
+        _tensor(q_scale, "q_scale", F32, (T,))
+    if sum is None and y is None and q is None:
+        raise ValueError("sum, y, q: at least one output")
+    with _On(x, residual, weight, sum, y, q, q_scale):
+        _check(lib().moe_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), eps, T, H, _ptr(sum),
+                                 _ptr(y), _ptr(q), _ptr(q_scale), _stream(stream, x.device)),
+               "moe_norm_i8")
+
+
+def moe_quant_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
+    """Rows of bf16 [R, K] as codes q int8 [R, K] and scales fp32 [R]."""
+    R, K = _x_of(x)
+    _tensor(q, "q", I8, (R, K))
+    _tensor(scale, "scale", F32, (R,))
+    with _On(x, q, scale):
+        _check(lib().moe_quant_i8(_ptr(x), R, K, _ptr(q), _ptr(scale), _stream(stream, x.device)),
+               "moe_quant_i8")
+
+
+def moe_dequant_i8_bf16(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, stream=None):
+    """out bf16 [R, K] = codes int8 [R, K] times the rows' scales fp32 [R]."""
+    R, K = _codes_of(q, scale, "q")
+    _tensor(out, "out", BF16, (R, K))
+    with _On(q, scale, out):
+        _check(lib().moe_dequant_i8_bf16(_ptr(q), _ptr(scale), R, K, _ptr(out),
+                                         _stream(stream, q.device)), "moe_dequant_i8_bf16")
+
+
+def moe_i8_prepack(src: torch.Tensor, dst: torch.Tensor, stream=None):
+    """Row-major codes int8 [n_exp, N, K] into 16 x 64 tiles."""
+    _tensor(src, "src", I8)
+    if src.dim() != 3:
+        raise ValueError("src: expected [n_exp, N, K]")
+    _tensor(dst, "dst", I8, src.shape)
+    with _On(src, dst):
+        _check(lib().moe_i8_prepack(_ptr(src), *src.shape, _ptr(dst), _stream(stream, src.device)),
+               "moe_i8_prepack")
+
+
+def linear_i8_workspace_bytes(M, N, K) -> int:
+    return lib().moe_linear_i8_workspace_bytes(M, N, K)
+
+
+def moe_linear_i8(a: torch.Tensor, a_scale: torch.Tensor, w: DeviceI8Mat, out: torch.Tensor, ws=None,
+                  stream=None):
+    """out bf16 [M, N] = a [M, K] times w's one matrix [N, K], both 8-bit codes with their rows'
+    scales.  ws: linear_i8_workspace_bytes(M, N, K) bytes (None where that is 0)."""
+    M, K = _codes_of(a, a_scale, "a")
+    if not isinstance(w, DeviceI8Mat):
+        raise TypeError("w: expected a DeviceI8Mat")
+    N = w.shape[1]
+    _i8mat_for(w, "w", 1, N, K)
+    _tensor(out, "out", BF16, (M, N))
+    if ws is not None:
+        _ws(ws)
+    with _On(a, a_scale, w.codes, out, ws):
+        _check(lib().moe_linear_i8(_ptr(a), _ptr(a_scale), M, K, _i8mat(w), N, _ptr(out), _ptr(ws),
+                                   0 if ws is None else ws.numel() * ws.element_size(),
+                                   _stream(stream, a.device)), "moe_linear_i8")
+
+
+def moe_route_scored(logits: torch.Tensor, bias, rule: ScoreRule, k: int, block_rows: int,
+                     routing: DeviceRouting, ws: torch.Tensor, stream=None):
+    """moe_route by a ScoreRule, with an optional selection bias fp32 [E]."""
+    _tensor(logits, "logits", F32)
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [T, E]")
+    T, E = logits.shape
+    if bias is not None:
+        _tensor(bias, "bias", F32, (E,))
+    if not isinstance(rule, ScoreRule):
+        raise TypeError("rule: expected a ScoreRule")
+    _routing_for(routing, "routing", T, E, k, block_rows)
+    _ws(ws, "route_ws")
+    with _On(logits, bias, routing.topk_idx, ws):
+        _check(lib().moe_route_scored(_ptr(logits), _ptr(bias), ctypes.byref(rule.struct), T, E, k,
+                                      block_rows, _rt(routing), _ptr(ws),
+                                      ws.numel() * ws.element_size(),
+                                      _stream(stream, logits.device)), "moe_route_scored")
+
+
+def gemm_i8_workspace_bytes(T, H, I, I_sh, E, k, block_rows) -> int:
+    return lib().moe_gemm_i8_workspace_bytes(T, H, I, I_sh, E, k, block_rows)
+
+
+def _expert_i8_mats(mats, E, H, I, I_sh):
+    sh = I_sh > 0
+    for m, name, shape, present in zip(
+            mats, ("gate", "up", "down", "sh_gate", "sh_up", "sh_down"),
+            ((E, I, H), (E, I, H), (E, H, I), (1, I_sh, H), (1, I_sh, H), (1, H, I_sh)),
+            (True, True, True, sh, sh, sh)):
+        _i8mat_for(m, name, *shape, present=present)
+
+
+def moe_grouped_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, I: int, I_sh: int, E: int, k: int,
+                        block_rows: int, routing: DeviceRouting, gate, up, down, sh_gate, sh_up,
+                        sh_down, expert_out: torch.Tensor, shared_out, ws: torch.Tensor,
+                        stream=None):
+    T, H = _codes_of(x, x_scale)
+    _routing_for(routing, "routing", T, E, k, block_rows)
+    mats = (gate, up, down, sh_gate, sh_up, sh_down)
+    _expert_i8_mats(mats, E, H, I, I_sh)
+    _tensor(expert_out, "expert_out", BF16, (T * k, H))
+    _opt_tensor(shared_out, "shared_out", I_sh > 0, BF16, (T, H))
+    _ws(ws)
+    with _On(x, x_scale, routing.topk_idx, *(m.codes for m in mats if m), expert_out, shared_out, ws):
+        _check(lib().moe_grouped_gemm_i8(
+            _ptr(x), _ptr(x_scale), T, H, I, I_sh, E, k, block_rows, _rt(routing),
+            *map(_i8mat, mats), _ptr(expert_out), _ptr(shared_out), _ptr(ws),
+            ws.numel() * ws.element_size(), _stream(stream, x.device)), "moe_grouped_gemm_i8")
+
+
+def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, score_bias, rule,
+                 I: int, I_sh: int, E: int, k: int, block_rows: int, routing: DeviceRouting,
+                 route_ws: torch.Tensor, gate, up, down, sh_gate, sh_up, sh_down,
+                 expert_out: torch.Tensor, shared_out, gemm_ws: torch.Tensor, y: torch.Tensor,
+                 stream=None):
+    """moe_route (rule None) or moe_route_scored, moe_grouped_gemm_i8 and moe_combine in one
+    call."""
+    T, H = _codes_of(x, x_scale)
+    _tensor(logits, "logits", F32, (T, E))
+    if rule is not None and not isinstance(rule, ScoreRule):
+        raise TypeError("rule: expected a ScoreRule")
+    if score_bias is not None:
+        if rule is None:
+            raise ValueError("score_bias: needs a rule")
+        _tensor(score_bias, "score_bias", F32, (E,))
+    _routing_for(routing, "routing", T, E, k, block_rows)
+    mats = (gate, up, down, sh_gate, sh_up, sh_down)
+    _expert_i8_mats(mats, E, H, I, I_sh)
+    _tensor(expert_out, "expert_out", BF16, (T * k, H))
+    _opt_tensor(shared_out, "shared_out", I_sh > 0, BF16, (T, H))
+    _tensor(y, "y", BF16, (T, H))
+    _ws(route_ws, "route_ws")
+    _ws(gemm_ws, "gemm_ws")
+    with _On(x, x_scale, logits, score_bias, routing.topk_idx, route_ws,
+             *(m.codes for m in mats if m), expert_out, shared_out, gemm_ws, y):
+        _check(lib().moe_layer_i8(
+            _ptr(x), _ptr(x_scale), _ptr(logits), _ptr(score_bias),
+            None if rule is None else ctypes.byref(rule.struct), T, H, I, I_sh, E, k, block_rows,
+            *map(_i8mat, mats), _rt(routing), _ptr(route_ws),
+            route_ws.numel() * route_ws.element_size(), _ptr(expert_out), _ptr(shared_out),
+            _ptr(gemm_ws), gemm_ws.numel() * gemm_ws.element_size(), _ptr(y),
+            _stream(stream, x.device)), "moe_layer_i8")
+
+
+# ---------------------------------------------------------------------------
 # Convenience: one layer's device weights and buffers, running the three calls
 # ---------------------------------------------------------------------------
 
@@ -789,6 +1089,74 @@ class MoeLayer:
         moe_layer_chunked(x, logits, self.I, self.I_sh, self.k, self.block_rows, chunk_tokens,
                           *self.weight_mats(), y, ws, stream)
         return ws
+
+
+class MoeLayerI8:
+    """Device-resident 8-bit weights of one layer plus per-call buffers for T tokens."""
+
+    def __init__(self, mats, H: int, I: int, I_sh: int, E: int, k: int, device,
+                 block_rows: int = 32, rule: ScoreRule | None = None, score_bias=None):
+        """mats: DeviceI8Mat objects (gate, up, down, sh_gate, sh_up, sh_down; the shared three
+        None when I_sh is 0).  rule: None routes as moe_route does (softmax over the k chosen)."""
+        self.H, self.I, self.I_sh, self.E, self.k = H, I, I_sh, E, k
+        self.block_rows, self.device = block_rows, torch.device(device)
+        self.mats = tuple(mats)
+        _expert_i8_mats(self.mats, E, H, I, I_sh)
+        self.rule, self.score_bias = rule, score_bias
+        self._bufs = {}
+
+    @classmethod
+    def from_bf16(cls, weights, H: int, I: int, I_sh: int, E: int, k: int, device,
+                  **kw) -> "MoeLayerI8":
+        """weights: bf16 device tensors gate, up [E, I, H], down [E, H, I] and the shared
+        expert's [1, ..] (None when I_sh is 0), quantised by rows and put into tiles."""
+        return cls([None if w is None else DeviceI8Mat.from_bf16(w) for w in weights], H, I, I_sh,
+                   E, k, device, **kw)
+
+    def buffers(self, T: int) -> dict:
+        if T not in self._bufs:
+            d, bf = self.device, dict(dtype=torch.bfloat16, device=self.device)
+            shape = (self.H, self.I, self.I_sh, self.E, self.k, self.block_rows)
+            self._bufs[T] = dict(
+                routing=DeviceRouting(T, self.E, self.k, self.block_rows, d),
+                route_ws=_bytes_tensor(route_workspace_bytes(T, self.E, self.k, self.block_rows), d),
+                gemm_ws=_bytes_tensor(gemm_i8_workspace_bytes(T, *shape), d),
+                expert_out=torch.empty((T * self.k, self.H), **bf),
+                shared_out=torch.empty((T, self.H), **bf) if self.I_sh else None,
+                y=torch.empty((T, self.H), **bf))
+        return self._bufs[T]
+
+    def forward(self, x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor,
+                out: torch.Tensor | None = None, stream=None) -> dict:
+        """One moe_layer_i8 call over codes x int8 [T, H] and their scales; returns the buffers
+        used.  They are this object's and the next call's too: calls on several streams at once
+        need an object each."""
+        b = self.buffers(x.shape[0])
+        y = b["y"] if out is None else out
+        moe_layer_i8(x, x_scale, logits, self.score_bias, self.rule, self.I, self.I_sh, self.E,
+                     self.k, self.block_rows, b["routing"], b["route_ws"], *self.mats,
+                     b["expert_out"], b["shared_out"], b["gemm_ws"], y, stream)
+        return dict(b, y=y)
+
+    def forward_block(self, x: torch.Tensor, residual, norm_weight: torch.Tensor,
+                      w_router: torch.Tensor, eps: float = 1e-6, stream=None) -> dict:
+        """The block around the layer: moe_norm_i8 (x bf16 [T, H] plus the residual), moe_router
+        over the normed tokens, and the layer over their codes.  Returns the buffers used, with
+        the block's residual "sum", the normed tokens "normed", their codes "q" and "q_scale",
+        "logits" and the layer's "y"."""
+        T, H = _x_of(x)
+        b = self.buffers(T)
+        if "sum" not in b:
+            d = self.device
+            b["sum"], b["normed"] = (torch.empty((T, H), dtype=torch.bfloat16, device=d)
+                                     for _ in range(2))
+            b["q"] = torch.empty((T, H), dtype=I8, device=d)
+            b["q_scale"] = torch.empty(T, dtype=F32, device=d)
+            b["logits"] = torch.empty((T, self.E), dtype=F32, device=d)
+        moe_norm_i8(x, residual, norm_weight, eps, b["sum"], b["normed"], b["q"], b["q_scale"],
+                    stream)
+        moe_router(b["normed"], w_router, b["logits"], stream=stream)
+        return self.forward(b["q"], b["q_scale"], b["logits"], stream=stream)
 
 
 def bf16_from_bits(bits_np, device) -> torch.Tensor:

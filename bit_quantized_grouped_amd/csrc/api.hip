@@ -8,6 +8,7 @@
 #include <new>
 
 #include "../../include/moe_q4.h"
+#include "moe_i8.h"
 #include "moe_launch.h"
 
 using namespace moeq4;
@@ -793,6 +794,241 @@ int moe_layer_chunked(const uint16_t* x, const float* logits, int T, int H, int 
             if (st) return st;
         }
         return MOE_OK;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+// ---- 8-bit operators ----
+
+// Sums of products of two 8-bit codes stay below 2^31 up to here (128 * 128 * K).
+static constexpr int kMaxKI8 = 131072;
+
+static bool valid_k_i8(int K) { return K >= 64 && K % 64 == 0 && K < kMaxKI8; }
+
+static int check_i8_mat(const moe_i8_mat* m, int N) {
+    if (!m || !m->codes || !m->scales) return MOE_ERR_NULL;
+    if (!aligned(m->codes, 16) || !aligned(m->scales, 4)) return MOE_ERR_ALIGN;
+    if (m->layout != MOE_I8_LAYOUT_ROWS && m->layout != MOE_I8_LAYOUT_TILES) return MOE_ERR_SHAPE;
+    if (m->layout == MOE_I8_LAYOUT_TILES && N % 16) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+static I8MatDev i8_dev(const moe_i8_mat* m) {
+    return m ? I8MatDev{m->codes, m->scales, m->layout} : I8MatDev{};
+}
+
+int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                int T, int H, uint16_t* sum, uint16_t* y, int8_t* q, float* q_scale,
+                hipStream_t stream) {
+    try {
+        if (T < 1 || H < 64 || H % 64 || H > kMaxNormWidth) return MOE_ERR_SHAPE;
+        if (!(eps > 0.f) || eps > 3.4e38f) return MOE_ERR_SHAPE;
+        if (!x || !weight || !q != !q_scale || (!sum && !y && !q)) return MOE_ERR_NULL;
+        if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+            !aligned(sum, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(q_scale, 4))
+            return MOE_ERR_ALIGN;
+        const hipError_t e = launch_norm_i8(x, residual, weight, eps, T, H, sum, y, q, q_scale, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+int moe_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, hipStream_t stream) {
+    try {
+        if (R < 1 || K < 64 || K % 64 || K > kMaxNormWidth) return MOE_ERR_SHAPE;
+        if (!x || !q || !scale) return MOE_ERR_NULL;
+        if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_ALIGN;
+        const hipError_t e = launch_quant_i8(x, R, K, q, scale, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+int moe_dequant_i8_bf16(const int8_t* q, const float* scale, int R, int K, uint16_t* out,
+                        hipStream_t stream) {
+    try {
+        if (R < 1 || K < 64 || K % 64) return MOE_ERR_SHAPE;
+        if (!q || !scale || !out) return MOE_ERR_NULL;
+        if (!aligned(q, 16) || !aligned(scale, 4) || !aligned(out, 16)) return MOE_ERR_ALIGN;
+        const hipError_t e = launch_dequant_i8(q, scale, R, K, out, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+int moe_i8_prepack(const int8_t* src, int n_exp, int N, int K, int8_t* dst, hipStream_t stream) {
+    try {
+        if (n_exp < 1 || N < 16 || N % 16 || K < 64 || K % 64) return MOE_ERR_SHAPE;
+        if ((long double)n_exp * N * K >= (long double)(1ll << 40)) return MOE_ERR_SHAPE;
+        if (!src || !dst || src == dst) return MOE_ERR_NULL;
+        if (!aligned(src, 16) || !aligned(dst, 16)) return MOE_ERR_ALIGN;
+        const hipError_t e = launch_prepack_i8(src, n_exp, N, K, dst, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+static int check_linear_shape(int M, int N, int K) {
+    if (M < 1 || N < 1 || !valid_k_i8(K)) return MOE_ERR_SHAPE;
+    if ((long long)M * K >= (1ll << 31) || (long long)N * K >= (1ll << 31) ||
+        (long long)M * N >= (1ll << 40))
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+size_t moe_linear_i8_workspace_bytes(int M, int N, int K) {
+    return check_linear_shape(M, N, K) ? 0 : linear_i8_ws_bytes(M, N, K);
+}
+
+int moe_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
+                  uint16_t* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+    try {
+        int st = check_linear_shape(M, N, K);
+        if (st) return st;
+        if (!a || !a_scale || !out) return MOE_ERR_NULL;
+        if ((st = check_i8_mat(w, N))) return st;
+        if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(out, 16)) return MOE_ERR_ALIGN;
+        const size_t need = linear_i8_ws_bytes(M, N, K);
+        if (need && (st = check_ws(ws, ws_bytes, need))) return st;
+        const hipError_t e = launch_linear_i8(a, a_scale, M, K, i8_dev(w), N, out, ws, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+static int check_rule(const moe_score_rule* rule, int E, int k, ScoreRule* dev) {
+    if (!rule) return MOE_ERR_NULL;
+    if (rule->score != MOE_SCORE_SOFTMAX && rule->score != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
+    if (rule->group_score != MOE_GROUP_MAX && rule->group_score != MOE_GROUP_TOP2)
+        return MOE_ERR_SHAPE;
+    if (rule->renormalise != 0 && rule->renormalise != 1) return MOE_ERR_SHAPE;
+    if (!(rule->scale >= -3.4e38f && rule->scale <= 3.4e38f)) return MOE_ERR_SHAPE;
+    const int G = rule->n_groups;
+    if (G < 1 || G > kScoredMaxGroups || E % G || rule->topk_groups < 1 || rule->topk_groups > G)
+        return MOE_ERR_SHAPE;
+    if (G > 1 && rule->group_score == MOE_GROUP_TOP2 && E / G < 2) return MOE_ERR_SHAPE;
+    if (k > kScoredMaxK || k > rule->topk_groups * (E / G)) return MOE_ERR_SHAPE;
+    *dev = ScoreRule{rule->score, G, rule->topk_groups, rule->group_score, rule->renormalise,
+                     rule->scale};
+    return MOE_OK;
+}
+
+int moe_route_scored(const float* logits, const float* bias, const moe_score_rule* rule, int T,
+                     int E, int k, int block_rows, const moe_routing* out, void* ws,
+                     size_t ws_bytes, hipStream_t stream) {
+    try {
+        int st = check_route_shape(T, E, k, block_rows);
+        if (st) return st;
+        ScoreRule dev;
+        if ((st = check_rule(rule, E, k, &dev))) return st;
+        const size_t need = moe_route_workspace_bytes(T, E, k, block_rows);
+        if (!logits || (need && !ws)) return MOE_ERR_NULL;
+        if ((st = check_routing(out))) return st;
+        if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ws, 256)) return MOE_ERR_ALIGN;
+        if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+        const hipError_t e =
+            launch_route_scored(logits, bias, dev, T, E, k, block_rows,
+                                max_blocks_of(T, E, k, block_rows), to_dev(out), ws, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+static int check_layer_i8_shape(int T, int H, int I, int I_sh, int E, int k, int block_rows) {
+    const int st = check_layer_shape(T, H, I, I_sh, E, k, block_rows);
+    if (st) return st;
+    if (H >= kMaxKI8 || I >= kMaxKI8 || I_sh >= kMaxKI8) return MOE_ERR_SHAPE;
+    if ((long long)H * (I > I_sh ? I : I_sh) >= (1ll << 31)) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+size_t moe_gemm_i8_workspace_bytes(int T, int H, int I, int I_sh, int E, int k, int block_rows) {
+    if (check_layer_i8_shape(T, H, I, I_sh, E, k, block_rows)) return 0;
+    return gemm_i8_ws_layout(T, I, I_sh, k).total;
+}
+
+static int gemm_i8_args(const int8_t* x, const float* x_scale, int T, int H, int I, int I_sh, int E,
+                        int k, int block_rows, const moe_routing* r, const moe_i8_mat* gate,
+                        const moe_i8_mat* up, const moe_i8_mat* down, const moe_i8_mat* sh_gate,
+                        const moe_i8_mat* sh_up, const moe_i8_mat* sh_down, uint16_t* expert_out,
+                        uint16_t* shared_out, void* ws, size_t ws_bytes, GemmI8Problem* p) {
+    int st = check_layer_i8_shape(T, H, I, I_sh, E, k, block_rows);
+    if (st) return st;
+    if (!x || !x_scale || !expert_out) return MOE_ERR_NULL;
+    if ((st = check_routing(r))) return st;
+    if ((st = check_i8_mat(gate, I)) || (st = check_i8_mat(up, I)) || (st = check_i8_mat(down, H)))
+        return st;
+    if (gate->layout != up->layout) return MOE_ERR_SHAPE;
+    if (I_sh) {
+        if (!shared_out) return MOE_ERR_NULL;
+        if ((st = check_i8_mat(sh_gate, I_sh)) || (st = check_i8_mat(sh_up, I_sh)) ||
+            (st = check_i8_mat(sh_down, H)))
+            return st;
+        if (sh_gate->layout != sh_up->layout) return MOE_ERR_SHAPE;
+        if (!aligned(shared_out, 16)) return MOE_ERR_ALIGN;
+    } else if (sh_gate || sh_up || sh_down || shared_out) {
+        return MOE_ERR_SHAPE;   // shared matrices given but I_sh == 0
+    }
+    if (!aligned(x, 16) || !aligned(x_scale, 4) || !aligned(expert_out, 16)) return MOE_ERR_ALIGN;
+    if ((st = check_ws(ws, ws_bytes, gemm_i8_ws_layout(T, I, I_sh, k).total))) return st;
+    *p = GemmI8Problem{x, x_scale, T, H, I, I_sh, E, k, block_rows, max_blocks_of(T, E, k, block_rows),
+                       to_dev(r), i8_dev(gate), i8_dev(up), i8_dev(down), i8_dev(sh_gate),
+                       i8_dev(sh_up), i8_dev(sh_down), expert_out, shared_out};
+    return MOE_OK;
+}
+
+int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int I, int I_sh, int E,
+                        int k, int block_rows, const moe_routing* r, const moe_i8_mat* gate,
+                        const moe_i8_mat* up, const moe_i8_mat* down, const moe_i8_mat* sh_gate,
+                        const moe_i8_mat* sh_up, const moe_i8_mat* sh_down, uint16_t* expert_out,
+                        uint16_t* shared_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+    try {
+        GemmI8Problem p;
+        const int st = gemm_i8_args(x, x_scale, T, H, I, I_sh, E, k, block_rows, r, gate, up, down,
+                                    sh_gate, sh_up, sh_down, expert_out, shared_out, ws, ws_bytes, &p);
+        if (st) return st;
+        return launch_grouped_i8(p, ws, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
+                 const float* score_bias, const moe_score_rule* rule, int T, int H, int I, int I_sh,
+                 int E, int k, int block_rows, const moe_i8_mat* gate, const moe_i8_mat* up,
+                 const moe_i8_mat* down, const moe_i8_mat* sh_gate, const moe_i8_mat* sh_up,
+                 const moe_i8_mat* sh_down, const moe_routing* r, void* route_ws,
+                 size_t route_ws_bytes, uint16_t* expert_out, uint16_t* shared_out, void* gemm_ws,
+                 size_t gemm_ws_bytes, uint16_t* y, hipStream_t stream) {
+    try {
+        GemmI8Problem p;
+        int st = gemm_i8_args(x, x_scale, T, H, I, I_sh, E, k, block_rows, r, gate, up, down,
+                              sh_gate, sh_up, sh_down, expert_out, shared_out, gemm_ws,
+                              gemm_ws_bytes, &p);
+        if (st) return st;
+        if (!logits || !y) return MOE_ERR_NULL;
+        if (!aligned(logits, 4) || !aligned(score_bias, 4) || !aligned(y, 16)) return MOE_ERR_ALIGN;
+        ScoreRule dev{};
+        if (rule && (st = check_rule(rule, E, k, &dev))) return st;
+        if (!rule && score_bias) return MOE_ERR_SHAPE;   // a bias orders scores: it needs a rule
+        const size_t need = moe_route_workspace_bytes(T, E, k, block_rows);
+        if (need && (st = check_ws(route_ws, route_ws_bytes, need))) return st;
+        hipError_t e = rule ? launch_route_scored(logits, score_bias, dev, T, E, k, block_rows,
+                                                  p.max_blocks, p.r, route_ws, stream)
+                            : launch_route(logits, T, E, k, block_rows, p.max_blocks, p.r, route_ws,
+                                           stream);
+        if (e == hipSuccess) e = launch_grouped_i8(p, gemm_ws, stream);
+        if (e == hipSuccess)
+            e = launch_combine(expert_out, shared_out, nullptr, p.r.assign_row, p.r.topk_w, T, H, k,
+                               y, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
     } catch (...) {
         return MOE_ERR_HIP;
     }

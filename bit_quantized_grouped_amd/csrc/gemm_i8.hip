@@ -1,0 +1,339 @@
+// Products of 8-bit codes with one scale per activation row and one per weight
+// row: out[m, n] = a_scale[m] * w_scale[n] * sum_k a[m, k] * w[n, k].  The sum
+// is a 32-bit integer and exact (K <= kMaxKI8), so its order does not matter;
+// the two scales are applied in fp32 and the result rounded once.
+//
+// moe_linear_i8 is the dense form.  The experts' FFNs run over the row blocks of
+// moe_route: gate/up with SwiGLU into fp32 h, a row-wise quantisation of h, and
+// down; the shared expert's rows are dense row blocks in front of the routed ones.
+//
+// Tiles go straight from memory into the MFMA operands: lane l of a 16 x 64
+// tile holds row l % 16, K 16*(l/16) .. +15, 16 bytes, for the weights (A
+// operand) and the activations (B operand) alike.
+#include "moe_device.h"
+#include "moe_i8.h"
+
+namespace moeq4 {
+
+// D = A(16x64) * B(64x16) + C.  Lane l supplies A[l%16][16*(l/16) .. +16] and
+// B[16*(l/16) .. +16][l%16]; it holds D[4*(l/16) + i][l%16], i = 0..3.
+__device__ __forceinline__ i32x4_t mfma_i8(i32x4_t a, i32x4_t b, i32x4_t c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// acc[n][m] += weight tile n x activation tile m over the 64-K steps [s0, s1), by
+// one wave, D steps ahead.  w: tile n's first byte (uniform), w_lane its lane
+// offset, w_step the bytes from one step to the next; a_lane: the lane's row and
+// K offset in a, 64 bytes a step.
+template <int NT, int MT, int D>
+__device__ __forceinline__ void wave_product(const int8_t* const (&w)[NT],
+                                             const uint32_t (&w_lane)[NT], uint32_t w_step,
+                                             const int8_t* a, const uint32_t (&a_lane)[MT], int s0,
+                                             int s1, i32x4_t (&acc)[NT][MT]) {
+    i32x4_t wv[D][NT], av[D][MT];
+    auto load = [&](int d, int s) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            wv[d][n] = *(const i32x4_t*)(w[n] + (w_lane[n] + (uint32_t)s * w_step));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            av[d][m] = *(const i32x4_t*)(a + (a_lane[m] + (uint32_t)s * 64u));
+    };
+    auto mul = [&](int d) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[n][m] = mfma_i8(wv[d][n], av[d][m], acc[n][m]);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (s0 + d < s1) load(d, s0 + d);
+    int s = s0;
+    for (; s + 2 * D <= s1; s += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            mul(d);
+            load(d, s + D + d);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (s + d < s1) {
+            mul(d);
+            if (s + D + d < s1) load(d, s + D + d);
+        }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (s + D + d < s1) mul(d);
+}
+
+// Sum over the WK waves that share a tile; the first of them holds the result.
+template <int NT, int MT, int WN, int WK>
+__device__ __forceinline__ void reduce_waves(i32x4_t (&acc)[NT][MT], int wn, int wk) {
+    if (WK == 1) return;
+    __shared__ i32x4_t s_part[WK > 1 ? (WK - 1) * WN * NT * MT * WAVE : 1];
+    const int lane = threadIdx.x % WAVE;
+    if (wk) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                s_part[((((wk - 1) * WN + wn) * NT + n) * MT + m) * WAVE + lane] = acc[n][m];
+    }
+    __syncthreads();
+    if (wk) return;
+    for (int o = 0; o < WK - 1; ++o)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[n][m] += s_part[(((o * WN + wn) * NT + n) * MT + m) * WAVE + lane];
+}
+
+// One part of a launch: the dense rows (the shared expert's, or a linear's) or
+// the routed rows.
+struct PartI8 {
+    const int8_t* a;
+    const float* a_scale;
+    I8MatDev w, w2;         // w2: the up matrices of gate/up
+    int M, N, K;            // M: rows of a dense part
+    void* out;              // bf16, or fp32 h of gate/up
+};
+
+struct ProductArgs {
+    PartI8 dense, routed;
+    int dense_blocks, dense_tiles, routed_tiles;
+    int block_rows, k;
+    const int32_t* block_expert;
+    const int32_t* block_row;
+    const int32_t* offsets;
+    const int32_t* sorted_assign;   // gate/up: row -> assignment
+};
+
+// Workgroup of WN x WK waves: WN*NT*16 columns of MT*16 rows, K split over WK waves.
+// GATEUP: the wave's NT tiles are the gate's and then the up's same NT/2 tiles.
+template <int MT, int NT, int WN, int WK, int D, bool GATEUP>
+__global__ __launch_bounds__(WN* WK* WAVE) void product_i8_kernel(ProductArgs p) {
+    constexpr int COLS = GATEUP ? NT / 2 : NT;   // 16-column tiles per wave
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+    const int wn = wave % WN, wk = wave / WN;
+    const int dense_wgs = p.dense_blocks * p.dense_tiles;
+    const bool dense = (int)blockIdx.x < dense_wgs;
+    const int id = dense ? blockIdx.x : blockIdx.x - dense_wgs;
+    const int tiles = dense ? p.dense_tiles : p.routed_tiles;
+    const int block = id / tiles, tile = id - block * tiles;
+    const PartI8& part = dense ? p.dense : p.routed;
+    int e = 0, row0 = block * MT * 16, rows = part.M - row0;
+    if (!dense) {
+        e = p.block_expert[block];
+        if (e < 0) return;
+        row0 = p.block_row[block];
+        rows = p.offsets[e + 1] - row0;
+    }
+    rows = min(rows, dense ? MT * 16 : p.block_rows);
+    const int K = part.K, N = part.N;
+    const int col0 = (tile * WN + wn) * COLS * 16;
+    if (col0 >= N && WK == 1) return;
+
+    uint32_t a_lane[MT];
+    float a_scale[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        // rows behind the block's last read its last row; their results go nowhere
+        int r = row0 + min(m * 16 + lane % 16, rows - 1);
+        if (GATEUP && !dense) r = p.sorted_assign[r] / p.k;
+        a_lane[m] = (uint32_t)r * (uint32_t)K + (lane / 16) * 16;
+        a_scale[m] = part.a_scale[r];
+    }
+    const bool tiled = part.w.tiles;
+    const size_t expert = (size_t)e * N * K;
+    const int8_t* w[NT];
+    uint32_t w_lane[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const I8MatDev& mat = GATEUP && n >= COLS ? part.w2 : part.w;
+        const int c = min(col0 + (GATEUP ? n % COLS : n) * 16, (N - 1) / 16 * 16);
+        w[n] = mat.codes + expert + (size_t)c * K;
+        w_lane[n] = tiled ? lane * 16
+                          : (uint32_t)min(lane % 16, N - 1 - c) * (uint32_t)K + (lane / 16) * 16;
+    }
+    i32x4_t acc[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
+    const int steps = K / 64;
+    wave_product<NT, MT, D>(w, w_lane, tiled ? 1024u : 64u, part.a, a_lane, steps * wk / WK,
+                            steps * (wk + 1) / WK, acc);
+    reduce_waves<NT, MT, WN, WK>(acc, wn, wk);
+    if (WK > 1 && wk) return;
+
+#pragma unroll
+    for (int n = 0; n < COLS; ++n) {
+        const int c = col0 + n * 16 + (lane / 16) * 4;
+        if (c >= N) continue;
+        float ws[4], ws2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ci = min(c + i, N - 1);
+            ws[i] = part.w.scales[(size_t)e * N + ci];
+            if (GATEUP) ws2[i] = part.w2.scales[(size_t)e * N + ci];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = m * 16 + lane % 16;
+            if (r >= rows) continue;
+            const size_t at = (size_t)(row0 + r) * N + c;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = (float)acc[n][m][i] * a_scale[m] * ws[i];
+                if (GATEUP)
+                    v[i] = silu_f32(v[i]) * ((float)acc[n + COLS][m][i] * a_scale[m] * ws2[i]);
+            }
+            if (GATEUP) {
+                *(f32x4_t*)((float*)part.out + at) = f32x4_t{v[0], v[1], v[2], v[3]};
+            } else {
+                uint16_t* o = (uint16_t*)part.out + at;
+                if (N % 4 == 0) {
+                    *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < N) o[i] = (uint16_t)pack_bf16x2(v[i], 0.f);
+                }
+            }
+        }
+    }
+}
+
+// Row-wise quantisation of h: one workgroup per row, the routed rows and then the
+// shared expert's.
+constexpr int kQuantThreads = 128;
+__global__ __launch_bounds__(kQuantThreads) void quant_h_kernel(
+    const float* __restrict__ h, const float* __restrict__ h_sh, int n_routed, int I, int I_sh,
+    int8_t* __restrict__ q, int8_t* __restrict__ q_sh, float* __restrict__ scale,
+    float* __restrict__ scale_sh) {
+    const bool routed = (int)blockIdx.x < n_routed;
+    const int r = routed ? blockIdx.x : blockIdx.x - n_routed;
+    const int K = routed ? I : I_sh;
+    const float* src = (routed ? h : h_sh) + (size_t)r * K;
+    int8_t* dst = (routed ? q : q_sh) + (size_t)r * K;
+    float top = 0.f;
+    for (int c = threadIdx.x * 4; c < K; c += kQuantThreads * 4) {
+        const f32x4_t v = *(const f32x4_t*)(src + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int off = WAVE / 2; off >= 1; off >>= 1) top = fmaxf(top, shfl_xor(top, off));
+    __shared__ float s_top[kQuantThreads / WAVE];
+    if (threadIdx.x % WAVE == 0) s_top[threadIdx.x / WAVE] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQuantThreads / WAVE; ++i) top = fmaxf(top, s_top[i]);
+    const float to_code = top > 0.f ? 127.0f / top : 0.f;
+    if (threadIdx.x == 0) (routed ? scale : scale_sh)[r] = top / 127.0f;
+    for (int c = threadIdx.x * 4; c < K; c += kQuantThreads * 4) {
+        const f32x4_t v = *(const f32x4_t*)(src + c);
+        *(uint32_t*)(dst + c) =
+            pack_codes(v[0] * to_code, v[1] * to_code, v[2] * to_code, v[3] * to_code);
+    }
+}
+
+// Rows to 16 x 64 tiles: piece (n, k / 16) of 16 bytes to its place.
+__global__ void prepack_i8_kernel(const i32x4_t* __restrict__ src, size_t pieces, int N, int K,
+                                  i32x4_t* __restrict__ dst) {
+    const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= pieces) return;
+    // i counts destination pieces: tile (row tile, K step), then 16-K piece, then row
+    const size_t tile = i / 64;
+    const int in = (int)(i % 64), steps = K / 64;
+    const size_t rt = tile / steps;   // 16-row tile over all experts (N is a multiple of 16)
+    const int s = (int)(tile % steps);
+    dst[i] = src[(rt * 16 + in % 16) * (size_t)(K / 16) + s * 4 + in / 16];
+}
+
+hipError_t launch_prepack_i8(const int8_t* src, int n_exp, int N, int K, int8_t* dst,
+                             hipStream_t stream) {
+    const size_t pieces = (size_t)n_exp * N * K / 16;
+    prepack_i8_kernel<<<(unsigned)((pieces + 255) / 256), 256, 0, stream>>>(
+        (const i32x4_t*)src, pieces, N, K, (i32x4_t*)dst);
+    return hipGetLastError();
+}
+
+size_t linear_i8_ws_bytes(int, int, int) { return 0; }
+
+static int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+template <int MT, int NT, int WN, int WK, int D, bool GATEUP>
+static void launch_product(ProductArgs& p, int routed_blocks, hipStream_t stream) {
+    const int cols = (GATEUP ? NT / 2 : NT) * 16 * WN;
+    p.dense_blocks = p.dense.out ? cdiv(p.dense.M, MT * 16) : 0;
+    p.dense_tiles = p.dense.out ? cdiv(p.dense.N, cols) : 1;
+    p.routed_tiles = routed_blocks ? cdiv(p.routed.N, cols) : 1;
+    const unsigned grid = (unsigned)(p.dense_blocks * p.dense_tiles + routed_blocks * p.routed_tiles);
+    product_i8_kernel<MT, NT, WN, WK, D, GATEUP><<<grid, WN * WK * WAVE, 0, stream>>>(p);
+}
+
+hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
+                            int N, uint16_t* out, void*, hipStream_t stream) {
+    ProductArgs p{};
+    p.dense = PartI8{a, a_scale, w, {}, M, N, K, out};
+    if (M <= 16) launch_product<1, 1, 1, 4, 8, false>(p, 0, stream);
+    else launch_product<4, 2, 4, 1, 2, false>(p, 0, stream);
+    return hipGetLastError();
+}
+
+GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k) {
+    GemmI8Ws L{};
+    const size_t n = (size_t)T * k;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += align_up(bytes, 256);
+        return at;
+    };
+    L.h = take(n * I * 4);
+    L.h_sh = take((size_t)T * I_sh * 4);
+    L.q = take(n * I);
+    L.q_sh = take((size_t)T * I_sh);
+    L.scale = take(n * 4);
+    L.scale_sh = take(I_sh ? (size_t)T * 4 : 0);
+    L.total = o;
+    return L;
+}
+
+hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t stream) {
+    const GemmI8Ws L = gemm_i8_ws_layout(g.T, g.I, g.I_sh, g.k);
+    char* base = (char*)ws;
+    float *h = (float*)(base + L.h), *h_sh = (float*)(base + L.h_sh);
+    int8_t *q = (int8_t*)(base + L.q), *q_sh = (int8_t*)(base + L.q_sh);
+    float *scale = (float*)(base + L.scale), *scale_sh = (float*)(base + L.scale_sh);
+    ProductArgs p{};
+    p.block_rows = g.block_rows;
+    p.k = g.k;
+    p.block_expert = g.r.block_expert;
+    p.block_row = g.r.block_row;
+    p.offsets = g.r.offsets;
+    p.sorted_assign = g.r.sorted_assign;
+    p.routed = PartI8{g.x, g.x_scale, g.gate, g.up, 0, g.I, g.H, h};
+    if (g.I_sh) p.dense = PartI8{g.x, g.x_scale, g.sh_gate, g.sh_up, g.T, g.I_sh, g.H, h_sh};
+    if (g.block_rows == 16) launch_product<1, 2, 4, 1, 4, true>(p, g.max_blocks, stream);
+    else if (g.block_rows == 32) launch_product<2, 2, 4, 1, 4, true>(p, g.max_blocks, stream);
+    else launch_product<4, 2, 4, 1, 2, true>(p, g.max_blocks, stream);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const int n = g.T * g.k;
+    quant_h_kernel<<<n + (g.I_sh ? g.T : 0), kQuantThreads, 0, stream>>>(
+        h, h_sh, n, g.I, g.I_sh, q, q_sh, scale, scale_sh);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out};
+    if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out};
+    if (g.block_rows == 16) launch_product<1, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
+    else if (g.block_rows == 32) launch_product<2, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
+    else launch_product<4, 2, 4, 1, 2, false>(p, g.max_blocks, stream);
+    return hipGetLastError();
+}
+
+}  // namespace moeq4

@@ -1,0 +1,84 @@
+// Internal interface and device helpers of the 8-bit operators (norm_i8.hip,
+// gemm_i8.hip, the scored routing of route.hip).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_launch.h"
+
+namespace moeq4 {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// Widest row of the norm and the row quantisation: 8 waves of 4 pieces of 8.
+constexpr int kMaxNormWidth = 16384;
+
+struct I8MatDev {
+    const int8_t* codes;
+    const float* scales;   // [n_exp, N]
+    int tiles;             // 0: rows [N, K]; 1: 16 x 64 tiles (moe_i8_prepack)
+};
+
+constexpr int kScoredMaxK = 64;        // one slot per lane of the selecting wave
+constexpr int kScoredMaxGroups = 64;   // one group per lane
+
+// Selection rule of the scored routing (moe_score_rule with its checks done).
+struct ScoreRule {
+    int sigmoid;       // 0: softmax
+    int n_groups, topk_groups;
+    int top2;          // a group's worth: its two best choices' sum, else its best choice
+    int renormalise;
+    float scale;
+};
+
+#ifdef __HIPCC__
+// Four values rounded to nearest even as 8-bit codes, the first in the low byte.
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
+    const int ia = (int)__builtin_rintf(a), ib = (int)__builtin_rintf(b);
+    const int ic = (int)__builtin_rintf(c), id = (int)__builtin_rintf(d);
+    return (uint32_t)(ia & 255) | (uint32_t)(ib & 255) << 8 | (uint32_t)(ic & 255) << 16 |
+           (uint32_t)id << 24;
+}
+#endif
+
+// norm_i8.hip
+hipError_t launch_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                          float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,
+                          float* q_scale, hipStream_t stream);
+hipError_t launch_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale,
+                           hipStream_t stream);
+hipError_t launch_dequant_i8(const int8_t* q, const float* scale, int R, int K, uint16_t* out,
+                             hipStream_t stream);
+
+// route.hip
+hipError_t launch_route_scored(const float* logits, const float* bias, const ScoreRule& rule, int T,
+                               int E, int k, int block_rows, int max_blocks, const RoutingDev& r,
+                               void* ws, hipStream_t stream);
+
+// gemm_i8.hip
+hipError_t launch_prepack_i8(const int8_t* src, int n_exp, int N, int K, int8_t* dst,
+                             hipStream_t stream);
+size_t linear_i8_ws_bytes(int M, int N, int K);
+hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
+                            int N, uint16_t* out, void* ws, hipStream_t stream);
+struct GemmI8Problem {
+    const int8_t* x;          // [T, H]
+    const float* x_scale;     // [T]
+    int T, H, I, I_sh, E, k, block_rows, max_blocks;
+    RoutingDev r;
+    I8MatDev gate, up, down, sh_gate, sh_up, sh_down;
+    uint16_t* expert_out;
+    uint16_t* shared_out;
+};
+// Workspace: SwiGLU activations fp32 (routed rows, then the shared expert's),
+// their 8-bit codes and one scale per row.
+struct GemmI8Ws {
+    size_t h, h_sh, q, q_sh, scale, scale_sh, total;
+};
+GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k);
+hipError_t launch_grouped_i8(const GemmI8Problem& p, void* ws, hipStream_t stream);
+
+}  // namespace moeq4

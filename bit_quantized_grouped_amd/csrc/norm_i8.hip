@@ -1,0 +1,180 @@
+// Root-mean-square norm with the residual's addition and an 8-bit output, the
+// row-wise 8-bit quantisation alone, and the way back to bf16.
+//
+//   v = x + residual (fp32), m = mean(v^2), y = v * weight / sqrt(m + eps),
+//   scale = max|y| / 127, q = rne(y * (127 / max|y|)); a row of zeros has scale 0.
+//
+// max|y| = max|v * weight| / sqrt(m + eps), so the sum of squares and the
+// maximum come out of one pass over registers and one joint reduction: a row
+// is read once and written once.
+#include "moe_device.h"
+#include "moe_i8.h"
+
+namespace moeq4 {
+
+constexpr int kNormRows = 4;   // rows per workgroup where one wave takes a row
+
+__device__ __forceinline__ void unpack_bf16x8(u32x4_t w, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+        f[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ u32x4_t pack_bf16x8(const float (&f)[8]) {
+    u32x4_t w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    return w;
+}
+
+// NW waves per row, V 8-element pieces per lane, NORM false: quantisation only.
+template <int NW, int V, bool NORM>
+__global__ __launch_bounds__(NW == 1 ? kNormRows * WAVE : NW * WAVE) void norm_i8_kernel(
+    const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
+    int T, int H, uint16_t* sum, uint16_t* y, int8_t* q, float* q_scale) {
+    // sum may be x or residual: a lane stores only what it has loaded itself
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+    const int t = NW == 1 ? blockIdx.x * kNormRows + wave : blockIdx.x;
+    if (NW == 1 && t >= T) return;
+    const int tid = NW == 1 ? lane : (int)threadIdx.x;
+    const size_t row = (size_t)t * H;
+    float f[V][8], w[V][8];
+    float sq = 0.f, top = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * NW * WAVE + tid) * 8;
+        u32x4_t a = {0, 0, 0, 0};
+        if (c < H) a = *(const u32x4_t*)(x + row + c);
+        unpack_bf16x8(a, f[v]);
+        if (NORM) {
+            u32x4_t wv = {0, 0, 0, 0};
+            if (c < H) wv = *(const u32x4_t*)(weight + c);
+            unpack_bf16x8(wv, w[v]);
+            if (residual && c < H) {
+                float r[8];
+                unpack_bf16x8(*(const u32x4_t*)(residual + row + c), r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[v][i] += r[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (NORM) {
+                sq = __builtin_fmaf(f[v][i], f[v][i], sq);
+                w[v][i] *= f[v][i];
+                top = fmaxf(top, fabsf(w[v][i]));
+            } else {
+                top = fmaxf(top, fabsf(f[v][i]));
+            }
+        }
+#pragma unroll
+    for (int off = WAVE / 2; off >= 1; off >>= 1) {
+        if (NORM) sq += shfl_xor(sq, off);
+        top = fmaxf(top, shfl_xor(top, off));
+    }
+    if (NW > 1) {
+        __shared__ float s_sq[NW], s_top[NW];
+        if (lane == 0) {
+            s_sq[wave] = sq;
+            s_top[wave] = top;
+        }
+        __syncthreads();
+        sq = s_sq[0];
+        top = s_top[0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) {
+            sq += s_sq[i];
+            top = fmaxf(top, s_top[i]);
+        }
+    }
+    const float inv = NORM ? 1.0f / sqrtf(sq / (float)H + eps) : 1.0f;
+    top *= inv;
+    const float to_code = top > 0.f ? 127.0f / top : 0.f;
+    if (q_scale && tid == 0) q_scale[t] = top / 127.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * NW * WAVE + tid) * 8;
+        if (c >= H) break;
+        if (NORM && sum) *(u32x4_t*)(sum + row + c) = pack_bf16x8(f[v]);
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = NORM ? w[v][i] * inv : f[v][i];
+        if (NORM && y) *(u32x4_t*)(y + row + c) = pack_bf16x8(o);
+        if (q) {
+            u32x2_t p;
+            p[0] = pack_codes(o[0] * to_code, o[1] * to_code, o[2] * to_code, o[3] * to_code);
+            p[1] = pack_codes(o[4] * to_code, o[5] * to_code, o[6] * to_code, o[7] * to_code);
+            *(u32x2_t*)(q + row + c) = p;
+        }
+    }
+}
+
+template <bool NORM>
+static hipError_t launch_rows(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                              float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,
+                              float* q_scale, hipStream_t stream) {
+#define MOE_NORM(NW, V)                                                                         \
+    norm_i8_kernel<NW, V, NORM><<<NW == 1 ? (T + kNormRows - 1) / kNormRows : T,                \
+                                  NW == 1 ? kNormRows * WAVE : NW * WAVE, 0, stream>>>(         \
+        x, residual, weight, eps, T, H, sum, y, q, q_scale)
+    if (H <= 512) MOE_NORM(1, 1);
+    else if (H <= 1024) MOE_NORM(1, 2);
+    else if (H <= 2048) MOE_NORM(1, 4);
+    else if (H <= 4096) MOE_NORM(4, 2);
+    else if (H <= 8192) MOE_NORM(4, 4);
+    else MOE_NORM(8, 4);   // up to kMaxNormWidth
+#undef MOE_NORM
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                          float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,
+                          float* q_scale, hipStream_t stream) {
+    return launch_rows<true>(x, residual, weight, eps, T, H, sum, y, q, q_scale, stream);
+}
+
+hipError_t launch_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale,
+                           hipStream_t stream) {
+    return launch_rows<false>(x, nullptr, nullptr, 0.f, R, K, nullptr, nullptr, q, scale, stream);
+}
+
+// One wave per row: 16 codes in, 16 bf16 out per lane and step.
+constexpr int kDequantRows = 4;
+__global__ __launch_bounds__(kDequantRows * WAVE) void dequant_i8_kernel(
+    const int8_t* __restrict__ q, const float* __restrict__ scale, int R, int K,
+    uint16_t* __restrict__ out) {
+    const int lane = threadIdx.x % WAVE;
+    const int r = blockIdx.x * kDequantRows + threadIdx.x / WAVE;
+    if (r >= R) return;
+    const float s = scale[r];
+    const int8_t* src = q + (size_t)r * K;
+    uint16_t* dst = out + (size_t)r * K;
+#pragma unroll 4
+    for (int c = lane * 16; c < K; c += WAVE * 16) {
+        const i32x4_t w = *(const i32x4_t*)(src + c);
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = (float)((w[i / 4] << (24 - 8 * (i % 4))) >> 24) * s;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            u32x4_t o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(f[8 * p + 2 * i], f[8 * p + 2 * i + 1]);
+            *(u32x4_t*)(dst + c + 8 * p) = o;
+        }
+    }
+}
+
+hipError_t launch_dequant_i8(const int8_t* q, const float* scale, int R, int K, uint16_t* out,
+                             hipStream_t stream) {
+    dequant_i8_kernel<<<(R + kDequantRows - 1) / kDequantRows, kDequantRows * WAVE, 0, stream>>>(
+        q, scale, R, K, out);
+    return hipGetLastError();
+}
+
+}  // namespace moeq4

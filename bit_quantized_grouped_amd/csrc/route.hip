@@ -25,6 +25,7 @@
 // Every output is a deterministic function of the logits.
 #include "moe_device.h"
 #include "moe_launch.h"
+#include "moe_score.h"
 #include "moe_topk.h"
 
 namespace moeq4 {
@@ -537,6 +538,121 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int block_rows
     route_group_kernel<<<1, kGroupThreads,
                          group_lds_bytes(E) + (stage ? (size_t)n * sizeof(int) : 0), stream>>>(
         r.topk_idx, n, E, block_rows, max_blocks, stage_off, r);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Scored routing (moe_score.h): its own selection kernels, in the same three
+// forms as above, in front of the same grouping.
+// ---------------------------------------------------------------------------
+
+template <int EPL>
+__global__ __launch_bounds__(kTopkWaves * WAVE) void route_scored_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, ScoreRule rule, int T, int E,
+    int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+    const int t = blockIdx.x * kTopkWaves + threadIdx.x / WAVE;
+    if (t < T)
+        score_topk_token<EPL>(logits + (size_t)t * E, bias, E, k, rule, topk_idx + (size_t)t * k,
+                              topk_w + (size_t)t * k);
+}
+
+template <int EPL, int KK>
+__global__ __launch_bounds__((WAVE / KK) * WAVE) void route_scored_chunk_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, ScoreRule rule, int T, int E,
+    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, uint32_t* __restrict__ info) {
+    constexpr int TOK = WAVE / KK;   // tokens per workgroup: one 64-assignment chunk
+    __shared__ int s_chunk[WAVE];
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int t = blockIdx.x * TOK + wave;
+    if (t < T)
+        score_topk_token<EPL>(logits + (size_t)t * E, bias, E, KK, rule, topk_idx + (size_t)t * KK,
+                              topk_w + (size_t)t * KK, s_chunk + wave * KK);
+    __syncthreads();
+    if (wave == 0) {
+        const int a = blockIdx.x * WAVE + lane;
+        const bool valid = a < T * KK;
+        const int e = valid ? s_chunk[lane] : 0;
+        const int nbits = E > 1 ? 32 - __builtin_clz((unsigned)(E - 1)) : 0;
+        const uint64_t m = match_mask(e, valid, nbits);
+        if (valid) info[a] = chunk_info(m);
+    }
+}
+
+template <int EPL>
+__global__ __launch_bounds__(kGroupThreads) void route_scored_fused_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, ScoreRule rule, int T, int E,
+    int k, int block_rows, int max_blocks, RoutingDev r) {
+    extern __shared__ int smem_i[];
+    const int wave = threadIdx.x / WAVE;
+    int* s_hist = smem_i;
+    int* s_eids = s_hist + group_lds_ints(E);   // T*k
+    for (int t = wave; t < T; t += kGroupWaves)
+        score_topk_token<EPL>(logits + (size_t)t * E, bias, E, k, rule, r.topk_idx + (size_t)t * k,
+                              r.topk_w + (size_t)t * k, s_eids + t * k);
+    __syncthreads();
+    group_all(s_eids, T * k, E, block_rows, max_blocks, r, s_hist);
+}
+
+hipError_t launch_route_scored(const float* logits, const float* bias, const ScoreRule& rule, int T,
+                               int E, int k, int block_rows, int max_blocks, const RoutingDev& r,
+                               void* ws, hipStream_t stream) {
+    const int epl = (E + WAVE - 1) / WAVE;
+    const int n = T * k;
+#define MOE_BY_EPL(CALL)              \
+    if (epl <= 1) CALL(1);            \
+    else if (epl <= 2) CALL(2);       \
+    else if (epl <= 4) CALL(4);       \
+    else if (epl <= 8) CALL(8);       \
+    else CALL(16);
+    if (use_fused(T, E, k)) {
+        const size_t smem = (size_t)(group_lds_ints(E) + n) * sizeof(int);
+#define MOE_CALL(N)                                                                              \
+    route_scored_fused_kernel<N><<<1, kGroupThreads, smem, stream>>>(logits, bias, rule, T, E, k, \
+                                                                    block_rows, max_blocks, r)
+        MOE_BY_EPL(MOE_CALL)
+#undef MOE_CALL
+        return hipGetLastError();
+    }
+    const bool chunks = use_chunk_info(T, E, k);
+    uint32_t* info = chunks ? (uint32_t*)ws : nullptr;
+    if (chunks) {
+        const int tok = WAVE / k;
+        const int grid = (T + tok - 1) / tok;
+#define MOE_CALL4(N)                                                                       \
+    route_scored_chunk_kernel<N, 4><<<grid, tok * WAVE, 0, stream>>>(logits, bias, rule, T, E, \
+                                                                     r.topk_idx, r.topk_w, info)
+#define MOE_CALL8(N)                                                                       \
+    route_scored_chunk_kernel<N, 8><<<grid, tok * WAVE, 0, stream>>>(logits, bias, rule, T, E, \
+                                                                     r.topk_idx, r.topk_w, info)
+#define MOE_CALL16(N)                                                                       \
+    route_scored_chunk_kernel<N, 16><<<grid, tok * WAVE, 0, stream>>>(logits, bias, rule, T, E, \
+                                                                      r.topk_idx, r.topk_w, info)
+        if (k == 4) { MOE_BY_EPL(MOE_CALL4) }
+        else if (k == 8) { MOE_BY_EPL(MOE_CALL8) }
+        else { MOE_BY_EPL(MOE_CALL16) }
+#undef MOE_CALL4
+#undef MOE_CALL8
+#undef MOE_CALL16
+    } else {
+        const int grid = (T + kTopkWaves - 1) / kTopkWaves;
+#define MOE_CALL(N)                                                                           \
+    route_scored_kernel<N><<<grid, kTopkWaves * WAVE, 0, stream>>>(logits, bias, rule, T, E, k, \
+                                                                   r.topk_idx, r.topk_w)
+        MOE_BY_EPL(MOE_CALL)
+#undef MOE_CALL
+    }
+#undef MOE_BY_EPL
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const bool stage = n <= kStageMaxAssign;
+    const int stage_off = stage ? (int)(group_lds_bytes(E) / sizeof(int)) : 0;
+    const size_t smem = group_lds_bytes(E) + (stage ? (size_t)n * sizeof(int) : 0);
+    if (chunks)
+        route_group_info_kernel<<<1, kGroupThreads, smem, stream>>>(
+            r.topk_idx, info, n, E, block_rows, max_blocks, stage_off, r);
+    else
+        route_group_kernel<<<1, kGroupThreads, smem, stream>>>(r.topk_idx, n, E, block_rows,
+                                                               max_blocks, stage_off, r);
     return hipGetLastError();
 }
 

@@ -424,6 +424,138 @@ int moe_layer_chunked(const uint16_t* x, const float* logits, int T, int H, int 
                       const moe_q4_mat* sh_down,
                       uint16_t* y, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- 8-bit operators: the pre-norm with 8-bit output, scored routing and
+ * products of 8-bit codes.  A row of K values is held as K signed 8-bit codes
+ * and one fp32 scale: value = code * scale, scale = max|row| / 127, code =
+ * rne(value * (127 / max|row|)); a row of zeros has scale 0 and codes 0.
+ * Codes are -128 .. 127; the calls that quantise write -127 .. 127.
+ * ---- */
+
+/* One set of 8-bit matrices [n_exp, N, K] (K innermost):
+ *   codes   int8, 16-byte aligned, ordered by `layout`:
+ *             MOE_I8_LAYOUT_ROWS   row-major;
+ *             MOE_I8_LAYOUT_TILES  16 x 64 tiles (moe_i8_prepack), N a
+ *                                  multiple of 16;
+ *   scales  fp32 [n_exp, N], 4-byte aligned, row-major in both layouts.
+ * A zero-initialised layout is MOE_I8_LAYOUT_ROWS; the matrices of one call
+ * may differ in layout, except gate and up (and sh_gate and sh_up). */
+#define MOE_I8_LAYOUT_ROWS  0
+#define MOE_I8_LAYOUT_TILES 1
+typedef struct {
+    const int8_t* codes;
+    const float*  scales;
+    int32_t layout;
+} moe_i8_mat;
+
+/* Root-mean-square norm with the residual's addition and an 8-bit output:
+ *   v = x + residual (fp32; v = x when residual is NULL)
+ *   sum = bf16(v);  y = bf16(n), n = v / sqrt(mean(v^2) + eps) * weight
+ *   q, q_scale: n's rows as codes and scales (from n before its rounding)
+ *   x, residual, sum, y  bf16 [T, H];  weight bf16 [H];  q int8 [T, H] (all
+ *   16-byte aligned);  q_scale fp32 [T].  residual, sum, y may be NULL, and q
+ *   and q_scale together; at least one output is given.  sum may be x or
+ *   residual itself (the same address); no other outputs alias inputs.
+ * H a multiple of 64 up to 16384, T >= 1, eps > 0 and finite.  Enqueues one
+ * kernel. */
+int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                int T, int H, uint16_t* sum, uint16_t* y, int8_t* q, float* q_scale,
+                hipStream_t stream);
+
+/* Rows of bf16 [R, K] as codes int8 [R, K] and scales fp32 [R] (weights at load
+ * time, activations that need no norm).  x and q 16-byte aligned, K a multiple
+ * of 64 up to 16384.  Enqueues one kernel. */
+int moe_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, hipStream_t stream);
+
+/* The way back: out = bf16(code * scale), [R, K] row-major, K a multiple of 64;
+ * q and out 16-byte aligned.  Enqueues one kernel. */
+int moe_dequant_i8_bf16(const int8_t* q, const float* scale, int R, int K, uint16_t* out,
+                        hipStream_t stream);
+
+/* Row-major codes [n_exp, N, K] into 16 x 64 tiles (load time):
+ * code (n, k) of a matrix goes to
+ *   (n/16)*16*K + (k/64)*1024 + ((k%64)/16)*256 + (n%16)*16 + k%16,
+ * so a tile is one contiguous kilobyte in the order in which a wave's lanes
+ * hold it.  Distinct device buffers, 16-byte aligned; N a multiple of 16, K of
+ * 64, n_exp*N*K < 2^40.  Enqueues one kernel. */
+int moe_i8_prepack(const int8_t* src, int n_exp, int N, int K, int8_t* dst, hipStream_t stream);
+
+/* out[m, n] = bf16(a_scale[m] * w_scale[n] * sum_k a[m, k] * w[n, k]).
+ *   a int8 [M, K], a_scale fp32 [M];  w one matrix [N, K];  out bf16 [M, N]
+ * a, out 16-byte aligned.  K a multiple of 64 below 131072 (the sum is exact in
+ * 32 bits), M and N >= 1, M*K and N*K < 2^31, M*N < 2^40.  ws: device workspace of at least
+ * moe_linear_i8_workspace_bytes() bytes, 256-byte aligned (may be NULL when
+ * that is 0); two calls that may run at the same time need one each. */
+size_t moe_linear_i8_workspace_bytes(int M, int N, int K);
+int moe_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
+                  uint16_t* out, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Selection rule of the scored routing.
+ *   score        MOE_SCORE_SOFTMAX: softmax over all E logits, or
+ *                MOE_SCORE_SIGMOID: sigmoid of each logit; formed in 64 bits,
+ *                rounded once to fp32
+ *   n_groups     the experts in this many groups of E / n_groups consecutive
+ *                ones (1: no groups; at most 64; divides E)
+ *   topk_groups  groups that stay, 1 .. n_groups
+ *   group_score  a group's worth: MOE_GROUP_MAX its best choice, MOE_GROUP_TOP2
+ *                the fp32 sum of its two best (groups of two or more)
+ *   renormalise  0: weights are the chosen scores; 1: divided by their sum
+ *                (by 1e-30 where it is less)
+ *   scale        factor on every weight (finite) */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX     0
+#define MOE_GROUP_TOP2    1
+typedef struct {
+    int32_t score;
+    int32_t n_groups;
+    int32_t topk_groups;
+    int32_t group_score;
+    int32_t renormalise;
+    float   scale;
+} moe_score_rule;
+
+/* moe_route with scores, a selection bias and groups.
+ *   choice[t, e] = score[t, e] + bias[e] (one fp32 addition; bias fp32 [E] or
+ *   NULL) orders the experts; the weights come from the scores alone.  Ties, of
+ *   groups too, go to the lower index.  topk_idx is by descending choice; the
+ *   other outputs are moe_route's for these indices.
+ * A logit of -inf has score 0; NaN counts as -inf, for a choice too; a +inf
+ * logit shares the softmax with the row's other +inf.  A row of -inf alone has
+ * score 0 everywhere: it keeps k experts, of weight 0.
+ * k <= 64 and k <= topk_groups * (E / n_groups); otherwise arguments, workspace
+ * (moe_route_workspace_bytes) and launches are moe_route's. */
+int moe_route_scored(const float* logits, const float* bias, const moe_score_rule* rule, int T,
+                     int E, int k, int block_rows, const moe_routing* out, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/* Device workspace bytes moe_grouped_gemm_i8 needs (0 on bad shapes). */
+size_t moe_gemm_i8_workspace_bytes(int T, int H, int I, int I_sh, int E, int k, int block_rows);
+
+/* moe_grouped_gemm_q4 over 8-bit activations and weights:
+ *   x int8 [T, H], x_scale fp32 [T] (e.g. moe_norm_i8's q and q_scale)
+ *   h = silu(x Wg^T) * (x Wu^T) in fp32, held as 8-bit codes with one scale per
+ *   row;  expert_out / shared_out = bf16(h Wd^T)
+ * Sums of products are exact 32-bit integers.  Shapes as for the 4-bit calls,
+ * and H, I, I_sh below 131072, H*max(I, I_sh) < 2^31.  Other arguments, status
+ * codes and the order of rows as for moe_grouped_gemm_q4. */
+int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int I, int I_sh, int E,
+                        int k, int block_rows, const moe_routing* r, const moe_i8_mat* gate,
+                        const moe_i8_mat* up, const moe_i8_mat* down, const moe_i8_mat* sh_gate,
+                        const moe_i8_mat* sh_up, const moe_i8_mat* sh_down, uint16_t* expert_out,
+                        uint16_t* shared_out, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* One whole layer call over 8-bit activations and weights: moe_route (rule
+ * NULL, score_bias NULL) or moe_route_scored, moe_grouped_gemm_i8 and
+ * moe_combine in order on `stream`, with those calls' arguments and results.
+ * A call for one token may leave expert_out and shared_out unwritten. */
+int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
+                 const float* score_bias, const moe_score_rule* rule, int T, int H, int I, int I_sh,
+                 int E, int k, int block_rows, const moe_i8_mat* gate, const moe_i8_mat* up,
+                 const moe_i8_mat* down, const moe_i8_mat* sh_gate, const moe_i8_mat* sh_up,
+                 const moe_i8_mat* sh_down, const moe_routing* r, void* route_ws,
+                 size_t route_ws_bytes, uint16_t* expert_out, uint16_t* shared_out, void* gemm_ws,
+                 size_t gemm_ws_bytes, uint16_t* y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
