@@ -673,26 +673,60 @@ def moe_layer_chunked(x: torch.Tensor, logits: torch.Tensor, I: int, I_sh: int, 
 I8 = torch.int8
 
 
-class _On:
-    """Makes the device of a call's tensors the current one, and refuses tensors of another."""
+def _arg(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of `dtype` and `shape` on device `dev` (an index, -1 for the
+    CPU, which _run refuses): one pass over the checks of _tensor and _ptr.  A launch of one token
+    costs the host 4 us; separate helpers, with a stream object, added 6.7 us to it, this 2."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's first tensor is elsewhere")
+    return t.data_ptr()
 
-    __slots__ = ("guard",)
 
-    def __init__(self, first, *others):
-        d = first.get_device()
-        for t in others:
-            if t is not None and t.get_device() != d:
-                raise ValueError(f"arguments on different devices: {first.device} and {t.device}")
-        self.guard = (None if d < 0 or d == torch.cuda.current_device()
-                      else torch.cuda.device(d))
+def _opt_arg(t, name, dtype, shape, dev):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _ws_arg(t, name, dev):
+    """(address, bytes) of a workspace: any contiguous tensor on `dev`."""
+    _tensor(t, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's first tensor is elsewhere")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _two_dims(t, name, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected {dims}")
+    return t.shape
+
+
+def _run(fn, where, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device as the current one."""
+    if dev < 0:
+        raise ValueError("arguments must be device tensors (got tensors on the CPU)")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on cuda:{dev}")
+    else:
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status:
+        raise MoeError(status, where)
 
 
 class DeviceI8Mat:
@@ -757,7 +791,8 @@ class ScoreRule:
                                    int(group_score == "top2"), int(self.renormalise), self.scale)
 
 
-def _i8mat_for(m, name, n_exp, N, K, present=True):
+def _i8mat(m, name, n_exp, N, K, dev, present=True):
+    """The argument of one matrix set (None where it is not present)."""
     if not present:
         if m is not None:
             raise ValueError(f"{name}: must be None here")
@@ -766,63 +801,49 @@ def _i8mat_for(m, name, n_exp, N, K, present=True):
         raise TypeError(f"{name}: expected a DeviceI8Mat")
     if m.shape != (n_exp, N, K):
         raise ValueError(f"{name}: codes {m.shape} are not a [{n_exp}, {N}, {K}] set")
-    return m
-
-
-def _i8mat(m):
-    if m is None:
-        return None
-    _ptr(m.codes)
+    if m.codes.get_device() != dev:
+        raise ValueError(f"{name}: on {m.codes.device}, the call's first tensor is elsewhere")
     return ctypes.byref(m.struct)
 
 
-def _codes_of(x, x_scale, name="x"):
-    _tensor(x, name, I8)
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected two dimensions")
-    _tensor(x_scale, f"{name}_scale", F32, (x.shape[0],))
-    return x.shape
+def _routing_arg(r, name, T, E, k, block_rows, dev):
+    _routing_for(r, name, T, E, k, block_rows)
+    if r.topk_idx.get_device() != dev:
+        raise ValueError(f"{name}: on {r.topk_idx.device}, the call's first tensor is elsewhere")
+    return ctypes.byref(r.struct)
 
 
 def moe_norm_i8(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, sum=None, y=None,
                 q=None, q_scale=None, stream=None):
     """x, residual bf16 [T, H], weight bf16 [H]; writes those of sum, y (bf16 [T, H]), q (int8)
     and q_scale (fp32 [T]) that are given.  sum may be x or residual."""
-    T, H = _x_of(x)
-    _tensor(weight, "weight", BF16, (H,))
-    for name, t in (("residual", residual), ("sum", sum), ("y", y)):
-        if t is not None:
-            _tensor(t, name, BF16, (T, H))
+    shape = T, H = _two_dims(x, "x", "[T, H]")
+    d = x.get_device()
+    args = (_arg(x, "x", BF16, shape, d), _opt_arg(residual, "residual", BF16, shape, d),
+            _arg(weight, "weight", BF16, (H,), d), eps, T, H, _opt_arg(sum, "sum", BF16, shape, d),
+            _opt_arg(y, "y", BF16, shape, d), _opt_arg(q, "q", I8, shape, d),
+            _opt_arg(q_scale, "q_scale", F32, (T,), d))
     if (q is None) != (q_scale is None):
         raise ValueError("q and q_scale: both or neither")
-    if q is not None:
-        _tensor(q, "q", I8, (T, H))
-        _tensor(q_scale, "q_scale", F32, (T,))
     if sum is None and y is None and q is None:
         raise ValueError("sum, y, q: at least one output")
-    with _On(x, residual, weight, sum, y, q, q_scale):
-        _check(lib().moe_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), eps, T, H, _ptr(sum),
-                                 _ptr(y), _ptr(q), _ptr(q_scale), _stream(stream, x.device)),
-               "moe_norm_i8")
+    _run(lib().moe_norm_i8, "moe_norm_i8", d, stream, *args)
 
 
 def moe_quant_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
     """Rows of bf16 [R, K] as codes q int8 [R, K] and scales fp32 [R]."""
-    R, K = _x_of(x)
-    _tensor(q, "q", I8, (R, K))
-    _tensor(scale, "scale", F32, (R,))
-    with _On(x, q, scale):
-        _check(lib().moe_quant_i8(_ptr(x), R, K, _ptr(q), _ptr(scale), _stream(stream, x.device)),
-               "moe_quant_i8")
+    shape = R, K = _two_dims(x, "x", "[R, K]")
+    d = x.get_device()
+    _run(lib().moe_quant_i8, "moe_quant_i8", d, stream, _arg(x, "x", BF16, shape, d), R, K,
+         _arg(q, "q", I8, shape, d), _arg(scale, "scale", F32, (R,), d))
 
 
 def moe_dequant_i8_bf16(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, stream=None):
     """out bf16 [R, K] = codes int8 [R, K] times the rows' scales fp32 [R]."""
-    R, K = _codes_of(q, scale, "q")
-    _tensor(out, "out", BF16, (R, K))
-    with _On(q, scale, out):
-        _check(lib().moe_dequant_i8_bf16(_ptr(q), _ptr(scale), R, K, _ptr(out),
-                                         _stream(stream, q.device)), "moe_dequant_i8_bf16")
+    shape = R, K = _two_dims(q, "q", "[R, K]")
+    d = q.get_device()
+    _run(lib().moe_dequant_i8_bf16, "moe_dequant_i8_bf16", d, stream, _arg(q, "q", I8, shape, d),
+         _arg(scale, "scale", F32, (R,), d), R, K, _arg(out, "out", BF16, shape, d))
 
 
 def moe_i8_prepack(src: torch.Tensor, dst: torch.Tensor, stream=None):
@@ -830,10 +851,9 @@ def moe_i8_prepack(src: torch.Tensor, dst: torch.Tensor, stream=None):
     _tensor(src, "src", I8)
     if src.dim() != 3:
         raise ValueError("src: expected [n_exp, N, K]")
-    _tensor(dst, "dst", I8, src.shape)
-    with _On(src, dst):
-        _check(lib().moe_i8_prepack(_ptr(src), *src.shape, _ptr(dst), _stream(stream, src.device)),
-               "moe_i8_prepack")
+    d = src.get_device()
+    _run(lib().moe_i8_prepack, "moe_i8_prepack", d, stream, src.data_ptr(), *src.shape,
+         _arg(dst, "dst", I8, src.shape, d))
 
 
 def linear_i8_workspace_bytes(M, N, K) -> int:
@@ -844,69 +864,65 @@ def moe_linear_i8(a: torch.Tensor, a_scale: torch.Tensor, w: DeviceI8Mat, out: t
                   stream=None):
     """out bf16 [M, N] = a [M, K] times w's one matrix [N, K], both 8-bit codes with their rows'
     scales.  ws: linear_i8_workspace_bytes(M, N, K) bytes (None where that is 0)."""
-    M, K = _codes_of(a, a_scale, "a")
+    shape = M, K = _two_dims(a, "a", "[M, K]")
     if not isinstance(w, DeviceI8Mat):
         raise TypeError("w: expected a DeviceI8Mat")
-    N = w.shape[1]
-    _i8mat_for(w, "w", 1, N, K)
-    _tensor(out, "out", BF16, (M, N))
-    if ws is not None:
-        _ws(ws)
-    with _On(a, a_scale, w.codes, out, ws):
-        _check(lib().moe_linear_i8(_ptr(a), _ptr(a_scale), M, K, _i8mat(w), N, _ptr(out), _ptr(ws),
-                                   0 if ws is None else ws.numel() * ws.element_size(),
-                                   _stream(stream, a.device)), "moe_linear_i8")
+    d, N = a.get_device(), w.shape[1]
+    _run(lib().moe_linear_i8, "moe_linear_i8", d, stream, _arg(a, "a", I8, shape, d),
+         _arg(a_scale, "a_scale", F32, (M,), d), M, K, _i8mat(w, "w", 1, N, K, d), N,
+         _arg(out, "out", BF16, (M, N), d), *((None, 0) if ws is None else _ws_arg(ws, "ws", d)))
 
 
 def moe_route_scored(logits: torch.Tensor, bias, rule: ScoreRule, k: int, block_rows: int,
                      routing: DeviceRouting, ws: torch.Tensor, stream=None):
     """moe_route by a ScoreRule, with an optional selection bias fp32 [E]."""
-    _tensor(logits, "logits", F32)
-    if logits.dim() != 2:
-        raise ValueError("logits: expected [T, E]")
-    T, E = logits.shape
-    if bias is not None:
-        _tensor(bias, "bias", F32, (E,))
+    shape = T, E = _two_dims(logits, "logits", "[T, E]")
     if not isinstance(rule, ScoreRule):
         raise TypeError("rule: expected a ScoreRule")
-    _routing_for(routing, "routing", T, E, k, block_rows)
-    _ws(ws, "route_ws")
-    with _On(logits, bias, routing.topk_idx, ws):
-        _check(lib().moe_route_scored(_ptr(logits), _ptr(bias), ctypes.byref(rule.struct), T, E, k,
-                                      block_rows, _rt(routing), _ptr(ws),
-                                      ws.numel() * ws.element_size(),
-                                      _stream(stream, logits.device)), "moe_route_scored")
+    d = logits.get_device()
+    _run(lib().moe_route_scored, "moe_route_scored", d, stream, _arg(logits, "logits", F32, shape, d),
+         _opt_arg(bias, "bias", F32, (E,), d), ctypes.byref(rule.struct), T, E, k, block_rows,
+         _routing_arg(routing, "routing", T, E, k, block_rows, d), *_ws_arg(ws, "route_ws", d))
 
 
 def gemm_i8_workspace_bytes(T, H, I, I_sh, E, k, block_rows) -> int:
     return lib().moe_gemm_i8_workspace_bytes(T, H, I, I_sh, E, k, block_rows)
 
 
-def _expert_i8_mats(mats, E, H, I, I_sh):
+def _expert_i8_mats(mats, E, H, I, I_sh, dev):
     sh = I_sh > 0
-    for m, name, shape, present in zip(
-            mats, ("gate", "up", "down", "sh_gate", "sh_up", "sh_down"),
-            ((E, I, H), (E, I, H), (E, H, I), (1, I_sh, H), (1, I_sh, H), (1, H, I_sh)),
-            (True, True, True, sh, sh, sh)):
-        _i8mat_for(m, name, *shape, present=present)
+    return [_i8mat(m, name, *shape, dev, present=present) for m, name, shape, present in zip(
+        mats, ("gate", "up", "down", "sh_gate", "sh_up", "sh_down"),
+        ((E, I, H), (E, I, H), (E, H, I), (1, I_sh, H), (1, I_sh, H), (1, H, I_sh)),
+        (True, True, True, sh, sh, sh))]
+
+
+def _shared_out_arg(t, I_sh, shape, dev):
+    _opt_tensor(t, "shared_out", I_sh > 0, BF16, shape)
+    return _opt_arg(t, "shared_out", BF16, shape, dev)
 
 
 def moe_grouped_gemm_i8(x: torch.Tensor, x_scale: torch.Tensor, I: int, I_sh: int, E: int, k: int,
                         block_rows: int, routing: DeviceRouting, gate, up, down, sh_gate, sh_up,
                         sh_down, expert_out: torch.Tensor, shared_out, ws: torch.Tensor,
                         stream=None):
-    T, H = _codes_of(x, x_scale)
-    _routing_for(routing, "routing", T, E, k, block_rows)
-    mats = (gate, up, down, sh_gate, sh_up, sh_down)
-    _expert_i8_mats(mats, E, H, I, I_sh)
-    _tensor(expert_out, "expert_out", BF16, (T * k, H))
-    _opt_tensor(shared_out, "shared_out", I_sh > 0, BF16, (T, H))
-    _ws(ws)
-    with _On(x, x_scale, routing.topk_idx, *(m.codes for m in mats if m), expert_out, shared_out, ws):
-        _check(lib().moe_grouped_gemm_i8(
-            _ptr(x), _ptr(x_scale), T, H, I, I_sh, E, k, block_rows, _rt(routing),
-            *map(_i8mat, mats), _ptr(expert_out), _ptr(shared_out), _ptr(ws),
-            ws.numel() * ws.element_size(), _stream(stream, x.device)), "moe_grouped_gemm_i8")
+    shape = T, H = _two_dims(x, "x", "[T, H]")
+    d = x.get_device()
+    _run(lib().moe_grouped_gemm_i8, "moe_grouped_gemm_i8", d, stream, _arg(x, "x", I8, shape, d),
+         _arg(x_scale, "x_scale", F32, (T,), d), T, H, I, I_sh, E, k, block_rows,
+         _routing_arg(routing, "routing", T, E, k, block_rows, d),
+         *_expert_i8_mats((gate, up, down, sh_gate, sh_up, sh_down), E, H, I, I_sh, d),
+         _arg(expert_out, "expert_out", BF16, (T * k, H), d),
+         _shared_out_arg(shared_out, I_sh, (T, H), d), *_ws_arg(ws, "ws", d))
+
+
+def _rule_args(rule, score_bias, E, dev):
+    if rule is not None and not isinstance(rule, ScoreRule):
+        raise TypeError("rule: expected a ScoreRule")
+    if score_bias is not None and rule is None:
+        raise ValueError("score_bias: needs a rule")
+    return (_opt_arg(score_bias, "score_bias", F32, (E,), dev),
+            None if rule is None else ctypes.byref(rule.struct))
 
 
 def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, score_bias, rule,
@@ -916,31 +932,16 @@ def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, s
                  stream=None):
     """moe_route (rule None) or moe_route_scored, moe_grouped_gemm_i8 and moe_combine in one
     call."""
-    T, H = _codes_of(x, x_scale)
-    _tensor(logits, "logits", F32, (T, E))
-    if rule is not None and not isinstance(rule, ScoreRule):
-        raise TypeError("rule: expected a ScoreRule")
-    if score_bias is not None:
-        if rule is None:
-            raise ValueError("score_bias: needs a rule")
-        _tensor(score_bias, "score_bias", F32, (E,))
-    _routing_for(routing, "routing", T, E, k, block_rows)
-    mats = (gate, up, down, sh_gate, sh_up, sh_down)
-    _expert_i8_mats(mats, E, H, I, I_sh)
-    _tensor(expert_out, "expert_out", BF16, (T * k, H))
-    _opt_tensor(shared_out, "shared_out", I_sh > 0, BF16, (T, H))
-    _tensor(y, "y", BF16, (T, H))
-    _ws(route_ws, "route_ws")
-    _ws(gemm_ws, "gemm_ws")
-    with _On(x, x_scale, logits, score_bias, routing.topk_idx, route_ws,
-             *(m.codes for m in mats if m), expert_out, shared_out, gemm_ws, y):
-        _check(lib().moe_layer_i8(
-            _ptr(x), _ptr(x_scale), _ptr(logits), _ptr(score_bias),
-            None if rule is None else ctypes.byref(rule.struct), T, H, I, I_sh, E, k, block_rows,
-            *map(_i8mat, mats), _rt(routing), _ptr(route_ws),
-            route_ws.numel() * route_ws.element_size(), _ptr(expert_out), _ptr(shared_out),
-            _ptr(gemm_ws), gemm_ws.numel() * gemm_ws.element_size(), _ptr(y),
-            _stream(stream, x.device)), "moe_layer_i8")
+    shape = T, H = _two_dims(x, "x", "[T, H]")
+    d = x.get_device()
+    _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, _arg(x, "x", I8, shape, d),
+         _arg(x_scale, "x_scale", F32, (T,), d), _arg(logits, "logits", F32, (T, E), d),
+         *_rule_args(rule, score_bias, E, d), T, H, I, I_sh, E, k, block_rows,
+         *_expert_i8_mats((gate, up, down, sh_gate, sh_up, sh_down), E, H, I, I_sh, d),
+         _routing_arg(routing, "routing", T, E, k, block_rows, d), *_ws_arg(route_ws, "route_ws", d),
+         _arg(expert_out, "expert_out", BF16, (T * k, H), d),
+         _shared_out_arg(shared_out, I_sh, (T, H), d), *_ws_arg(gemm_ws, "gemm_ws", d),
+         _arg(y, "y", BF16, shape, d))
 
 
 # ---------------------------------------------------------------------------
@@ -1100,10 +1101,16 @@ class MoeLayerI8:
         None when I_sh is 0).  rule: None routes as moe_route does (softmax over the k chosen)."""
         self.H, self.I, self.I_sh, self.E, self.k = H, I, I_sh, E, k
         self.block_rows, self.device = block_rows, torch.device(device)
-        self.mats = tuple(mats)
-        _expert_i8_mats(self.mats, E, H, I, I_sh)
+        self._mats = tuple(mats)
+        _expert_i8_mats(self._mats, E, H, I, I_sh, mats[0].codes.get_device()
+                        if isinstance(mats[0], DeviceI8Mat) else -1)
         self.rule, self.score_bias = rule, score_bias
-        self._bufs = {}
+        self._bufs, self._fixed = {}, {}
+
+    @property
+    def mats(self):
+        """The six matrix sets (gate, up, down, sh_gate, sh_up, sh_down)."""
+        return self._mats
 
     @classmethod
     def from_bf16(cls, weights, H: int, I: int, I_sh: int, E: int, k: int, device,
@@ -1131,11 +1138,25 @@ class MoeLayerI8:
         """One moe_layer_i8 call over codes x int8 [T, H] and their scales; returns the buffers
         used.  They are this object's and the next call's too: calls on several streams at once
         need an object each."""
-        b = self.buffers(x.shape[0])
+        shape = T, H = _two_dims(x, "x", "[T, H]")
+        d = x.get_device()
+        b = self.buffers(T)
         y = b["y"] if out is None else out
-        moe_layer_i8(x, x_scale, logits, self.score_bias, self.rule, self.I, self.I_sh, self.E,
-                     self.k, self.block_rows, b["routing"], b["route_ws"], *self.mats,
-                     b["expert_out"], b["shared_out"], b["gemm_ws"], y, stream)
+        if T not in self._fixed:   # the arguments that belong to this object, checked once
+            self._fixed[T] = (
+                [T, self.H, self.I, self.I_sh, self.E, self.k, self.block_rows,
+                 *_expert_i8_mats(self._mats, self.E, self.H, self.I, self.I_sh, d),
+                 _routing_arg(b["routing"], "routing", T, self.E, self.k, self.block_rows, d),
+                 *_ws_arg(b["route_ws"], "route_ws", d),
+                 _arg(b["expert_out"], "expert_out", BF16, (T * self.k, self.H), d),
+                 _shared_out_arg(b["shared_out"], self.I_sh, (T, self.H), d),
+                 *_ws_arg(b["gemm_ws"], "gemm_ws", d)], d)
+        fixed, on = self._fixed[T]
+        if d != on or H != self.H:
+            raise ValueError(f"x: {tuple(shape)} on {x.device}, the layer is H={self.H} on cuda:{on}")
+        _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, _arg(x, "x", I8, shape, d),
+             _arg(x_scale, "x_scale", F32, (T,), d), _arg(logits, "logits", F32, (T, self.E), d),
+             *_rule_args(self.rule, self.score_bias, self.E, d), *fixed, _arg(y, "y", BF16, shape, d))
         return dict(b, y=y)
 
     def forward_block(self, x: torch.Tensor, residual, norm_weight: torch.Tensor,
