@@ -196,10 +196,16 @@ int moe_route_max_blocks(int T, int E, int k, int block_rows) {
     return max_blocks_of(T, E, k, block_rows);
 }
 
-size_t moe_route_workspace_bytes(int T, int E, int k, int block_rows) {
-    if (check_route_shape(T, E, k, block_rows)) return 0;
+// What moe_route itself needs of the workspace.
+static size_t route_need(int T, int E, int k) {
     size_t a, b;
     return route_ws_layout(T, E, k, &a, &b);
+}
+
+size_t moe_route_workspace_bytes(int T, int E, int k, int block_rows) {
+    if (check_route_shape(T, E, k, block_rows)) return 0;
+    const size_t need = route_need(T, E, k), scored = scored_ws_bytes(T, E, k);
+    return need > scored ? need : scored;
 }
 
 int moe_route(const float* logits, int T, int E, int k, int block_rows, const moe_routing* out,
@@ -207,7 +213,7 @@ int moe_route(const float* logits, int T, int E, int k, int block_rows, const mo
     try {
         int st = check_route_shape(T, E, k, block_rows);
         if (st) return st;
-        const size_t need = moe_route_workspace_bytes(T, E, k, block_rows);
+        const size_t need = route_need(T, E, k);
         if (!logits || (need && !ws)) return MOE_ERR_NULL;
         if ((st = check_routing(out))) return st;
         if (!aligned(logits, 4) || !aligned(ws, 256)) return MOE_ERR_ALIGN;
@@ -308,8 +314,8 @@ int moe_layer_q4(const uint16_t* x, const float* logits, int T, int H, int I, in
         if (st) return st;
         if (!logits || !y) return MOE_ERR_NULL;
         if (!aligned(logits, 4) || !aligned(y, 16)) return MOE_ERR_ALIGN;
-        const size_t route_need = moe_route_workspace_bytes(T, E, k, block_rows);
-        if (route_need && (st = check_ws(route_ws, route_ws_bytes, route_need))) return st;
+        const size_t need = route_need(T, E, k);
+        if (need && (st = check_ws(route_ws, route_ws_bytes, need))) return st;
         if ((st = check_ws(gemm_ws, gemm_ws_bytes,
                            moe_gemm_workspace_bytes(T, H, I, I_sh, E, k, block_rows))))
             return st;
@@ -927,7 +933,7 @@ int moe_route_scored(const float* logits, const float* bias, const moe_score_rul
         if (st) return st;
         ScoreRule dev;
         if ((st = check_rule(rule, E, k, &dev))) return st;
-        const size_t need = moe_route_workspace_bytes(T, E, k, block_rows);
+        const size_t need = scored_ws_bytes(T, E, k);
         if (!logits || (need && !ws)) return MOE_ERR_NULL;
         if ((st = check_routing(out))) return st;
         if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ws, 256)) return MOE_ERR_ALIGN;
@@ -1018,7 +1024,7 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
         ScoreRule dev{};
         if (rule && (st = check_rule(rule, E, k, &dev))) return st;
         if (!rule && score_bias) return MOE_ERR_SHAPE;   // a bias orders scores: it needs a rule
-        const size_t need = moe_route_workspace_bytes(T, E, k, block_rows);
+        const size_t need = rule ? scored_ws_bytes(T, E, k) : route_need(T, E, k);
         if (need && (st = check_ws(route_ws, route_ws_bytes, need))) return st;
         hipError_t e = rule ? launch_route_scored(logits, score_bias, dev, T, E, k, block_rows,
                                                   p.max_blocks, p.r, route_ws, stream)

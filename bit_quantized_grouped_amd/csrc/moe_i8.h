@@ -54,6 +54,7 @@ hipError_t launch_dequant_i8(const int8_t* q, const float* scale, int R, int K, 
                              hipStream_t stream);
 
 // route.hip
+size_t scored_ws_bytes(int T, int E, int k);
 hipError_t launch_route_scored(const float* logits, const float* bias, const ScoreRule& rule, int T,
                                int E, int k, int block_rows, int max_blocks, const RoutingDev& r,
                                void* ws, hipStream_t stream);

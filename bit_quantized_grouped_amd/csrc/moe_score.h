@@ -24,28 +24,71 @@ __device__ __forceinline__ uint32_t choice_key(float v) {
     return float_key(v != v ? -__builtin_huge_valf() : v);
 }
 
+// Sum over the wave in a fixed order, returned uniform (row_shr 1, 2, 4, 8 and
+// row_bcast 15, 31 as in wave_incl_sum, both halves moved).
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#define MOE_DPP_ADD64(ctrl, rows)                                                           \
+    {                                                                                       \
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);                                 \
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, ctrl, rows, 0xf, false); \
+        const uint32_t hi =                                                                 \
+            __builtin_amdgcn_update_dpp(0, (int)(u >> 32), ctrl, rows, 0xf, false);         \
+        v += __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);                           \
+    }
+    MOE_DPP_ADD64(0x111, 0xf)
+    MOE_DPP_ADD64(0x112, 0xf)
+    MOE_DPP_ADD64(0x114, 0xf)
+    MOE_DPP_ADD64(0x118, 0xf)
+    MOE_DPP_ADD64(0x142, 0xa)
+    MOE_DPP_ADD64(0x143, 0xc)
+#undef MOE_DPP_ADD64
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)u, WAVE - 1);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), WAVE - 1);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// 1 / d for finite d >= 1: the hardware's estimate and two Newton steps, within 2^-52.
+__device__ __forceinline__ double recip_f64(double d) {
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+
 // Lane l holds experts l*EPL .. l*EPL+EPL-1; absent and dropped experts get key 0.
 template <int EPL>
 __device__ __forceinline__ void drop_groups(uint32_t (&key)[EPL], int E, const ScoreRule& rule) {
     const int lane = __lane_id();
     const int gs = E / rule.n_groups, span = gs / EPL;
-    if (gs % EPL == 0 && (span & (span - 1)) == 0) {
-        // whole groups in 2^n neighbouring lanes: the two best by a butterfly
+    if (gs % EPL == 0) {
+        // whole groups in `span` neighbouring lanes: every lane gathers its group's two best,
+        // by a butterfly where span is a power of two and lane by lane otherwise
         uint32_t m1 = 0, m2 = 0;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             m2 = max(m2, min(m1, key[j]));
             m1 = max(m1, key[j]);
         }
-        for (int off = 1; off < span; off <<= 1) {
-            const uint32_t o1 = shfl_xor(m1, off), o2 = shfl_xor(m2, off);
-            m2 = max(max(m2, o2), min(m1, o1));
-            m1 = max(m1, o1);
+        const int mine = lane / span;
+        if ((span & (span - 1)) == 0) {
+            for (int off = 1; off < span; off <<= 1) {
+                const uint32_t o1 = shfl_xor(m1, off), o2 = shfl_xor(m2, off);
+                m2 = max(max(m2, o2), min(m1, o1));
+                m1 = max(m1, o1);
+            }
+        } else {
+            const uint32_t l1 = m1, l2 = m2;
+            m1 = m2 = 0;
+            for (int i = 0; i < span; ++i) {
+                const int from = mine * span + i;   // past lane 63 for lanes without experts only
+                const uint32_t o1 = __shfl(l1, from, WAVE), o2 = __shfl(l2, from, WAVE);
+                m2 = max(max(m2, o2), min(m1, o1));
+                m1 = max(m1, o1);
+            }
         }
         uint32_t worth = rule.top2 ? choice_key(key_float(m1) + key_float(m2)) : m1;
         if (lane >= E / EPL) worth = 0;
         bool keep = false;
-        const int mine = lane / span;
         for (int r = 0; r < rule.topk_groups; ++r) {
             const uint32_t m = wave_max_u32(worth);
             const int g = __builtin_ctzll(__ballot(worth == m)) / span;
@@ -112,7 +155,8 @@ __device__ __forceinline__ void score_topk_token(const float* __restrict__ row,
     }
     if (rule.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) sc[j] = (float)(1.0 / (1.0 + exp(-(double)l[j])));
+        for (int j = 0; j < EPL; ++j)   // below -700 a score is 0 in fp32
+            sc[j] = (float)recip_f64(1.0 + exp(fmin(-(double)l[j], 700.0)));
     } else {
         float best = l[0];
 #pragma unroll
@@ -126,10 +170,10 @@ __device__ __forceinline__ void score_topk_token(const float* __restrict__ row,
             else p[j] = exp((double)l[j] - (double)best);
             part += p[j];
         }
+        part = wave_sum_f64(part);   // at least 1, or 0 for a row of -inf alone
+        const double inv = part > 0.0 ? recip_f64(part) : 0.0;
 #pragma unroll
-        for (int off = WAVE / 2; off >= 1; off >>= 1) part += shfl_xor(part, off);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) sc[j] = part > 0.0 ? (float)(p[j] / part) : 0.f;
+        for (int j = 0; j < EPL; ++j) sc[j] = (float)(p[j] * inv);
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {

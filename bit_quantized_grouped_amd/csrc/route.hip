@@ -542,8 +542,8 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int block_rows
 }
 
 // ---------------------------------------------------------------------------
-// Scored routing (moe_score.h): its own selection kernels, in the same three
-// forms as above, in front of the same grouping.
+// Scored routing (moe_score.h): one launch for few tokens, segments (below), or
+// one wave per token in front of the one-workgroup grouping.
 // ---------------------------------------------------------------------------
 
 template <int EPL>
@@ -554,28 +554,6 @@ __global__ __launch_bounds__(kTopkWaves * WAVE) void route_scored_kernel(
     if (t < T)
         score_topk_token<EPL>(logits + (size_t)t * E, bias, E, k, rule, topk_idx + (size_t)t * k,
                               topk_w + (size_t)t * k);
-}
-
-template <int EPL, int KK>
-__global__ __launch_bounds__((WAVE / KK) * WAVE) void route_scored_chunk_kernel(
-    const float* __restrict__ logits, const float* __restrict__ bias, ScoreRule rule, int T, int E,
-    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, uint32_t* __restrict__ info) {
-    constexpr int TOK = WAVE / KK;   // tokens per workgroup: one 64-assignment chunk
-    __shared__ int s_chunk[WAVE];
-    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
-    const int t = blockIdx.x * TOK + wave;
-    if (t < T)
-        score_topk_token<EPL>(logits + (size_t)t * E, bias, E, KK, rule, topk_idx + (size_t)t * KK,
-                              topk_w + (size_t)t * KK, s_chunk + wave * KK);
-    __syncthreads();
-    if (wave == 0) {
-        const int a = blockIdx.x * WAVE + lane;
-        const bool valid = a < T * KK;
-        const int e = valid ? s_chunk[lane] : 0;
-        const int nbits = E > 1 ? 32 - __builtin_clz((unsigned)(E - 1)) : 0;
-        const uint64_t m = match_mask(e, valid, nbits);
-        if (valid) info[a] = chunk_info(m);
-    }
 }
 
 template <int EPL>
@@ -591,6 +569,184 @@ __global__ __launch_bounds__(kGroupThreads) void route_scored_fused_kernel(
                               r.topk_w + (size_t)t * k, s_eids + t * k);
     __syncthreads();
     group_all(s_eids, T * k, E, block_rows, max_blocks, r, s_hist);
+}
+
+// Segments: above the one-launch size the tokens are cut into segments of 8 or
+// 16, one token per wave of a workgroup that selects their experts and counts
+// them, one byte per expert (a token takes an expert once, so a count is at most
+// 16).  A
+// workgroup of the scatter kernel takes up to 1024 assignments of whole segments:
+// it sums the segments' counts (those before its own, and all of them), scans the
+// experts' totals, and places its assignments: wave w owns their 64-assignment
+// chunk w, so rows follow assignment order and the sort is stable.  Every
+// workgroup repeats the scan, which costs less than a third launch: n_seg * E
+// bytes from L2.  The counts of segments of 16 fit the T * k words of moe_route's
+// workspace for any E <= 64 k.
+constexpr int kSegTokens = kGroupWaves;                // most tokens of a segment
+constexpr int kSegMaxK = kGroupThreads / kSegTokens;   // a segment fits a scatter workgroup
+
+__host__ __device__ constexpr int seg_words(int E) { return (E + 3) / 4; }   // of one segment's counts
+
+template <int EPL>
+__global__ __launch_bounds__(kGroupThreads) void route_scored_seg_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, ScoreRule rule, int T, int E,
+    int k, int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
+    uint32_t* __restrict__ seg_counts) {
+    extern __shared__ int smem_i[];   // [seg_words] packed counts, then [tokens * k] experts
+    const int words = seg_words(E);
+    int* s_eids = smem_i + words;
+    const int wave = threadIdx.x / WAVE, tokens = blockDim.x / WAVE;
+    const int t0 = blockIdx.x * tokens, nt = min(tokens, T - t0);
+    for (int i = threadIdx.x; i < words; i += blockDim.x) smem_i[i] = 0;
+    if (wave < nt) {
+        const size_t t = t0 + wave;
+        score_topk_token<EPL>(logits + t * E, bias, E, k, rule, topk_idx + t * k, topk_w + t * k,
+                              s_eids + wave * k);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * k; i += blockDim.x) {
+        const int e = s_eids[i];
+        atomicAdd(&smem_i[e / 4], 1 << (8 * (e % 4)));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < words; i += blockDim.x)
+        seg_counts[(size_t)blockIdx.x * words + i] = (uint32_t)smem_i[i];
+}
+
+__global__ __launch_bounds__(kGroupThreads) void route_seg_scatter_kernel(
+    const int32_t* __restrict__ topk_idx, const uint32_t* __restrict__ seg_counts, int n, int E,
+    int own, int segs, int n_seg, int block_rows, int max_blocks, RoutingDev r) {
+    extern __shared__ int s_hist[];   // [kGroupWaves][E], the scan's wave totals, [parts][2][4*words]
+    int* s_wave = s_hist + kGroupWaves * E;
+    int* s_sum = s_wave + 2 * (kGroupWaves + 1);
+    const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
+    const int words = seg_words(E), parts = kGroupThreads / words;
+    const int seg0 = blockIdx.x * segs;   // own: the assignments of its segments
+    // this wave's chunk of the workgroup's assignments
+    const int a = blockIdx.x * own + wave * WAVE + lane;
+    const bool valid = wave * WAVE + lane < own && a < n;
+    const int mine = valid ? topk_idx[a] : 0;
+    // four experts' counts before seg0 and in all, by parts of the segments
+    const int part = tid / words, pw = tid - part * words;
+    if (part < parts) {
+        const int s0 = (int)((long long)n_seg * part / parts);
+        const int s1 = (int)((long long)n_seg * (part + 1) / parts);
+        // counts of experts 0, 2 and 1, 3 of the word in halves of a sum, which 4088
+        // segments of 16 cannot fill; eight loads in flight, past the end repeated and
+        // not counted
+        int before[4] = {0, 0, 0, 0}, all[4] = {0, 0, 0, 0};
+        for (int s = s0; s < s1; s += 4088) {
+            const int end = min(s1, s + 4088);
+            uint32_t even_b = 0, odd_b = 0, even = 0, odd = 0;
+            for (int q = s; q < end; q += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = seg_counts[(size_t)min(q + i, end - 1) * words + pw];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t in = q + i < end ? w[i] : 0u, ahead = q + i < seg0 ? in : 0u;
+                    even += in & 0x00FF00FFu;
+                    odd += (in >> 8) & 0x00FF00FFu;
+                    even_b += ahead & 0x00FF00FFu;
+                    odd_b += (ahead >> 8) & 0x00FF00FFu;
+                }
+            }
+            before[0] += even_b & 0xFFFF;
+            before[2] += even_b >> 16;
+            before[1] += odd_b & 0xFFFF;
+            before[3] += odd_b >> 16;
+            all[0] += even & 0xFFFF;
+            all[2] += even >> 16;
+            all[1] += odd & 0xFFFF;
+            all[3] += odd >> 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s_sum[(part * 2 + 0) * 4 * words + 4 * pw + i] = before[i];
+            s_sum[(part * 2 + 1) * 4 * words + 4 * pw + i] = all[i];
+        }
+    }
+    for (int i = tid; i < kGroupWaves * E; i += kGroupThreads) s_hist[i] = 0;
+    const int nbits = E > 1 ? 32 - __builtin_clz((unsigned)(E - 1)) : 0;
+    const uint64_t match = match_mask(mine, valid, nbits);
+    const uint64_t lt = lanemask_lt();
+    __syncthreads();
+    if (valid && (match & lt) == 0) s_hist[wave * E + mine] = __popcll(match);
+    const int e = tid;
+    int cnt = 0, before = 0;
+    if (e < E)
+        for (int p = 0; p < parts; ++p) {
+            before += s_sum[(p * 2 + 0) * 4 * words + e];
+            cnt += s_sum[(p * 2 + 1) * 4 * words + e];
+        }
+    const int nb = e < E ? (cnt + block_rows - 1) / block_rows : 0;
+    int off, bstart, total_rows, total_blocks;
+    block_exclusive_scan2(cnt, nb, s_wave, &off, &bstart, &total_rows, &total_blocks);
+    if (e < E) {
+        int run = off + before;   // first row of this workgroup's assignments to e
+        int h[kGroupWaves];
+#pragma unroll
+        for (int w = 0; w < kGroupWaves; ++w) h[w] = s_hist[w * E + e];
+#pragma unroll
+        for (int w = 0; w < kGroupWaves; ++w) {
+            s_hist[w * E + e] = run;
+            run += h[w];
+        }
+    }
+    __syncthreads();
+    if (valid) {
+        const int row = s_hist[wave * E + mine] + __popcll(match & lt);
+        r.sorted_assign[row] = a;
+        r.assign_row[a] = row;
+    }
+    // the block map, a share per workgroup: block b belongs to the last expert that
+    // starts at or before b and has blocks
+    int* s_bstart = s_sum;
+    int* s_off = s_sum + E;
+    if (e < E) {
+        s_bstart[e] = bstart;
+        s_off[e] = off;
+    }
+    __syncthreads();
+    for (int b = blockIdx.x * kGroupThreads + tid; b < max_blocks; b += gridDim.x * kGroupThreads) {
+        int lo = 0;
+        for (int step = 1 << (nbits ? nbits - 1 : 0); step; step >>= 1)
+            if (lo + step < E && s_bstart[lo + step] <= b) lo += step;
+        const bool in = b < total_blocks;
+        r.block_expert[b] = in ? lo : -1;
+        r.block_row[b] = in ? s_off[lo] + block_rows * (b - s_bstart[lo]) : -1;
+    }
+    if (blockIdx.x) return;
+    if (e < E) {
+        r.counts[e] = cnt;
+        r.offsets[e] = off;
+    }
+    if (e == 0) {
+        r.offsets[E] = total_rows;
+        r.n_blocks[0] = total_blocks;
+    }
+}
+
+static size_t seg_bytes(int T, int E, int tokens) {
+    return align_up((size_t)((T + tokens - 1) / tokens) * seg_words(E) * sizeof(uint32_t), 256);
+}
+
+// Tokens of a segment, 0 where segments are not used: they are where the counts
+// fit the workspace that moe_route has, or where one workgroup would group for long
+// (49152 assignments take it 87 us).  Segments of 8 spread up to 4096 tokens over
+// twice the CUs.
+static int seg_tokens_of(int T, int E, int k) {
+    if (use_fused(T, E, k) || k > kSegMaxK) return 0;
+    size_t a, b;
+    const size_t have = (size_t)T * k > kStageMaxAssign ? ~(size_t)0 : route_ws_layout(T, E, k, &a, &b);
+    if (T <= 1024 && seg_bytes(T, E, 8) <= have) return 8;
+    return seg_bytes(T, E, kSegTokens) <= have ? kSegTokens : 0;
+}
+
+size_t scored_ws_bytes(int T, int E, int k) {
+    const int tokens = seg_tokens_of(T, E, k);
+    return tokens ? seg_bytes(T, E, tokens) : 0;
 }
 
 hipError_t launch_route_scored(const float* logits, const float* bias, const ScoreRule& rule, int T,
@@ -613,46 +769,38 @@ hipError_t launch_route_scored(const float* logits, const float* bias, const Sco
 #undef MOE_CALL
         return hipGetLastError();
     }
-    const bool chunks = use_chunk_info(T, E, k);
-    uint32_t* info = chunks ? (uint32_t*)ws : nullptr;
-    if (chunks) {
-        const int tok = WAVE / k;
-        const int grid = (T + tok - 1) / tok;
-#define MOE_CALL4(N)                                                                       \
-    route_scored_chunk_kernel<N, 4><<<grid, tok * WAVE, 0, stream>>>(logits, bias, rule, T, E, \
-                                                                     r.topk_idx, r.topk_w, info)
-#define MOE_CALL8(N)                                                                       \
-    route_scored_chunk_kernel<N, 8><<<grid, tok * WAVE, 0, stream>>>(logits, bias, rule, T, E, \
-                                                                     r.topk_idx, r.topk_w, info)
-#define MOE_CALL16(N)                                                                       \
-    route_scored_chunk_kernel<N, 16><<<grid, tok * WAVE, 0, stream>>>(logits, bias, rule, T, E, \
-                                                                      r.topk_idx, r.topk_w, info)
-        if (k == 4) { MOE_BY_EPL(MOE_CALL4) }
-        else if (k == 8) { MOE_BY_EPL(MOE_CALL8) }
-        else { MOE_BY_EPL(MOE_CALL16) }
-#undef MOE_CALL4
-#undef MOE_CALL8
-#undef MOE_CALL16
-    } else {
-        const int grid = (T + kTopkWaves - 1) / kTopkWaves;
+    if (const int tokens = seg_tokens_of(T, E, k)) {
+        const int n_seg = (T + tokens - 1) / tokens, words = seg_words(E);
+        const size_t smem = (size_t)(words + tokens * k) * sizeof(int);
+#define MOE_CALL(N)                                                                       \
+    route_scored_seg_kernel<N><<<n_seg, tokens * WAVE, smem, stream>>>(                   \
+        logits, bias, rule, T, E, k, r.topk_idx, r.topk_w, (uint32_t*)ws)
+        MOE_BY_EPL(MOE_CALL)
+#undef MOE_CALL
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        const int segs = kGroupThreads / (tokens * k);   // whole segments of 1024 assignments
+        const int parts = kGroupThreads / words;
+        const size_t smem_s = (size_t)(group_lds_ints(E) + parts * 2 * 4 * words) * sizeof(int);
+        route_seg_scatter_kernel<<<(n_seg + segs - 1) / segs, kGroupThreads, smem_s, stream>>>(
+            r.topk_idx, (const uint32_t*)ws, n, E, segs * tokens * k, segs, n_seg, block_rows,
+            max_blocks, r);
+        return hipGetLastError();
+    }
+    const int grid = (T + kTopkWaves - 1) / kTopkWaves;
 #define MOE_CALL(N)                                                                           \
     route_scored_kernel<N><<<grid, kTopkWaves * WAVE, 0, stream>>>(logits, bias, rule, T, E, k, \
                                                                    r.topk_idx, r.topk_w)
-        MOE_BY_EPL(MOE_CALL)
+    MOE_BY_EPL(MOE_CALL)
 #undef MOE_CALL
-    }
 #undef MOE_BY_EPL
-    hipError_t err = hipGetLastError();
+    const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const bool stage = n <= kStageMaxAssign;
     const int stage_off = stage ? (int)(group_lds_bytes(E) / sizeof(int)) : 0;
-    const size_t smem = group_lds_bytes(E) + (stage ? (size_t)n * sizeof(int) : 0);
-    if (chunks)
-        route_group_info_kernel<<<1, kGroupThreads, smem, stream>>>(
-            r.topk_idx, info, n, E, block_rows, max_blocks, stage_off, r);
-    else
-        route_group_kernel<<<1, kGroupThreads, smem, stream>>>(r.topk_idx, n, E, block_rows,
-                                                               max_blocks, stage_off, r);
+    route_group_kernel<<<1, kGroupThreads,
+                         group_lds_bytes(E) + (stage ? (size_t)n * sizeof(int) : 0), stream>>>(
+        r.topk_idx, n, E, block_rows, max_blocks, stage_off, r);
     return hipGetLastError();
 }
 

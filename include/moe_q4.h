@@ -149,7 +149,8 @@ int moe_route_max_blocks(int T, int E, int k, int block_rows);
  * 16 and T above the one-launch size (T > 64, or a one-launch LDS need above
  * 64 KB) it is T*k 32-bit words, rounded up to 256 bytes: the top-k pass
  * records each 64-assignment chunk's match information there for the
- * grouping pass.  Otherwise it is 0 and ws may be NULL. */
+ * grouping pass.  Otherwise moe_route needs 0 and ws may be NULL; above 16384
+ * assignments the size also covers moe_route_scored's segment histograms. */
 size_t moe_route_workspace_bytes(int T, int E, int k, int block_rows);
 
 /* GPU-resident routing ([P1] "Prefill optimizations", GPU-resident routing

@@ -159,11 +159,13 @@ def check_scored(lg, bias, k, br=32, score="softmax", **rule):
     assert int(got["n_blocks"][0]) == int(g["n_blocks"])
 
 
-# sizes of one launch (T <= 64), of chunks (k = 4, 8, 16) and of the plain two launches; group
+# sizes of one launch (T <= 64), of segments (k = 4, 8, 16, and above 16384 assignments) and of
+# the one-workgroup grouping; group
 # sizes that are whole lanes (32 of 256), that are not (5 of 60, 20 of 160) and groups of one
 @pytest.mark.parametrize("T,E,k,n_groups,topk_groups", [
     (1, 256, 8, 8, 4), (1, 1, 1, 1, 1), (5, 2, 2, 1, 1), (64, 64, 6, 8, 3), (65, 256, 8, 8, 4), (33, 60, 5, 12, 4),
     (130, 160, 6, 8, 3), (97, 160, 4, 8, 7), (70, 128, 16, 2, 1), (9, 1000, 10, 10, 3), (66, 1000, 8, 8, 2),
+    (2731, 36, 6, 4, 2), (1025, 40, 16, 1, 1), (129, 8, 8, 1, 1), (4099, 12, 4, 3, 2),
     (40, 96, 2, 48, 5), (20, 512, 64, 16, 2), (70, 64, 64, 64, 64), (18, 256, 3, 64, 9), (12, 320, 4, 64, 1)])
 @pytest.mark.parametrize("score,group_score", [("sigmoid", "top2"), ("softmax", "max"), ("softmax", "top2")])
 def test_scored_routing(T, E, k, n_groups, topk_groups, score, group_score):
