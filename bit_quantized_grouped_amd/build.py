@@ -14,7 +14,7 @@ LIB_NAME = "libmoe_q4.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 SOURCES = ["api.hip", "route.hip", "gemm_q4.hip", "combine.hip", "decode.hip", "dequant.hip", "router.hip",
-           "probe.hip", "norm_i8.hip", "gemm_i8.hip"]
+           "probe.hip", "norm_i8.hip", "gemm_i8.hip", "decode_i8.hip"]
 ARCH = "gfx950"
 
 

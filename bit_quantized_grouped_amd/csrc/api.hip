@@ -1026,6 +1026,11 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
         if (!rule && score_bias) return MOE_ERR_SHAPE;   // a bias orders scores: it needs a rule
         const size_t need = rule ? scored_ws_bytes(T, E, k) : route_need(T, E, k);
         if (need && (st = check_ws(route_ws, route_ws_bytes, need))) return st;
+        if (decode_i8_fits(p))
+            return launch_decode_i8(p, logits, score_bias, rule ? &dev : nullptr, gemm_ws, y, stream) ==
+                           hipSuccess
+                       ? MOE_OK
+                       : MOE_ERR_HIP;
         hipError_t e = rule ? launch_route_scored(logits, score_bias, dev, T, E, k, block_rows,
                                                   p.max_blocks, p.r, route_ws, stream)
                             : launch_route(logits, T, E, k, block_rows, p.max_blocks, p.r, route_ws,

@@ -217,4 +217,37 @@ __device__ __forceinline__ void score_topk_token(const float* __restrict__ row,
     __builtin_amdgcn_wave_barrier();
 }
 
+// Routing arrays of one token from its k chosen experts and weights in LDS, by all
+// `threads` threads of a workgroup (the experts differ, so an assignment's row is
+// the number of chosen experts below its own).
+__device__ __forceinline__ void write_one_token(const RoutingDev& r, int E, int k, int max_blocks,
+                                                const int* s_idx, const float* s_w, int tid,
+                                                int threads) {
+    for (int e = tid; e <= E; e += threads) {
+        int off = 0, cnt = 0;
+        for (int j = 0; j < k; ++j) {
+            off += s_idx[j] < e ? 1 : 0;
+            cnt += s_idx[j] == e ? 1 : 0;
+        }
+        r.offsets[e] = off;
+        if (e < E) r.counts[e] = cnt;
+    }
+    for (int j = tid; j < k; j += threads) {
+        const int e = s_idx[j];
+        int row = 0;
+        for (int i = 0; i < k; ++i) row += s_idx[i] < e ? 1 : 0;
+        r.topk_idx[j] = e;
+        r.topk_w[j] = s_w[j];
+        r.sorted_assign[row] = j;
+        r.assign_row[j] = row;
+        r.block_expert[row] = e;
+        r.block_row[row] = row;
+    }
+    for (int b = k + tid; b < max_blocks; b += threads) {
+        r.block_expert[b] = -1;
+        r.block_row[b] = -1;
+    }
+    if (tid == 0) r.n_blocks[0] = k;
+}
+
 }  // namespace moeq4

@@ -571,6 +571,20 @@ __global__ __launch_bounds__(kGroupThreads) void route_scored_fused_kernel(
     group_all(s_eids, T * k, E, block_rows, max_blocks, r, s_hist);
 }
 
+// One token: a wave selects, then 256 threads write the arrays without a scan
+// (7.3 us through the fused kernel's sixteen waves, figures below).
+constexpr int kOneThreads = 256;
+template <int EPL>
+__global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
+    const float* __restrict__ logits, const float* __restrict__ bias, ScoreRule rule, int E, int k,
+    int max_blocks, RoutingDev r) {
+    __shared__ int s_idx[kScoredMaxK];
+    __shared__ float s_w[kScoredMaxK];
+    if (threadIdx.x < WAVE) score_topk_token<EPL>(logits, bias, E, k, rule, s_idx, s_w);
+    __syncthreads();
+    write_one_token(r, E, k, max_blocks, s_idx, s_w, threadIdx.x, kOneThreads);
+}
+
 // Segments: above the one-launch size the tokens are cut into segments of 8 or
 // 16, one token per wave of a workgroup that selects their experts and counts
 // them, one byte per expert (a token takes an expert once, so a count is at most
@@ -760,6 +774,13 @@ hipError_t launch_route_scored(const float* logits, const float* bias, const Sco
     else if (epl <= 4) CALL(4);       \
     else if (epl <= 8) CALL(8);       \
     else CALL(16);
+    if (T == 1) {
+#define MOE_CALL(N)                                                                            \
+    route_scored_one_kernel<N><<<1, kOneThreads, 0, stream>>>(logits, bias, rule, E, k, max_blocks, r)
+        MOE_BY_EPL(MOE_CALL)
+#undef MOE_CALL
+        return hipGetLastError();
+    }
     if (use_fused(T, E, k)) {
         const size_t smem = (size_t)(group_lds_ints(E) + n) * sizeof(int);
 #define MOE_CALL(N)                                                                              \
