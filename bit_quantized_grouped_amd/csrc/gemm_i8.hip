@@ -12,6 +12,7 @@
 // operand) and the activations (B operand) alike.
 #include "moe_device.h"
 #include "moe_i8.h"
+#include "moe_lds.h"
 
 namespace moeq4 {
 
@@ -207,6 +208,133 @@ __global__ __launch_bounds__(WN* WK* WAVE) void product_i8_kernel(ProductArgs p)
     }
 }
 
+// ---- Dense product of many rows: tiles through LDS ----
+// A workgroup of WM x WN waves owns a BM x BN tile; a wave WM-th of its rows and
+// WN-th of its columns, MF x NF products of 16 x 16.  128 K of both operands (one
+// stage) go straight from memory into LDS, the next stage's while this one is
+// multiplied.  A stage keeps rows of 128 bytes whose eight 16-byte pieces are
+// permuted: place j of row r holds piece j ^ (r % 8), chosen on the source side (a
+// load writes LDS in lane order), so the 16 rows that a fragment read touches lie in
+// different banks while a load still takes whole 128-byte lines.
+template <int BM, int BN, int THREADS>
+struct StageLoads {
+    static constexpr int A = BM * 128 / (THREADS * 16), B = BN * 128 / (THREADS * 16);
+};
+
+template <int WM, int MF, int WN, int NF>
+__global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
+    const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
+    uint16_t* __restrict__ out, int m_tiles, int n_tiles) {
+    constexpr int BM = WM * MF * 16, BN = WN * NF * 16, THREADS = WM * WN * WAVE;
+    constexpr int LA = StageLoads<BM, BN, THREADS>::A, LB = StageLoads<BM, BN, THREADS>::B;
+    constexpr uint32_t kPast = 0xC0000000u;   // past every buffer (both are below 2^31 bytes)
+    __shared__ __attribute__((aligned(16))) int8_t s_a0[BM * 128], s_a1[BM * 128];
+    __shared__ __attribute__((aligned(16))) int8_t s_b0[BN * 128], s_b1[BN * 128];
+    const int lane = threadIdx.x % WAVE;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int wm = wave % WM, wn = wave / WM;
+    // Workgroups go round the 8 XCDs in launch order; each XCD takes a contiguous share of
+    // the tiles, in bands of 4 row tiles, so that its L2 holds what its tiles share.
+    const int total = m_tiles * n_tiles;
+    const int xcd = blockIdx.x % 8, in = blockIdx.x / 8;
+    const int share = total / 8, extra = total % 8;
+    const int id = xcd * share + min(xcd, extra) + in;
+    const int band = id / (4 * n_tiles), rest = id - band * 4 * n_tiles;
+    const int rows_in = min(4, m_tiles - band * 4);
+    const int mt = band * 4 + rest % rows_in, nt = rest / rows_in;
+    const int m0 = mt * BM, n0 = nt * BN;
+
+    const buf_rsrc_t ra = make_buf(a, (uint32_t)M * (uint32_t)K);
+    const buf_rsrc_t rb = make_buf(w.codes, (uint32_t)N * (uint32_t)K);
+    const int piece = (lane % 8) ^ (lane / 8);   // K piece of this lane's place
+    uint32_t va[LA], vb[LB];
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const uint32_t r = m0 + (i * WM * WN + wave) * 8 + lane / 8;
+        va[i] = r < (uint32_t)M ? r * (uint32_t)K + piece * 16 : kPast;
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        const uint32_t r = n0 + (i * WM * WN + wave) * 8 + lane / 8;
+        vb[i] = r >= (uint32_t)N ? kPast
+                : w.tiles ? r / 16 * 16 * (uint32_t)K + piece / 4 * 1024 + piece % 4 * 256 + r % 16 * 16
+                          : r * (uint32_t)K + piece * 16;
+    }
+    const int steps = (K + 127) / 128;
+    const uint32_t b_step = w.tiles ? 2048 : 128;
+    auto load = [&](int8_t* da, int8_t* db, int s) {
+        // pieces past K, of half a last stage or of the stages behind it, are zeros
+        const uint32_t past = s * 128 + (piece & 4) * 16 >= K ? kPast : 0u;
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            buf_to_lds16(ra, da + (i * WM * WN + wave) * 1024, va[i] | past, (uint32_t)s * 128u);
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+            buf_to_lds16(rb, db + (i * WM * WN + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
+    };
+    i32x4_t acc[NF][MF];
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
+    const int fr = lane % 16, fp = lane / 16;
+    auto multiply = [&](const int8_t* sa, const int8_t* sb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = fr * 128 + ((h * 4 + fp) ^ (fr % 8)) * 16;
+            i32x4_t fb[NF];
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+                fb[n] = *(const i32x4_t*)(sb + (wn * NF + n) * 2048 + at);
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const i32x4_t fa = *(const i32x4_t*)(sa + (wm * MF + m) * 2048 + at);
+#pragma unroll
+                for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[n], fa, acc[n][m]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one half's fragments in registers at a time
+        }
+    };
+    load(s_a0, s_b0, 0);
+    landed_barrier();
+    for (int s = 0; s < steps; s += 2) {
+        load(s_a1, s_b1, s + 1);
+        multiply(s_a0, s_b0);
+        landed_barrier();
+        load(s_a0, s_b0, s + 2);
+        multiply(s_a1, s_b1);
+        landed_barrier();
+    }
+    float as[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+        as[m] = a_scale[min(m0 + (wm * MF + m) * 16 + fr, M - 1)];
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+        const int c = n0 + (wn * NF + n) * 16 + fp * 4;
+        if (c >= N) continue;
+        float ws[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws[i] = w.scales[min(c + i, N - 1)];
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int r = m0 + (wm * MF + m) * 16 + fr;
+            if (r >= M) continue;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (float)acc[n][m][i] * as[m] * ws[i];
+            uint16_t* o = out + (size_t)r * N + c;
+            if (N % 4 == 0) {
+                *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < N) o[i] = (uint16_t)pack_bf16x2(v[i], 0.f);
+            }
+        }
+    }
+}
+
 // Row-wise quantisation of h: one workgroup per row, the routed rows and then the
 // shared expert's.
 constexpr int kQuantThreads = 128;
@@ -280,8 +408,17 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
                             int N, uint16_t* out, void*, hipStream_t stream) {
     ProductArgs p{};
     p.dense = PartI8{a, a_scale, w, {}, M, N, K, out};
+#define MOE_TILES(WM, MF, WN, NF)                                                             \
+    {                                                                                         \
+        const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
+        linear_tiles_kernel<WM, MF, WN, NF><<<mt * nt, WM * WN * WAVE, 0, stream>>>(          \
+            a, a_scale, M, K, w, N, out, mt, nt);                                             \
+    }
     if (M <= 16) launch_product<1, 1, 1, 4, 8, false>(p, 0, stream);
-    else launch_product<4, 2, 4, 1, 2, false>(p, 0, stream);
+    else if ((long long)cdiv(M, 256) * cdiv(N, 256) >= 200) MOE_TILES(2, 8, 4, 4)
+    else if ((long long)cdiv(M, 128) * cdiv(N, 128) >= 128) MOE_TILES(2, 4, 2, 4)
+    else MOE_TILES(2, 2, 2, 2)
+#undef MOE_TILES
     return hipGetLastError();
 }
 

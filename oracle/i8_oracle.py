@@ -27,7 +27,7 @@ def norm(x: np.ndarray, residual, weight: np.ndarray, eps: float):
 
 def linear(a, a_scale, w, w_scale) -> np.ndarray:
     """a [M, K], w [N, K] codes with their rows' scales -> [M, N] float64."""
-    prod = a.astype(np.int64) @ w.astype(np.int64).T
+    prod = a.astype(np.float64) @ w.astype(np.float64).T   # integers below 2^53: exact
     return prod * a_scale.astype(np.float64)[:, None] * w_scale.astype(np.float64)[None, :]
 
 
