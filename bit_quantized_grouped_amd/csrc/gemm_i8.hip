@@ -278,7 +278,11 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
         for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
     const int fr = lane % 16, fp = lane / 16;
+    // The fragments of the next products are read while the present ones run: the order
+    // below is what the scheduler keeps (2 row fragments ahead, and the next half's columns
+    // with the last ones).
     auto multiply = [&](const int8_t* sa, const int8_t* sb) {
+        __builtin_amdgcn_sched_barrier(0);   // behind the requests of the next stage
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int at = fr * 128 + ((h * 4 + fp) ^ (fr % 8)) * 16;
@@ -292,8 +296,19 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
                 for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[n], fa, acc[n][m]);
             }
-            __builtin_amdgcn_sched_barrier(0);   // one half's fragments in registers at a time
         }
+        constexpr int kRead = 0x100, kMul = 0x8;
+        __builtin_amdgcn_sched_group_barrier(kRead, NF + (MF < 4 ? MF : 4), 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MF; m += 2) {
+                __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
+                if (m + 4 < MF) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+                else if (h == 0 && m + 2 < MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + 2, 0);
+                else if (h == 0) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+            }
+        __builtin_amdgcn_sched_barrier(0);
     };
     load(s_a0, s_b0, 0);
     landed_barrier();
