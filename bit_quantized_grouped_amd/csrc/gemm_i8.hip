@@ -210,26 +210,43 @@ __global__ __launch_bounds__(WN* WK* WAVE) void product_i8_kernel(ProductArgs p)
 
 // ---- Dense product of many rows: tiles through LDS ----
 // A workgroup of WM x WN waves owns a BM x BN tile; a wave WM-th of its rows and
-// WN-th of its columns, MF x NF products of 16 x 16.  128 K of both operands (one
-// stage) go straight from memory into LDS, the next stage's while this one is
-// multiplied.  A stage keeps rows of 128 bytes whose eight 16-byte pieces are
-// permuted: place j of row r holds piece j ^ (r % 8), chosen on the source side (a
-// load writes LDS in lane order), so the 16 rows that a fragment read touches lie in
-// different banks while a load still takes whole 128-byte lines.
-template <int BM, int BN, int THREADS>
-struct StageLoads {
-    static constexpr int A = BM * 128 / (THREADS * 16), B = BN * 128 / (THREADS * 16);
-};
-
-template <int WM, int MF, int WN, int NF>
+// WN-th of its columns, MF x NF products of 16 x 16.  64 K of both operands (one
+// stage) go straight from memory into LDS, ST - 1 stages ahead of the one that is
+// multiplied: a stage of the 256 x 256 tile is 1024 cycles of products, and a load
+// takes two to four times that under full traffic.  Stages past K are zeros and
+// multiplied like the others.  A stage keeps rows of 64 bytes
+// whose four 16-byte pieces are permuted: place j of row r holds piece
+// j ^ (r / 4 % 4), chosen on the source side (a load writes LDS in lane order), so
+// the 16 rows that a fragment read touches lie in different banks.
+// Waits count this wave's own loads (LA + LB a stage): the kernel must not spill,
+// which the build checks.
+template <int WM, int MF, int WN, int NF, int ST>
 __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
     uint16_t* __restrict__ out, int m_tiles, int n_tiles) {
-    constexpr int BM = WM * MF * 16, BN = WN * NF * 16, THREADS = WM * WN * WAVE;
-    constexpr int LA = StageLoads<BM, BN, THREADS>::A, LB = StageLoads<BM, BN, THREADS>::B;
+    constexpr int BM = WM * MF * 16, BN = WN * NF * 16, WAVES = WM * WN;
+    constexpr int LA = BM / 16 / WAVES, LB = BN / 16 / WAVES;   // 1 KB loads per wave and stage
+    static_assert(BM / 16 % WAVES == 0 && BN / 16 % WAVES == 0, "whole loads per wave");
     constexpr uint32_t kPast = 0xC0000000u;   // past every buffer (both are below 2^31 bytes)
-    __shared__ __attribute__((aligned(16))) int8_t s_a0[BM * 128], s_a1[BM * 128];
-    __shared__ __attribute__((aligned(16))) int8_t s_b0[BN * 128], s_b1[BN * 128];
+    // an array for each stage: loads into one would otherwise hold up reads of the others
+#define MOE_STAGE(i) \
+    __shared__ __attribute__((aligned(16))) int8_t s_a##i[ST > i ? BM * 64 : 16], s_b##i[ST > i ? BN * 64 : 16]
+    MOE_STAGE(0);
+    MOE_STAGE(1);
+    MOE_STAGE(2);
+    MOE_STAGE(3);
+    MOE_STAGE(4);
+    MOE_STAGE(5);
+    MOE_STAGE(6);
+    MOE_STAGE(7);
+#undef MOE_STAGE
+    static_assert(ST >= 4 && ST <= 8 && ST % 2 == 0, "a stage for each array; fragments alternate");
+    auto s_a = [&](int i) {
+        return i == 0 ? s_a0 : i == 1 ? s_a1 : i == 2 ? s_a2 : i == 3 ? s_a3 : i == 4 ? s_a4 : i == 5 ? s_a5 : i == 6 ? s_a6 : s_a7;
+    };
+    auto s_b = [&](int i) {
+        return i == 0 ? s_b0 : i == 1 ? s_b1 : i == 2 ? s_b2 : i == 3 ? s_b3 : i == 4 ? s_b4 : i == 5 ? s_b5 : i == 6 ? s_b6 : s_b7;
+    };
     const int lane = threadIdx.x % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wm = wave % WM, wn = wave / WM;
@@ -246,31 +263,30 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 
     const buf_rsrc_t ra = make_buf(a, (uint32_t)M * (uint32_t)K);
     const buf_rsrc_t rb = make_buf(w.codes, (uint32_t)N * (uint32_t)K);
-    const int piece = (lane % 8) ^ (lane / 8);   // K piece of this lane's place
+    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 4);   // row and K piece of this lane's place
     uint32_t va[LA], vb[LB];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-        const uint32_t r = m0 + (i * WM * WN + wave) * 8 + lane / 8;
+        const uint32_t r = m0 + (i * WAVES + wave) * 16 + lr;
         va[i] = r < (uint32_t)M ? r * (uint32_t)K + piece * 16 : kPast;
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-        const uint32_t r = n0 + (i * WM * WN + wave) * 8 + lane / 8;
+        const uint32_t r = n0 + (i * WAVES + wave) * 16 + lr;
         vb[i] = r >= (uint32_t)N ? kPast
-                : w.tiles ? r / 16 * 16 * (uint32_t)K + piece / 4 * 1024 + piece % 4 * 256 + r % 16 * 16
-                          : r * (uint32_t)K + piece * 16;
+                : w.tiles        ? (r - lr) * (uint32_t)K + piece * 256 + lr * 16
+                                 : r * (uint32_t)K + piece * 16;
     }
-    const int steps = (K + 127) / 128;
-    const uint32_t b_step = w.tiles ? 2048 : 128;
-    auto load = [&](int8_t* da, int8_t* db, int s) {
-        // pieces past K, of half a last stage or of the stages behind it, are zeros
-        const uint32_t past = s * 128 + (piece & 4) * 16 >= K ? kPast : 0u;
+    const int steps = K / 64;
+    const uint32_t b_step = w.tiles ? 1024 : 64;
+    auto load = [&](int st, int s) {
+        const uint32_t past = s < steps ? 0u : kPast;   // stages behind the last are zeros
 #pragma unroll
         for (int i = 0; i < LA; ++i)
-            buf_to_lds16(ra, da + (i * WM * WN + wave) * 1024, va[i] | past, (uint32_t)s * 128u);
+            buf_to_lds16(ra, s_a(st) + (i * WAVES + wave) * 1024, va[i] | past, (uint32_t)s * 64u);
 #pragma unroll
         for (int i = 0; i < LB; ++i)
-            buf_to_lds16(rb, db + (i * WM * WN + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
+            buf_to_lds16(rb, s_b(st) + (i * WAVES + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
     };
     i32x4_t acc[NF][MF];
 #pragma unroll
@@ -278,48 +294,50 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
         for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
     const int fr = lane % 16, fp = lane / 16;
-    // The fragments of the next products are read while the present ones run: the order
-    // below is what the scheduler keeps (2 row fragments ahead, and the next half's columns
-    // with the last ones).
-    auto multiply = [&](const int8_t* sa, const int8_t* sb) {
-        __builtin_amdgcn_sched_barrier(0);   // behind the requests of the next stage
+    const int at = fr * 64 + (fp ^ (fr / 4)) * 16;
+    auto read_b = [&](int st, int n) { return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 + at); };
+    auto read_a = [&](int st, int m) { return *(const i32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + at); };
+    // A step multiplies stage s while it reads, in the order below, the row fragments it
+    // lacks and the next stage's columns and first FA row fragments, so that the products
+    // go on at once behind the barrier: that stage landed a barrier earlier.
+    constexpr int FA = MF < 4 ? MF : 4;
+    i32x4_t fb[2][NF], fa[2][FA];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = fr * 128 + ((h * 4 + fp) ^ (fr % 8)) * 16;
-            i32x4_t fb[NF];
+    for (int st = 0; st < ST - 1; ++st) load(st, st);
+    wait_loads<(ST - 3) * (LA + LB)>();
+    bare_barrier_i8();
 #pragma unroll
-            for (int n = 0; n < NF; ++n)
-                fb[n] = *(const i32x4_t*)(sb + (wn * NF + n) * 2048 + at);
+    for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, n);
+#pragma unroll
+    for (int m = 0; m < FA; ++m) fa[0][m] = read_a(0, m);
+    for (int s = 0; s < steps; s += ST) {
+#pragma unroll
+        for (int st = 0; st < ST; ++st) {
+            const int c = st % 2, next = (st + 1) % ST;
+            load((st + ST - 1) % ST, s + st + ST - 1);
+            __builtin_amdgcn_sched_barrier(0);   // the requests go out first
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-                const i32x4_t fa = *(const i32x4_t*)(sa + (wm * MF + m) * 2048 + at);
+                const i32x4_t f = m < FA ? fa[c][m] : read_a(st, m);
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[n], fa, acc[n][m]);
+                for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[c][n], f, acc[n][m]);
             }
-        }
-        constexpr int kRead = 0x100, kMul = 0x8;
-        __builtin_amdgcn_sched_group_barrier(kRead, NF + (MF < 4 ? MF : 4), 0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(next, n);
+#pragma unroll
+            for (int m = 0; m < FA; ++m) fa[1 - c][m] = read_a(next, m);
+            constexpr int kRead = 0x100, kMul = 0x8;
 #pragma unroll
             for (int m = 0; m < MF; m += 2) {
-                __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
                 if (m + 4 < MF) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
-                else if (h == 0 && m + 2 < MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + 2, 0);
-                else if (h == 0) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+                else if (m + 2 >= MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + FA, 0);
+                __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
             }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    load(s_a0, s_b0, 0);
-    landed_barrier();
-    for (int s = 0; s < steps; s += 2) {
-        load(s_a1, s_b1, s + 1);
-        multiply(s_a0, s_b0);
-        landed_barrier();
-        load(s_a0, s_b0, s + 2);
-        multiply(s_a1, s_b1);
-        landed_barrier();
+            wait_loads<(ST - 3) * (LA + LB)>();
+            bare_barrier_i8();
+        }
     }
+    wait_loads<0>();
     float as[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -423,16 +441,16 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
                             int N, uint16_t* out, void*, hipStream_t stream) {
     ProductArgs p{};
     p.dense = PartI8{a, a_scale, w, {}, M, N, K, out};
-#define MOE_TILES(WM, MF, WN, NF)                                                             \
+#define MOE_TILES(WM, MF, WN, NF, ST)                                                         \
     {                                                                                         \
         const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
-        linear_tiles_kernel<WM, MF, WN, NF><<<mt * nt, WM * WN * WAVE, 0, stream>>>(          \
+        linear_tiles_kernel<WM, MF, WN, NF, ST><<<mt * nt, WM * WN * WAVE, 0, stream>>>(      \
             a, a_scale, M, K, w, N, out, mt, nt);                                             \
     }
     if (M <= 16) launch_product<1, 1, 1, 4, 8, false>(p, 0, stream);
-    else if ((long long)cdiv(M, 256) * cdiv(N, 256) >= 200) MOE_TILES(2, 8, 4, 4)
-    else if ((long long)cdiv(M, 128) * cdiv(N, 128) >= 128) MOE_TILES(2, 4, 2, 4)
-    else MOE_TILES(2, 2, 2, 2)
+    else if ((long long)cdiv(M, 256) * cdiv(N, 256) >= 200) MOE_TILES(2, 8, 4, 4, 4)
+    else if ((long long)cdiv(M, 128) * cdiv(N, 128) >= 128) MOE_TILES(2, 4, 2, 4, 4)
+    else MOE_TILES(2, 2, 2, 2, 8)
 #undef MOE_TILES
     return hipGetLastError();
 }

@@ -21,10 +21,16 @@ __device__ __forceinline__ void buf_to_lds16(buf_rsrc_t r, void* lds, uint32_t v
 #endif
 }
 
-// Waits for this wave's vector loads, then for the workgroup; no fence beyond that,
-// which would also wait for nothing more but keep LDS reads from moving up.
-__device__ __forceinline__ void landed_barrier() {
-    __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xF << 8));   // vmcnt(0)
+// Waits until at most N of this wave's vector loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+// Workgroup barrier without a memory fence, which would wait for every load still in
+// flight: the caller has waited for what the other waves must see.  Nothing moves
+// across it.
+__device__ __forceinline__ void bare_barrier_i8() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
