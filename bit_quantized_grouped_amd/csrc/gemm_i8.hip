@@ -251,32 +251,40 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wm = wave % WM, wn = wave / WM;
     // Workgroups go round the 8 XCDs in launch order; each XCD takes a contiguous share of
-    // the tiles, in bands of 4 row tiles, so that its L2 holds what its tiles share.
+    // the tiles, in bands of 4 row tiles, so that its L2 holds what its tiles share, and
+    // its workgroups go through that share.
     const int total = m_tiles * n_tiles;
-    const int xcd = blockIdx.x % 8, in = blockIdx.x / 8;
-    const int share = total / 8, extra = total % 8;
-    const int id = xcd * share + min(xcd, extra) + in;
-    const int band = id / (4 * n_tiles), rest = id - band * 4 * n_tiles;
-    const int rows_in = min(4, m_tiles - band * 4);
-    const int mt = band * 4 + rest % rows_in, nt = rest / rows_in;
-    const int m0 = mt * BM, n0 = nt * BN;
+    const int xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+    const int first = xcd * (total / 8) + min(xcd, total % 8);
+    const int mine = total / 8 + (xcd < total % 8 ? 1 : 0);
+    int in = blockIdx.x / 8;
+    if (in >= mine) return;
+    auto corner = [&](int i, int& m0, int& n0) {
+        const int id = first + i;
+        const int band = id / (4 * n_tiles), rest = id - band * 4 * n_tiles;
+        const int rows_in = min(4, m_tiles - band * 4);
+        m0 = (band * 4 + rest % rows_in) * BM;
+        n0 = rest / rows_in * BN;
+    };
 
     const buf_rsrc_t ra = make_buf(a, (uint32_t)M * (uint32_t)K);
     const buf_rsrc_t rb = make_buf(w.codes, (uint32_t)N * (uint32_t)K);
     const int lr = lane / 4, piece = (lane % 4) ^ (lr / 4);   // row and K piece of this lane's place
     uint32_t va[LA], vb[LB];
+    auto sources = [&](int m0, int n0) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-        const uint32_t r = m0 + (i * WAVES + wave) * 16 + lr;
-        va[i] = r < (uint32_t)M ? r * (uint32_t)K + piece * 16 : kPast;
-    }
+        for (int i = 0; i < LA; ++i) {
+            const uint32_t r = m0 + (i * WAVES + wave) * 16 + lr;
+            va[i] = r < (uint32_t)M ? r * (uint32_t)K + piece * 16 : kPast;
+        }
 #pragma unroll
-    for (int i = 0; i < LB; ++i) {
-        const uint32_t r = n0 + (i * WAVES + wave) * 16 + lr;
-        vb[i] = r >= (uint32_t)N ? kPast
-                : w.tiles        ? (r - lr) * (uint32_t)K + piece * 256 + lr * 16
-                                 : r * (uint32_t)K + piece * 16;
-    }
+        for (int i = 0; i < LB; ++i) {
+            const uint32_t r = n0 + (i * WAVES + wave) * 16 + lr;
+            vb[i] = r >= (uint32_t)N ? kPast
+                    : w.tiles        ? (r - lr) * (uint32_t)K + piece * 256 + lr * 16
+                                     : r * (uint32_t)K + piece * 16;
+        }
+    };
     const int steps = K / 64;
     const uint32_t b_step = w.tiles ? 1024 : 64;
     auto load = [&](int st, int s) {
@@ -289,10 +297,6 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
             buf_to_lds16(rb, s_b(st) + (i * WAVES + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
     };
     i32x4_t acc[NF][MF];
-#pragma unroll
-    for (int n = 0; n < NF; ++n)
-#pragma unroll
-        for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
     const int fr = lane % 16, fp = lane / 16;
     const int at = fr * 64 + (fp ^ (fr / 4)) * 16;
     auto read_b = [&](int st, int n) { return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 + at); };
@@ -302,6 +306,9 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     // go on at once behind the barrier: that stage landed a barrier earlier.
     constexpr int FA = MF < 4 ? MF : 4;
     i32x4_t fb[2][NF], fa[2][FA];
+    int m0, n0, m1 = 0, n1 = 0;
+    corner(in, m0, n0);
+    sources(m0, n0);
 #pragma unroll
     for (int st = 0; st < ST - 1; ++st) load(st, st);
     wait_loads<(ST - 3) * (LA + LB)>();
@@ -310,62 +317,110 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, n);
 #pragma unroll
     for (int m = 0; m < FA; ++m) fa[0][m] = read_a(0, m);
-    for (int s = 0; s < steps; s += ST) {
+    const int rounds = (steps + ST - 1) / ST;
+    for (;;) {
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-            const int c = st % 2, next = (st + 1) % ST;
-            load((st + ST - 1) % ST, s + st + ST - 1);
-            __builtin_amdgcn_sched_barrier(0);   // the requests go out first
+        for (int n = 0; n < NF; ++n)
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                const i32x4_t f = m < FA ? fa[c][m] : read_a(st, m);
+            for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
+        in += stride;
+        const bool more = in < mine;
+        if (more) corner(in, m1, n1);
+        for (int round = 0; round < rounds; ++round) {
+            int s = round * ST + ST - 1;   // stage that the step requests
 #pragma unroll
-                for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[c][n], f, acc[n][m]);
+            for (int st = 0; st < ST; ++st) {
+                const int c = st % 2, next = (st + 1) % ST;
+                load((st + ST - 1) % ST, s + st);
+                if (st == 0 && round == rounds - 1) {   // from here on the next tile's stages
+                    if (more) sources(m1, n1);
+                    s = more ? -1 : steps;   // no tile: zeros
+                }
+                __builtin_amdgcn_sched_barrier(0);   // the requests go out first
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    const i32x4_t f = m < FA ? fa[c][m] : read_a(st, m);
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[c][n], f, acc[n][m]);
+                }
+#pragma unroll
+                for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(next, n);
+#pragma unroll
+                for (int m = 0; m < FA; ++m) fa[1 - c][m] = read_a(next, m);
+                constexpr int kRead = 0x100, kMul = 0x8;
+#pragma unroll
+                for (int m = 0; m < MF; m += 2) {
+                    if (m + 4 < MF) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+                    else if (m + 2 >= MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + FA, 0);
+                    __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
+                }
+                wait_loads<(ST - 3) * (LA + LB)>();
+                bare_barrier_i8();
             }
-#pragma unroll
-            for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(next, n);
-#pragma unroll
-            for (int m = 0; m < FA; ++m) fa[1 - c][m] = read_a(next, m);
-            constexpr int kRead = 0x100, kMul = 0x8;
-#pragma unroll
-            for (int m = 0; m < MF; m += 2) {
-                if (m + 4 < MF) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
-                else if (m + 2 >= MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + FA, 0);
-                __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
-            }
-            wait_loads<(ST - 3) * (LA + LB)>();
-            bare_barrier_i8();
         }
+        // The tile's values.  Where rows of out start at 16 bytes they go through the wave's
+        // share of the last stage (the next tile's stages lie in the others), 32 rows at a
+        // time, so that a store covers whole 128-byte lines; a wave's LDS operations complete
+        // in order, so no barrier is needed inside it.
+        constexpr int kLdc = NF * 16 + 8;   // bf16 of a staged row, padded against bank conflicts
+        uint16_t* s_o = (uint16_t*)(wave < WAVES / 2 ? s_a(ST - 1) + wave * (BM * 64 / (WAVES / 2))
+                                                     : s_b(ST - 1) + (wave - WAVES / 2) * (BN * 64 / (WAVES / 2)));
+        constexpr int kRows = BM * 64 / (WAVES / 2) / (kLdc * 2) >= 32 ? 32 : 16;
+        static_assert(BM == BN && kRows * kLdc * 2 <= BM * 64 / (WAVES / 2) && MF * 16 % kRows == 0,
+                      "a wave's staged rows fit its share");
+        const bool wide = N % 8 == 0;
+        float as[MF], ws[NF][4];
+#pragma unroll
+        for (int m = 0; m < MF; ++m) as[m] = a_scale[min(m0 + (wm * MF + m) * 16 + fr, M - 1)];
+#pragma unroll
+        for (int n = 0; n < NF; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ws[n][i] = w.scales[min(n0 + (wn * NF + n) * 16 + fp * 4 + i, N - 1)];
+#pragma unroll
+        for (int mb = 0; mb < MF; mb += kRows / 16) {
+#pragma unroll
+            for (int mi = 0; mi < kRows / 16; ++mi) {
+                const int m = mb + mi, r = m0 + (wm * MF + m) * 16 + fr;
+#pragma unroll
+                for (int n = 0; n < NF; ++n) {
+                    const int c = n0 + (wn * NF + n) * 16 + fp * 4;
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = (float)acc[n][m][i] * as[m] * ws[n][i];
+                    const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    if (wide) {
+                        *(u32x2_t*)(s_o + (mi * 16 + fr) * kLdc + n * 16 + fp * 4) = o;
+                    } else if (r < M) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (c + i < N) out[(size_t)r * N + c + i] = (uint16_t)(o[i / 2] >> 16 * (i % 2));
+                    }
+                }
+            }
+            if (wide) {
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int i = 0; i < kRows * NF * 2 / WAVE; ++i) {
+                    const int p = i * WAVE + lane, row = p / (NF * 2), c8 = p % (NF * 2) * 8;
+                    const int r = m0 + (wm * MF + mb) * 16 + row, c = n0 + wn * NF * 16 + c8;
+                    if (r < M && c < N)
+                        *(u32x4_t*)(out + (size_t)r * N + c) = *(const u32x4_t*)(s_o + row * kLdc + c8);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        if (!more) break;
+        m0 = m1;
+        n0 = n1;
+        // The staging place is the next request's.  Stores still in flight only make the
+        // counted waits of the next tile stricter.
+        bare_barrier_i8();
     }
     wait_loads<0>();
-    float as[MF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m)
-        as[m] = a_scale[min(m0 + (wm * MF + m) * 16 + fr, M - 1)];
-#pragma unroll
-    for (int n = 0; n < NF; ++n) {
-        const int c = n0 + (wn * NF + n) * 16 + fp * 4;
-        if (c >= N) continue;
-        float ws[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ws[i] = w.scales[min(c + i, N - 1)];
-#pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int r = m0 + (wm * MF + m) * 16 + fr;
-            if (r >= M) continue;
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (float)acc[n][m][i] * as[m] * ws[i];
-            uint16_t* o = out + (size_t)r * N + c;
-            if (N % 4 == 0) {
-                *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i < N) o[i] = (uint16_t)pack_bf16x2(v[i], 0.f);
-            }
-        }
-    }
 }
 
 // Row-wise quantisation of h: one workgroup per row, the routed rows and then the
@@ -425,6 +480,8 @@ hipError_t launch_prepack_i8(const int8_t* src, int n_exp, int N, int K, int8_t*
 
 size_t linear_i8_ws_bytes(int, int, int) { return 0; }
 
+constexpr int kCUs = 256, kLdsBytes = 160 * 1024;   // of an MI355X, of a CU
+
 static int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 template <int MT, int NT, int WN, int WK, int D, bool GATEUP>
@@ -444,7 +501,9 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
 #define MOE_TILES(WM, MF, WN, NF, ST)                                                         \
     {                                                                                         \
         const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
-        linear_tiles_kernel<WM, MF, WN, NF, ST><<<mt * nt, WM * WN * WAVE, 0, stream>>>(      \
+        const int lds = (WM * MF + WN * NF) * 1024 * ST, most = kCUs * (kLdsBytes / lds);     \
+        const int grid = mt * nt < most ? (mt * nt + 7) / 8 * 8 : most;                       \
+        linear_tiles_kernel<WM, MF, WN, NF, ST><<<grid, WM * WN * WAVE, 0, stream>>>(         \
             a, a_scale, M, K, w, N, out, mt, nt);                                             \
     }
     if (M <= 16) launch_product<1, 1, 1, 4, 8, false>(p, 0, stream);
