@@ -35,12 +35,14 @@ def common_flags() -> list[str]:
 
 # Kernels whose pipeline waits count their own vector loads (s_waitcnt vmcnt with
 # a fixed count, then a barrier without a fence): the gate/up kernel on packed
-# scale|bias words with 128-K chunks, whose x rows go straight into LDS.  A
+# scale|bias words with 128-K chunks, whose x rows go straight into LDS, and the
+# 8-bit product's tile kernel, whose operands do.  A
 # register spill would add scratch loads and stores to that count and turn the
 # waits into races, so the build fails if any of them uses scratch.
 # Template arguments: NMAT 2, MT, KC 128, NSUB, DEPTH, WAVES, BF false, SB true.
 COUNTED_WAIT_KERNELS = re.compile(
-    r"grouped_q4_kernelILi2ELi\d+ELi128ELi\d+ELi\d+ELi\d+ELb0ELb1EE")
+    r"grouped_q4_kernelILi2ELi\d+ELi128ELi\d+ELi\d+ELi\d+ELb0ELb1EE|linear_tiles_kernelI")
+COUNTED_WAIT_SOURCES = ("gemm_q4.hip", "gemm_i8.hip")
 
 
 def check_no_scratch(remarks: str) -> int:
@@ -63,7 +65,7 @@ def check_no_scratch(remarks: str) -> int:
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
-    extra = ["-Rpass-analysis=kernel-resource-usage"] if src == "gemm_q4.hip" else []
+    extra = ["-Rpass-analysis=kernel-resource-usage"] if src in COUNTED_WAIT_SOURCES else []
     cmd = [hipcc(), *common_flags(), *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -71,7 +73,7 @@ def _compile(src: str, verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stdout}\n{r.stderr}")
     if extra and check_no_scratch(r.stderr) == 0:
-        raise RuntimeError("gemm_q4.hip: no counted-wait kernel in the resource remarks")
+        raise RuntimeError(f"{src}: no counted-wait kernel in the resource remarks")
     return obj
 
 

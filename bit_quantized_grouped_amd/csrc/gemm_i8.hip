@@ -210,27 +210,27 @@ __global__ __launch_bounds__(WN* WK* WAVE) void product_i8_kernel(ProductArgs p)
 
 // ---- Dense product of many rows: tiles through LDS ----
 // A workgroup of WM x WN waves owns a BM x BN tile; a wave WM-th of its rows and
-// WN-th of its columns, MF x NF products of 16 x 16.  64 K of both operands (one
-// stage) go straight from memory into LDS, ST - 1 stages ahead of the one that is
+// WN-th of its columns, MF x NF products of 16 x 16.  KS blocks of 64 K of both
+// operands (one stage) go straight from memory into LDS, ST - 1 stages ahead of the one that is
 // multiplied: a stage of the 256 x 256 tile is 1024 cycles of products, and a load
 // takes two to four times that under full traffic.  Stages past K are zeros and
-// multiplied like the others.  A stage keeps rows of 64 bytes
+// multiplied like the others.  A block keeps rows of 64 bytes
 // whose four 16-byte pieces are permuted: place j of row r holds piece
 // j ^ (r / 4 % 4), chosen on the source side (a load writes LDS in lane order), so
 // the 16 rows that a fragment read touches lie in different banks.
-// Waits count this wave's own loads (LA + LB a stage): the kernel must not spill,
+// Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
 // which the build checks.
-template <int WM, int MF, int WN, int NF, int ST>
+template <int WM, int MF, int WN, int NF, int ST, int KS>
 __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
     uint16_t* __restrict__ out, int m_tiles, int n_tiles) {
     constexpr int BM = WM * MF * 16, BN = WN * NF * 16, WAVES = WM * WN;
-    constexpr int LA = BM / 16 / WAVES, LB = BN / 16 / WAVES;   // 1 KB loads per wave and stage
+    constexpr int LA = BM / 16 / WAVES, LB = BN / 16 / WAVES;   // 1 KB loads per wave and block
     static_assert(BM / 16 % WAVES == 0 && BN / 16 % WAVES == 0, "whole loads per wave");
     constexpr uint32_t kPast = 0xC0000000u;   // past every buffer (both are below 2^31 bytes)
     // an array for each stage: loads into one would otherwise hold up reads of the others
 #define MOE_STAGE(i) \
-    __shared__ __attribute__((aligned(16))) int8_t s_a##i[ST > i ? BM * 64 : 16], s_b##i[ST > i ? BN * 64 : 16]
+    __shared__ __attribute__((aligned(16))) int8_t s_a##i[ST > i ? BM * 64 * KS : 16], s_b##i[ST > i ? BN * 64 * KS : 16]
     MOE_STAGE(0);
     MOE_STAGE(1);
     MOE_STAGE(2);
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     MOE_STAGE(6);
     MOE_STAGE(7);
 #undef MOE_STAGE
-    static_assert(ST >= 4 && ST <= 8 && ST % 2 == 0, "a stage for each array; fragments alternate");
+    static_assert(ST >= 4 && ST <= 8 && ST * KS % 2 == 0, "a stage for each array; fragments alternate");
     auto s_a = [&](int i) {
         return i == 0 ? s_a0 : i == 1 ? s_a1 : i == 2 ? s_a2 : i == 3 ? s_a3 : i == 4 ? s_a4 : i == 5 ? s_a5 : i == 6 ? s_a6 : s_a7;
     };
@@ -285,25 +285,33 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
                                      : r * (uint32_t)K + piece * 16;
         }
     };
-    const int steps = K / 64;
+    const int blocks = K / 64, steps = (blocks + KS - 1) / KS;
     const uint32_t b_step = w.tiles ? 1024 : 64;
     auto load = [&](int st, int s) {
-        const uint32_t past = s < steps ? 0u : kPast;   // stages behind the last are zeros
 #pragma unroll
-        for (int i = 0; i < LA; ++i)
-            buf_to_lds16(ra, s_a(st) + (i * WAVES + wave) * 1024, va[i] | past, (uint32_t)s * 64u);
+        for (int q = 0; q < KS; ++q) {
+            const uint32_t k = (uint32_t)(s * KS + q);
+            const uint32_t past = k < (uint32_t)blocks ? 0u : kPast;   // blocks behind the last are zeros
 #pragma unroll
-        for (int i = 0; i < LB; ++i)
-            buf_to_lds16(rb, s_b(st) + (i * WAVES + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
+            for (int i = 0; i < LA; ++i)
+                buf_to_lds16(ra, s_a(st) + q * BM * 64 + (i * WAVES + wave) * 1024, va[i] | past, k * 64u);
+#pragma unroll
+            for (int i = 0; i < LB; ++i)
+                buf_to_lds16(rb, s_b(st) + q * BN * 64 + (i * WAVES + wave) * 1024, vb[i] | past, k * b_step);
+        }
     };
     i32x4_t acc[NF][MF];
     const int fr = lane % 16, fp = lane / 16;
     const int at = fr * 64 + (fp ^ (fr / 4)) * 16;
-    auto read_b = [&](int st, int n) { return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 + at); };
-    auto read_a = [&](int st, int m) { return *(const i32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + at); };
-    // A step multiplies stage s while it reads, in the order below, the row fragments it
-    // lacks and the next stage's columns and first FA row fragments, so that the products
-    // go on at once behind the barrier: that stage landed a barrier earlier.
+    auto read_b = [&](int st, int q, int n) {
+        return *(const i32x4_t*)(s_b(st) + q * BN * 64 + (wn * NF + n) * 1024 + at);
+    };
+    auto read_a = [&](int st, int q, int m) {
+        return *(const i32x4_t*)(s_a(st) + q * BM * 64 + (wm * MF + m) * 1024 + at);
+    };
+    // While it multiplies a block a wave reads, in the order below, the row fragments it
+    // lacks and the next block's columns and first FA row fragments, so that the products
+    // go on at once behind a barrier: the next stage landed a barrier earlier.
     constexpr int FA = MF < 4 ? MF : 4;
     i32x4_t fb[2][NF], fa[2][FA];
     int m0, n0, m1 = 0, n1 = 0;
@@ -311,12 +319,12 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     sources(m0, n0);
 #pragma unroll
     for (int st = 0; st < ST - 1; ++st) load(st, st);
-    wait_loads<(ST - 3) * (LA + LB)>();
+    wait_loads<(ST - 3) * KS * (LA + LB)>();
     bare_barrier_i8();
 #pragma unroll
-    for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, n);
+    for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, 0, n);
 #pragma unroll
-    for (int m = 0; m < FA; ++m) fa[0][m] = read_a(0, m);
+    for (int m = 0; m < FA; ++m) fa[0][m] = read_a(0, 0, m);
     const int rounds = (steps + ST - 1) / ST;
     for (;;) {
 #pragma unroll
@@ -330,7 +338,6 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
             int s = round * ST + ST - 1;   // stage that the step requests
 #pragma unroll
             for (int st = 0; st < ST; ++st) {
-                const int c = st % 2, next = (st + 1) % ST;
                 load((st + ST - 1) % ST, s + st);
                 if (st == 0 && round == rounds - 1) {   // from here on the next tile's stages
                     if (more) sources(m1, n1);
@@ -338,35 +345,40 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
                 }
                 __builtin_amdgcn_sched_barrier(0);   // the requests go out first
 #pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                    const i32x4_t f = m < FA ? fa[c][m] : read_a(st, m);
+                for (int q = 0; q < KS; ++q) {
+                    const int c = (st * KS + q) % 2;
+                    const int nst = q + 1 < KS ? st : (st + 1) % ST, nq = (q + 1) % KS;
 #pragma unroll
-                    for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[c][n], f, acc[n][m]);
+                    for (int m = 0; m < MF; ++m) {
+                        const i32x4_t f = m < FA ? fa[c][m] : read_a(st, q, m);
+#pragma unroll
+                        for (int n = 0; n < NF; ++n) acc[n][m] = mfma_i8(fb[c][n], f, acc[n][m]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(nst, nq, n);
+#pragma unroll
+                    for (int m = 0; m < FA; ++m) fa[1 - c][m] = read_a(nst, nq, m);
+                    constexpr int kRead = 0x100, kMul = 0x8;
+#pragma unroll
+                    for (int m = 0; m < MF; m += 2) {
+                        if (m + 4 < MF) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+                        else if (m + 2 >= MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + FA, 0);
+                        __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
+                    }
                 }
-#pragma unroll
-                for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(next, n);
-#pragma unroll
-                for (int m = 0; m < FA; ++m) fa[1 - c][m] = read_a(next, m);
-                constexpr int kRead = 0x100, kMul = 0x8;
-#pragma unroll
-                for (int m = 0; m < MF; m += 2) {
-                    if (m + 4 < MF) __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
-                    else if (m + 2 >= MF) __builtin_amdgcn_sched_group_barrier(kRead, NF + FA, 0);
-                    __builtin_amdgcn_sched_group_barrier(kMul, 2 * NF, 0);
-                }
-                wait_loads<(ST - 3) * (LA + LB)>();
+                wait_loads<(ST - 3) * KS * (LA + LB)>();
                 bare_barrier_i8();
             }
         }
         // The tile's values.  Where rows of out start at 16 bytes they go through the wave's
-        // share of the last stage (the next tile's stages lie in the others), 32 rows at a
+        // share of the last stage (the next tile's stages lie in the others), 16 rows at a
         // time, so that a store covers whole 128-byte lines; a wave's LDS operations complete
         // in order, so no barrier is needed inside it.
         constexpr int kLdc = NF * 16 + 8;   // bf16 of a staged row, padded against bank conflicts
-        uint16_t* s_o = (uint16_t*)(wave < WAVES / 2 ? s_a(ST - 1) + wave * (BM * 64 / (WAVES / 2))
-                                                     : s_b(ST - 1) + (wave - WAVES / 2) * (BN * 64 / (WAVES / 2)));
-        constexpr int kRows = BM * 64 / (WAVES / 2) / (kLdc * 2) >= 32 ? 32 : 16;
-        static_assert(BM == BN && kRows * kLdc * 2 <= BM * 64 / (WAVES / 2) && MF * 16 % kRows == 0,
+        constexpr int kHalf = WAVES / 2, kRows = 16;
+        uint16_t* s_o = (uint16_t*)(wave < kHalf ? s_a(ST - 1) + wave * (BM * 64 * KS / kHalf)
+                                                 : s_b(ST - 1) + (wave - kHalf) * (BN * 64 * KS / kHalf));
+        static_assert(kRows * kLdc * 2 <= (BM < BN ? BM : BN) * 64 * KS / kHalf && kRows * NF * 2 % WAVE == 0,
                       "a wave's staged rows fit its share");
         const bool wide = N % 8 == 0;
         float as[MF], ws[NF][4];
@@ -498,18 +510,31 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
                             int N, uint16_t* out, void*, hipStream_t stream) {
     ProductArgs p{};
     p.dense = PartI8{a, a_scale, w, {}, M, N, K, out};
-#define MOE_TILES(WM, MF, WN, NF, ST)                                                         \
+#define MOE_TILES(WM, MF, WN, NF, ST, KS)                                                         \
     {                                                                                         \
         const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
-        const int lds = (WM * MF + WN * NF) * 1024 * ST, most = kCUs * (kLdsBytes / lds);     \
+        const int lds = (WM * MF + WN * NF) * 1024 * ST * KS, most = kCUs * (kLdsBytes / lds);     \
         const int grid = mt * nt < most ? (mt * nt + 7) / 8 * 8 : most;                       \
-        linear_tiles_kernel<WM, MF, WN, NF, ST><<<grid, WM * WN * WAVE, 0, stream>>>(         \
+        linear_tiles_kernel<WM, MF, WN, NF, ST, KS><<<grid, WM * WN * WAVE, 0, stream>>>(         \
             a, a_scale, M, K, w, N, out, mt, nt);                                             \
     }
-    if (M <= 16) launch_product<1, 1, 1, 4, 8, false>(p, 0, stream);
-    else if ((long long)cdiv(M, 256) * cdiv(N, 256) >= 200) MOE_TILES(2, 8, 4, 4, 4)
-    else if ((long long)cdiv(M, 128) * cdiv(N, 128) >= 128) MOE_TILES(2, 4, 2, 4, 4)
-    else MOE_TILES(2, 2, 2, 2, 8)
+    // The smallest tile that still makes no more than one round of the CUs (the larger ones
+    // read less but leave CUs idle; us measured, small against next larger):
+    //   16 x 16, K over 8 waves, up to two rounds: 17x4096x4096 6.7 / 10.7, 200x512x2048
+    //     5.1 / 6.6, but 64x4096x4096 (1024 tiles) 12.5 / 10.8;
+    //   32 x 64: 333x1001x2048 6.2 / 8.4;  64 x 64: 128x8192x7168 19.4 / 27;
+    //   128 x 64: 333x4096x4096 17.2 / 24, 1000x2048x2048 11.2 / 15;
+    // beyond that 128 x 128 (two on a CU) or 256 x 256, whichever takes fewer rounds:
+    //   2048x4096x4096 44 / 48 (one each), 8192x4096x4096 127 by 256 x 256.
+    auto tiles = [&](int bm, int bn) { return (long long)cdiv(M, bm) * cdiv(N, bn); };
+    const long long r128 = (tiles(128, 128) + 2 * kCUs - 1) / (2 * kCUs);
+    const long long r256 = (tiles(256, 256) + kCUs - 1) / kCUs;
+    if (M <= 16 || tiles(16, 16) <= 2 * kCUs) launch_product<1, 1, 1, 8, 8, false>(p, 0, stream);
+    else if (tiles(32, 64) <= kCUs) MOE_TILES(1, 2, 2, 2, 8, 1)
+    else if (tiles(64, 64) <= kCUs) MOE_TILES(2, 2, 2, 2, 4, 2)
+    else if (tiles(128, 64) <= kCUs) MOE_TILES(2, 4, 2, 2, 4, 2)
+    else if (r128 <= r256) MOE_TILES(2, 4, 2, 4, 4, 2)
+    else MOE_TILES(2, 8, 4, 4, 4, 1)
 #undef MOE_TILES
     return hipGetLastError();
 }
