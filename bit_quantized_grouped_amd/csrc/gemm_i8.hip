@@ -435,6 +435,161 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     wait_loads<0>();
 }
 
+// ---- The experts' products over row blocks: the same ring of stages, one tile per
+// workgroup, BM rows of a block (block_rows) x BN weight rows.  GATEUP: the BN rows are
+// BN / 2 of the gate's and the same of the up's, a wave's NF column fragments half and
+// half, so that a lane holds both sums of a value of h.  Rows behind a partial block's
+// last are requested past the buffer: zeros, without traffic.
+template <int WM, int MF, int WN, int NF, int ST, bool GATEUP>
+__global__ __launch_bounds__(WM* WN* WAVE) void grouped_tiles_kernel(ProductArgs p, uint32_t dense_rows,
+                                                                     uint32_t routed_rows) {
+    constexpr int BM = WM * MF * 16, BN = WN * NF * 16, WAVES = WM * WN;
+    constexpr int NA = BM / 16, NB = BN / 16;                       // 1 KB loads of a stage
+    constexpr int LA = (NA + WAVES - 1) / WAVES, LB = NB / WAVES;   // of a wave, some past the end
+    static_assert(NB % WAVES == 0, "whole weight loads per wave");
+    constexpr uint32_t kPast = 0xC0000000u;
+    constexpr int COLS = GATEUP ? BN / 2 : BN, NW = GATEUP ? NF / 2 : NF;
+#define MOE_STAGE(i) \
+    __shared__ __attribute__((aligned(16))) int8_t s_a##i[ST > i ? LA * WAVES * 1024 : 16], s_b##i[ST > i ? BN * 64 : 16]
+    MOE_STAGE(0);
+    MOE_STAGE(1);
+    MOE_STAGE(2);
+    MOE_STAGE(3);
+    MOE_STAGE(4);
+    MOE_STAGE(5);
+    MOE_STAGE(6);
+    MOE_STAGE(7);
+#undef MOE_STAGE
+    static_assert(ST >= 4 && ST <= 8 && ST % 2 == 0, "a stage for each array; fragments alternate");
+    auto s_a = [&](int i) {
+        return i == 0 ? s_a0 : i == 1 ? s_a1 : i == 2 ? s_a2 : i == 3 ? s_a3 : i == 4 ? s_a4 : i == 5 ? s_a5 : i == 6 ? s_a6 : s_a7;
+    };
+    auto s_b = [&](int i) {
+        return i == 0 ? s_b0 : i == 1 ? s_b1 : i == 2 ? s_b2 : i == 3 ? s_b3 : i == 4 ? s_b4 : i == 5 ? s_b5 : i == 6 ? s_b6 : s_b7;
+    };
+    const int lane = threadIdx.x % WAVE;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int wm = wave % WM, wn = wave / WM;
+    const int dense_wgs = p.dense_blocks * p.dense_tiles;
+    const bool dense = (int)blockIdx.x < dense_wgs;
+    const int id = dense ? blockIdx.x : blockIdx.x - dense_wgs;
+    const int tiles = dense ? p.dense_tiles : p.routed_tiles;
+    const int block = id / tiles, n0 = (id - block * tiles) * COLS;
+    const PartI8& part = dense ? p.dense : p.routed;
+    int e = 0, row0 = block * BM, rows = part.M - row0;
+    if (!dense) {
+        e = p.block_expert[block];
+        if (e < 0) return;
+        row0 = p.block_row[block];
+        rows = p.offsets[e + 1] - row0;
+    }
+    rows = min(rows, BM);
+    const int K = part.K, N = part.N;
+    const size_t expert = (size_t)e * N * K;
+    const buf_rsrc_t ra = make_buf(part.a, (dense ? dense_rows : routed_rows) * (uint32_t)K);
+    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 4);   // row and K piece of this lane's place
+    uint32_t va[LA], vb[LB];
+    buf_rsrc_t rb[LB];
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const int r = (i * WAVES + wave) * 16 + lr;
+        int src = row0 + min(r, rows - 1);
+        if (GATEUP && !dense) src = p.sorted_assign[src] / p.k;
+        va[i] = r < rows ? (uint32_t)src * (uint32_t)K + piece * 16 : kPast;
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        const int f = i * WAVES + wave;   // 16 weight rows; those of wave f / NF's fragments
+        const bool up = GATEUP && f % NF >= NW;
+        const I8MatDev& mat = up ? part.w2 : part.w;
+        rb[i] = make_buf(mat.codes + expert, (uint32_t)N * (uint32_t)K);
+        const uint32_t c = n0 + (GATEUP ? f / NF * NW + f % NW : f) * 16;
+        vb[i] = c >= (uint32_t)N ? kPast
+                : mat.tiles      ? c * (uint32_t)K + piece * 256 + lr * 16
+                                 : (c + lr) * (uint32_t)K + piece * 16;
+    }
+    const int blocks = K / 64;
+    const uint32_t b_step = part.w.tiles ? 1024 : 64;
+    auto load = [&](int st, int s) {
+        const uint32_t past = s < blocks ? 0u : kPast;
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            buf_to_lds16(ra, s_a(st) + (i * WAVES + wave) * 1024, va[i] | past, (uint32_t)s * 64u);
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+            buf_to_lds16(rb[i], s_b(st) + (i * WAVES + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
+    };
+    const int fr = lane % 16, fp = lane / 16;
+    const int at = fr * 64 + (fp ^ (fr / 4)) * 16;
+    auto read_b = [&](int st, int n) { return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 + at); };
+    auto read_a = [&](int st, int m) { return *(const i32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + at); };
+    i32x4_t acc[NF][MF], fb[2][NF], fa[2][MF];
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int st = 0; st < ST - 1; ++st) load(st, st);
+    wait_loads<(ST - 3) * (LA + LB)>();
+    bare_barrier_i8();
+#pragma unroll
+    for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, n);
+#pragma unroll
+    for (int m = 0; m < MF; ++m) fa[0][m] = read_a(0, m);
+    for (int s = 0; s < blocks; s += ST) {
+#pragma unroll
+        for (int st = 0; st < ST; ++st) {
+            const int c = st % 2, next = (st + 1) % ST;
+            load((st + ST - 1) % ST, s + st + ST - 1);
+            __builtin_amdgcn_sched_barrier(0);   // the requests go out first
+            // the next block's fragments arrive while this one's products run: its stage
+            // landed a barrier earlier
+#pragma unroll
+            for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(next, n);
+#pragma unroll
+            for (int m = 0; m < MF; ++m) fa[1 - c][m] = read_a(next, m);
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+#pragma unroll
+                for (int m = 0; m < MF; ++m) acc[n][m] = mfma_i8(fb[c][n], fa[c][m], acc[n][m]);
+            wait_loads<(ST - 3) * (LA + LB)>();
+            bare_barrier_i8();
+        }
+    }
+    wait_loads<0>();
+    float as[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        int r = row0 + min((wm * MF + m) * 16 + fr, rows - 1);
+        if (GATEUP && !dense) r = p.sorted_assign[r] / p.k;
+        as[m] = part.a_scale[r];
+    }
+#pragma unroll
+    for (int n = 0; n < NW; ++n) {
+        const int c = n0 + (wn * NW + n) * 16 + fp * 4;
+        if (c >= N) continue;   // N is a multiple of 64
+        const f32x4_t ws = *(const f32x4_t*)(part.w.scales + (size_t)e * N + c);
+        f32x4_t ws2 = ws;
+        if (GATEUP) ws2 = *(const f32x4_t*)(part.w2.scales + (size_t)e * N + c);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int r = (wm * MF + m) * 16 + fr;
+            if (r >= rows) continue;
+            const size_t o = (size_t)(row0 + r) * N + c;
+            f32x4_t v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = (float)acc[n][m][i] * as[m] * ws[i];
+                if (GATEUP) v[i] = silu_f32(v[i]) * ((float)acc[n + NW][m][i] * as[m] * ws2[i]);
+            }
+            if (GATEUP) *(f32x4_t*)((float*)part.out + o) = v;
+            else
+                *(u32x2_t*)((uint16_t*)part.out + o) =
+                    u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+    }
+}
+
 // Row-wise quantisation of h: one workgroup per row, the routed rows and then the
 // shared expert's.
 constexpr int kQuantThreads = 128;
@@ -506,6 +661,18 @@ static void launch_product(ProductArgs& p, int routed_blocks, hipStream_t stream
     product_i8_kernel<MT, NT, WN, WK, D, GATEUP><<<grid, WN * WK * WAVE, 0, stream>>>(p);
 }
 
+// T: tokens, n: routed rows.
+template <int WM, int MF, int WN, int NF, int ST, bool GATEUP>
+static void launch_grouped_tiles(ProductArgs& p, int routed_blocks, int T, int n, hipStream_t stream) {
+    constexpr int cols = (GATEUP ? NF / 2 : NF) * 16 * WN;
+    p.dense_blocks = p.dense.out ? cdiv(p.dense.M, WM * MF * 16) : 0;
+    p.dense_tiles = p.dense.out ? cdiv(p.dense.N, cols) : 1;
+    p.routed_tiles = cdiv(p.routed.N, cols);
+    const unsigned grid = (unsigned)(p.dense_blocks * p.dense_tiles + routed_blocks * p.routed_tiles);
+    grouped_tiles_kernel<WM, MF, WN, NF, ST, GATEUP>
+        <<<grid, WM * WN * WAVE, 0, stream>>>(p, (uint32_t)T, (uint32_t)(GATEUP ? T : n));
+}
+
 hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
                             int N, uint16_t* out, void*, hipStream_t stream) {
     ProductArgs p{};
@@ -573,20 +740,26 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     p.sorted_assign = g.r.sorted_assign;
     p.routed = PartI8{g.x, g.x_scale, g.gate, g.up, 0, g.I, g.H, h};
     if (g.I_sh) p.dense = PartI8{g.x, g.x_scale, g.sh_gate, g.sh_up, g.T, g.I_sh, g.H, h_sh};
-    if (g.block_rows == 16) launch_product<1, 2, 4, 1, 4, true>(p, g.max_blocks, stream);
-    else if (g.block_rows == 32) launch_product<2, 2, 4, 1, 4, true>(p, g.max_blocks, stream);
-    else launch_product<4, 2, 4, 1, 2, true>(p, g.max_blocks, stream);
+    const int n = g.T * g.k;
+    // us measured at H 2048, I 512, 256 experts, k 8, weights out of memory: straight from
+    // memory into registers up to 32 rows (512 tokens 97 with K over two waves, 110 without,
+    // 101 through LDS), through LDS for 64 (2048 tokens 147 against 166, skewed 127 against 137)
+    if (g.block_rows == 16) launch_product<1, 4, 2, 2, 4, true>(p, g.max_blocks, stream);
+    else if (g.block_rows == 32) launch_product<2, 4, 2, 2, 2, true>(p, g.max_blocks, stream);
+    else launch_grouped_tiles<1, 4, 4, 2, 4, true>(p, g.max_blocks, g.T, n, stream);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const int n = g.T * g.k;
     quant_h_kernel<<<n + (g.I_sh ? g.T : 0), kQuantThreads, 0, stream>>>(
         h, h_sh, n, g.I, g.I_sh, q, q_sh, scale, scale_sh);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out};
     if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out};
+    // a wave's 32 columns reuse its rows more than 16 would, once blocks are mostly full:
+    // 2048 tokens 110 against 125, but 512 tokens 60 against 57
     if (g.block_rows == 16) launch_product<1, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
-    else if (g.block_rows == 32) launch_product<2, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
-    else launch_product<4, 2, 4, 1, 2, false>(p, g.max_blocks, stream);
+    else if (g.block_rows == 32 && n <= 32 * g.E) launch_product<2, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
+    else if (g.block_rows == 32) launch_product<2, 4, 4, 1, 2, false>(p, g.max_blocks, stream);
+    else launch_grouped_tiles<1, 4, 4, 2, 4, false>(p, g.max_blocks, g.T, n, stream);
     return hipGetLastError();
 }
 
