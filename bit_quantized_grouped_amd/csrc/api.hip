@@ -1026,15 +1026,21 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
         if (!rule && score_bias) return MOE_ERR_SHAPE;   // a bias orders scores: it needs a rule
         const size_t need = rule ? scored_ws_bytes(T, E, k) : route_need(T, E, k);
         if (need && (st = check_ws(route_ws, route_ws_bytes, need))) return st;
-        if (decode_i8_fits(p))
-            return launch_decode_i8(p, logits, score_bias, rule ? &dev : nullptr, gemm_ws, y, stream) ==
-                           hipSuccess
-                       ? MOE_OK
-                       : MOE_ERR_HIP;
-        hipError_t e = rule ? launch_route_scored(logits, score_bias, dev, T, E, k, block_rows,
-                                                  p.max_blocks, p.r, route_ws, stream)
-                            : launch_route(logits, T, E, k, block_rows, p.max_blocks, p.r, route_ws,
-                                           stream);
+        const bool few = decode_i8_fits(p);
+        hipError_t e = hipSuccess;
+        if (few && T == 1) {
+            // the selection is part of the first launch
+        } else if (rule) {
+            e = launch_route_scored(logits, score_bias, dev, T, E, k, block_rows, p.max_blocks, p.r,
+                                    route_ws, stream);
+        } else {
+            e = launch_route(logits, T, E, k, block_rows, p.max_blocks, p.r, route_ws, stream);
+        }
+        if (few) {
+            if (e == hipSuccess)
+                e = launch_decode_i8(p, logits, score_bias, rule ? &dev : nullptr, gemm_ws, y, stream);
+            return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+        }
         if (e == hipSuccess) e = launch_grouped_i8(p, gemm_ws, stream);
         if (e == hipSuccess)
             e = launch_combine(expert_out, shared_out, nullptr, p.r.assign_row, p.r.topk_w, T, H, k,

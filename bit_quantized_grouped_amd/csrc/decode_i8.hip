@@ -1,25 +1,32 @@
-// One token through the layer over 8-bit codes: two launches.
+// A few tokens, each on its own, through the layer over 8-bit codes: two launches for one
+// token, and the routing in front for more.
 //
 //   decode_i8_gateup_kernel: a workgroup owns 16 columns of one slot (a chosen
-//     expert, or the shared expert); its wave 0 selects the token's experts itself
-//     (the same selection as the routing call), then its waves split K, stream the
-//     gate's and up's tiles, and join their integer sums through LDS:
-//     h = silu(g) * u in fp32.  One more workgroup writes the routing arrays.
-//   decode_i8_down_kernel: a workgroup owns 16 columns of the output; its waves
+//     expert, or the shared expert) of one token; for a single token its wave 0
+//     selects the experts itself (the same selection as the routing call), then its
+//     waves split K, stream the gate's and up's tiles, and join their integer sums
+//     through LDS: h = silu(g) * u in fp32.  One more workgroup writes the routing
+//     arrays of a single token.
+//   decode_i8_down_kernel: a workgroup owns 8 columns of a token's output; its waves
 //     take a slot each, quantise the slot's h to codes (scale max|h| / 127 as in
-//     the grouped path), stream the slot's 16 down rows, and y is the weighted sum
+//     the grouped path), stream the slot's 8 down rows, and y is the weighted sum
 //     over the slots in slot order, the shared expert last, rounded once.
 //
 // Bound by bytes and by the chain of waits: the selection must end before a weight
-// address is known, and down starts after all of gate/up.
+// address is known, and down starts after all of gate/up.  Tokens that share an expert
+// read it once each, so this form is for few tokens among many experts; it has two
+// launches less than the grouped one and no expert_out.
 #include "moe_device.h"
 #include "moe_i8.h"
 #include "moe_score.h"
 
 namespace moeq4 {
 
-constexpr int kDgWaves = 4;     // waves that split K in gate/up
-constexpr int kDgAhead = 8;     // 64-K steps whose loads a wave has in flight
+// Waves that split K in gate/up, and the 64-K steps whose loads a wave has in flight: at H =
+// 2048 8 x 4 takes 6.6 us, 4 x 8 7.4, 16 x 2 8.7.
+constexpr int kDgWaves = 8;
+constexpr int kDgAhead = 4;
+constexpr int kDdAhead = 8;     // the same of a wave of down
 constexpr int kDdMaxWaves = 16;
 
 struct DecodeI8Args {
@@ -37,6 +44,7 @@ __device__ __forceinline__ i32x4_t mfma16(i32x4_t a, i32x4_t b, i32x4_t c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
+// EPL 0: the experts are chosen already, in p.r.
 template <int EPL>
 __global__ __launch_bounds__(kDgWaves* WAVE) void decode_i8_gateup_kernel(DecodeI8Args d) {
     __shared__ int s_idx[kScoredMaxK];
@@ -46,11 +54,11 @@ __global__ __launch_bounds__(kDgWaves* WAVE) void decode_i8_gateup_kernel(Decode
     const GemmI8Problem& p = d.p;
     const int tid = threadIdx.x, lane = tid % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
-    const int k = p.k, H = p.H;
+    const int k = p.k, H = p.H, token = blockIdx.y;
     const int tiles = p.I / 16, routed = k * tiles, all = routed + p.I_sh / 16;
     const int id = blockIdx.x;
     const bool shared = id >= routed && id < all;
-    if (!shared) {
+    if constexpr (EPL > 0) if (!shared) {
         if (wave == 0) {
             if (d.scored) score_topk_token<EPL>(d.logits, d.bias, p.E, k, d.rule, s_idx, s_w);
             else
@@ -65,7 +73,9 @@ __global__ __launch_bounds__(kDgWaves* WAVE) void decode_i8_gateup_kernel(Decode
     }
     const int slot = shared ? k : id / tiles;
     const int tile = shared ? id - routed : id - slot * tiles;
-    const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(s_idx[slot]);
+    const int e = shared ? 0
+                         : __builtin_amdgcn_readfirstlane(EPL > 0 ? s_idx[slot]
+                                                                  : p.r.topk_idx[token * k + slot]);
     const I8MatDev& mg = shared ? p.sh_gate : p.gate;
     const I8MatDev& mu = shared ? p.sh_up : p.up;
     const int N = shared ? p.I_sh : p.I, c0 = tile * 16;
@@ -74,7 +84,7 @@ __global__ __launch_bounds__(kDgWaves* WAVE) void decode_i8_gateup_kernel(Decode
     const uint32_t w_lane =
         mg.tiles ? lane * 16 : (uint32_t)(lane % 16) * (uint32_t)H + (lane / 16) * 16;
     const uint32_t w_step = mg.tiles ? 1024u : 64u;
-    const int8_t* x = p.x + (lane / 16) * 16;
+    const int8_t* x = p.x + (size_t)token * H + (lane / 16) * 16;
     const int steps = H / 64, s0 = steps * wave / kDgWaves, s1 = steps * (wave + 1) / kDgWaves;
     i32x4_t ag = {0, 0, 0, 0}, au = {0, 0, 0, 0};
     for (int s = s0; s < s1; s += kDgAhead) {
@@ -107,40 +117,44 @@ __global__ __launch_bounds__(kDgWaves* WAVE) void decode_i8_gateup_kernel(Decode
             g += s_part[w][0][tid / 4][tid % 4];
             u += s_part[w][1][tid / 4][tid % 4];
         }
-        const float xs = p.x_scale[0];
+        const float xs = p.x_scale[token];
         const size_t col = (size_t)e * N + c0 + tid;
         const float gv = (float)g * xs * mg.scales[col], uv = (float)u * xs * mu.scales[col];
-        (shared ? d.h_sh : d.h + (size_t)slot * N)[c0 + tid] = silu_f32(gv) * uv;
+        (shared ? d.h_sh + (size_t)token * N : d.h + (size_t)(token * k + slot) * N)[c0 + tid] = silu_f32(gv) * uv;
     }
 }
 
 __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(DecodeI8Args d, int ldq) {
     extern __shared__ __attribute__((aligned(16))) int8_t s_q[];   // [waves][ldq] codes of a wave's slot
-    __shared__ float s_y[kDdMaxWaves][16];
+    __shared__ float s_y[kDdMaxWaves][8];
     const GemmI8Problem& p = d.p;
     const int tid = threadIdx.x, lane = tid % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int waves = blockDim.x / WAVE;
-    const int k = p.k, slots = k + (p.I_sh ? 1 : 0);
-    const int c0 = blockIdx.x * 16;
+    const int k = p.k, slots = k + (p.I_sh ? 1 : 0), token = blockIdx.y;
+    // 8 of a tile's 16 columns: twice the workgroups, one for each CU at H = 2048
+    const int c0 = blockIdx.x * 8, cols = c0 / 16 * 16;
+    const bool on = (lane % 16) / 8 == (int)blockIdx.x % 2;
     int8_t* q = s_q + wave * ldq;
-    float y = 0.f;   // lanes 0 .. 15: column c0 + lane
+    float y = 0.f;   // lanes 0 .. 7: column c0 + lane
     for (int j = wave; j < slots; j += waves) {
         const bool shared = j == k;
         const int K = shared ? p.I_sh : p.I;
-        const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(p.r.topk_idx[j]);
+        const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(p.r.topk_idx[token * k + j]);
         const I8MatDev& m = shared ? p.sh_down : p.down;
-        const int8_t* w = m.codes + (size_t)e * p.H * K + (size_t)c0 * K;
+        const int8_t* w = m.codes + (size_t)e * p.H * K + (size_t)cols * K;
         const uint32_t w_lane =
             m.tiles ? lane * 16 : (uint32_t)(lane % 16) * (uint32_t)K + (lane / 16) * 16;
         const uint32_t w_step = m.tiles ? 1024u : 64u;
-        const float* h = shared ? d.h_sh : d.h + (size_t)j * K;
+        const float* h = shared ? d.h_sh + (size_t)token * K : d.h + (size_t)(token * k + j) * K;
         const int steps = K / 64;
-        i32x4_t wv[kDgAhead];
+        i32x4_t wv[kDdAhead];
 #pragma unroll
-        for (int i = 0; i < kDgAhead; ++i)
-            if (i < steps)
+        for (int i = 0; i < kDdAhead; ++i)
+            if (i < steps && on)
                 wv[i] = __builtin_nontemporal_load((const i32x4_t*)(w + (w_lane + i * w_step)));
+            else
+                wv[i] = i32x4_t{0, 0, 0, 0};
         // the slot's row: maximum, then codes into LDS while the first weights arrive
         constexpr int KEEP = 2;   // pieces of 256 values that stay in registers
         f32x4_t v[KEEP];
@@ -174,37 +188,38 @@ __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(Decod
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         i32x4_t acc = {0, 0, 0, 0};
-        for (int s = 0; s < steps; s += kDgAhead) {
+        for (int s = 0; s < steps; s += kDdAhead) {
             if (s) {
 #pragma unroll
-                for (int i = 0; i < kDgAhead; ++i)
-                    if (s + i < steps)
+                for (int i = 0; i < kDdAhead; ++i)
+                    if (s + i < steps && on)
                         wv[i] = __builtin_nontemporal_load(
                             (const i32x4_t*)(w + (w_lane + (uint32_t)(s + i) * w_step)));
             }
 #pragma unroll
-            for (int i = 0; i < kDgAhead; ++i)
+            for (int i = 0; i < kDdAhead; ++i)
                 if (s + i < steps)
                     acc = mfma16(wv[i], *(const i32x4_t*)(q + (s + i) * 64 + (lane / 16) * 16), acc);
         }
         __builtin_amdgcn_wave_barrier();   // the next slot's codes take this one's place
-        // column c of 16 into lane c: it lies in lane 16 * (c / 4), element c % 4
+        // column c of 8 into lane c: the tile's c + 8 or c lies in lane 16 * (column / 4),
+        // element column % 4
         int sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = __shfl(acc[i], (lane / 4) % 4 * 16, WAVE);
+            const int t = __shfl(acc[i], ((lane % 8 + c0 % 16) / 4) * 16, WAVE);
             sum = lane % 4 == i ? t : sum;
         }
-        const float wgt = shared ? 1.f : p.r.topk_w[j];
-        const float ws = m.scales[(size_t)e * p.H + c0 + lane % 16];
+        const float wgt = shared ? 1.f : p.r.topk_w[token * k + j];
+        const float ws = m.scales[(size_t)e * p.H + c0 + lane % 8];
         y += wgt * ((float)sum * (top / 127.0f) * ws);
     }
-    if (lane < 16) s_y[wave][lane] = y;
+    if (lane < 8) s_y[wave][lane] = y;
     __syncthreads();
-    if (tid < 16) {
+    if (tid < 8) {
         float t = 0.f;
         for (int w = 0; w < waves; ++w) t += s_y[w][tid];
-        d.y[c0 + tid] = (uint16_t)pack_bf16x2(t, 0.f);
+        d.y[(size_t)token * p.H + c0 + tid] = (uint16_t)pack_bf16x2(t, 0.f);
     }
 }
 
@@ -212,12 +227,15 @@ __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(Decod
 constexpr int kDecodeI8MaxInter = 4096;
 
 bool decode_i8_fits(const GemmI8Problem& p) {
-    return p.T == 1 && p.k <= kScoredMaxK && p.I <= kDecodeI8MaxInter && p.I_sh <= kDecodeI8MaxInter;
+    // more than one token: as long as few of their experts are the same (at most a quarter of
+    // all chosen: 8 tokens of 8 of 256 read 12 % twice)
+    if (p.T > 1 && (p.T > 64 || 4 * p.T * p.k > p.E)) return false;
+    return p.k <= kScoredMaxK && p.I <= kDecodeI8MaxInter && p.I_sh <= kDecodeI8MaxInter;
 }
 
 hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const float* bias,
                             const ScoreRule* rule, void* ws, uint16_t* y, hipStream_t stream) {
-    const GemmI8Ws L = gemm_i8_ws_layout(1, p.I, p.I_sh, p.k);
+    const GemmI8Ws L = gemm_i8_ws_layout(p.T, p.I, p.I_sh, p.k);
     DecodeI8Args d{};
     d.p = p;
     d.logits = logits;
@@ -227,10 +245,12 @@ hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const f
     d.h = (float*)((char*)ws + L.h);
     d.h_sh = (float*)((char*)ws + L.h_sh);
     d.y = y;
-    const int grid = p.k * (p.I / 16) + p.I_sh / 16 + 1;
+    const int grid = p.k * (p.I / 16) + p.I_sh / 16;
     const int epl = (p.E + WAVE - 1) / WAVE;
-#define MOE_GU(N) decode_i8_gateup_kernel<N><<<grid, kDgWaves * WAVE, 0, stream>>>(d)
-    if (epl <= 1) MOE_GU(1);
+#define MOE_GU(N) \
+    decode_i8_gateup_kernel<N><<<dim3(grid + (N > 0 ? 1 : 0), p.T), kDgWaves * WAVE, 0, stream>>>(d)
+    if (p.T > 1) MOE_GU(0);
+    else if (epl <= 1) MOE_GU(1);
     else if (epl <= 2) MOE_GU(2);
     else if (epl <= 4) MOE_GU(4);
     else if (epl <= 8) MOE_GU(8);
@@ -240,7 +260,7 @@ hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const f
     if (err != hipSuccess) return err;
     const int slots = p.k + (p.I_sh ? 1 : 0), waves = slots < kDdMaxWaves ? slots : kDdMaxWaves;
     const int ldq = p.I > p.I_sh ? p.I : p.I_sh;
-    decode_i8_down_kernel<<<p.H / 16, waves * WAVE, (size_t)waves * ldq, stream>>>(d, ldq);
+    decode_i8_down_kernel<<<dim3(p.H / 8, p.T), waves * WAVE, (size_t)waves * ldq, stream>>>(d, ldq);
     return hipGetLastError();
 }
 

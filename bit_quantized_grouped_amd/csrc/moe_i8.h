@@ -82,7 +82,7 @@ struct GemmI8Ws {
 GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k);
 hipError_t launch_grouped_i8(const GemmI8Problem& p, void* ws, hipStream_t stream);
 
-// decode_i8.hip: one token (moe_layer_i8 at T = 1), the routing arrays included
+// decode_i8.hip: moe_layer_i8 of few tokens; a single one's routing arrays included
 bool decode_i8_fits(const GemmI8Problem& p);
 hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const float* bias,
                             const ScoreRule* rule, void* ws, uint16_t* y, hipStream_t stream);
