@@ -216,8 +216,9 @@ __global__ __launch_bounds__(WN* WK* WAVE) void product_i8_kernel(ProductArgs p)
 // takes two to four times that under full traffic.  Stages past K are zeros and
 // multiplied like the others.  A block keeps rows of 64 bytes
 // whose four 16-byte pieces are permuted: place j of row r holds piece
-// j ^ (r / 4 % 4), chosen on the source side (a load writes LDS in lane order), so
-// the 16 rows that a fragment read touches lie in different banks.
+// j ^ (r / 2 % 4), chosen on the source side (a load writes LDS in lane order), so
+// that 8 neighbouring rows of a fragment read, 128 bytes, lie in different banks
+// (with r / 4 half of the LDS cycles were conflicts).
 // Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
 // which the build checks.
 template <int WM, int MF, int WN, int NF, int ST, int KS>
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 
     const buf_rsrc_t ra = make_buf(a, (uint32_t)M * (uint32_t)K);
     const buf_rsrc_t rb = make_buf(w.codes, (uint32_t)N * (uint32_t)K);
-    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 4);   // row and K piece of this lane's place
+    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 2 % 4);   // row and K piece of this lane's place
     uint32_t va[LA], vb[LB];
     auto sources = [&](int m0, int n0) {
 #pragma unroll
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     };
     i32x4_t acc[NF][MF];
     const int fr = lane % 16, fp = lane / 16;
-    const int at = fr * 64 + (fp ^ (fr / 4)) * 16;
+    const int at = fr * 64 + (fp ^ (fr / 2 % 4)) * 16;
     auto read_b = [&](int st, int q, int n) {
         return *(const i32x4_t*)(s_b(st) + q * BN * 64 + (wn * NF + n) * 1024 + at);
     };
@@ -487,7 +488,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void grouped_tiles_kernel(ProductArgs
     const int K = part.K, N = part.N;
     const size_t expert = (size_t)e * N * K;
     const buf_rsrc_t ra = make_buf(part.a, (dense ? dense_rows : routed_rows) * (uint32_t)K);
-    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 4);   // row and K piece of this lane's place
+    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 2 % 4);   // row and K piece of this lane's place
     uint32_t va[LA], vb[LB];
     buf_rsrc_t rb[LB];
 #pragma unroll
@@ -520,7 +521,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void grouped_tiles_kernel(ProductArgs
             buf_to_lds16(rb[i], s_b(st) + (i * WAVES + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
     };
     const int fr = lane % 16, fp = lane / 16;
-    const int at = fr * 64 + (fp ^ (fr / 4)) * 16;
+    const int at = fr * 64 + (fp ^ (fr / 2 % 4)) * 16;
     auto read_b = [&](int st, int n) { return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 + at); };
     auto read_a = [&](int st, int m) { return *(const i32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + at); };
     i32x4_t acc[NF][MF], fb[2][NF], fa[2][MF];
