@@ -36,12 +36,12 @@ def common_flags() -> list[str]:
 # Kernels whose pipeline waits count their own vector loads (s_waitcnt vmcnt with
 # a fixed count, then a barrier without a fence): the gate/up kernel on packed
 # scale|bias words with 128-K chunks, whose x rows go straight into LDS, and the
-# 8-bit products' tile kernels, whose operands do.  A
+# 8-bit products' kernels, whose operands or rows do.  A
 # register spill would add scratch loads and stores to that count and turn the
 # waits into races, so the build fails if any of them uses scratch.
 # Template arguments: NMAT 2, MT, KC 128, NSUB, DEPTH, WAVES, BF false, SB true.
 COUNTED_WAIT_KERNELS = re.compile(
-    r"grouped_q4_kernelILi2ELi\d+ELi128ELi\d+ELi\d+ELi\d+ELb0ELb1EE|(?:linear|grouped)_tiles_kernelI")
+    r"grouped_q4_kernelILi2ELi\d+ELi128ELi\d+ELi\d+ELi\d+ELb0ELb1EE|(?:linear_tiles|grouped_stream)_kernelI")
 COUNTED_WAIT_SOURCES = ("gemm_q4.hip", "gemm_i8.hip")
 
 

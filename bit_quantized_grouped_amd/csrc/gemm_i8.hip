@@ -22,75 +22,6 @@ __device__ __forceinline__ i32x4_t mfma_i8(i32x4_t a, i32x4_t b, i32x4_t c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// acc[n][m] += weight tile n x activation tile m over the 64-K steps [s0, s1), by
-// one wave, D steps ahead.  w: tile n's first byte (uniform), w_lane its lane
-// offset, w_step the bytes from one step to the next; a_lane: the lane's row and
-// K offset in a, 64 bytes a step.
-template <int NT, int MT, int D>
-__device__ __forceinline__ void wave_product(const int8_t* const (&w)[NT],
-                                             const uint32_t (&w_lane)[NT], uint32_t w_step,
-                                             const int8_t* a, const uint32_t (&a_lane)[MT], int s0,
-                                             int s1, i32x4_t (&acc)[NT][MT]) {
-    i32x4_t wv[D][NT], av[D][MT];
-    auto load = [&](int d, int s) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            wv[d][n] = *(const i32x4_t*)(w[n] + (w_lane[n] + (uint32_t)s * w_step));
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            av[d][m] = *(const i32x4_t*)(a + (a_lane[m] + (uint32_t)s * 64u));
-    };
-    auto mul = [&](int d) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[n][m] = mfma_i8(wv[d][n], av[d][m], acc[n][m]);
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (s0 + d < s1) load(d, s0 + d);
-    int s = s0;
-    for (; s + 2 * D <= s1; s += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            mul(d);
-            load(d, s + D + d);
-        }
-    }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (s + d < s1) {
-            mul(d);
-            if (s + D + d < s1) load(d, s + D + d);
-        }
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (s + D + d < s1) mul(d);
-}
-
-// Sum over the WK waves that share a tile; the first of them holds the result.
-template <int NT, int MT, int WN, int WK>
-__device__ __forceinline__ void reduce_waves(i32x4_t (&acc)[NT][MT], int wn, int wk) {
-    if (WK == 1) return;
-    __shared__ i32x4_t s_part[WK > 1 ? (WK - 1) * WN * NT * MT * WAVE : 1];
-    const int lane = threadIdx.x % WAVE;
-    if (wk) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                s_part[((((wk - 1) * WN + wn) * NT + n) * MT + m) * WAVE + lane] = acc[n][m];
-    }
-    __syncthreads();
-    if (wk) return;
-    for (int o = 0; o < WK - 1; ++o)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                acc[n][m] += s_part[(((o * WN + wn) * NT + n) * MT + m) * WAVE + lane];
-}
-
 // One part of a launch: the dense rows (the shared expert's, or a linear's) or
 // the routed rows.
 struct PartI8 {
@@ -105,106 +36,68 @@ struct ProductArgs {
     PartI8 dense, routed;
     int dense_blocks, dense_tiles, routed_tiles;
     int block_rows, k;
+    int dense_wgs;                  // of grouped_stream_kernel
     const int32_t* block_expert;
     const int32_t* block_row;
     const int32_t* offsets;
+    const int32_t* n_blocks;
     const int32_t* sorted_assign;   // gate/up: row -> assignment
 };
 
-// Workgroup of WN x WK waves: WN*NT*16 columns of MT*16 rows, K split over WK waves.
-// GATEUP: the wave's NT tiles are the gate's and then the up's same NT/2 tiles.
-template <int MT, int NT, int WN, int WK, int D, bool GATEUP>
-__global__ __launch_bounds__(WN* WK* WAVE) void product_i8_kernel(ProductArgs p) {
-    constexpr int COLS = GATEUP ? NT / 2 : NT;   // 16-column tiles per wave
-    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-    const int wn = wave % WN, wk = wave / WN;
-    const int dense_wgs = p.dense_blocks * p.dense_tiles;
-    const bool dense = (int)blockIdx.x < dense_wgs;
-    const int id = dense ? blockIdx.x : blockIdx.x - dense_wgs;
-    const int tiles = dense ? p.dense_tiles : p.routed_tiles;
-    const int block = id / tiles, tile = id - block * tiles;
-    const PartI8& part = dense ? p.dense : p.routed;
-    int e = 0, row0 = block * MT * 16, rows = part.M - row0;
-    if (!dense) {
-        e = p.block_expert[block];
-        if (e < 0) return;
-        row0 = p.block_row[block];
-        rows = p.offsets[e + 1] - row0;
-    }
-    rows = min(rows, dense ? MT * 16 : p.block_rows);
-    const int K = part.K, N = part.N;
-    const int col0 = (tile * WN + wn) * COLS * 16;
-    if (col0 >= N && WK == 1) return;
+// Shares of the row blocks among the XCDs that have one column tile in common.
+__host__ __device__ constexpr int xcd_shares(int tiles) { return tiles == 2 || tiles == 4 ? 8 / tiles : 1; }
 
-    uint32_t a_lane[MT];
-    float a_scale[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        // rows behind the block's last read its last row; their results go nowhere
-        int r = row0 + min(m * 16 + lane % 16, rows - 1);
-        if (GATEUP && !dense) r = p.sorted_assign[r] / p.k;
-        a_lane[m] = (uint32_t)r * (uint32_t)K + (lane / 16) * 16;
-        a_scale[m] = part.a_scale[r];
-    }
-    const bool tiled = part.w.tiles;
-    const size_t expert = (size_t)e * N * K;
-    const int8_t* w[NT];
-    uint32_t w_lane[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const I8MatDev& mat = GATEUP && n >= COLS ? part.w2 : part.w;
-        const int c = min(col0 + (GATEUP ? n % COLS : n) * 16, (N - 1) / 16 * 16);
-        w[n] = mat.codes + expert + (size_t)c * K;
-        w_lane[n] = tiled ? lane * 16
-                          : (uint32_t)min(lane % 16, N - 1 - c) * (uint32_t)K + (lane / 16) * 16;
-    }
-    i32x4_t acc[NT][MT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
-    const int steps = K / 64;
-    wave_product<NT, MT, D>(w, w_lane, tiled ? 1024u : 64u, part.a, a_lane, steps * wk / WK,
-                            steps * (wk + 1) / WK, acc);
-    reduce_waves<NT, MT, WN, WK>(acc, wn, wk);
-    if (WK > 1 && wk) return;
+// ---- Dense product of few tiles: a workgroup per 16 x 16 tile, K split over its 8 waves,
+// each with kFewAhead steps of 64 K in flight straight from memory; the waves' integer sums
+// meet in LDS.  Bound by the latency of one round of loads.
+constexpr int kFewWaves = 8, kFewAhead = 8;
 
+__global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
+    const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
+    uint16_t* __restrict__ out) {
+    __shared__ i32x4_t s_part[kFewWaves - 1][WAVE];
+    const int lane = threadIdx.x % WAVE;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int n_tiles = (N + 15) / 16;
+    const int m0 = blockIdx.x / n_tiles * 16, n0 = blockIdx.x % n_tiles * 16;
+    // rows behind the last read the last; their results go nowhere
+    const int8_t* pa = a + (size_t)min(m0 + lane % 16, M - 1) * K + lane / 16 * 16;
+    const int8_t* pw = w.codes + (size_t)n0 * K +
+                       (w.tiles ? (size_t)lane * 16
+                                : (size_t)min(lane % 16, N - 1 - n0) * K + lane / 16 * 16);
+    const int w_step = w.tiles ? 1024 : 64;
+    const int steps = K / 64, s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
+    i32x4_t acc = {0, 0, 0, 0};
+    for (int s = s0; s < s1; s += kFewAhead) {
+        i32x4_t va[kFewAhead], vw[kFewAhead];
 #pragma unroll
-    for (int n = 0; n < COLS; ++n) {
-        const int c = col0 + n * 16 + (lane / 16) * 4;
-        if (c >= N) continue;
-        float ws[4], ws2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ci = min(c + i, N - 1);
-            ws[i] = part.w.scales[(size_t)e * N + ci];
-            if (GATEUP) ws2[i] = part.w2.scales[(size_t)e * N + ci];
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int r = m * 16 + lane % 16;
-            if (r >= rows) continue;
-            const size_t at = (size_t)(row0 + r) * N + c;
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = (float)acc[n][m][i] * a_scale[m] * ws[i];
-                if (GATEUP)
-                    v[i] = silu_f32(v[i]) * ((float)acc[n + COLS][m][i] * a_scale[m] * ws2[i]);
+        for (int i = 0; i < kFewAhead; ++i)
+            if (s + i < s1) {
+                vw[i] = *(const i32x4_t*)(pw + (size_t)(s + i) * w_step);
+                va[i] = *(const i32x4_t*)(pa + (size_t)(s + i) * 64);
             }
-            if (GATEUP) {
-                *(f32x4_t*)((float*)part.out + at) = f32x4_t{v[0], v[1], v[2], v[3]};
-            } else {
-                uint16_t* o = (uint16_t*)part.out + at;
-                if (N % 4 == 0) {
-                    *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c + i < N) o[i] = (uint16_t)pack_bf16x2(v[i], 0.f);
-                }
-            }
-        }
+        for (int i = 0; i < kFewAhead; ++i)
+            if (s + i < s1) acc = mfma_i8(vw[i], va[i], acc);
+    }
+    if (wave) s_part[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int i = 0; i < kFewWaves - 1; ++i) acc += s_part[i][lane];
+    const int r = m0 + lane % 16, c = n0 + lane / 16 * 4;
+    if (r >= M || c >= N) return;
+    const float as = a_scale[r];
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * as * w.scales[min(c + i, N - 1)];
+    uint16_t* o = out + (size_t)r * N + c;
+    if (N % 4 == 0) {
+        *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < N) o[i] = (uint16_t)pack_bf16x2(v[i], 0.f);
     }
 }
 
@@ -436,47 +329,43 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     wait_loads<0>();
 }
 
-// ---- The experts' products over row blocks: the same ring of stages, one tile per
-// workgroup, BM rows of a block (block_rows) x BN weight rows.  GATEUP: the BN rows are
-// BN / 2 of the gate's and the same of the up's, a wave's NF column fragments half and
-// half, so that a lane holds both sums of a value of h.  Rows behind a partial block's
-// last are requested past the buffer: zeros, without traffic.
-template <int WM, int MF, int WN, int NF, int ST, bool GATEUP>
-__global__ __launch_bounds__(WM* WN* WAVE) void grouped_tiles_kernel(ProductArgs p, uint32_t dense_rows,
+// ---- The experts' products with weights streamed into registers ----
+// A workgroup of 4 waves owns BM = 16 MF rows of a block and 64 NT weight rows, a wave
+// 16 NT of them (GATEUP: half the gate's, half the up's).  Each weight row is read once
+// per block, so the weights go straight into registers, D steps of 64 K ahead: 64 to
+// 256 KB in flight on a CU, which the latency of HBM under load (2 us and more) needs.
+// (Through an LDS ring as above, 72 KB in flight, 2048 tokens took 147 us for gate/up
+// instead of 129; a variant without its products took as long.)  The rows' codes are
+// shared by the waves: 512 K of them at a time go straight into LDS, the next 512 while
+// these are multiplied, laid out as in the tile kernel.  Bound by HBM: 541 MB of gate
+// and up weights of 256 experts in 96 us are 5.6 TB/s, of the 6.2 a plain read reaches.
+template <int MF, int NT, int D, bool GATEUP>
+__global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs p, uint32_t dense_rows,
                                                                      uint32_t routed_rows) {
-    constexpr int BM = WM * MF * 16, BN = WN * NF * 16, WAVES = WM * WN;
-    constexpr int NA = BM / 16, NB = BN / 16;                       // 1 KB loads of a stage
-    constexpr int LA = (NA + WAVES - 1) / WAVES, LB = NB / WAVES;   // of a wave, some past the end
-    static_assert(NB % WAVES == 0, "whole weight loads per wave");
+    constexpr int BM = MF * 16, NW = GATEUP ? NT / 2 : NT, COLS = 4 * NW * 16, Q = 8;
+    constexpr int LA = Q * MF / 4;   // 1 KB loads of a wave and chunk
+    static_assert(Q % D == 0 && Q * MF % 4 == 0, "a slot for each step of a chunk, whole loads");
     constexpr uint32_t kPast = 0xC0000000u;
-    constexpr int COLS = GATEUP ? BN / 2 : BN, NW = GATEUP ? NF / 2 : NF;
-#define MOE_STAGE(i) \
-    __shared__ __attribute__((aligned(16))) int8_t s_a##i[ST > i ? LA * WAVES * 1024 : 16], s_b##i[ST > i ? BN * 64 : 16]
-    MOE_STAGE(0);
-    MOE_STAGE(1);
-    MOE_STAGE(2);
-    MOE_STAGE(3);
-    MOE_STAGE(4);
-    MOE_STAGE(5);
-    MOE_STAGE(6);
-    MOE_STAGE(7);
-#undef MOE_STAGE
-    static_assert(ST >= 4 && ST <= 8 && ST % 2 == 0, "a stage for each array; fragments alternate");
-    auto s_a = [&](int i) {
-        return i == 0 ? s_a0 : i == 1 ? s_a1 : i == 2 ? s_a2 : i == 3 ? s_a3 : i == 4 ? s_a4 : i == 5 ? s_a5 : i == 6 ? s_a6 : s_a7;
-    };
-    auto s_b = [&](int i) {
-        return i == 0 ? s_b0 : i == 1 ? s_b1 : i == 2 ? s_b2 : i == 3 ? s_b3 : i == 4 ? s_b4 : i == 5 ? s_b5 : i == 6 ? s_b6 : s_b7;
-    };
+    __shared__ __attribute__((aligned(16))) int8_t s_a0[Q * BM * 64], s_a1[Q * BM * 64];
     const int lane = threadIdx.x % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int wm = wave % WM, wn = wave / WM;
-    const int dense_wgs = p.dense_blocks * p.dense_tiles;
+    const int dense_wgs = p.dense_wgs;
     const bool dense = (int)blockIdx.x < dense_wgs;
     const int id = dense ? blockIdx.x : blockIdx.x - dense_wgs;
     const int tiles = dense ? p.dense_tiles : p.routed_tiles;
-    const int block = id / tiles, n0 = (id - block * tiles) * COLS;
     const PartI8& part = dense ? p.dense : p.routed;
+    // Workgroups go round the 8 XCDs: with 8 column tiles, or a multiple, the blocks of an
+    // expert meet its tile in one XCD's L2; with 2 or 4 an XCD takes a contiguous share of
+    // the blocks besides.
+    int block = id / tiles, tile = id - block * tiles;
+    if (const int shares = xcd_shares(tiles); shares > 1) {
+        const int n = dense ? p.dense_blocks : *p.n_blocks, per = (n + shares - 1) / shares;
+        const int x = id % 8;
+        tile = x % tiles;
+        block = x / tiles * per + id / 8;
+        if (id / 8 >= per || block >= n) return;
+    }
+    const int n0 = tile * COLS;
     int e = 0, row0 = block * BM, rows = part.M - row0;
     if (!dense) {
         e = p.block_expert[block];
@@ -485,109 +374,125 @@ __global__ __launch_bounds__(WM* WN* WAVE) void grouped_tiles_kernel(ProductArgs
         rows = p.offsets[e + 1] - row0;
     }
     rows = min(rows, BM);
-    const int K = part.K, N = part.N;
+    const int K = part.K, N = part.N, blocks = K / 64;
     const size_t expert = (size_t)e * N * K;
+    const buf_rsrc_t rg = make_buf(part.w.codes + expert, (uint32_t)N * (uint32_t)K);
+    const buf_rsrc_t ru = make_buf(GATEUP ? part.w2.codes + expert : nullptr, (uint32_t)N * (uint32_t)K);
+    const uint32_t w_step = part.w.tiles ? 1024u : 64u;
+    uint32_t vw[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const uint32_t c = n0 + (wave * NW + n % NW) * 16;
+        vw[n] = c >= (uint32_t)N ? kPast
+                : part.w.tiles   ? c * (uint32_t)K + lane * 16
+                                 : (c + lane % 16) * (uint32_t)K + lane / 16 * 16;
+    }
+    i32x4_t w[D][NT];
+    auto load_w = [&](int slot, int s) {
+        const uint32_t past = s < blocks ? 0u : kPast;   // steps behind the last are zeros
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            w[slot][n] = __builtin_bit_cast(
+                i32x4_t, buf_load16_u(GATEUP && n >= NW ? ru : rg, vw[n] | past, (uint32_t)s * w_step));
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_w(d, d);
+
     const buf_rsrc_t ra = make_buf(part.a, (dense ? dense_rows : routed_rows) * (uint32_t)K);
-    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 2 % 4);   // row and K piece of this lane's place
-    uint32_t va[LA], vb[LB];
-    buf_rsrc_t rb[LB];
+    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 2 % 4);
+    const int group = wave % MF;   // the 16 rows that this wave loads
+    int src = row0 + min(group * 16 + lr, rows - 1);
+    if (GATEUP && !dense) src = p.sorted_assign[src] / p.k;
+    const uint32_t va = group * 16 + lr < rows ? (uint32_t)src * (uint32_t)K + piece * 16 : kPast;
+    auto load_a = [&](int8_t* to, int chunk) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-        const int r = (i * WAVES + wave) * 16 + lr;
-        int src = row0 + min(r, rows - 1);
-        if (GATEUP && !dense) src = p.sorted_assign[src] / p.k;
-        va[i] = r < rows ? (uint32_t)src * (uint32_t)K + piece * 16 : kPast;
-    }
-#pragma unroll
-    for (int i = 0; i < LB; ++i) {
-        const int f = i * WAVES + wave;   // 16 weight rows; those of wave f / NF's fragments
-        const bool up = GATEUP && f % NF >= NW;
-        const I8MatDev& mat = up ? part.w2 : part.w;
-        rb[i] = make_buf(mat.codes + expert, (uint32_t)N * (uint32_t)K);
-        const uint32_t c = n0 + (GATEUP ? f / NF * NW + f % NW : f) * 16;
-        vb[i] = c >= (uint32_t)N ? kPast
-                : mat.tiles      ? c * (uint32_t)K + piece * 256 + lr * 16
-                                 : (c + lr) * (uint32_t)K + piece * 16;
-    }
-    const int blocks = K / 64;
-    const uint32_t b_step = part.w.tiles ? 1024 : 64;
-    auto load = [&](int st, int s) {
-        const uint32_t past = s < blocks ? 0u : kPast;
-#pragma unroll
-        for (int i = 0; i < LA; ++i)
-            buf_to_lds16(ra, s_a(st) + (i * WAVES + wave) * 1024, va[i] | past, (uint32_t)s * 64u);
-#pragma unroll
-        for (int i = 0; i < LB; ++i)
-            buf_to_lds16(rb[i], s_b(st) + (i * WAVES + wave) * 1024, vb[i] | past, (uint32_t)s * b_step);
+        for (int i = 0; i < LA; ++i) {
+            const int q = (i * 4 + wave) / MF;
+            const uint32_t k = (uint32_t)(chunk * Q + q);
+            const uint32_t past = k < (uint32_t)blocks ? 0u : kPast;
+            buf_to_lds16(ra, to + (q * MF + group) * 1024, va | past, k * 64u);
+        }
     };
     const int fr = lane % 16, fp = lane / 16;
     const int at = fr * 64 + (fp ^ (fr / 2 % 4)) * 16;
-    auto read_b = [&](int st, int n) { return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 + at); };
-    auto read_a = [&](int st, int m) { return *(const i32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + at); };
-    i32x4_t acc[NF][MF], fb[2][NF], fa[2][MF];
+    i32x4_t acc[NT][MF];
 #pragma unroll
-    for (int n = 0; n < NF; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
+    auto chunk_products = [&](const int8_t* sa, int8_t* other, int chunk) {
+        load_a(other, chunk + 1);
+        // Before this chunk's weights: the wait below counts on it.  All but vector memory
+        // instructions may be moved across.
+        __builtin_amdgcn_sched_barrier(0x38E);
 #pragma unroll
-    for (int st = 0; st < ST - 1; ++st) load(st, st);
-    wait_loads<(ST - 3) * (LA + LB)>();
-    bare_barrier_i8();
+        for (int q = 0; q < Q; ++q) {
+            i32x4_t fa[MF];
 #pragma unroll
-    for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, n);
+            for (int m = 0; m < MF; ++m) fa[m] = *(const i32x4_t*)(sa + (q * MF + m) * 1024 + at);
 #pragma unroll
-    for (int m = 0; m < MF; ++m) fa[0][m] = read_a(0, m);
-    for (int s = 0; s < blocks; s += ST) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int st = 0; st < ST; ++st) {
-            const int c = st % 2, next = (st + 1) % ST;
-            load((st + ST - 1) % ST, s + st + ST - 1);
-            __builtin_amdgcn_sched_barrier(0);   // the requests go out first
-            // the next block's fragments arrive while this one's products run: its stage
-            // landed a barrier earlier
-#pragma unroll
-            for (int n = 0; n < NF; ++n) fb[1 - c][n] = read_b(next, n);
-#pragma unroll
-            for (int m = 0; m < MF; ++m) fa[1 - c][m] = read_a(next, m);
-#pragma unroll
-            for (int n = 0; n < NF; ++n)
-#pragma unroll
-                for (int m = 0; m < MF; ++m) acc[n][m] = mfma_i8(fb[c][n], fa[c][m], acc[n][m]);
-            wait_loads<(ST - 3) * (LA + LB)>();
-            bare_barrier_i8();
+                for (int m = 0; m < MF; ++m) acc[n][m] = mfma_i8(w[q % D][n], fa[m], acc[n][m]);
+            load_w(q % D, chunk * Q + q + D);
         }
-    }
+        // the next chunk's rows were requested before this chunk's weights: they have landed
+        // once only the last D steps' weights are in flight
+        wait_loads<D * NT>();
+        bare_barrier_i8();
+    };
+    load_a(s_a0, 0);
     wait_loads<0>();
-    float as[MF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-        int r = row0 + min((wm * MF + m) * 16 + fr, rows - 1);
-        if (GATEUP && !dense) r = p.sorted_assign[r] / p.k;
-        as[m] = part.a_scale[r];
+    bare_barrier_i8();
+    const int chunks = (blocks + Q - 1) / Q;
+    for (int c = 0; c < chunks; c += 2) {
+        chunk_products(s_a0, s_a1, c);
+        if (c + 1 < chunks) chunk_products(s_a1, s_a0, c + 1);
     }
+    // The values, 16 rows of the wave at a time through its share of the LDS (the run-out
+    // loads into it have landed), so that a store covers whole lines; a wave's LDS operations
+    // complete in order, so no barrier is needed inside it.
+    constexpr int ES = GATEUP ? 4 : 2, ROW = NW * 16 * ES, STRIDE = ROW + 16;   // bytes
+    static_assert(4 * 16 * STRIDE <= Q * BM * 64 && 16 * ROW / 16 % WAVE == 0, "staged rows");
+    const int col0 = n0 + wave * NW * 16;
+    if (col0 >= N) return;   // N is a multiple of 64: the wave's columns are all in or all out
+    int8_t* s_o = s_a0 + wave * 16 * STRIDE;
+    f32x4_t ws[NW], ws2[NW];
 #pragma unroll
     for (int n = 0; n < NW; ++n) {
-        const int c = n0 + (wn * NW + n) * 16 + fp * 4;
-        if (c >= N) continue;   // N is a multiple of 64
-        const f32x4_t ws = *(const f32x4_t*)(part.w.scales + (size_t)e * N + c);
-        f32x4_t ws2 = ws;
-        if (GATEUP) ws2 = *(const f32x4_t*)(part.w2.scales + (size_t)e * N + c);
+        const size_t c = (size_t)e * N + col0 + n * 16 + fp * 4;
+        ws[n] = *(const f32x4_t*)(part.w.scales + c);
+        if (GATEUP) ws2[n] = *(const f32x4_t*)(part.w2.scales + c);
+    }
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int r = (wm * MF + m) * 16 + fr;
-            if (r >= rows) continue;
-            const size_t o = (size_t)(row0 + r) * N + c;
+    for (int m = 0; m < MF; ++m) {
+        int r = row0 + min(m * 16 + fr, rows - 1);
+        if (GATEUP && !dense) r = p.sorted_assign[r] / p.k;
+        const float as = part.a_scale[r];
+#pragma unroll
+        for (int n = 0; n < NW; ++n) {
             f32x4_t v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[i] = (float)acc[n][m][i] * as[m] * ws[i];
-                if (GATEUP) v[i] = silu_f32(v[i]) * ((float)acc[n + NW][m][i] * as[m] * ws2[i]);
+                v[i] = (float)acc[n][m][i] * as * ws[n][i];
+                if (GATEUP)
+                    v[i] = silu_f32(v[i]) * ((float)acc[n + (GATEUP ? NW : 0)][m][i] * as * ws2[n][i]);
             }
-            if (GATEUP) *(f32x4_t*)((float*)part.out + o) = v;
-            else
-                *(u32x2_t*)((uint16_t*)part.out + o) =
-                    u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            int8_t* to = s_o + fr * STRIDE + (n * 16 + fp * 4) * ES;
+            if (GATEUP) *(f32x4_t*)to = v;
+            else *(u32x2_t*)to = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 16 * ROW / 16 / WAVE; ++i) {
+            const int piece16 = i * WAVE + lane, row = piece16 / (ROW / 16), at16 = piece16 % (ROW / 16) * 16;
+            if (m * 16 + row < rows)
+                *(i32x4_t*)((int8_t*)part.out + ((size_t)(row0 + m * 16 + row) * N + col0) * ES + at16) =
+                    *(const i32x4_t*)(s_o + row * STRIDE + at16);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -652,32 +557,25 @@ constexpr int kCUs = 256, kLdsBytes = 160 * 1024;   // of an MI355X, of a CU
 
 static int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <int MT, int NT, int WN, int WK, int D, bool GATEUP>
-static void launch_product(ProductArgs& p, int routed_blocks, hipStream_t stream) {
-    const int cols = (GATEUP ? NT / 2 : NT) * 16 * WN;
-    p.dense_blocks = p.dense.out ? cdiv(p.dense.M, MT * 16) : 0;
-    p.dense_tiles = p.dense.out ? cdiv(p.dense.N, cols) : 1;
-    p.routed_tiles = routed_blocks ? cdiv(p.routed.N, cols) : 1;
-    const unsigned grid = (unsigned)(p.dense_blocks * p.dense_tiles + routed_blocks * p.routed_tiles);
-    product_i8_kernel<MT, NT, WN, WK, D, GATEUP><<<grid, WN * WK * WAVE, 0, stream>>>(p);
-}
-
 // T: tokens, n: routed rows.
-template <int WM, int MF, int WN, int NF, int ST, bool GATEUP>
-static void launch_grouped_tiles(ProductArgs& p, int routed_blocks, int T, int n, hipStream_t stream) {
-    constexpr int cols = (GATEUP ? NF / 2 : NF) * 16 * WN;
-    p.dense_blocks = p.dense.out ? cdiv(p.dense.M, WM * MF * 16) : 0;
+template <int MF, int NT, int D, bool GATEUP>
+static void launch_grouped_stream(ProductArgs& p, int routed_blocks, int T, int n, hipStream_t stream) {
+    constexpr int cols = (GATEUP ? NT / 2 : NT) * 64;
+    p.dense_blocks = p.dense.out ? cdiv(p.dense.M, MF * 16) : 0;
     p.dense_tiles = p.dense.out ? cdiv(p.dense.N, cols) : 1;
     p.routed_tiles = cdiv(p.routed.N, cols);
-    const unsigned grid = (unsigned)(p.dense_blocks * p.dense_tiles + routed_blocks * p.routed_tiles);
-    grouped_tiles_kernel<WM, MF, WN, NF, ST, GATEUP>
-        <<<grid, WM * WN * WAVE, 0, stream>>>(p, (uint32_t)T, (uint32_t)(GATEUP ? T : n));
+    auto wgs = [](int blocks, int tiles) {   // whole shares
+        const int shares = xcd_shares(tiles);
+        return cdiv(blocks, shares) * shares * tiles;
+    };
+    p.dense_wgs = wgs(p.dense_blocks, p.dense_tiles);
+    const unsigned grid = (unsigned)(p.dense_wgs + wgs(routed_blocks, p.routed_tiles));
+    grouped_stream_kernel<MF, NT, D, GATEUP>
+        <<<grid, 4 * WAVE, 0, stream>>>(p, (uint32_t)T, (uint32_t)(GATEUP ? T : n));
 }
 
 hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
                             int N, uint16_t* out, void*, hipStream_t stream) {
-    ProductArgs p{};
-    p.dense = PartI8{a, a_scale, w, {}, M, N, K, out};
 #define MOE_TILES(WM, MF, WN, NF, ST, KS)                                                         \
     {                                                                                         \
         const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
@@ -697,7 +595,8 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     auto tiles = [&](int bm, int bn) { return (long long)cdiv(M, bm) * cdiv(N, bn); };
     const long long r128 = (tiles(128, 128) + 2 * kCUs - 1) / (2 * kCUs);
     const long long r256 = (tiles(256, 256) + kCUs - 1) / kCUs;
-    if (M <= 16 || tiles(16, 16) <= 2 * kCUs) launch_product<1, 1, 1, 8, 8, false>(p, 0, stream);
+    if (M <= 16 || tiles(16, 16) <= 2 * kCUs)
+        linear_few_kernel<<<(unsigned)tiles(16, 16), kFewWaves * WAVE, 0, stream>>>(a, a_scale, M, K, w, N, out);
     else if (tiles(32, 64) <= kCUs) MOE_TILES(1, 2, 2, 2, 8, 1)
     else if (tiles(64, 64) <= kCUs) MOE_TILES(2, 2, 2, 2, 4, 2)
     else if (tiles(128, 64) <= kCUs) MOE_TILES(2, 4, 2, 2, 4, 2)
@@ -738,16 +637,21 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     p.block_expert = g.r.block_expert;
     p.block_row = g.r.block_row;
     p.offsets = g.r.offsets;
+    p.n_blocks = g.r.n_blocks;
     p.sorted_assign = g.r.sorted_assign;
     p.routed = PartI8{g.x, g.x_scale, g.gate, g.up, 0, g.I, g.H, h};
     if (g.I_sh) p.dense = PartI8{g.x, g.x_scale, g.sh_gate, g.sh_up, g.T, g.I_sh, g.H, h_sh};
     const int n = g.T * g.k;
-    // us measured at H 2048, I 512, 256 experts, k 8, weights out of memory: straight from
-    // memory into registers up to 32 rows (512 tokens 97 with K over two waves, 110 without,
-    // 101 through LDS), through LDS for 64 (2048 tokens 147 against 166, skewed 127 against 137)
-    if (g.block_rows == 16) launch_product<1, 4, 2, 2, 4, true>(p, g.max_blocks, stream);
-    else if (g.block_rows == 32) launch_product<2, 4, 2, 2, 2, true>(p, g.max_blocks, stream);
-    else launch_grouped_tiles<1, 4, 4, 2, 4, true>(p, g.max_blocks, g.T, n, stream);
+    // Rows / 16, weight rows of a wave / 16, steps ahead; us measured at H 2048, I 512, 256
+    // experts, k 8.  Gate/up: 64 tokens 1,2,4 76; 512 tokens 2,2,4 96 (2,4,4 103, 1,2,4 101,
+    // 4,4,2 110); 2048 tokens 4,4,2 129, skewed 97 (2,2,4 139 and 116, 4,4,4 128 and 105).
+    // Down: 64 tokens 1,2,4 42; 512 tokens 2,4,2 53 (1,2,4 55, 4,4,4 58); 2048 tokens 4,4,4 77,
+    // skewed 67 (2,4,2 78 and 65).  Blocks of 32 rows that are mostly full take the wider waves.
+    const bool full = n > 32 * g.E;
+    if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, true>(p, g.max_blocks, g.T, n, stream);
+    else if (g.block_rows == 32 && !full) launch_grouped_stream<2, 2, 4, true>(p, g.max_blocks, g.T, n, stream);
+    else if (g.block_rows == 32) launch_grouped_stream<2, 4, 4, true>(p, g.max_blocks, g.T, n, stream);
+    else launch_grouped_stream<4, 4, 2, true>(p, g.max_blocks, g.T, n, stream);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     quant_h_kernel<<<n + (g.I_sh ? g.T : 0), kQuantThreads, 0, stream>>>(
@@ -755,12 +659,9 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     if ((err = hipGetLastError()) != hipSuccess) return err;
     p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out};
     if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out};
-    // a wave's 32 columns reuse its rows more than 16 would, once blocks are mostly full:
-    // 2048 tokens 110 against 125, but 512 tokens 60 against 57
-    if (g.block_rows == 16) launch_product<1, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
-    else if (g.block_rows == 32 && n <= 32 * g.E) launch_product<2, 2, 4, 1, 4, false>(p, g.max_blocks, stream);
-    else if (g.block_rows == 32) launch_product<2, 4, 4, 1, 2, false>(p, g.max_blocks, stream);
-    else launch_grouped_tiles<1, 4, 4, 2, 4, false>(p, g.max_blocks, g.T, n, stream);
+    if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, false>(p, g.max_blocks, g.T, n, stream);
+    else if (g.block_rows == 32) launch_grouped_stream<2, 4, 2, false>(p, g.max_blocks, g.T, n, stream);
+    else launch_grouped_stream<4, 4, 4, false>(p, g.max_blocks, g.T, n, stream);
     return hipGetLastError();
 }
 

@@ -21,6 +21,15 @@ __device__ __forceinline__ void buf_to_lds16(buf_rsrc_t r, void* lds, uint32_t v
 #endif
 }
 
+// 16 bytes per lane into registers.
+__device__ __forceinline__ u32x4_t buf_load16_u(buf_rsrc_t r, uint32_t voff, uint32_t soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+#else
+    return u32x4_t{0, 0, 0, 0};
+#endif
+}
+
 // Waits until at most N of this wave's vector loads are in flight.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
