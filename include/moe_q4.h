@@ -456,8 +456,9 @@ typedef struct {
  *   16-byte aligned);  q_scale fp32 [T].  residual, sum, y may be NULL, and q
  *   and q_scale together; at least one output is given.  sum may be x or
  *   residual itself (the same address); no other outputs alias inputs.
- * H a multiple of 64 up to 16384, T >= 1, eps > 0 and finite.  Enqueues one
- * kernel. */
+ * H a multiple of 64 up to 16384, T >= 1, eps > 0 and finite; values finite,
+ * |v| and |v * weight| below 1e17 (a row's squares are summed in fp32).
+ * Enqueues one kernel. */
 int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
                 int T, int H, uint16_t* sum, uint16_t* y, int8_t* q, float* q_scale,
                 hipStream_t stream);

@@ -434,3 +434,79 @@ def test_two_streams_with_an_object_each():
     sync()
     for layer, v in zip(layers, want):
         assert torch.equal(layer.buffers(T)["y"], v)
+
+
+# ---- sizes at which offsets pass 31 and 32 bits, and variants chosen by size ----
+
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_streamed_norm_equals_the_cached_one(with_residual):
+    """Inputs over 128 MB take non-temporal loads; slices of the same rows do not."""
+    require_gpu()
+    T, H = (8200, 4160) if with_residual else (16400, 4160)
+    announce(f"norm T={T} H={H}")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((T, H), device=DEV, generator=g).bfloat16()
+    r = torch.randn((T, H), device=DEV, generator=g).bfloat16() if with_residual else None
+    w = torch.randn(H, device=DEV, generator=g).bfloat16()
+    out = lambda n: (torch.empty((n, H), dtype=torch.bfloat16, device=DEV), torch.empty((n, H), dtype=torch.bfloat16, device=DEV),  # noqa: E731
+                     torch.empty((n, H), dtype=torch.int8, device=DEV), torch.empty(n, device=DEV))
+    whole, q, qs = out(T), torch.empty((T, H), dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    bq.moe_norm_i8(x, r, w, EPS, *whole)
+    bq.moe_quant_i8(x, q, qs)
+    for at in (0, T // 2, T - 77):
+        part, pq, ps = out(77), torch.empty((77, H), dtype=torch.int8, device=DEV), torch.empty(77, device=DEV)
+        bq.moe_norm_i8(x[at:at + 77], None if r is None else r[at:at + 77], w, EPS, *part)
+        bq.moe_quant_i8(x[at:at + 77], pq, ps)
+        sync()
+        for a, b in zip(whole + (q, qs), part + (pq, ps)):
+            assert torch.equal(a[at:at + 77], b)
+
+
+def test_rows_past_32_bit_offsets():
+    require_gpu()
+    R, K = 131073 + 5, 16384   # 2^31 elements and some
+    announce(f"quant R={R} K={K}")
+    x = torch.zeros((R, K), dtype=torch.bfloat16, device=DEV)
+    x[-1] = torch.arange(K, device=DEV).remainder(255).sub(127).bfloat16()
+    q, s = torch.full((R, K), 1, dtype=torch.int8, device=DEV), torch.full((R,), -1.0, device=DEV)
+    out = torch.full((R, K), 1.0, dtype=torch.bfloat16, device=DEV)
+    bq.moe_quant_i8(x, q, s)
+    bq.moe_dequant_i8_bf16(q, s, out)
+    sync()
+    assert float(s[-1]) == 1.0 and torch.equal(q[-1].float(), x[-1].float()) and torch.equal(out[-1], x[-1])
+    assert not q[-2].any() and float(s[0]) == 0 and not out[R // 2].any()
+
+
+def test_linear_of_outputs_past_31_bits():
+    require_gpu()
+    M, N, K = 33_500_000, 66, 64   # M * N = 2.2e9
+    announce(f"linear M={M} N={N} K={K}")
+    a = torch.zeros((M, K), dtype=torch.int8, device=DEV)
+    a[-1] = 1
+    w = bq.DeviceI8Mat(torch.arange(N, device=DEV, dtype=torch.int8).view(1, N, 1).expand(1, N, K).contiguous(),
+                       torch.ones((1, N), device=DEV))
+    out = torch.full((M, N), 9.0, dtype=torch.bfloat16, device=DEV)
+    bq.moe_linear_i8(a, torch.ones(M, device=DEV), w, out)
+    sync()
+    assert torch.equal(out[-1].float(), 64 * torch.arange(N, device=DEV).float())
+    assert not out[0].any() and not out[M // 2].any() and not out[-2].any()
+
+
+def test_large_layer_equals_its_slices():
+    """A token's sums do not depend on the others, and the integer sums are exact: the same tokens
+    in a call of 40000 (2^31 bytes of expert rows and more) and in calls of any block size."""
+    require_gpu()
+    T, H, I, I_sh, E, k = 40000, 2048, 256, 128, 64, 8
+    announce(f"layer T={T}")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rnd = lambda *s: torch.randint(-127, 128, s, device=DEV, generator=g, dtype=torch.int8)  # noqa: E731
+    mats = [bq.DeviceI8Mat(rnd(*s), torch.rand(s[:2], device=DEV, generator=g) * 1e-3)
+            for s in ((E, I, H), (E, I, H), (E, H, I), (1, I_sh, H), (1, I_sh, H), (1, H, I_sh))]
+    x, sx = rnd(T, H), torch.rand(T, device=DEV, generator=g) * 0.02
+    lg = torch.randn((T, E), device=DEV, generator=g)
+    whole = bq.MoeLayerI8(mats, H, I, I_sh, E, k, DEV).forward(x, sx, lg)["y"]
+    for at, n, rows in ((0, 40, 16), (20000, 300, 32), (39000, 1000, 32), (37000, 3000, 64)):
+        part = bq.MoeLayerI8(mats, H, I, I_sh, E, k, DEV, block_rows=rows)
+        y = part.forward(x[at:at + n], sx[at:at + n], lg[at:at + n])["y"]
+        sync()
+        assert torch.equal(whole[at:at + n], y), (at, n, rows)
