@@ -571,8 +571,9 @@ __global__ __launch_bounds__(kGroupThreads) void route_scored_fused_kernel(
     group_all(s_eids, T * k, E, block_rows, max_blocks, r, s_hist);
 }
 
-// One token: a wave selects, then 256 threads write the arrays without a scan
-// (7.3 us through the fused kernel's sixteen waves, figures below).
+// One token: a wave selects, then 256 threads write the arrays without a scan (256
+// experts, 8 groups, k 8: 4.9 us; 7.3 through the fused kernel's sixteen waves).  Bound
+// by the chain of one wave: logits, scores, group and top-k rounds.
 constexpr int kOneThreads = 256;
 template <int EPL>
 __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
@@ -595,7 +596,9 @@ __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
 // chunk w, so rows follow assignment order and the sort is stable.  Every
 // workgroup repeats the scan, which costs less than a third launch: n_seg * E
 // bytes from L2.  The counts of segments of 16 fit the T * k words of moe_route's
-// workspace for any E <= 64 k.
+// workspace for any E <= 64 k.  Bound by instructions in the selection (about 1000 a
+// token) and by the chain of waits in the scatter: 2048 tokens x 8 of 256 take 6.7 + 7.0
+// us, 8192 x 6 of 160 13 + 8 (one grouping workgroup: 87 for the latter's scatter).
 constexpr int kSegTokens = kGroupWaves;                // most tokens of a segment
 constexpr int kSegMaxK = kGroupThreads / kSegTokens;   // a segment fits a scatter workgroup
 
@@ -754,7 +757,7 @@ static int seg_tokens_of(int T, int E, int k) {
     if (use_fused(T, E, k) || k > kSegMaxK) return 0;
     size_t a, b;
     const size_t have = (size_t)T * k > kStageMaxAssign ? ~(size_t)0 : route_ws_layout(T, E, k, &a, &b);
-    if (T <= 1024 && seg_bytes(T, E, 8) <= have) return 8;
+    if (T <= 4096 && seg_bytes(T, E, 8) <= have) return 8;
     return seg_bytes(T, E, kSegTokens) <= have ? kSegTokens : 0;
 }
 
