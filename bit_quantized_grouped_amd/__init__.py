@@ -1139,8 +1139,8 @@ class MoeLayerI8:
     def rows_for(self, T: int) -> int:
         """Rows of a block for T tokens.  Below 8 rows an expert blocks of 16 hold the fewest
         empty rows; 32 and, from 32 rows an expert, 64 pass the weights through fewer times (gate/up
-        and down of 256 experts, k 8: 64 tokens 117, 120 us with 16, 32; 512 tokens 155, 149, 162
-        with 16, 32, 64; 2048 skewed tokens 171, 163 with 32, 64)."""
+        and down of 256 experts, k 8: 64 tokens 117, 120 us with 16, 32; 512 tokens 153, 146, 160
+        with 16, 32, 64; 2048 skewed tokens 169, 148 with 32, 64)."""
         if self.block_rows is not None:
             return self.block_rows
         n = T * self.k

@@ -332,21 +332,25 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 // ---- The experts' products with weights streamed into registers ----
 // A workgroup of 4 waves owns BM = 16 MF rows of a block and 64 NT weight rows, a wave
 // 16 NT of them (GATEUP: half the gate's, half the up's).  Each weight row is read once
-// per block, so the weights go straight into registers, D steps of 64 K ahead: 64 to
-// 256 KB in flight on a CU, which the latency of HBM under load (2 us and more) needs.
-// (Through an LDS ring as above, 72 KB in flight, 2048 tokens took 147 us for gate/up
-// instead of 129; a variant without its products took as long.)  The rows' codes are
-// shared by the waves: 512 K of them at a time go straight into LDS, the next 512 while
-// these are multiplied, laid out as in the tile kernel.  Bound by HBM: 541 MB of gate
-// and up weights of 256 experts in 96 us are 5.6 TB/s, of the 6.2 a plain read reaches.
-template <int MF, int NT, int D, bool GATEUP>
+// per block, so the weights go straight into registers, D steps of 64 K ahead, 64 KB
+// and more in flight on a CU, which the latency of HBM under load (2 us and more)
+// needs.  (Through an LDS ring as above 2048 tokens took 147 us for gate/up instead of
+// 120; a variant without its products took as long.)  The rows' codes are shared by the
+// waves: Q steps of 64 K at a time go straight into LDS, the next Q while these are
+// multiplied, laid out as in the tile kernel; small chunks leave room for three
+// workgroups on a CU, which cover each other's waits (Q = 8: two).  Bound by HBM: 541 MB
+// of gate and up weights of 256 experts in 94 us are 5.8 TB/s, of the 6.2 a plain read
+// reaches.
+template <int MF, int NT, int D, int Q, bool GATEUP>
 __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs p, uint32_t dense_rows,
                                                                      uint32_t routed_rows) {
-    constexpr int BM = MF * 16, NW = GATEUP ? NT / 2 : NT, COLS = 4 * NW * 16, Q = 8;
+    constexpr int BM = MF * 16, NW = GATEUP ? NT / 2 : NT, COLS = 4 * NW * 16;
     constexpr int LA = Q * MF / 4;   // 1 KB loads of a wave and chunk
     static_assert(Q % D == 0 && Q * MF % 4 == 0, "a slot for each step of a chunk, whole loads");
     constexpr uint32_t kPast = 0xC0000000u;
-    __shared__ __attribute__((aligned(16))) int8_t s_a0[Q * BM * 64], s_a1[Q * BM * 64];
+    constexpr int ES = GATEUP ? 4 : 2, ROW = NW * 16 * ES, STRIDE = ROW + 16;   // bytes of staged rows
+    constexpr int A0 = Q * BM * 64, STAGE = 4 * 16 * STRIDE;
+    __shared__ __attribute__((aligned(16))) int8_t s_a0[A0 > STAGE ? A0 : STAGE], s_a1[A0];
     const int lane = threadIdx.x % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int dense_wgs = p.dense_wgs;
@@ -452,8 +456,7 @@ __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs
     // The values, 16 rows of the wave at a time through its share of the LDS (the run-out
     // loads into it have landed), so that a store covers whole lines; a wave's LDS operations
     // complete in order, so no barrier is needed inside it.
-    constexpr int ES = GATEUP ? 4 : 2, ROW = NW * 16 * ES, STRIDE = ROW + 16;   // bytes
-    static_assert(4 * 16 * STRIDE <= Q * BM * 64 && 16 * ROW / 16 % WAVE == 0, "staged rows");
+    static_assert(16 * ROW / 16 % WAVE == 0, "whole stores");
     const int col0 = n0 + wave * NW * 16;
     if (col0 >= N) return;   // N is a multiple of 64: the wave's columns are all in or all out
     int8_t* s_o = s_a0 + wave * 16 * STRIDE;
@@ -558,7 +561,7 @@ constexpr int kCUs = 256, kLdsBytes = 160 * 1024;   // of an MI355X, of a CU
 static int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // T: tokens, n: routed rows.
-template <int MF, int NT, int D, bool GATEUP>
+template <int MF, int NT, int D, int Q, bool GATEUP>
 static void launch_grouped_stream(ProductArgs& p, int routed_blocks, int T, int n, hipStream_t stream) {
     constexpr int cols = (GATEUP ? NT / 2 : NT) * 64;
     p.dense_blocks = p.dense.out ? cdiv(p.dense.M, MF * 16) : 0;
@@ -570,7 +573,7 @@ static void launch_grouped_stream(ProductArgs& p, int routed_blocks, int T, int 
     };
     p.dense_wgs = wgs(p.dense_blocks, p.dense_tiles);
     const unsigned grid = (unsigned)(p.dense_wgs + wgs(routed_blocks, p.routed_tiles));
-    grouped_stream_kernel<MF, NT, D, GATEUP>
+    grouped_stream_kernel<MF, NT, D, Q, GATEUP>
         <<<grid, 4 * WAVE, 0, stream>>>(p, (uint32_t)T, (uint32_t)(GATEUP ? T : n));
 }
 
@@ -642,16 +645,17 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     p.routed = PartI8{g.x, g.x_scale, g.gate, g.up, 0, g.I, g.H, h};
     if (g.I_sh) p.dense = PartI8{g.x, g.x_scale, g.sh_gate, g.sh_up, g.T, g.I_sh, g.H, h_sh};
     const int n = g.T * g.k;
-    // Rows / 16, weight rows of a wave / 16, steps ahead; us measured at H 2048, I 512, 256
-    // experts, k 8.  Gate/up: 64 tokens 1,2,4 76; 512 tokens 2,2,4 96 (2,4,4 103, 1,2,4 101,
-    // 4,4,2 110); 2048 tokens 4,4,2 129, skewed 97 (2,2,4 139 and 116, 4,4,4 128 and 105).
-    // Down: 64 tokens 1,2,4 42; 512 tokens 2,4,2 53 (1,2,4 55, 4,4,4 58); 2048 tokens 4,4,4 77,
-    // skewed 67 (2,4,2 78 and 65).  Blocks of 32 rows that are mostly full take the wider waves.
+    // Rows / 16, weight rows of a wave / 16, steps ahead, steps of a chunk; us measured at H
+    // 2048, I 512, 256 experts, k 8.  Gate/up: 64 tokens 1,2,4,4 76; 512 tokens 2,2,4,4 94
+    // (2,4,4,4 103, 1,2,4,4 99, 4,4,2,2 105); 2048 tokens 4,4,2,2 120, skewed 90 (2,2,4,4 138
+    // and 115, 2,4,4,4 129 and 106, 4,4,2,8 132 and 104).  Down: 64 tokens 1,2,4,4 42; 512
+    // tokens 2,4,2,4 52 (1,2,4,4 54, 4,4,4,4 55); 2048 tokens 4,4,4,4 72, skewed 58 (2,4,2,4 76
+    // and 63, 4,4,4,8 77 and 67).  Blocks of 32 rows that are mostly full take the wider waves.
     const bool full = n > 32 * g.E;
-    if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, true>(p, g.max_blocks, g.T, n, stream);
-    else if (g.block_rows == 32 && !full) launch_grouped_stream<2, 2, 4, true>(p, g.max_blocks, g.T, n, stream);
-    else if (g.block_rows == 32) launch_grouped_stream<2, 4, 4, true>(p, g.max_blocks, g.T, n, stream);
-    else launch_grouped_stream<4, 4, 2, true>(p, g.max_blocks, g.T, n, stream);
+    if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, 4, true>(p, g.max_blocks, g.T, n, stream);
+    else if (g.block_rows == 32 && !full) launch_grouped_stream<2, 2, 4, 4, true>(p, g.max_blocks, g.T, n, stream);
+    else if (g.block_rows == 32) launch_grouped_stream<2, 4, 4, 4, true>(p, g.max_blocks, g.T, n, stream);
+    else launch_grouped_stream<4, 4, 2, 2, true>(p, g.max_blocks, g.T, n, stream);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     quant_h_kernel<<<n + (g.I_sh ? g.T : 0), kQuantThreads, 0, stream>>>(
@@ -659,9 +663,9 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     if ((err = hipGetLastError()) != hipSuccess) return err;
     p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out};
     if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out};
-    if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, false>(p, g.max_blocks, g.T, n, stream);
-    else if (g.block_rows == 32) launch_grouped_stream<2, 4, 2, false>(p, g.max_blocks, g.T, n, stream);
-    else launch_grouped_stream<4, 4, 4, false>(p, g.max_blocks, g.T, n, stream);
+    if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, 4, false>(p, g.max_blocks, g.T, n, stream);
+    else if (g.block_rows == 32) launch_grouped_stream<2, 4, 2, 4, false>(p, g.max_blocks, g.T, n, stream);
+    else launch_grouped_stream<4, 4, 4, 4, false>(p, g.max_blocks, g.T, n, stream);
     return hipGetLastError();
 }
 
