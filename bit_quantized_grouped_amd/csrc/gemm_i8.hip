@@ -499,37 +499,66 @@ __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs
     }
 }
 
-// Row-wise quantisation of h: one workgroup per row, the routed rows and then the
-// shared expert's.
-constexpr int kQuantThreads = 128;
-__global__ __launch_bounds__(kQuantThreads) void quant_h_kernel(
-    const float* __restrict__ h, const float* __restrict__ h_sh, int n_routed, int I, int I_sh,
-    int8_t* __restrict__ q, int8_t* __restrict__ q_sh, float* __restrict__ scale,
+// Row-wise quantisation of h, the routed rows and then the shared expert's.  V > 0: a wave
+// per row, V pieces of 4 values a lane in registers (rows up to 256 V); V = 0: a workgroup
+// per row, read twice.  Bound by the launch and, from some 10 MB, by the caches h lies in.
+constexpr int kQuantWaves = 4;
+template <int V>
+__global__ __launch_bounds__(kQuantWaves* WAVE) void quant_h_kernel(
+    const float* __restrict__ h, const float* __restrict__ h_sh, int n_routed, int n_sh, int I,
+    int I_sh, int8_t* __restrict__ q, int8_t* __restrict__ q_sh, float* __restrict__ scale,
     float* __restrict__ scale_sh) {
-    const bool routed = (int)blockIdx.x < n_routed;
-    const int r = routed ? blockIdx.x : blockIdx.x - n_routed;
+    constexpr bool kWave = V > 0;
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+    const int at = kWave ? blockIdx.x * kQuantWaves + wave : blockIdx.x;
+    if (at >= n_routed + n_sh) return;
+    const bool routed = at < n_routed;
+    const int r = routed ? at : at - n_routed;
     const int K = routed ? I : I_sh;
     const float* src = (routed ? h : h_sh) + (size_t)r * K;
     int8_t* dst = (routed ? q : q_sh) + (size_t)r * K;
+    const int tid = kWave ? lane : (int)threadIdx.x;
+    constexpr int STEP = kWave ? WAVE * 4 : kQuantWaves * WAVE * 4;
+    f32x4_t v[kWave ? V : 1];
     float top = 0.f;
-    for (int c = threadIdx.x * 4; c < K; c += kQuantThreads * 4) {
-        const f32x4_t v = *(const f32x4_t*)(src + c);
+    if constexpr (kWave) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(v[i]));
+        for (int i = 0; i < V; ++i) {
+            const int c = i * STEP + tid * 4;
+            v[i] = c < K ? *(const f32x4_t*)(src + c) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(v[i][j]));
+    } else {
+        for (int c = tid * 4; c < K; c += STEP) {
+            const f32x4_t t = *(const f32x4_t*)(src + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(t[j]));
+        }
     }
 #pragma unroll
     for (int off = WAVE / 2; off >= 1; off >>= 1) top = fmaxf(top, shfl_xor(top, off));
-    __shared__ float s_top[kQuantThreads / WAVE];
-    if (threadIdx.x % WAVE == 0) s_top[threadIdx.x / WAVE] = top;
-    __syncthreads();
+    if constexpr (!kWave) {
+        __shared__ float s_top[kQuantWaves];
+        if (lane == 0) s_top[wave] = top;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQuantThreads / WAVE; ++i) top = fmaxf(top, s_top[i]);
+        for (int i = 0; i < kQuantWaves; ++i) top = fmaxf(top, s_top[i]);
+    }
     const float to_code = top > 0.f ? 127.0f / top : 0.f;
-    if (threadIdx.x == 0) (routed ? scale : scale_sh)[r] = top / 127.0f;
-    for (int c = threadIdx.x * 4; c < K; c += kQuantThreads * 4) {
-        const f32x4_t v = *(const f32x4_t*)(src + c);
+    if (tid == 0) (routed ? scale : scale_sh)[r] = top / 127.0f;
+    auto put = [&](int c, const f32x4_t& t) {
         *(uint32_t*)(dst + c) =
-            pack_codes(v[0] * to_code, v[1] * to_code, v[2] * to_code, v[3] * to_code);
+            pack_codes(t[0] * to_code, t[1] * to_code, t[2] * to_code, t[3] * to_code);
+    };
+    if constexpr (kWave) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * STEP + tid * 4 < K) put(i * STEP + tid * 4, v[i]);
+    } else {
+        for (int c = tid * 4; c < K; c += STEP) put(c, *(const f32x4_t*)(src + c));
     }
 }
 
@@ -658,8 +687,16 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     else launch_grouped_stream<4, 4, 2, 2, true>(p, g.max_blocks, g.T, n, stream);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    quant_h_kernel<<<n + (g.I_sh ? g.T : 0), kQuantThreads, 0, stream>>>(
-        h, h_sh, n, g.I, g.I_sh, q, q_sh, scale, scale_sh);
+    const int n_sh = g.I_sh ? g.T : 0, widest = g.I > g.I_sh ? g.I : g.I_sh;
+#define MOE_QUANT(V)                                                                              \
+    quant_h_kernel<V><<<V ? cdiv(n + n_sh, kQuantWaves) : n + n_sh, kQuantWaves * WAVE, 0, stream>>>( \
+        h, h_sh, n, n_sh, g.I, g.I_sh, q, q_sh, scale, scale_sh)
+    if (widest <= 256) MOE_QUANT(1);
+    else if (widest <= 512) MOE_QUANT(2);
+    else if (widest <= 1024) MOE_QUANT(4);
+    else if (widest <= 2048) MOE_QUANT(8);
+    else MOE_QUANT(0);
+#undef MOE_QUANT
     if ((err = hipGetLastError()) != hipSuccess) return err;
     p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out};
     if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out};

@@ -302,7 +302,7 @@ def check_layer(got, x, sx, idx, w, host, I_sh, what):
 LAYERS = [  # T, H, I, I_sh, E, k
     (1, 64, 64, 0, 4, 1), (1, 256, 128, 128, 16, 4), (1, 2048, 512, 512, 16, 8), (1, 128, 1088, 64, 70, 20), (1, 192, 4160, 0, 4, 2), (3, 256, 128, 64, 60, 4), (8, 2048, 512, 512, 256, 8), (2, 192, 64, 320, 8, 3), (7, 256, 192, 64, 16, 2),
     (33, 320, 128, 0, 6, 6), (65, 512, 64, 128, 60, 4), (130, 128, 448, 64, 16, 8), (257, 256, 128, 192, 4, 2),
-    (40, 64, 1088, 1152, 3, 2)]
+    (40, 64, 1088, 1152, 3, 2), (9, 64, 640, 64, 6, 2), (5, 128, 2112, 576, 6, 2)]
 
 
 @pytest.mark.parametrize("T,H,I,I_sh,E,k", LAYERS)
