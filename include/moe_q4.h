@@ -1,5 +1,6 @@
 /*
- * moe_q4.h - C ABI of the 4-bit grouped MoE layer for MI355X (gfx950).
+ * moe_q4.h - C ABI of the 4-bit grouped MoE layer for MI355X (gfx950), and of
+ * the 8-bit operators around it (their section is at the end).
  *
  * The layer: a router picks k of E experts per token and one shared expert
  * sees every token; each expert is a SwiGLU FFN whose weights are 4-bit
