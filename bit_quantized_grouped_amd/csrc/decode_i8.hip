@@ -173,7 +173,8 @@ __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(Decod
         }
 #pragma unroll
         for (int off = WAVE / 2; off >= 1; off >>= 1) top = fmaxf(top, shfl_xor(top, off));
-        const float to_code = top > 0.f ? 127.0f / top : 0.f;
+        float to_code;
+        const float scale = row_scale(top, &to_code);
         auto put = [&](int c, const f32x4_t& t) {
             *(uint32_t*)(q + c) =
                 pack_codes(t[0] * to_code, t[1] * to_code, t[2] * to_code, t[3] * to_code);
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(Decod
         }
         const float wgt = shared ? 1.f : p.r.topk_w[token * k + j];
         const float ws = m.scales[(size_t)e * p.H + c0 + lane % 8];
-        y += wgt * ((float)sum * (top / 127.0f) * ws);
+        y += wgt * ((float)sum * scale * ws);
     }
     if (lane < 8) s_y[wave][lane] = y;
     __syncthreads();

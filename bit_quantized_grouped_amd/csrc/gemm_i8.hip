@@ -35,8 +35,7 @@ struct PartI8 {
 struct ProductArgs {
     PartI8 dense, routed;
     int dense_blocks, dense_tiles, routed_tiles;
-    int block_rows, k;
-    int dense_wgs;                  // of grouped_stream_kernel
+    int dense_wgs, k;
     const int32_t* block_expert;
     const int32_t* block_row;
     const int32_t* offsets;
@@ -104,14 +103,16 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
 // ---- Dense product of many rows: tiles through LDS ----
 // A workgroup of WM x WN waves owns a BM x BN tile; a wave WM-th of its rows and
 // WN-th of its columns, MF x NF products of 16 x 16.  KS blocks of 64 K of both
-// operands (one stage) go straight from memory into LDS, ST - 1 stages ahead of the one that is
-// multiplied: a stage of the 256 x 256 tile is 1024 cycles of products, and a load
-// takes two to four times that under full traffic.  Stages past K are zeros and
-// multiplied like the others.  A block keeps rows of 64 bytes
-// whose four 16-byte pieces are permuted: place j of row r holds piece
-// j ^ (r / 2 % 4), chosen on the source side (a load writes LDS in lane order), so
-// that 8 neighbouring rows of a fragment read, 128 bytes, lie in different banks
-// (with r / 4 half of the LDS cycles were conflicts).
+// operands (one stage) go straight from memory into LDS, ST - 1 stages ahead of the
+// one that is multiplied: a stage of the 256 x 256 tile is 1024 cycles of products,
+// and a load takes two to four times that under full traffic.  Stages past K are
+// zeros and multiplied like the others.  A block keeps rows of 64 bytes whose four
+// 16-byte pieces are permuted: place j of row r holds piece j ^ (r / 2 % 4), chosen on
+// the source side (a load writes LDS in lane order), so that 8 neighbouring rows of a
+// fragment read, 128 bytes, lie in different banks (with r / 4 half of the LDS cycles
+// were conflicts).  A workgroup requests its next tile's first stages during the last
+// products of a tile.  8192 x 4096 x 4096 takes 117 us (2350 TOP/s), MFMA 56 % busy at
+// 2.0 GHz; with codes of zero, at a higher clock, 92.
 // Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
 // which the build checks.
 template <int WM, int MF, int WN, int NF, int ST, int KS>
@@ -547,8 +548,9 @@ __global__ __launch_bounds__(kQuantWaves* WAVE) void quant_h_kernel(
 #pragma unroll
         for (int i = 0; i < kQuantWaves; ++i) top = fmaxf(top, s_top[i]);
     }
-    const float to_code = top > 0.f ? 127.0f / top : 0.f;
-    if (tid == 0) (routed ? scale : scale_sh)[r] = top / 127.0f;
+    float to_code;
+    const float s = row_scale(top, &to_code);
+    if (tid == 0) (routed ? scale : scale_sh)[r] = s;
     auto put = [&](int c, const f32x4_t& t) {
         *(uint32_t*)(dst + c) =
             pack_codes(t[0] * to_code, t[1] * to_code, t[2] * to_code, t[3] * to_code);
@@ -623,7 +625,7 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     //   32 x 64: 333x1001x2048 6.2 / 8.4;  64 x 64: 128x8192x7168 19.4 / 27;
     //   128 x 64: 333x4096x4096 17.2 / 24, 1000x2048x2048 11.2 / 15;
     // beyond that 128 x 128 (two on a CU) or 256 x 256, whichever takes fewer rounds:
-    //   2048x4096x4096 44 / 48 (one each), 8192x4096x4096 127 by 256 x 256.
+    //   2048x4096x4096 44 / 48 (one each), 8192x4096x4096 117 by 256 x 256.
     auto tiles = [&](int bm, int bn) { return (long long)cdiv(M, bm) * cdiv(N, bn); };
     const long long r128 = (tiles(128, 128) + 2 * kCUs - 1) / (2 * kCUs);
     const long long r256 = (tiles(256, 256) + kCUs - 1) / kCUs;
@@ -664,7 +666,6 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     int8_t *q = (int8_t*)(base + L.q), *q_sh = (int8_t*)(base + L.q_sh);
     float *scale = (float*)(base + L.scale), *scale_sh = (float*)(base + L.scale_sh);
     ProductArgs p{};
-    p.block_rows = g.block_rows;
     p.k = g.k;
     p.block_expert = g.r.block_expert;
     p.block_row = g.r.block_row;

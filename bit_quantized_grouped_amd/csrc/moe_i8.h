@@ -44,6 +44,16 @@ __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float 
 }
 #endif
 
+#ifdef __HIPCC__
+// Scale of a row of largest magnitude `top`, and the factor from its values to codes.  A row
+// below 2^-119 counts as zeros: 127 / top would pass fp32's range.
+__device__ __forceinline__ float row_scale(float top, float* to_code) {
+    const bool any = top >= 0x1p-119f;
+    *to_code = any ? 127.0f / top : 0.f;
+    return any ? top / 127.0f : 0.f;
+}
+#endif
+
 // norm_i8.hip
 hipError_t launch_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                           float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,

@@ -101,8 +101,9 @@ __global__ __launch_bounds__(NW == 1 ? kNormRows * WAVE : NW * WAVE) void norm_i
     }
     const float inv = NORM ? 1.0f / sqrtf(sq / (float)H + eps) : 1.0f;
     top *= inv;
-    const float to_code = top > 0.f ? 127.0f / top : 0.f;
-    if (q_scale && tid == 0) q_scale[t] = top / 127.0f;
+    float to_code;
+    const float scale = row_scale(top, &to_code);
+    if (q_scale && tid == 0) q_scale[t] = scale;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * NW * WAVE + tid) * 8;

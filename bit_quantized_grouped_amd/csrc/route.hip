@@ -589,9 +589,8 @@ __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
 // Segments: above the one-launch size the tokens are cut into segments of 8 or
 // 16, one token per wave of a workgroup that selects their experts and counts
 // them, one byte per expert (a token takes an expert once, so a count is at most
-// 16).  A
-// workgroup of the scatter kernel takes up to 1024 assignments of whole segments:
-// it sums the segments' counts (those before its own, and all of them), scans the
+// 16).  A workgroup of the scatter kernel takes up to 1024 assignments of whole
+// segments: it sums the segments' counts (those before its own, and all of them), scans the
 // experts' totals, and places its assignments: wave w owns their 64-assignment
 // chunk w, so rows follow assignment order and the sort is stable.  Every
 // workgroup repeats the scan, which costs less than a third launch: n_seg * E

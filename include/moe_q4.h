@@ -429,7 +429,8 @@ int moe_layer_chunked(const uint16_t* x, const float* logits, int T, int H, int 
 /* ---- 8-bit operators: the pre-norm with 8-bit output, scored routing and
  * products of 8-bit codes.  A row of K values is held as K signed 8-bit codes
  * and one fp32 scale: value = code * scale, scale = max|row| / 127, code =
- * rne(value * (127 / max|row|)); a row of zeros has scale 0 and codes 0.
+ * rne(value * (127 / max|row|)); a row of zeros, or of values below 2^-119 alone,
+ * has scale 0 and codes 0.
  * Codes are -128 .. 127; the calls that quantise write -127 .. 127.
  * ---- */
 

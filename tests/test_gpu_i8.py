@@ -120,6 +120,21 @@ def test_quant_and_back(R, K):
     within(f64(out), v, np.abs(v) * (HALF + 2.0 ** -23), "values")
 
 
+def test_rows_on_both_sides_of_the_smallest_scale():
+    """127 / max|row| must stay in fp32's range: rows below 2^-119 count as zeros."""
+    require_gpu()
+    x = torch.zeros((5, 64), dtype=torch.bfloat16, device=DEV)
+    for i, v in enumerate((2.0 ** -119, 2.0 ** -120, 2.0 ** -133, 2.0 ** 127, 3e38)):
+        x[i, 3], x[i, 9] = v, -v / 2
+    q, s = torch.full((5, 64), 5, dtype=torch.int8, device=DEV), torch.empty(5, device=DEV)
+    bq.moe_quant_i8(x, q, s)
+    sync()
+    assert not q[1:3].any() and not s[1:3].any()
+    for i in (0, 3, 4):
+        assert int(q[i, 3]) == 127 and int(q[i, 9]) in (-63, -64) and int(q[i].abs().sum()) <= 191
+        assert float(s[i]) == pytest.approx(float(x[i, 3]) / 127, rel=2.0 ** -22)
+
+
 def test_dequant_takes_every_code():
     require_gpu()
     q = torch.arange(-128, 128, dtype=torch.int16, device=DEV).to(torch.int8).repeat(5, 1)
@@ -165,7 +180,7 @@ def check_scored(lg, bias, k, br=32, score="softmax", **rule):
 @pytest.mark.parametrize("T,E,k,n_groups,topk_groups", [
     (1, 256, 8, 8, 4), (1, 1, 1, 1, 1), (5, 2, 2, 1, 1), (64, 64, 6, 8, 3), (65, 256, 8, 8, 4), (33, 60, 5, 12, 4),
     (130, 160, 6, 8, 3), (97, 160, 4, 8, 7), (70, 128, 16, 2, 1), (9, 1000, 10, 10, 3), (66, 1000, 8, 8, 2),
-    (2731, 36, 6, 4, 2), (1025, 40, 16, 1, 1), (129, 8, 8, 1, 1), (4099, 12, 4, 3, 2),
+    (2731, 36, 6, 4, 2), (2101, 1000, 8, 8, 2), (1025, 40, 16, 1, 1), (129, 8, 8, 1, 1), (4099, 12, 4, 3, 2),
     (40, 96, 2, 48, 5), (20, 512, 64, 16, 2), (70, 64, 64, 64, 64), (18, 256, 3, 64, 9), (12, 320, 4, 64, 1)])
 @pytest.mark.parametrize("score,group_score", [("sigmoid", "top2"), ("softmax", "max"), ("softmax", "top2")])
 def test_scored_routing(T, E, k, n_groups, topk_groups, score, group_score):
