@@ -737,6 +737,13 @@ def _run(fn, where, dev, stream, *args):
         raise MoeError(status, where)
 
 
+def _wait_for_allocations(stream, device):
+    """New tensors come from the current stream's memory, where work enqueued there may not have
+    ended: `stream` (None: the current one) waits for it before it uses them."""
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream(device))
+
+
 class DeviceI8Mat:
     """One set of 8-bit matrices [n_exp, N, K] resident on the device."""
 
@@ -765,6 +772,7 @@ class DeviceI8Mat:
         n_exp, N, K = w.shape
         codes = torch.empty((n_exp, N, K), dtype=I8, device=w.device)
         scales = torch.empty((n_exp, N), dtype=F32, device=w.device)
+        _wait_for_allocations(stream, w.device)
         moe_quant_i8(w.view(n_exp * N, K), codes.view(n_exp * N, K), scales.view(-1), stream)
         m = cls(codes, scales)
         if not (prepack and N % 16 == 0):
@@ -778,6 +786,7 @@ class DeviceI8Mat:
         if self.layout != LAYOUT_ROWS:
             raise ValueError("prepacked: the codes are in tiles already")
         dst = torch.empty_like(self.codes)
+        _wait_for_allocations(stream, dst.device)
         moe_i8_prepack(self.codes, dst, stream)
         return DeviceI8Mat(dst, self.scales, LAYOUT_TILES)
 
@@ -946,7 +955,7 @@ def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, s
                  expert_out: torch.Tensor, shared_out, gemm_ws: torch.Tensor, y: torch.Tensor,
                  stream=None):
     """moe_route (rule None) or moe_route_scored, moe_grouped_gemm_i8 and moe_combine in one
-    call."""
+    call.  For few tokens (one, or T * k <= E / 4) expert_out and shared_out may stay unwritten."""
     shape = T, H = _two_dims(x, "x", "[T, H]")
     d = x.get_device()
     _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, _arg(x, "x", I8, shape, d),
@@ -1163,8 +1172,10 @@ class MoeLayerI8:
     def forward(self, x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor,
                 out: torch.Tensor | None = None, stream=None) -> dict:
         """One moe_layer_i8 call over codes x int8 [T, H] and their scales; returns the buffers
-        used.  They are this object's and the next call's too: calls on several streams at once
-        need an object each."""
+        used (expert_out and shared_out unwritten for few tokens).  They are this object's and the
+        next call's too: calls on several streams at once need an object each, which lives until
+        its calls have ended.  The first call for a T allocates them; its stream then waits for
+        the current one."""
         shape = T, H = _two_dims(x, "x", "[T, H]")
         d = x.get_device()
         b = self.buffers(T)
@@ -1178,6 +1189,7 @@ class MoeLayerI8:
                  _arg(b["expert_out"], "expert_out", BF16, (T * self.k, self.H), d),
                  _shared_out_arg(b["shared_out"], self.I_sh, (T, self.H), d),
                  *_ws_arg(b["gemm_ws"], "gemm_ws", d)], d)
+            _wait_for_allocations(stream, x.device)
         fixed, on = self._fixed[T]
         if d != on or H != self.H:
             raise ValueError(f"x: {tuple(shape)} on {x.device}, the layer is H={self.H} on cuda:{on}")
@@ -1201,6 +1213,7 @@ class MoeLayerI8:
             b["q"] = torch.empty((T, H), dtype=I8, device=d)
             b["q_scale"] = torch.empty(T, dtype=F32, device=d)
             b["logits"] = torch.empty((T, self.E), dtype=F32, device=d)
+            _wait_for_allocations(stream, x.device)
         moe_norm_i8(x, residual, norm_weight, eps, b["sum"], b["normed"], b["q"], b["q_scale"],
                     stream)
         moe_router(b["normed"], w_router, b["logits"], stream=stream)

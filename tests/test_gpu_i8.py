@@ -315,7 +315,7 @@ def check_layer(got, x, sx, idx, w, host, I_sh, what):
 
 
 LAYERS = [  # T, H, I, I_sh, E, k
-    (1, 64, 64, 0, 4, 1), (1, 256, 128, 128, 16, 4), (1, 2048, 512, 512, 16, 8), (1, 128, 1088, 64, 70, 20), (1, 192, 4160, 0, 4, 2), (3, 256, 128, 64, 60, 4), (8, 2048, 512, 512, 256, 8), (2, 192, 64, 320, 8, 3), (7, 256, 192, 64, 16, 2),
+    (1, 64, 64, 0, 4, 1), (1, 256, 128, 128, 16, 4), (1, 2048, 512, 512, 16, 8), (1, 128, 1088, 64, 70, 20), (1, 192, 4160, 0, 4, 2), (1, 64, 4096, 64, 32, 17), (3, 256, 128, 64, 60, 4), (8, 2048, 512, 512, 256, 8), (2, 192, 64, 320, 8, 3), (7, 256, 192, 64, 16, 2),
     (33, 320, 128, 0, 6, 6), (65, 512, 64, 128, 60, 4), (130, 128, 448, 64, 16, 8), (257, 256, 128, 192, 4, 2),
     (40, 64, 1088, 1152, 3, 2), (9, 64, 640, 64, 6, 2), (5, 128, 2112, 576, 6, 2)]
 
@@ -449,6 +449,60 @@ def test_two_streams_with_an_object_each():
     sync()
     for layer, v in zip(layers, want):
         assert torch.equal(layer.buffers(T)["y"], v)
+
+
+def test_new_buffers_wait_for_the_current_stream():
+    """A first call on another stream allocates from the current stream's memory: it must not run
+    before what is enqueued there."""
+    require_gpu()
+    H, I, E, k, T = 256, 128, 16, 2, 50
+    g = np.random.default_rng(5)
+    host = layer_weights(g, E, H, I, 0)
+    mats = [i8mat(q, s, 1) for q, s in host] + [None] * 3
+    x, r, w = norm_inputs(T, H, 4)
+    router = dev(g.normal(size=(E, H)) * H ** -0.5, torch.bfloat16)
+    bf = dev(g.normal(size=(E, I, H)), torch.bfloat16)
+    want = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV).forward_block(x, r, w, router)
+    want_mat = bq.DeviceI8Mat.from_bf16(bf)
+    big = torch.zeros(1 << 28, device=DEV)
+    side = torch.cuda.Stream()
+    sync()
+
+    def behind_work(call):
+        done = torch.cuda.Event()
+        for _ in range(20):
+            big.add_(1.0)   # 2 GiB of traffic each, about 8 ms in all
+        done.record()
+        out = call()
+        side.synchronize()
+        assert done.query()
+        return out
+
+    layer = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV)
+    got = behind_work(lambda: layer.forward_block(x, r, w, router, stream=side))
+    other = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV)
+    y = behind_work(lambda: other.forward(want["q"], want["q_scale"], want["logits"], stream=side))["y"]
+    m = behind_work(lambda: bq.DeviceI8Mat.from_bf16(bf, stream=side))
+    sync()
+    assert torch.equal(got["y"], want["y"]) and torch.equal(y, want["y"])
+    assert torch.equal(m.codes, want_mat.codes) and torch.equal(m.scales, want_mat.scales)
+
+
+@pytest.mark.parametrize("T", [1, 3, 100])
+def test_matrices_of_both_layouts_in_one_call(T):
+    """Only gate and up (and the shared two) need the same layout; every mix gives the same bits."""
+    require_gpu()
+    H, I, I_sh, E, k = 256, 128, 192, 64, 4
+    g = np.random.default_rng(T)
+    host = layer_weights(g, E, H, I, I_sh)
+    x, sx = dev(codes(g, T, H), torch.int8), dev(g.random(T), torch.float32) * 0.02
+    lg = dev(g.normal(size=(T, E)), torch.float32)
+    ys = []
+    for pair, down, sh_pair, sh_down in ((1, 1, 1, 1), (1, 0, 0, 1), (0, 1, 1, 0)):
+        mats = [i8mat(q, s, v) for (q, s), v in zip(host, (pair, pair, down, sh_pair, sh_pair, sh_down))]
+        ys.append(bq.MoeLayerI8(mats, H, I, I_sh, E, k, DEV).forward(x, sx, lg)["y"].clone())
+    sync()
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
 
 
 # ---- sizes at which offsets pass 31 and 32 bits, and variants chosen by size ----
