@@ -505,6 +505,30 @@ def test_matrices_of_both_layouts_in_one_call(T):
     assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
 
 
+@pytest.mark.parametrize("M", [3, 200])
+def test_scales_need_four_bytes_alignment_only(M):
+    require_gpu()
+    N, K, E = 64, 128, 3
+    g = np.random.default_rng(M)
+    wq, ws = dev(codes(g, E, N, K), torch.int8), dev(g.random((E, N)) * 0.01, torch.float32)
+    odd = torch.empty(E * N + 1, device=DEV)[1:].view(E, N)
+    odd.copy_(ws)
+    x, sx = dev(codes(g, M, K), torch.int8), dev(g.random(M), torch.float32)
+    odd_sx = torch.empty(M + 1, device=DEV)[1:]
+    odd_sx.copy_(sx)
+    outs = [torch.empty((M, N), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    bq.moe_linear_i8(x, sx, bq.DeviceI8Mat(wq[:1], ws[:1]), outs[0])
+    bq.moe_linear_i8(x, odd_sx, bq.DeviceI8Mat(wq[:1], odd[:1]), outs[1])
+    down = dev(codes(g, E, K, N), torch.int8), dev(g.random((E, K)) * 0.01, torch.float32)
+    lg, ys = dev(g.normal(size=(M, E)), torch.float32), []
+    for s, rs in ((ws, sx), (odd, odd_sx)):
+        m = bq.DeviceI8Mat(wq, s)
+        layer = bq.MoeLayerI8([m, m, bq.DeviceI8Mat(*down)] + [None] * 3, K, N, 0, E, 2, DEV)
+        ys.append(layer.forward(x, rs, lg)["y"])
+    sync()
+    assert torch.equal(*outs) and torch.equal(*ys)
+
+
 # ---- sizes at which offsets pass 31 and 32 bits, and variants chosen by size ----
 
 @pytest.mark.parametrize("with_residual", [True, False])
