@@ -920,7 +920,7 @@ static int check_rule(const moe_score_rule* rule, int E, int k, ScoreRule* dev) 
         return MOE_ERR_SHAPE;
     if (G > 1 && rule->group_score == MOE_GROUP_TOP2 && E / G < 2) return MOE_ERR_SHAPE;
     if (k > kScoredMaxK || k > rule->topk_groups * (E / G)) return MOE_ERR_SHAPE;
-    *dev = ScoreRule{rule->score, G, rule->topk_groups, rule->group_score, rule->renormalise,
+    *dev = ScoreRule{rule->score, G, rule->topk_groups, E / G, rule->group_score, rule->renormalise,
                      rule->scale};
     return MOE_OK;
 }

@@ -28,7 +28,7 @@ constexpr int kScoredMaxGroups = 64;   // one group per lane
 // Selection rule of the scored routing (moe_score_rule with its checks done).
 struct ScoreRule {
     int sigmoid;       // 0: softmax
-    int n_groups, topk_groups;
+    int n_groups, topk_groups, group_size;
     int top2;          // a group's worth: its two best choices' sum, else its best choice
     int renormalise;
     float scale;

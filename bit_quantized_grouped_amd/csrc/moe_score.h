@@ -10,8 +10,9 @@
 //
 // A selection hangs on the last bit of a score, so a score is formed in 64 bits
 // and rounded once: it is then the nearest fp32 value whatever the order of the
-// sum, but for sums within 1e-16 of a rounding border.  A NaN logit or choice
-// counts as -inf; a row of -inf alone has scores 0 and takes the lowest indices.
+// sum, but for values within 1e-15 of themselves of a rounding border.  A NaN logit
+// or choice counts as -inf; a row of -inf alone has scores 0 and takes the lowest
+// indices.
 #pragma once
 
 #include "moe_i8.h"
@@ -55,12 +56,18 @@ __device__ __forceinline__ double recip_f64(double d) {
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
+// a / b for 0 <= a < 2^16, 1 <= b < 2^16 without an integer division's thirty instructions:
+// (a + 1/2) / b is at least 1 / 2b from a whole number, the rounding far nearer.
+__device__ __forceinline__ int small_div(int a, int b) {
+    return (int)(((float)a + 0.5f) * __builtin_amdgcn_rcpf((float)b));
+}
+
 // Lane l holds experts l*EPL .. l*EPL+EPL-1; absent and dropped experts get key 0.
 template <int EPL>
 __device__ __forceinline__ void drop_groups(uint32_t (&key)[EPL], int E, const ScoreRule& rule) {
     const int lane = __lane_id();
-    const int gs = E / rule.n_groups, span = gs / EPL;
-    if (gs % EPL == 0) {
+    const int gs = rule.group_size, span = (int)((unsigned)gs / EPL);
+    if ((unsigned)gs % EPL == 0) {
         // whole groups in `span` neighbouring lanes: every lane gathers its group's two best,
         // by a butterfly where span is a power of two and lane by lane otherwise
         uint32_t m1 = 0, m2 = 0;
@@ -69,7 +76,7 @@ __device__ __forceinline__ void drop_groups(uint32_t (&key)[EPL], int E, const S
             m2 = max(m2, min(m1, key[j]));
             m1 = max(m1, key[j]);
         }
-        const int mine = lane / span;
+        const int mine = small_div(lane, span);
         if ((span & (span - 1)) == 0) {
             for (int off = 1; off < span; off <<= 1) {
                 const uint32_t o1 = shfl_xor(m1, off), o2 = shfl_xor(m2, off);
@@ -87,11 +94,11 @@ __device__ __forceinline__ void drop_groups(uint32_t (&key)[EPL], int E, const S
             }
         }
         uint32_t worth = rule.top2 ? choice_key(key_float(m1) + key_float(m2)) : m1;
-        if (lane >= E / EPL) worth = 0;
+        if (lane * EPL >= E) worth = 0;
         bool keep = false;
         for (int r = 0; r < rule.topk_groups; ++r) {
             const uint32_t m = wave_max_u32(worth);
-            const int g = __builtin_ctzll(__ballot(worth == m)) / span;
+            const int g = __builtin_amdgcn_readlane(mine, __builtin_ctzll(__ballot(worth == m)));
             if (mine == g) {
                 keep = true;
                 worth = 0;
@@ -133,7 +140,7 @@ __device__ __forceinline__ void drop_groups(uint32_t (&key)[EPL], int E, const S
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane * EPL + j;
-        const int g = e < E ? e / gs : 0;
+        const int g = e < E ? small_div(e, gs) : 0;
         key[j] = (kept >> g) & 1 ? key[j] : 0u;
     }
 }
