@@ -146,6 +146,17 @@ def test_dequant_takes_every_code():
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("R,K", [(1, 64), (3, 1024), (7, 1088), (2047, 2112), (2048, 1088), (2050, 2048), (2500, 64)])
+def test_dequant_in_parts_and_by_rows(R, K):
+    require_gpu()
+    g = np.random.default_rng(R + K)
+    q, s = dev(codes(g, R, K), torch.int8), dev(g.normal(size=R), torch.float32)
+    out = torch.full((R + 1, K), float("nan"), dtype=torch.bfloat16, device=DEV)
+    bq.moe_dequant_i8_bf16(q, s, out[:R])
+    sync()
+    assert torch.equal(out[:R], (q.float() * s[:, None]).bfloat16()) and out[R].isnan().all()
+
+
 # ---- scored routing ----
 
 def scored(lg, bias, k, br=32, **rule):
@@ -568,6 +579,17 @@ def test_rows_past_32_bit_offsets():
     sync()
     assert float(s[-1]) == 1.0 and torch.equal(q[-1].float(), x[-1].float()) and torch.equal(out[-1], x[-1])
     assert not q[-2].any() and float(s[0]) == 0 and not out[R // 2].any()
+
+
+def test_dequant_of_the_widest_row():
+    require_gpu()
+    K = (1 << 31) - 64
+    q = torch.full((1, K), 3, dtype=torch.int8, device=DEV)
+    q[0, -1] = -7
+    out = torch.zeros((1, K), dtype=torch.bfloat16, device=DEV)
+    bq.moe_dequant_i8_bf16(q, torch.full((1,), 0.5, device=DEV), out)
+    sync()
+    assert float(out[0, -1]) == -3.5 and bool((out[0, :-1] == 1.5).all())
 
 
 def test_linear_of_outputs_past_31_bits():
