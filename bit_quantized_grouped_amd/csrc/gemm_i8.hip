@@ -101,6 +101,101 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
     }
 }
 
+// ---- Dense product of some ten to some hundred rows: a workgroup per 16 MF x 16 NF tile, K
+// split over its 8 waves as above, so every byte of a tile's rows goes once from the caches to
+// registers, without LDS or barriers until the waves' sums meet.  A wave takes 128 K at a
+// time, D of them ahead: the two halves of an activation row's cache line are requested one
+// after the other, while the line is in L1 (64 K at a time and deeper 128x2048x7168 took
+// 11.6 us, this 10.5; with contiguous rows it would take 7.8).  Bound by those half lines.
+template <int MF, int NF, int D>
+__global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
+    const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
+    uint16_t* __restrict__ out, int n_tiles) {
+    constexpr int W = kFewWaves, P = MF * NF, ROUND = P < W ? P : W;   // pieces of 16 x 16, and those joined at a time
+    static_assert(P % ROUND == 0, "whole rounds");
+    constexpr uint32_t kPast = 0xC0000000u;   // past every buffer (both are below 2^31 bytes)
+    __shared__ i32x4_t s_part[W][ROUND][WAVE];
+    const int lane = threadIdx.x % WAVE, fr = lane % 16, fp = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int m0 = (int)(blockIdx.x / n_tiles) * MF * 16, n0 = (int)(blockIdx.x % n_tiles) * NF * 16;
+    const buf_rsrc_t ra = make_buf(a, (uint32_t)M * (uint32_t)K);
+    const buf_rsrc_t rw = make_buf(w.codes, (uint32_t)N * (uint32_t)K);
+    const uint32_t w_step = w.tiles ? 1024u : 64u;
+    uint32_t oa[MF], ow[NF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const uint32_t r = m0 + m * 16 + fr;
+        oa[m] = r < (uint32_t)M ? r * (uint32_t)K + fp * 16 : kPast;
+    }
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+        const uint32_t c = n0 + n * 16;
+        ow[n] = w.tiles ? (c < (uint32_t)N ? c * (uint32_t)K + lane * 16 : kPast)
+                        : (c + fr < (uint32_t)N ? (c + fr) * (uint32_t)K + fp * 16 : kPast);
+    }
+    const int steps = K / 64, pairs = (steps + 1) / 2, s0 = pairs * wave / W, s1 = pairs * (wave + 1) / W;
+    i32x4_t va[D][2][MF], vw[D][2][NF];
+    auto load = [&](int slot, int s) {
+        const uint32_t past0 = s < s1 ? 0u : kPast, past1 = s < s1 && 2 * s + 1 < steps ? 0u : kPast;
+#pragma unroll
+        for (int n = 0; n < NF; ++n) {
+            vw[slot][0][n] = __builtin_bit_cast(i32x4_t, buf_load16_u(rw, ow[n] | past0, (uint32_t)(2 * s) * w_step));
+            vw[slot][1][n] = __builtin_bit_cast(i32x4_t, buf_load16_u(rw, ow[n] | past1, (uint32_t)(2 * s + 1) * w_step));
+        }
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            va[slot][0][m] = __builtin_bit_cast(i32x4_t, buf_load16_u(ra, oa[m] | past0, (uint32_t)s * 128u));
+            va[slot][1][m] = __builtin_bit_cast(i32x4_t, buf_load16_u(ra, oa[m] | past1, (uint32_t)s * 128u + 64u));
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, s0 + d);
+    i32x4_t acc[NF][MF];
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
+    for (int s = s0; s < s1; s += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) acc[n][m] = mfma_i8(vw[d][q][n], va[d][q][m], acc[n][m]);
+            load(d, s + d + D);
+        }
+    }
+#pragma unroll
+    for (int p0 = 0; p0 < P; p0 += ROUND) {
+        if (p0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ROUND; ++i) s_part[wave][i][lane] = acc[(p0 + i) / MF][(p0 + i) % MF];
+        __syncthreads();
+        if (wave < ROUND) {
+            i32x4_t sum = s_part[0][wave][lane];
+#pragma unroll
+            for (int i = 1; i < W; ++i) sum += s_part[i][wave][lane];
+            const int p = p0 + wave, r = m0 + p % MF * 16 + fr, c = n0 + p / MF * 16 + fp * 4;
+            if (r < M && c < N) {
+                const float as = a_scale[r];
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * as * w.scales[min(c + i, N - 1)];
+                uint16_t* o = out + (size_t)r * N + c;
+                if (N % 4 == 0) {
+                    *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < N) o[i] = (uint16_t)pack_bf16x2(v[i], 0.f);
+                }
+            }
+        }
+    }
+}
+
 // ---- Dense product of many rows: tiles through LDS ----
 // A workgroup of WM x WN waves owns a BM x BN tile; a wave WM-th of its rows and
 // WN-th of its columns, MF x NF products of 16 x 16.  KS blocks of 64 K of both
@@ -627,9 +722,13 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
             a, a_scale, M, K, w, N, out, mt, nt);                                             \
     }
     // The smallest tile that still makes no more than one round of the CUs (the larger ones
-    // read less but leave CUs idle; us measured, small against next larger):
-    //   16 x 16, K over 8 waves, up to two rounds: 17x4096x4096 6.7 / 10.7, 200x512x2048
-    //     5.1 / 6.6, but 64x4096x4096 (1024 tiles) 12.5 / 10.8;
+    // read less but leave CUs idle; us measured, small against next larger).  K over 8 waves:
+    //   16 x 16: 17x2048x7168 6.5 / 7.6, but two rounds 32x4096x4096 7.3 / 5.8;
+    //   16 x 32: 64x2048x7168 7.8 / 10.5;  32 x 32: 128x2048x7168 10.5 / 12.5, 64x4096x4096
+    //     7.5 / 8.8;  32 x 64: 256x2048x7168 12.7 / 16.9, 128x4096x4096 8.9 / 11.0, 512 rows
+    //     by 64 x 64 no faster than through LDS.  Weights in rows come as half lines too:
+    //     256x1001x4096 10.0 by 32 x 32 against 9.0 through LDS.
+    // K by one workgroup, through LDS:
     //   32 x 64: 333x1001x2048 6.2 / 8.4;  64 x 64: 128x8192x7168 19.4 / 27;
     //   128 x 64: 333x4096x4096 17.2 / 24, 1000x2048x2048 11.2 / 15;
     // beyond that 128 x 128 (two on a CU) or 256 x 256, whichever takes fewer rounds:
@@ -637,13 +736,20 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     auto tiles = [&](int bm, int bn) { return (long long)cdiv(M, bm) * cdiv(N, bn); };
     const long long r128 = (tiles(128, 128) + 2 * kCUs - 1) / (2 * kCUs);
     const long long r256 = (tiles(256, 256) + kCUs - 1) / kCUs;
-    if (M <= 16 || tiles(16, 16) <= 2 * kCUs)
+#define MOE_SPLIT(MF, NF, D)                                                                  \
+    linear_split_kernel<MF, NF, D><<<(unsigned)tiles(MF * 16, NF * 16), kFewWaves * WAVE, 0, stream>>>( \
+        a, a_scale, M, K, w, N, out, cdiv(N, NF * 16))
+    if (M <= 16 || tiles(16, 16) <= kCUs)
         linear_few_kernel<<<(unsigned)tiles(16, 16), kFewWaves * WAVE, 0, stream>>>(a, a_scale, M, K, w, N, out);
+    else if (tiles(16, 32) <= kCUs) MOE_SPLIT(1, 2, 2);
+    else if (w.tiles && tiles(32, 32) <= kCUs) MOE_SPLIT(2, 2, 1);
+    else if (w.tiles && tiles(32, 64) <= kCUs) MOE_SPLIT(2, 4, 1);
     else if (tiles(32, 64) <= kCUs) MOE_TILES(1, 2, 2, 2, 8, 1)
     else if (tiles(64, 64) <= kCUs) MOE_TILES(2, 2, 2, 2, 4, 2)
     else if (tiles(128, 64) <= kCUs) MOE_TILES(2, 4, 2, 2, 4, 2)
     else if (r128 <= r256) MOE_TILES(2, 4, 2, 4, 4, 2)
     else MOE_TILES(2, 8, 4, 4, 4, 1)
+#undef MOE_SPLIT
 #undef MOE_TILES
     return hipGetLastError();
 }

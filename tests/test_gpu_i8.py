@@ -257,6 +257,9 @@ def test_prepack_order():
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 64), (1, 16, 64), (1, 4096, 2048), (2, 33, 128), (15, 100, 192), (16, 16, 512), (17, 16, 512),
     (33, 65, 320), (64, 128, 256), (65, 129, 64), (100, 250, 448), (128, 256, 128), (129, 272, 576),
+    # K split over the waves of a workgroup: 16 x 32, 32 x 32 and 32 x 64
+    (33, 1411, 320), (50, 1440, 192), (20, 4096, 64), (45, 4064, 192), (64, 4096, 64), (64, 4080, 1088), (100, 4000, 576),
+    (128, 4096, 2048), (97, 4048, 64), (250, 2000, 1088),
     # each tile of the many-row kernel, with ragged edges, N in and out of eights, K of one block,
     # of an odd number and of many; the last three take several tiles a workgroup
     (300, 1500, 192), (333, 1001, 64), (700, 1000, 320), (650, 999, 1088), (1100, 1411, 320),
