@@ -202,11 +202,12 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
 // operands (one stage) go straight from memory into LDS, ST - 1 stages ahead of the
 // one that is multiplied: a stage of the 256 x 256 tile is 1024 cycles of products,
 // and a load takes two to four times that under full traffic.  Stages past K are
-// zeros and multiplied like the others.  A block keeps rows of 64 bytes whose four
-// 16-byte pieces are permuted: place j of row r holds piece j ^ (r / 2 % 4), chosen on
-// the source side (a load writes LDS in lane order), so that 8 neighbouring rows of a
-// fragment read, 128 bytes, lie in different banks (with r / 4 half of the LDS cycles
-// were conflicts).  A workgroup requests its next tile's first stages during the last
+// zeros and multiplied like the others.  A stage keeps rows of 64 KS bytes, so that with
+// KS 2 a load takes whole cache lines of 8 rows (half lines of 16 took 4 to 10 % longer
+// from K 4096 on), and their 16-byte pieces permuted: place j of row r holds piece
+// j ^ (r / 2 % (4 KS)), chosen on the source side (a load writes LDS in lane order), so
+// that neighbouring rows of a fragment read lie in different banks (with r / 4 half of
+// the LDS cycles were conflicts).  A workgroup requests its next tile's first stages during the last
 // products of a tile.  8192 x 4096 x 4096 takes 117 us (2350 TOP/s), MFMA 56 % busy at
 // 2.0 GHz; with codes of zero, at a higher clock, 92.
 // Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
@@ -260,45 +261,56 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 
     const buf_rsrc_t ra = make_buf(a, (uint32_t)M * (uint32_t)K);
     const buf_rsrc_t rb = make_buf(w.codes, (uint32_t)N * (uint32_t)K);
-    const int lr = lane / 4, piece = (lane % 4) ^ (lr / 2 % 4);   // row and K piece of this lane's place
-    uint32_t va[LA], vb[LB];
+    // row and K piece of this lane's place in a load; the second load of 128 K holds rows 8 .. 15
+    const int lr = lane / (4 * KS), piece = (lane % (4 * KS)) ^ (lr / 2 % 4);
+    uint32_t va[LA][KS], vb[LB][KS];
     auto sources = [&](int m0, int n0) {
 #pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            const uint32_t r = m0 + (i * WAVES + wave) * 16 + lr;
-            va[i] = r < (uint32_t)M ? r * (uint32_t)K + piece * 16 : kPast;
-        }
+        for (int i = 0; i < LA; ++i)
 #pragma unroll
-        for (int i = 0; i < LB; ++i) {
-            const uint32_t r = n0 + (i * WAVES + wave) * 16 + lr;
-            vb[i] = r >= (uint32_t)N ? kPast
-                    : w.tiles        ? (r - lr) * (uint32_t)K + piece * 256 + lr * 16
-                                     : r * (uint32_t)K + piece * 16;
-        }
+            for (int j = 0; j < KS; ++j) {
+                const uint32_t r = m0 + (i * WAVES + wave) * 16 + lr + j * 8;
+                va[i][j] = r < (uint32_t)M ? r * (uint32_t)K + (piece ^ j * 4) * 16 : kPast;
+            }
+#pragma unroll
+        for (int i = 0; i < LB; ++i)
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                const uint32_t r = n0 + (i * WAVES + wave) * 16 + lr + j * 8, p = piece ^ j * 4;
+                vb[i][j] = r >= (uint32_t)N ? kPast
+                           : w.tiles ? (r - r % 16) * (uint32_t)K + p / 4 * 1024 + p % 4 * 256 + r % 16 * 16
+                                     : r * (uint32_t)K + p * 16;
+            }
     };
     const int blocks = K / 64, steps = (blocks + KS - 1) / KS;
-    const uint32_t b_step = w.tiles ? 1024 : 64;
-    auto load = [&](int st, int s) {
+    const uint32_t b_step = (w.tiles ? 1024 : 64) * KS;
+    // K behind the last block is zeros: the second half of 128, or all
+    uint32_t half[KS];
 #pragma unroll
-        for (int q = 0; q < KS; ++q) {
-            const uint32_t k = (uint32_t)(s * KS + q);
-            const uint32_t past = k < (uint32_t)blocks ? 0u : kPast;   // blocks behind the last are zeros
+    for (int j = 0; j < KS; ++j) half[j] = KS == 2 && (piece ^ j * 4) >= 4 ? kPast : 0u;
+    auto load = [&](int st, int s) {
+        const bool in = s * KS < blocks, whole = s * KS + KS <= blocks;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            const uint32_t past = whole ? 0u : in ? half[j] : kPast;
 #pragma unroll
             for (int i = 0; i < LA; ++i)
-                buf_to_lds16(ra, s_a(st) + q * BM * 64 + (i * WAVES + wave) * 1024, va[i] | past, k * 64u);
+                buf_to_lds16(ra, s_a(st) + ((i * WAVES + wave) * KS + j) * 1024, va[i][j] | past,
+                             (uint32_t)s * (64u * KS));
 #pragma unroll
             for (int i = 0; i < LB; ++i)
-                buf_to_lds16(rb, s_b(st) + q * BN * 64 + (i * WAVES + wave) * 1024, vb[i] | past, k * b_step);
+                buf_to_lds16(rb, s_b(st) + ((i * WAVES + wave) * KS + j) * 1024, vb[i][j] | past,
+                             (uint32_t)s * b_step);
         }
     };
     i32x4_t acc[NF][MF];
     const int fr = lane % 16, fp = lane / 16;
-    const int at = fr * 64 + (fp ^ (fr / 2 % 4)) * 16;
+    const int at = fr * 64 * KS + (fp ^ (fr / 2 % (4 * KS))) * 16;
     auto read_b = [&](int st, int q, int n) {
-        return *(const i32x4_t*)(s_b(st) + q * BN * 64 + (wn * NF + n) * 1024 + at);
+        return *(const i32x4_t*)(s_b(st) + (wn * NF + n) * 1024 * KS + (at ^ q * 64));
     };
     auto read_a = [&](int st, int q, int m) {
-        return *(const i32x4_t*)(s_a(st) + q * BM * 64 + (wm * MF + m) * 1024 + at);
+        return *(const i32x4_t*)(s_a(st) + (wm * MF + m) * 1024 * KS + (at ^ q * 64));
     };
     // While it multiplies a block a wave reads, in the order below, the row fragments it
     // lacks and the next block's columns and first FA row fragments, so that the products
@@ -731,7 +743,7 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     // K by one workgroup, through LDS:
     //   32 x 64: 333x1001x2048 6.2 / 8.4;  64 x 64: 128x8192x7168 19.4 / 27;
     //   128 x 64: 333x4096x4096 17.2 / 24, 1000x2048x2048 11.2 / 15;
-    // beyond that 128 x 128 (two on a CU) or 256 x 256, whichever takes fewer rounds:
+    // beyond that 128 x 128 or 256 x 256, whichever takes fewer rounds:
     //   2048x4096x4096 44 / 48 (one each), 8192x4096x4096 117 by 256 x 256.
     auto tiles = [&](int bm, int bn) { return (long long)cdiv(M, bm) * cdiv(N, bn); };
     const long long r128 = (tiles(128, 128) + 2 * kCUs - 1) / (2 * kCUs);
