@@ -207,9 +207,10 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
 // from K 4096 on), and their 16-byte pieces permuted: place j of row r holds piece
 // j ^ (r / 2 % (4 KS)), chosen on the source side (a load writes LDS in lane order), so
 // that neighbouring rows of a fragment read lie in different banks (with r / 4 half of
-// the LDS cycles were conflicts).  A workgroup requests its next tile's first stages during the last
-// products of a tile.  8192 x 4096 x 4096 takes 117 us (2350 TOP/s), MFMA 56 % busy at
-// 2.0 GHz; with codes of zero, at a higher clock, 92.
+// the LDS cycles were conflicts).  A workgroup requests its next tile's first stages
+// during the last products of a tile.  8192 x 4096 x 4096 takes 117 us (2350 TOP/s), MFMA
+// 56 % busy at 2.0 GHz; with codes of zero, at a higher clock, 92.  Where a CU has one tile
+// or few it is bound by what L2 gives a CU, 40 to 48 bytes a ns in every form here.
 // Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
 // which the build checks.
 template <int WM, int MF, int WN, int NF, int ST, int KS>
@@ -743,11 +744,13 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     // K by one workgroup, through LDS:
     //   32 x 64: 333x1001x2048 6.2 / 8.4;  64 x 64: 128x8192x7168 19.4 / 27;
     //   128 x 64: 333x4096x4096 17.2 / 24, 1000x2048x2048 11.2 / 15;
-    // beyond that 128 x 128 or 256 x 256, whichever takes fewer rounds:
-    //   2048x4096x4096 44 / 48 (one each), 8192x4096x4096 117 by 256 x 256.
+    // beyond that 128 x 128, 256 x 128 or 256 x 256, by rounds that take 2, 3 and 5 (K 2048:
+    //   14.7, 20 to 25 and 37 us), the larger where they are even:
+    //   1024x4096x2048 14.7 / 18.0 / 27, 2048x4096x4096 45.9 / 38.2 / 47.7,
+    //   4096x2048x7168 75.7 / 63.0 / 75.9, 4096x4096x2048 53.3 / 43.8 / 37.3.
     auto tiles = [&](int bm, int bn) { return (long long)cdiv(M, bm) * cdiv(N, bn); };
-    const long long r128 = (tiles(128, 128) + 2 * kCUs - 1) / (2 * kCUs);
-    const long long r256 = (tiles(256, 256) + kCUs - 1) / kCUs;
+    auto rounds = [&](int bm, int bn) { return (tiles(bm, bn) + kCUs - 1) / kCUs; };
+    const long long c128 = 2 * rounds(128, 128), c192 = 3 * rounds(256, 128), c256 = 5 * rounds(256, 256);
 #define MOE_SPLIT(MF, NF, D)                                                                  \
     linear_split_kernel<MF, NF, D><<<(unsigned)tiles(MF * 16, NF * 16), kFewWaves * WAVE, 0, stream>>>( \
         a, a_scale, M, K, w, N, out, cdiv(N, NF * 16))
@@ -759,8 +762,9 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     else if (tiles(32, 64) <= kCUs) MOE_TILES(1, 2, 2, 2, 8, 1)
     else if (tiles(64, 64) <= kCUs) MOE_TILES(2, 2, 2, 2, 4, 2)
     else if (tiles(128, 64) <= kCUs) MOE_TILES(2, 4, 2, 2, 4, 2)
-    else if (r128 <= r256) MOE_TILES(2, 4, 2, 4, 4, 2)
-    else MOE_TILES(2, 8, 4, 4, 4, 1)
+    else if (c256 <= c192 && c256 <= c128) MOE_TILES(2, 8, 4, 4, 4, 1)
+    else if (c192 <= c128) MOE_TILES(2, 8, 4, 2, 4, 1)
+    else MOE_TILES(2, 4, 4, 2, 4, 2)
 #undef MOE_SPLIT
 #undef MOE_TILES
     return hipGetLastError();

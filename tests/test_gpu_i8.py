@@ -264,7 +264,7 @@ def test_prepack_order():
     # of an odd number and of many; the last three take several tiles a workgroup
     (300, 1500, 192), (333, 1001, 64), (700, 1000, 320), (650, 999, 1088), (1100, 1411, 320),
     (1030, 1480, 64), (1500, 1411, 320), (1536, 1408, 576), (3500, 3841, 192), (3585, 3600, 64),
-    (4400, 4360, 128), (4400, 4365, 64), (70000, 100, 64), (255, 1001, 192), (256, 256, 1024), (300, 528, 704), (513, 768, 320), (1, 100, 8192), (40, 48, 16384)])
+    (2000, 4000, 1088), (2200, 4090, 320), (8000, 4360, 64), (4400, 4360, 128), (4400, 4365, 64), (70000, 100, 64), (255, 1001, 192), (256, 256, 1024), (300, 528, 704), (513, 768, 320), (1, 100, 8192), (40, 48, 16384)])
 @pytest.mark.parametrize("layout", [0, 1])
 def test_linear(M, N, K, layout):
     require_gpu()
