@@ -955,7 +955,7 @@ def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, s
                  expert_out: torch.Tensor, shared_out, gemm_ws: torch.Tensor, y: torch.Tensor,
                  stream=None):
     """moe_route (rule None) or moe_route_scored, moe_grouped_gemm_i8 and moe_combine in one
-    call.  For few tokens (one, or T * k <= E / 4) expert_out and shared_out may stay unwritten."""
+    call.  For at most 64 tokens expert_out and shared_out may stay unwritten."""
     shape = T, H = _two_dims(x, "x", "[T, H]")
     d = x.get_device()
     _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, _arg(x, "x", I8, shape, d),
@@ -1172,10 +1172,10 @@ class MoeLayerI8:
     def forward(self, x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor,
                 out: torch.Tensor | None = None, stream=None) -> dict:
         """One moe_layer_i8 call over codes x int8 [T, H] and their scales; returns the buffers
-        used (expert_out and shared_out unwritten for few tokens).  They are this object's and the
-        next call's too: calls on several streams at once need an object each, which lives until
-        its calls have ended.  The first call for a T allocates them; its stream then waits for
-        the current one."""
+        used (expert_out and shared_out may be unwritten up to 64 tokens).  They are this
+        object's and the next call's too: calls on several streams at once need an object each,
+        which lives until its calls have ended.  The first call for a T allocates them; its
+        stream then waits for the current one."""
         shape = T, H = _two_dims(x, "x", "[T, H]")
         d = x.get_device()
         b = self.buffers(T)

@@ -14,8 +14,8 @@
 //
 // Bound by bytes and by the chain of waits: the selection must end before a weight
 // address is known, and down starts after all of gate/up.  Tokens that share an expert
-// read it once each, so this form is for few tokens among many experts; it has two
-// launches less than the grouped one and no expert_out.
+// read it once each, so this form is for few tokens, of many or of small experts; it has
+// two launches less than the grouped one and no expert_out.
 #include "moe_device.h"
 #include "moe_i8.h"
 #include "moe_score.h"
@@ -227,11 +227,23 @@ __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(Decod
 // LDS of the down kernel: a wave's codes.  Wider layers take the grouped path.
 constexpr int kDecodeI8MaxInter = 4096;
 
+// More than one token: as long as reading again what tokens share, experts chosen by several
+// (by chance: the tokens choose alike) and the shared expert, costs less than the grouped
+// path's two launches more and its start.  That is some 40 MB, 8 us (us by this path and by
+// the grouped one): E 256, k 8, H 2048, I 512, with a shared expert, 6 tokens (27 MB) 40.5 and
+// 42.5, 8 (43 MB) 50.3 and 48.0; E 128, k 6, H 1024, I 448, 12 (30 MB) 29.7 and 30.7, 16 (50 MB)
+// 35.1 and 33.8; E 16, k 2, H 1024, I 256, 8 (4 MB) 11.7 and 19.3, 32 (38 MB) 16.6 and 20.3.
+constexpr int kDecodeI8MaxTokens = 64;
+constexpr double kDecodeI8Again = 40e6;
+
 bool decode_i8_fits(const GemmI8Problem& p) {
-    // more than one token: as long as few of their experts are the same (at most a quarter of
-    // all chosen: 8 tokens of 8 of 256 read 12 % twice)
-    if (p.T > 1 && (p.T > 64 || 4 * p.T * p.k > p.E)) return false;
-    return p.k <= kScoredMaxK && p.I <= kDecodeI8MaxInter && p.I_sh <= kDecodeI8MaxInter;
+    if (p.k > kScoredMaxK || p.I > kDecodeI8MaxInter || p.I_sh > kDecodeI8MaxInter) return false;
+    if (p.T == 1) return true;
+    if (p.T > kDecodeI8MaxTokens) return false;
+    double missed = 1.0;   // the share of experts that no token chooses
+    for (int t = 0; t < p.T; ++t) missed *= 1.0 - (double)p.k / p.E;
+    const double again = (double)p.T * p.k - p.E * (1.0 - missed);
+    return 3.0 * p.H * (again * p.I + (p.T - 1.0) * p.I_sh) <= kDecodeI8Again;
 }
 
 hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const float* bias,

@@ -551,8 +551,8 @@ int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int
 /* One whole layer call over 8-bit activations and weights: moe_route (rule
  * NULL, score_bias NULL) or moe_route_scored, moe_grouped_gemm_i8 and
  * moe_combine in order on `stream`, with those calls' arguments and results.
- * A call for few tokens (one, or T*k <= E/4) may leave expert_out and shared_out
- * unwritten: it sums a token's experts without them. */
+ * A call for at most 64 tokens may leave expert_out and shared_out unwritten: it sums
+ * a token's experts without them. */
 int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
                  const float* score_bias, const moe_score_rule* rule, int T, int H, int I, int I_sh,
                  int E, int k, int block_rows, const moe_i8_mat* gate, const moe_i8_mat* up,
