@@ -542,8 +542,8 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int block_rows
 }
 
 // ---------------------------------------------------------------------------
-// Scored routing (moe_score.h): one launch for few tokens, segments (below), or
-// one wave per token in front of the one-workgroup grouping.
+// Scored routing (moe_score.h): one launch for few tokens, else one for the selection
+// and one for the grouping (below).
 // ---------------------------------------------------------------------------
 
 template <int EPL>
@@ -586,20 +586,21 @@ __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
     write_one_token(r, E, k, max_blocks, s_idx, s_w, threadIdx.x, kOneThreads);
 }
 
-// Segments: above the one-launch size the tokens are cut into segments of 8 or
-// 16, one token per wave of a workgroup that selects their experts and counts
-// them, one byte per expert (a token takes an expert once, so a count is at most
-// 16).  A workgroup of the scatter kernel takes up to 1024 assignments of whole
-// segments: it sums the segments' counts (those before its own, and all of them), scans the
-// experts' totals, and places its assignments: wave w owns their 64-assignment
-// chunk w, so rows follow assignment order and the sort is stable.  Every
-// workgroup repeats the scan, which costs less than a third launch: n_seg * E
-// bytes from L2.  The counts of segments of 16 fit the T * k words of moe_route's
-// workspace for any E <= 64 k.  Bound by instructions in the selection (about 1000 a
-// token) and by the chain of waits in the scatter: 2048 tokens x 8 of 256 take 6.7 + 7.0
-// us, 8192 x 6 of 160 13 + 8 (one grouping workgroup: 87 for the latter's scatter).
+// Above the one-launch size a wave per token selects, and a second launch groups, by
+// workgroups of 1024 assignments: each needs the experts' counts over all assignments
+// and over those before its own.  Up to kScoredCountAssign assignments it takes them from
+// the chosen experts themselves, into LDS: a read of all indices per workgroup.  Above,
+// the tokens are cut into segments of 8 or 16, a workgroup of the selection each, which
+// leaves its segment's counts, one byte per expert (a token takes an expert once, so a
+// count is at most 16), and a grouping workgroup takes whole segments and sums their
+// counts.  Then it scans the experts' totals and places its assignments: wave w owns
+// their 64-assignment chunk w, so rows follow assignment order and the sort is stable.
+// Every workgroup repeats the scan, which costs less than a third launch.  Bound by
+// instructions in the selection (about 650 a token) and by the chain of waits in the
+// grouping: 2048 tokens x 8 of 256 take 5.3 + 6.3 us (by segments 6.6 + 6.9), 8192 x 6 of
+// 160 12 + 8 (one grouping workgroup: 87 for the latter's grouping).
 constexpr int kSegTokens = kGroupWaves;                // most tokens of a segment
-constexpr int kSegMaxK = kGroupThreads / kSegTokens;   // a segment fits a scatter workgroup
+static_assert(kScoredMaxK * kSegTokens <= kGroupThreads, "a segment fits a grouping workgroup");
 
 __host__ __device__ constexpr int seg_words(int E) { return (E + 3) / 4; }   // of one segment's counts
 
@@ -629,6 +630,7 @@ __global__ __launch_bounds__(kGroupThreads) void route_scored_seg_kernel(
         seg_counts[(size_t)blockIdx.x * words + i] = (uint32_t)smem_i[i];
 }
 
+// The grouping; seg_counts NULL: counts from the indices, workgroups of `own` assignments.
 __global__ __launch_bounds__(kGroupThreads) void route_seg_scatter_kernel(
     const int32_t* __restrict__ topk_idx, const uint32_t* __restrict__ seg_counts, int n, int E,
     int own, int segs, int n_seg, int block_rows, int max_blocks, RoutingDev r) {
@@ -636,7 +638,7 @@ __global__ __launch_bounds__(kGroupThreads) void route_seg_scatter_kernel(
     int* s_wave = s_hist + kGroupWaves * E;
     int* s_sum = s_wave + 2 * (kGroupWaves + 1);
     const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
-    const int words = seg_words(E), parts = kGroupThreads / words;
+    const int words = seg_words(E), parts = seg_counts ? kGroupThreads / words : 1;
     const int seg0 = blockIdx.x * segs;   // own: the assignments of its segments
     // this wave's chunk of the workgroup's assignments
     const int a = blockIdx.x * own + wave * WAVE + lane;
@@ -644,7 +646,21 @@ __global__ __launch_bounds__(kGroupThreads) void route_seg_scatter_kernel(
     const int mine = valid ? topk_idx[a] : 0;
     // four experts' counts before seg0 and in all, by parts of the segments
     const int part = tid / words, pw = tid - part * words;
-    if (part < parts) {
+    if (!seg_counts) {
+        for (int i = tid; i < 8 * words; i += kGroupThreads) s_sum[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += 8 * kGroupThreads) {   // eight loads in flight
+            int x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = topk_idx[min(i + q * kGroupThreads, n - 1)];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int at = i + q * kGroupThreads;
+                if (at < n) atomicAdd(&s_sum[4 * words + x[q]], 1);
+                if (at < (int)blockIdx.x * own) atomicAdd(&s_sum[x[q]], 1);
+            }
+        }
+    } else if (part < parts) {
         const int s0 = (int)((long long)n_seg * part / parts);
         const int s1 = (int)((long long)n_seg * (part + 1) / parts);
         // counts of experts 0, 2 and 1, 3 of the word in halves of a sum, which 4088
@@ -748,17 +764,21 @@ static size_t seg_bytes(int T, int E, int tokens) {
     return align_up((size_t)((T + tokens - 1) / tokens) * seg_words(E) * sizeof(uint32_t), 256);
 }
 
-// Tokens of a segment, 0 where segments are not used: they are where the counts
-// fit the workspace that moe_route has, or where one workgroup would group for long
-// (49152 assignments take it 87 us).  Segments of 8 spread up to 4096 tokens over
-// twice the CUs.
+// Assignments up to which the grouping counts the indices itself (us, by indices and by
+// segments: 32768 = 4096 x 8 of 256 15.9 and 17.1, 36000 = 6000 x 6 of 160 18.7 and 17.5).
+constexpr size_t kScoredCountAssign = 32768;
+
+// Tokens of a segment, 0 where segments are not used.  Segments of 8 spread up to 4096
+// tokens over twice the CUs.
 static int seg_tokens_of(int T, int E, int k) {
-    if (use_fused(T, E, k) || k > kSegMaxK) return 0;
-    size_t a, b;
-    const size_t have = (size_t)T * k > kStageMaxAssign ? ~(size_t)0 : route_ws_layout(T, E, k, &a, &b);
-    if (T <= 4096 && seg_bytes(T, E, 8) <= have) return 8;
-    return seg_bytes(T, E, kSegTokens) <= have ? kSegTokens : 0;
+    if ((size_t)T * k <= kScoredCountAssign) return 0;
+    return T <= 4096 ? 8 : kSegTokens;
 }
+
+// Tokens up to which one workgroup selects and groups in one launch: its 16 waves take 64
+// tokens of 256 experts four at a time (24.3 us; two launches 8.7), and even 16 at once
+// take longer on one CU (10.0 against 8.4; 8 tokens 8.2 and 8.4).
+constexpr int kScoredFusedTokens = 8;
 
 size_t scored_ws_bytes(int T, int E, int k) {
     const int tokens = seg_tokens_of(T, E, k);
@@ -783,7 +803,7 @@ hipError_t launch_route_scored(const float* logits, const float* bias, const Sco
 #undef MOE_CALL
         return hipGetLastError();
     }
-    if (use_fused(T, E, k)) {
+    if (use_fused(T, E, k) && T <= kScoredFusedTokens) {
         const size_t smem = (size_t)(group_lds_ints(E) + n) * sizeof(int);
 #define MOE_CALL(N)                                                                              \
     route_scored_fused_kernel<N><<<1, kGroupThreads, smem, stream>>>(logits, bias, rule, T, E, k, \
@@ -819,11 +839,9 @@ hipError_t launch_route_scored(const float* logits, const float* bias, const Sco
 #undef MOE_BY_EPL
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const bool stage = n <= kStageMaxAssign;
-    const int stage_off = stage ? (int)(group_lds_bytes(E) / sizeof(int)) : 0;
-    route_group_kernel<<<1, kGroupThreads,
-                         group_lds_bytes(E) + (stage ? (size_t)n * sizeof(int) : 0), stream>>>(
-        r.topk_idx, n, E, block_rows, max_blocks, stage_off, r);
+    const size_t smem = (size_t)(group_lds_ints(E) + 8 * seg_words(E)) * sizeof(int);
+    route_seg_scatter_kernel<<<(n + kGroupThreads - 1) / kGroupThreads, kGroupThreads, smem, stream>>>(
+        r.topk_idx, nullptr, n, E, kGroupThreads, 0, 0, block_rows, max_blocks, r);
     return hipGetLastError();
 }
 

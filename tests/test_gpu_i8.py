@@ -185,13 +185,15 @@ def check_scored(lg, bias, k, br=32, score="softmax", **rule):
     assert int(got["n_blocks"][0]) == int(g["n_blocks"])
 
 
-# sizes of one launch (T <= 64), of segments (k = 4, 8, 16, and above 16384 assignments) and of
-# the one-workgroup grouping; group
+# sizes of one launch (T <= 8), of counts from the indices and, above 32768 assignments, of
+# segments of 8 (T <= 4096) and 16 tokens; group
 # sizes that are whole lanes (32 of 256), that are not (5 of 60, 20 of 160) and groups of one
 @pytest.mark.parametrize("T,E,k,n_groups,topk_groups", [
     (1, 256, 8, 8, 4), (1, 1, 1, 1, 1), (5, 2, 2, 1, 1), (64, 64, 6, 8, 3), (65, 256, 8, 8, 4), (33, 60, 5, 12, 4),
     (130, 160, 6, 8, 3), (97, 160, 4, 8, 7), (70, 128, 16, 2, 1), (9, 1000, 10, 10, 3), (66, 1000, 8, 8, 2),
     (2731, 36, 6, 4, 2), (2101, 1000, 8, 8, 2), (1025, 40, 16, 1, 1), (129, 8, 8, 1, 1), (4099, 12, 4, 3, 2),
+    (4096, 256, 8, 8, 4), (4097, 256, 8, 8, 4), (8201, 60, 4, 1, 1), (3000, 1000, 16, 8, 2), (4200, 20, 8, 4, 3),
+    (2050, 130, 17, 1, 1), (600, 64, 64, 64, 64), (8, 256, 8, 8, 4), (9, 256, 8, 8, 4), (1024, 33, 1, 1, 1), (513, 7, 2, 7, 5),
     (40, 96, 2, 48, 5), (20, 512, 64, 16, 2), (70, 64, 64, 64, 64), (18, 256, 3, 64, 9), (12, 320, 4, 64, 1)])
 @pytest.mark.parametrize("score,group_score", [("sigmoid", "top2"), ("softmax", "max"), ("softmax", "top2")])
 def test_scored_routing(T, E, k, n_groups, topk_groups, score, group_score):
@@ -203,6 +205,13 @@ def test_scored_routing(T, E, k, n_groups, topk_groups, score, group_score):
     bias = (0.1 * g.normal(size=E)).astype(np.float32) if T % 2 else None
     check_scored(lg, bias, k, 16 if T % 3 else 64, score, n_groups=n_groups, topk_groups=topk_groups,
                  group_score=group_score, renormalise=bool(T % 4), scale=2.5 if T % 5 else 1.0)
+
+
+@pytest.mark.parametrize("T,E,k", [(3000, 40, 8), (5000, 1000, 8)])
+def test_scored_routing_of_tokens_that_choose_alike(T, E, k):
+    require_gpu()
+    lg = np.tile(np.random.default_rng(E).normal(size=E).astype(np.float32), (T, 1))
+    check_scored(lg, None, k, 64, "softmax")
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])

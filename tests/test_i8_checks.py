@@ -93,7 +93,7 @@ def scored(lg=F, bias=F, r="ok", T=4, E=32, k=4, br=32, out="ok", ws=F, wsb=1 <<
 
 @pytest.mark.parametrize("kw,st", [
     (dict(T=0), SHAPE), (dict(E=1001), SHAPE), (dict(k=0), SHAPE), (dict(br=8), SHAPE),
-    (dict(lg=None), NULL), (dict(r=None), NULL), (dict(out=None), NULL), (dict(T=100, ws=None), NULL),
+    (dict(lg=None), NULL), (dict(r=None), NULL), (dict(out=None), NULL), (dict(T=20000, ws=None), NULL),
     (dict(r=raw(score=2)), SHAPE), (dict(r=raw(group_score=-1)), SHAPE), (dict(r=raw(renormalise=2)), SHAPE),
     (dict(r=raw(scale=float("nan"))), SHAPE), (dict(r=raw(scale=float("inf"))), SHAPE),
     (dict(r=raw(n_groups=0)), SHAPE), (dict(r=raw(n_groups=5, topk_groups=1)), SHAPE),
@@ -103,7 +103,7 @@ def scored(lg=F, bias=F, r="ok", T=4, E=32, k=4, br=32, out="ok", ws=F, wsb=1 <<
     (dict(r=raw(n_groups=16, topk_groups=1)), SHAPE),                   # k = 4 of groups of two
     (dict(r=raw(), E=128, k=65), SHAPE),
     (dict(lg=P(0x10002)), ALIGN), (dict(bias=P(0x10002)), ALIGN), (dict(ws=P(0x10010)), ALIGN),
-    (dict(T=100, wsb=16), WS)])
+    (dict(T=20000, wsb=16), WS)])
 def test_scored_routing_refusals(kw, st):
     assert scored(**kw) == st
 
