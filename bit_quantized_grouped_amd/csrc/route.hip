@@ -597,8 +597,8 @@ __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
 // their 64-assignment chunk w, so rows follow assignment order and the sort is stable.
 // Every workgroup repeats the scan, which costs less than a third launch.  Bound by
 // instructions in the selection (about 650 a token) and by the chain of waits in the
-// grouping: 2048 tokens x 8 of 256 take 5.3 + 6.3 us (by segments 6.6 + 6.9), 8192 x 6 of
-// 160 12 + 8 (one grouping workgroup: 87 for the latter's grouping).
+// grouping: 2048 tokens x 8 of 256 take 11.7 us (by segments 12.8), 8192 x 6 of 160 12 + 8
+// (one grouping workgroup: 87 for the latter's grouping).
 constexpr int kSegTokens = kGroupWaves;                // most tokens of a segment
 static_assert(kScoredMaxK * kSegTokens <= kGroupThreads, "a segment fits a grouping workgroup");
 
