@@ -1034,7 +1034,7 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
             e = launch_route_scored(logits, score_bias, dev, T, E, k, block_rows, p.max_blocks, p.r,
                                     route_ws, stream);
         } else {
-            e = launch_route(logits, T, E, k, block_rows, p.max_blocks, p.r, route_ws, stream);
+            e = launch_route_i8(logits, T, E, k, block_rows, p.max_blocks, p.r, route_ws, stream);
         }
         if (few) {
             if (e == hipSuccess)

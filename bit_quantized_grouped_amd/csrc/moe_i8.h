@@ -65,6 +65,8 @@ hipError_t launch_dequant_i8(const int8_t* q, const float* scale, int R, int K, 
 
 // route.hip
 size_t scored_ws_bytes(int T, int E, int k);
+hipError_t launch_route_i8(const float* logits, int T, int E, int k, int block_rows, int max_blocks,
+                           const RoutingDev& r, void* ws, hipStream_t stream);
 hipError_t launch_route_scored(const float* logits, const float* bias, const ScoreRule& rule, int T,
                                int E, int k, int block_rows, int max_blocks, const RoutingDev& r,
                                void* ws, hipStream_t stream);

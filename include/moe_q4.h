@@ -150,7 +150,7 @@ int moe_route_max_blocks(int T, int E, int k, int block_rows);
  * 16 and T above the one-launch size (T > 64, or a one-launch LDS need above
  * 64 KB) it is T*k 32-bit words, rounded up to 256 bytes: the top-k pass
  * records each 64-assignment chunk's match information there for the
- * grouping pass.  Otherwise moe_route needs 0 and ws may be NULL; above 16384
+ * grouping pass.  Otherwise moe_route needs 0 and ws may be NULL; above 32768
  * assignments the size also covers moe_route_scored's segment histograms. */
 size_t moe_route_workspace_bytes(int T, int E, int k, int block_rows);
 
@@ -526,8 +526,8 @@ typedef struct {
  * A logit of -inf has score 0; NaN counts as -inf, for a choice too; a +inf
  * logit shares the softmax with the row's other +inf.  A row of -inf alone has
  * score 0 everywhere: it keeps k experts, of weight 0.
- * k <= 64 and k <= topk_groups * (E / n_groups); otherwise arguments, workspace
- * (moe_route_workspace_bytes) and launches are moe_route's. */
+ * k <= 64 and k <= topk_groups * (E / n_groups); otherwise arguments and workspace
+ * (moe_route_workspace_bytes) are moe_route's.  One or two kernels. */
 int moe_route_scored(const float* logits, const float* bias, const moe_score_rule* rule, int T,
                      int E, int k, int block_rows, const moe_routing* out, void* ws,
                      size_t ws_bytes, hipStream_t stream);
