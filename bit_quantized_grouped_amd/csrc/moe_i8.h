@@ -45,12 +45,24 @@ __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float 
 #endif
 
 #ifdef __HIPCC__
-// Scale of a row of largest magnitude `top`, and the factor from its values to codes.  A row
-// below 2^-119 counts as zeros: 127 / top would pass fp32's range.
+// The larger of `top` and |v|; NaN wins over every number (fmaxf would drop it).
+__device__ __forceinline__ float max_abs(float top, float v) {
+    return __builtin_elementwise_maximum(top, __builtin_fabsf(v));
+}
+
+// Scale of a row of largest magnitude `top`, and the factor from its values to codes, 0 where
+// the codes are 0.  A row below 2^-119 counts as zeros: 127 / top would pass fp32's range.  The
+// scale of a row with an infinity or NaN is infinite or NaN, so all of it comes back as NaN.
 __device__ __forceinline__ float row_scale(float top, float* to_code) {
-    const bool any = top >= 0x1p-119f;
-    *to_code = any ? 127.0f / top : 0.f;
-    return any ? top / 127.0f : 0.f;
+    const bool tiny = top < 0x1p-119f;
+    *to_code = top >= 0x1p-119f && top <= 0x1.fffffep127f ? 127.0f / top : 0.f;
+    return tiny ? 0.f : top / 127.0f;
+}
+
+// Codes of four values of a row by row_scale's factor.
+__device__ __forceinline__ uint32_t row_codes(float a, float b, float c, float d, float to_code) {
+    const uint32_t p = pack_codes(a * to_code, b * to_code, c * to_code, d * to_code);
+    return to_code > 0.f ? p : 0u;   // a NaN has no code
 }
 #endif
 

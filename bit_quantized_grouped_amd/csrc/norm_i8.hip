@@ -2,7 +2,8 @@
 // row-wise 8-bit quantisation alone, and the way back to bf16.
 //
 //   v = x + residual (fp32), m = mean(v^2), y = v * weight / sqrt(m + eps),
-//   scale = max|y| / 127, q = rne(y * (127 / max|y|)); a row of zeros has scale 0.
+//   scale = max|y| / 127, q = rne(y * (127 / max|y|)); a row of zeros has scale 0, one with a
+//   NaN the scale NaN.
 //
 // max|y| = max|v * weight| / sqrt(m + eps), so the sum of squares and the
 // maximum come out of one pass over registers and one joint reduction: a row
@@ -74,15 +75,15 @@ __global__ __launch_bounds__(NW == 1 ? kNormRows * WAVE : NW * WAVE) void norm_i
             if (NORM) {
                 sq = __builtin_fmaf(f[v][i], f[v][i], sq);
                 w[v][i] *= f[v][i];
-                top = fmaxf(top, fabsf(w[v][i]));
+                top = max_abs(top, w[v][i]);
             } else {
-                top = fmaxf(top, fabsf(f[v][i]));
+                top = max_abs(top, f[v][i]);
             }
         }
 #pragma unroll
     for (int off = WAVE / 2; off >= 1; off >>= 1) {
         if (NORM) sq += shfl_xor(sq, off);
-        top = fmaxf(top, shfl_xor(top, off));
+        top = max_abs(top, shfl_xor(top, off));
     }
     if (NW > 1) {
         __shared__ float s_sq[NW], s_top[NW];
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(NW == 1 ? kNormRows * WAVE : NW * WAVE) void norm_i
 #pragma unroll
         for (int i = 1; i < NW; ++i) {
             sq += s_sq[i];
-            top = fmaxf(top, s_top[i]);
+            top = max_abs(top, s_top[i]);
         }
     }
     const float inv = NORM ? 1.0f / sqrtf(sq / (float)H + eps) : 1.0f;
@@ -119,8 +120,8 @@ __global__ __launch_bounds__(NW == 1 ? kNormRows * WAVE : NW * WAVE) void norm_i
         }
         if (q) {
             u32x2_t p;
-            p[0] = pack_codes(o[0] * to_code, o[1] * to_code, o[2] * to_code, o[3] * to_code);
-            p[1] = pack_codes(o[4] * to_code, o[5] * to_code, o[6] * to_code, o[7] * to_code);
+            p[0] = row_codes(o[0], o[1], o[2], o[3], to_code);
+            p[1] = row_codes(o[4], o[5], o[6], o[7], to_code);
             *(u32x2_t*)(q + row + c) = p;
         }
     }

@@ -430,7 +430,8 @@ int moe_layer_chunked(const uint16_t* x, const float* logits, int T, int H, int 
  * products of 8-bit codes.  A row of K values is held as K signed 8-bit codes
  * and one fp32 scale: value = code * scale, scale = max|row| / 127, code =
  * rne(value * (127 / max|row|)); a row of zeros, or of values below 2^-119 alone,
- * has scale 0 and codes 0.
+ * has scale 0 and codes 0.  A row with a NaN has scale NaN, else one with an infinity
+ * scale +inf, both with codes 0: every value of it comes back as NaN.
  * Codes are -128 .. 127; the calls that quantise write -127 .. 127.
  * ---- */
 
@@ -458,8 +459,8 @@ typedef struct {
  *   16-byte aligned);  q_scale fp32 [T].  residual, sum, y may be NULL, and q
  *   and q_scale together; at least one output is given.  sum may be x or
  *   residual itself (the same address); no other outputs alias inputs.
- * H a multiple of 64 up to 16384, T >= 1, eps > 0 and finite; values finite,
- * |v| and |v * weight| below 1e17 (a row's squares are summed in fp32).
+ * H a multiple of 64 up to 16384, T >= 1, eps > 0 and finite; finite |v| and
+ * |v * weight| below 1e17 (a row's squares are summed in fp32).
  * Enqueues one kernel. */
 int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
                 int T, int H, uint16_t* sum, uint16_t* y, int8_t* q, float* q_scale,
