@@ -647,29 +647,28 @@ __global__ __launch_bounds__(kQuantWaves* WAVE) void quant_h_kernel(
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(v[i][j]));
+            for (int j = 0; j < 4; ++j) top = max_abs(top, v[i][j]);
     } else {
         for (int c = tid * 4; c < K; c += STEP) {
             const f32x4_t t = *(const f32x4_t*)(src + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(t[j]));
+            for (int j = 0; j < 4; ++j) top = max_abs(top, t[j]);
         }
     }
 #pragma unroll
-    for (int off = WAVE / 2; off >= 1; off >>= 1) top = fmaxf(top, shfl_xor(top, off));
+    for (int off = WAVE / 2; off >= 1; off >>= 1) top = max_abs(top, shfl_xor(top, off));
     if constexpr (!kWave) {
         __shared__ float s_top[kQuantWaves];
         if (lane == 0) s_top[wave] = top;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kQuantWaves; ++i) top = fmaxf(top, s_top[i]);
+        for (int i = 0; i < kQuantWaves; ++i) top = max_abs(top, s_top[i]);
     }
     float to_code;
     const float s = row_scale(top, &to_code);
     if (tid == 0) (routed ? scale : scale_sh)[r] = s;
     auto put = [&](int c, const f32x4_t& t) {
-        *(uint32_t*)(dst + c) =
-            pack_codes(t[0] * to_code, t[1] * to_code, t[2] * to_code, t[3] * to_code);
+        *(uint32_t*)(dst + c) = row_codes(t[0], t[1], t[2], t[3], to_code);
     };
     if constexpr (kWave) {
 #pragma unroll

@@ -540,7 +540,8 @@ size_t moe_gemm_i8_workspace_bytes(int T, int H, int I, int I_sh, int E, int k, 
  *   x int8 [T, H], x_scale fp32 [T] (e.g. moe_norm_i8's q and q_scale)
  *   h = silu(x Wg^T) * (x Wu^T) in fp32, held as 8-bit codes with one scale per
  *   row;  expert_out / shared_out = bf16(h Wd^T)
- * Sums of products are exact 32-bit integers.  Shapes as for the 4-bit calls,
+ * Sums of products are exact 32-bit integers.  A NaN or infinite scale of x, gate
+ * or up, or an h past fp32's range, makes the whole row of such an h NaN.  Shapes as for the 4-bit calls,
  * and H, I, I_sh below 131072, H*max(I, I_sh) < 2^31.  Other arguments, status
  * codes and the order of rows as for moe_grouped_gemm_q4. */
 int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int I, int I_sh, int E,

@@ -9,7 +9,7 @@ import torch
 import bit_quantized_grouped_amd as bq
 from gpu_cases import DEV, announce, require_gpu
 from oracle import i8_oracle as ref
-from test_gpu_i8 import EPS, check_norm, dev, f64, norm_inputs, sync, within
+from test_gpu_i8 import EPS, check_norm, codes, dev, f64, i8mat, layer_weights, norm_inputs, sync, within
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,44 @@ def test_quant_of_rows_with_nan_and_infinities(K):
     _, scale, units = ref.quant_rows(f64(x[good]))
     within(f64(s[good]), scale, scale * 2.0 ** -24, "scale")
     within(f64(q[good]), units, 0.5 + 127 * 2 * 2.0 ** -24, "codes")
+
+
+def nan_layer(T, H, I, I_sh, E, k, block_rows):
+    """A layer with NaN in a token's scale, in a channel of one expert's gate and an infinity in a
+    channel of another's up: (y with them, y without, the tokens that they reach, both dicts)."""
+    g = np.random.default_rng(T + I)
+    host = layer_weights(g, E, H, I, I_sh)
+    x, lg = dev(codes(g, T, H), torch.int8), dev(g.normal(size=(T, E)), torch.float32)
+    sx = dev(g.uniform(0.01, 0.03, T), torch.float32)
+    mats = [i8mat(q, s, 1) for q, s in host] + [None] * (6 - len(host))
+    clean = bq.MoeLayerI8(mats, H, I, I_sh, E, k, DEV, block_rows=block_rows)
+    want = clean.forward(x, sx, lg)
+    idx = want["routing"].topk_idx
+    t_bad = T // 2
+    e_nan, e_inf = int(idx[0, 0]), int(idx[0, -1])
+    sx2 = sx.clone()
+    sx2[t_bad] = NAN
+    gate, up = (bq.DeviceI8Mat(m.codes, m.scales.clone(), m.layout) for m in mats[:2])
+    gate.scales[e_nan, I - 1] = NAN
+    up.scales[e_inf, 0] = INF
+    other = bq.MoeLayerI8([gate, up] + mats[2:], H, I, I_sh, E, k, DEV, block_rows=block_rows)
+    got = other.forward(x, sx2, lg)
+    sync()
+    reached = ((idx == e_nan) | (idx == e_inf)).any(1)
+    reached[t_bad] = True
+    return got["y"], want["y"], reached, got, want
+
+
+# h by a wave a row, one to eight pieces a lane, and by a workgroup a row; blocks of every size
+@pytest.mark.parametrize("I,I_sh,block_rows", [(64, 0, 16), (448, 192, 32), (1024, 64, 32), (1088, 0, 64), (2112, 576, 16),
+                                               (64, 2112, 64)])
+def test_nan_reaches_the_grouped_layers_output(I, I_sh, block_rows):
+    require_gpu()
+    announce(f"grouped layer with NaN I={I} I_sh={I_sh} rows={block_rows}")
+    T, k = 70, 2
+    y, want, reached, got, clean = nan_layer(T, 128, I, I_sh, 24, k, block_rows)
+    assert not reached.all() and y[reached].isnan().all() and torch.equal(y[~reached], want[~reached])
+    # a row of an expert or of the shared expert is NaN as a whole or what it is without
+    for name in ("expert_out", "shared_out") if I_sh else ("expert_out",):
+        rows = got[name].isnan().any(1)
+        assert got[name][rows].isnan().all() and torch.equal(got[name][~rows], clean[name][~rows])
