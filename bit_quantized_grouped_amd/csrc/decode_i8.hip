@@ -164,20 +164,19 @@ __global__ __launch_bounds__(kDdMaxWaves* WAVE) void decode_i8_down_kernel(Decod
             const int c = i * 256 + lane * 4;
             v[i] = c < K ? *(const f32x4_t*)(h + c) : f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(v[i][b]));
+            for (int b = 0; b < 4; ++b) top = max_abs(top, v[i][b]);
         }
         for (int c = KEEP * 256 + lane * 4; c < K; c += 256) {
             const f32x4_t t = *(const f32x4_t*)(h + c);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) top = fmaxf(top, fabsf(t[b]));
+            for (int b = 0; b < 4; ++b) top = max_abs(top, t[b]);
         }
 #pragma unroll
-        for (int off = WAVE / 2; off >= 1; off >>= 1) top = fmaxf(top, shfl_xor(top, off));
+        for (int off = WAVE / 2; off >= 1; off >>= 1) top = max_abs(top, shfl_xor(top, off));
         float to_code;
         const float scale = row_scale(top, &to_code);
         auto put = [&](int c, const f32x4_t& t) {
-            *(uint32_t*)(q + c) =
-                pack_codes(t[0] * to_code, t[1] * to_code, t[2] * to_code, t[3] * to_code);
+            *(uint32_t*)(q + c) = row_codes(t[0], t[1], t[2], t[3], to_code);
         };
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) {

@@ -102,3 +102,13 @@ def test_nan_reaches_the_grouped_layers_output(I, I_sh, block_rows):
     for name in ("expert_out", "shared_out") if I_sh else ("expert_out",):
         rows = got[name].isnan().any(1)
         assert got[name][rows].isnan().all() and torch.equal(got[name][~rows], clean[name][~rows])
+
+
+# h in registers (512 and less) and read twice; more slots than waves
+@pytest.mark.parametrize("T,I,I_sh,E,k", [(1, 64, 0, 8, 2), (1, 512, 1088, 8, 3), (1, 1088, 64, 40, 20), (3, 128, 64, 64, 2),
+                                          (12, 576, 0, 64, 4)])
+def test_nan_reaches_the_output_of_few_tokens(T, I, I_sh, E, k):
+    require_gpu()
+    announce(f"layer of few tokens with NaN T={T} I={I} I_sh={I_sh}")
+    y, want, reached, _, _ = nan_layer(T, 128, I, I_sh, E, k, None)
+    assert y[reached].isnan().all() and torch.equal(y[~reached], want[~reached])
