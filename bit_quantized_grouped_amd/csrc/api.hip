@@ -957,7 +957,7 @@ static int check_layer_i8_shape(int T, int H, int I, int I_sh, int E, int k, int
 
 size_t moe_gemm_i8_workspace_bytes(int T, int H, int I, int I_sh, int E, int k, int block_rows) {
     if (check_layer_i8_shape(T, H, I, I_sh, E, k, block_rows)) return 0;
-    return gemm_i8_ws_layout(T, I, I_sh, k).total;
+    return gemm_i8_ws_layout(T, H, I, I_sh, k).total;
 }
 
 static int gemm_i8_args(const int8_t* x, const float* x_scale, int T, int H, int I, int I_sh, int E,
@@ -983,7 +983,7 @@ static int gemm_i8_args(const int8_t* x, const float* x_scale, int T, int H, int
         return MOE_ERR_SHAPE;   // shared matrices given but I_sh == 0
     }
     if (!aligned(x, 16) || !aligned(x_scale, 4) || !aligned(expert_out, 16)) return MOE_ERR_ALIGN;
-    if ((st = check_ws(ws, ws_bytes, gemm_i8_ws_layout(T, I, I_sh, k).total))) return st;
+    if ((st = check_ws(ws, ws_bytes, gemm_i8_ws_layout(T, H, I, I_sh, k).total))) return st;
     *p = GemmI8Problem{x, x_scale, T, H, I, I_sh, E, k, block_rows, max_blocks_of(T, E, k, block_rows),
                        to_dev(r), i8_dev(gate), i8_dev(up), i8_dev(down), i8_dev(sh_gate),
                        i8_dev(sh_up), i8_dev(sh_down), expert_out, shared_out};
@@ -1000,7 +1000,7 @@ int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int
         const int st = gemm_i8_args(x, x_scale, T, H, I, I_sh, E, k, block_rows, r, gate, up, down,
                                     sh_gate, sh_up, sh_down, expert_out, shared_out, ws, ws_bytes, &p);
         if (st) return st;
-        return launch_grouped_i8(p, ws, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+        return launch_grouped_i8(p, ws, false, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
     } catch (...) {
         return MOE_ERR_HIP;
     }
@@ -1041,10 +1041,12 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
                 e = launch_decode_i8(p, logits, score_bias, rule ? &dev : nullptr, gemm_ws, y, stream);
             return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
         }
-        if (e == hipSuccess) e = launch_grouped_i8(p, gemm_ws, stream);
+        if (e == hipSuccess) e = launch_grouped_i8(p, gemm_ws, true, stream);
+        const GemmI8Ws L = gemm_i8_ws_layout(T, H, I, I_sh, k);
+        const int8_t* base = (const int8_t*)gemm_ws;
         if (e == hipSuccess)
-            e = launch_combine(expert_out, shared_out, nullptr, p.r.assign_row, p.r.topk_w, T, H, k,
-                               y, stream);
+            e = launch_combine_low(expert_out, base + L.low, shared_out, base + L.low_sh,
+                                   p.r.assign_row, p.r.topk_w, T, H, k, y, stream);
         return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
     } catch (...) {
         return MOE_ERR_HIP;

@@ -247,7 +247,7 @@ bool decode_i8_fits(const GemmI8Problem& p) {
 
 hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const float* bias,
                             const ScoreRule* rule, void* ws, uint16_t* y, hipStream_t stream) {
-    const GemmI8Ws L = gemm_i8_ws_layout(p.T, p.I, p.I_sh, p.k);
+    const GemmI8Ws L = gemm_i8_ws_layout(p.T, p.H, p.I, p.I_sh, p.k);
     DecodeI8Args d{};
     d.p = p;
     d.logits = logits;

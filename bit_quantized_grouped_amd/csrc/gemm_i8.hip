@@ -31,6 +31,7 @@ struct PartI8 {
     I8MatDev w, w2;         // w2: the up matrices of gate/up
     int M, N, K;            // M: rows of a dense part
     void* out;              // bf16, or fp32 h of gate/up
+    int8_t* low;            // low bytes of a bf16 out (low_byte), or NULL
 };
 
 struct ProductArgs {
@@ -583,6 +584,12 @@ __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs
     static_assert(16 * ROW / 16 % WAVE == 0, "whole stores");
     if (col0 >= N) return;   // N is a multiple of 64: the wave's columns are all in or all out
     int8_t* s_o = s_a0 + wave * 16 * STRIDE;
+    // The low bytes likewise, through the other rows' place.  2048 skewed tokens: down 60.5 -> 70.6
+    // us and the combine that reads them 15.2 -> 20.5; whole lines behind a barrier 69.8.
+    constexpr int LSTRIDE = NW * 16 + 16;
+    static_assert(GATEUP || 4 * 16 * LSTRIDE <= A0, "low bytes fit");
+    int8_t* s_l = s_a1 + wave * 16 * LSTRIDE;
+    const bool low = !GATEUP && part.low;
     f32x4_t ws[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) ws[n] = *(const f32x4_t*)(s_ws[wave] + n * 16 + fp * 4);
@@ -599,8 +606,19 @@ __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs
                     v[i] = silu_f32(v[i]) * ((float)acc[n + (GATEUP ? NW : 0)][m][i] * as * ws[n + (GATEUP ? NW : 0)][i]);
             }
             int8_t* to = s_o + fr * STRIDE + (n * 16 + fp * 4) * ES;
-            if (GATEUP) *(f32x4_t*)to = v;
-            else *(u32x2_t*)to = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            if constexpr (GATEUP) {
+                *(f32x4_t*)to = v;
+            } else {
+                const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                *(u32x2_t*)to = o;
+                if (low) {
+                    uint32_t b = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        b |= (uint32_t)(low_byte(v[i], o[i / 2] >> 16 * (i % 2) & 0xFFFF) & 255) << 8 * i;
+                    *(uint32_t*)(s_l + fr * LSTRIDE + n * 16 + fp * 4) = b;
+                }
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -610,6 +628,12 @@ __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs
             if (m * 16 + row < rows)
                 *(i32x4_t*)((int8_t*)part.out + ((size_t)(row0 + m * 16 + row) * N + col0) * ES + at16) =
                     *(const i32x4_t*)(s_o + row * STRIDE + at16);
+        }
+        if (low) {
+            const int row = lane / NW, at16 = lane % NW * 16;
+            if (row < 16 && m * 16 + row < rows)
+                *(i32x4_t*)(part.low + (size_t)(row0 + m * 16 + row) * N + col0 + at16) =
+                    *(const i32x4_t*)(s_l + row * LSTRIDE + at16);
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -769,7 +793,7 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     return hipGetLastError();
 }
 
-GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k) {
+GemmI8Ws gemm_i8_ws_layout(int T, int H, int I, int I_sh, int k) {
     GemmI8Ws L{};
     const size_t n = (size_t)T * k;
     size_t o = 0;
@@ -780,6 +804,11 @@ GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k) {
     };
     L.h = take(n * I * 4);
     L.h_sh = take((size_t)T * I_sh * 4);
+    const size_t end = o;
+    o = 0;   // down writes the low bytes when the activations have become codes
+    L.low = take(n * H);
+    L.low_sh = take(I_sh ? (size_t)T * H : 0);
+    if (o < end) o = end;
     L.q = take(n * I);
     L.q_sh = take((size_t)T * I_sh);
     L.scale = take(n * 4);
@@ -788,8 +817,8 @@ GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k) {
     return L;
 }
 
-hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t stream) {
-    const GemmI8Ws L = gemm_i8_ws_layout(g.T, g.I, g.I_sh, g.k);
+hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, bool want_low, hipStream_t stream) {
+    const GemmI8Ws L = gemm_i8_ws_layout(g.T, g.H, g.I, g.I_sh, g.k);
     char* base = (char*)ws;
     float *h = (float*)(base + L.h), *h_sh = (float*)(base + L.h_sh);
     int8_t *q = (int8_t*)(base + L.q), *q_sh = (int8_t*)(base + L.q_sh);
@@ -801,8 +830,8 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     p.offsets = g.r.offsets;
     p.n_blocks = g.r.n_blocks;
     p.sorted_assign = g.r.sorted_assign;
-    p.routed = PartI8{g.x, g.x_scale, g.gate, g.up, 0, g.I, g.H, h};
-    if (g.I_sh) p.dense = PartI8{g.x, g.x_scale, g.sh_gate, g.sh_up, g.T, g.I_sh, g.H, h_sh};
+    p.routed = PartI8{g.x, g.x_scale, g.gate, g.up, 0, g.I, g.H, h, nullptr};
+    if (g.I_sh) p.dense = PartI8{g.x, g.x_scale, g.sh_gate, g.sh_up, g.T, g.I_sh, g.H, h_sh, nullptr};
     const int n = g.T * g.k;
     // Rows / 16, weight rows of a wave / 16, steps ahead, steps of a chunk; us measured at H
     // 2048, I 512, 256 experts, k 8.  Gate/up: 64 tokens 1,2,4,4 76; 512 tokens 2,2,4,4 94
@@ -828,8 +857,10 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, hipStream_t strea
     else MOE_QUANT(0);
 #undef MOE_QUANT
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out};
-    if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out};
+    int8_t* low = want_low ? (int8_t*)(base + L.low) : nullptr;
+    int8_t* low_sh = want_low ? (int8_t*)(base + L.low_sh) : nullptr;
+    p.routed = PartI8{q, scale, g.down, {}, 0, g.H, g.I, g.expert_out, low};
+    if (g.I_sh) p.dense = PartI8{q_sh, scale_sh, g.sh_down, {}, g.T, g.H, g.I_sh, g.shared_out, low_sh};
     if (g.block_rows == 16) launch_grouped_stream<1, 2, 4, 4, false>(p, g.max_blocks, g.T, n, stream);
     else if (g.block_rows == 32) launch_grouped_stream<2, 4, 2, 4, false>(p, g.max_blocks, g.T, n, stream);
     else launch_grouped_stream<4, 4, 4, 4, false>(p, g.max_blocks, g.T, n, stream);

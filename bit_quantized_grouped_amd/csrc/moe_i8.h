@@ -66,6 +66,21 @@ __device__ __forceinline__ uint32_t row_codes(float a, float b, float c, float d
 }
 #endif
 
+#ifdef __HIPCC__
+// The byte that a value loses when it is rounded to bf16: its fp32 bits are the bf16's and 256
+// times this, within half a step of 24 bits (2^-16 of the value; a value midway between two
+// bf16 keeps 127 of 128: 2^-15).  A bf16 value itself has 0.
+__device__ __forceinline__ int low_byte(float v, uint32_t bf16) {
+    const int off = (int)(__builtin_bit_cast(uint32_t, v) - (bf16 << 16));
+    return max(-128, min(127, (off + 128) >> 8));
+}
+
+// Bits of the fp32 value of a bf16 in the high half of `high` and its low byte.
+__device__ __forceinline__ uint32_t with_low_byte(uint32_t high, int low) {
+    return high + ((uint32_t)low << 8);
+}
+#endif
+
 // norm_i8.hip
 hipError_t launch_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                           float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,
@@ -99,12 +114,19 @@ struct GemmI8Problem {
     uint16_t* shared_out;
 };
 // Workspace: SwiGLU activations fp32 (routed rows, then the shared expert's),
-// their 8-bit codes and one scale per row.
+// their 8-bit codes and one scale per row; and the low bytes of the outputs
+// (low_byte), where the activations were.
 struct GemmI8Ws {
-    size_t h, h_sh, q, q_sh, scale, scale_sh, total;
+    size_t h, h_sh, low, low_sh, q, q_sh, scale, scale_sh, total;
 };
-GemmI8Ws gemm_i8_ws_layout(int T, int I, int I_sh, int k);
-hipError_t launch_grouped_i8(const GemmI8Problem& p, void* ws, hipStream_t stream);
+GemmI8Ws gemm_i8_ws_layout(int T, int H, int I, int I_sh, int k);
+// want_low: the outputs' low bytes too, into the workspace
+hipError_t launch_grouped_i8(const GemmI8Problem& p, void* ws, bool want_low, hipStream_t stream);
+
+// combine.hip: the weighted sum over outputs with their low bytes
+hipError_t launch_combine_low(const uint16_t* expert_out, const int8_t* low, const uint16_t* shared_out,
+                              const int8_t* shared_low, const int32_t* assign_row, const float* topk_w,
+                              int T, int H, int k, uint16_t* y, hipStream_t stream);
 
 // decode_i8.hip: moe_layer_i8 of few tokens; a single one's routing arrays included
 bool decode_i8_fits(const GemmI8Problem& p);

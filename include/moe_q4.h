@@ -552,9 +552,11 @@ int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int
 
 /* One whole layer call over 8-bit activations and weights: moe_route (rule
  * NULL, score_bias NULL) or moe_route_scored, moe_grouped_gemm_i8 and
- * moe_combine in order on `stream`, with those calls' arguments and results.
+ * moe_combine in order on `stream`, with those calls' arguments and results, except that
+ * the sum takes the experts' outputs before their rounding to bf16 (within 2^-15 of each):
+ * y has the one rounding of the sum.
  * A call for at most 64 tokens may leave expert_out and shared_out unwritten: it sums
- * a token's experts without them. */
+ * a token's experts without them.  gemm_ws holds the outputs' further bits in between. */
 int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
                  const float* score_bias, const moe_score_rule* rule, int T, int H, int I, int I_sh,
                  int E, int k, int block_rows, const moe_i8_mat* gate, const moe_i8_mat* up,

@@ -9,7 +9,8 @@ import torch
 import bit_quantized_grouped_amd as bq
 from gpu_cases import DEV, announce, require_gpu
 from oracle import i8_oracle as ref
-from test_gpu_i8 import EPS, check_norm, codes, dev, f64, i8mat, layer_weights, norm_inputs, sync, within
+from test_gpu_i8 import (EPS, HALF, PROD_SHARE, check_norm, codes, dev, f64, i8mat, layer_weights, norm_inputs, sync,
+                         within)
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +113,42 @@ def test_nan_reaches_the_output_of_few_tokens(T, I, I_sh, E, k):
     announce(f"layer of few tokens with NaN T={T} I={I} I_sh={I_sh}")
     y, want, reached, _, _ = nan_layer(T, 128, I, I_sh, E, k, None)
     assert y[reached].isnan().all() and torch.equal(y[~reached], want[~reached])
+
+
+# ---- the sum over the experts ----
+
+@pytest.mark.parametrize("T,H,I,I_sh,E,k,block_rows", [
+    (70, 256, 128, 0, 6, 6, 16), (130, 128, 448, 64, 16, 8, 32), (300, 320, 64, 192, 8, 4, 64), (80, 1024, 64, 64, 4, 1, 16),
+    (200, 2112, 64, 0, 16, 12, 32), (96, 64, 320, 64, 70, 20, 16), (150, 192, 128, 128, 5, 3, 64)])
+def test_layer_sums_its_experts_before_rounding(T, H, I, I_sh, E, k, block_rows):
+    """y is one rounding of a sum in fp32, as it is for few tokens: an expert's output enters it
+    within 2^-15 of itself, where one rounded to bf16 would be 2^-9 of itself off."""
+    require_gpu()
+    what = f"layer sum T={T} H={H} I={I} I_sh={I_sh} E={E} k={k} rows={block_rows}"
+    announce(what)
+    g = np.random.default_rng(T * H + I)
+    host = layer_weights(g, E, H, I, I_sh)
+    x, sx = codes(g, T, H), g.uniform(0.01, 0.03, T).astype(np.float32)
+    lg = g.normal(size=(T, E)).astype(np.float32)
+    mats = [i8mat(q, s, 1) for q, s in host] + [None] * (6 - len(host))
+    layer = bq.MoeLayerI8(mats, H, I, I_sh, E, k, DEV, block_rows=block_rows)
+    got = layer.forward(dev(x, torch.int8), dev(sx, torch.float32), dev(lg, torch.float32))
+    sync()
+    idx = np.argsort(-lg, axis=1, kind="stable")[:, :k].astype(np.int32)
+    p = np.exp(np.take_along_axis(lg, idx, 1).astype(np.float64))
+    w = p / p.sum(1, keepdims=True)
+    eo, b, sh, b_sh, y = ref.layer(x, sx, idx, w, host[:3], host[3:] if I_sh else None)
+    # the expert's own error (codes of h at a border, fp32 products), its 2^-15, the fp32 weight
+    # (1e-6 as for moe_route) and the fp32 sum of k + 1
+    share = PROD_SHARE + 2.0 ** -15 + 1e-6 + (k + 2) * 2.0 ** -23
+    bound = ((b + np.abs(eo) * share).reshape(T, k, H) * w[:, :, None]).sum(1)
+    if I_sh:
+        bound = bound + b_sh + np.abs(sh) * share
+    within(f64(got["y"]), y, bound + HALF * (np.abs(y) + bound), what)
+    # the experts' rows of the call are still the grouped product's, in bf16
+    r = got["routing"]
+    eo2, so2 = torch.empty_like(got["expert_out"]), None if not I_sh else torch.empty_like(got["shared_out"])
+    ws = torch.empty(bq.gemm_i8_workspace_bytes(T, H, I, I_sh, E, k, block_rows), dtype=torch.uint8, device=DEV)
+    bq.moe_grouped_gemm_i8(dev(x, torch.int8), dev(sx, torch.float32), I, I_sh, E, k, block_rows, r, *mats, eo2, so2, ws)
+    sync()
+    assert torch.equal(eo2, got["expert_out"]) and (so2 is None or torch.equal(so2, got["shared_out"]))
