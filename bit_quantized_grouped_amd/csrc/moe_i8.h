@@ -81,6 +81,10 @@ __device__ __forceinline__ uint32_t with_low_byte(uint32_t high, int low) {
 }
 #endif
 
+// A grid dimension ends below 2^32 threads.  Work of up to 1024 threads an item goes by so many
+// items a launch.
+constexpr int kItemsALaunch = 1 << 21;
+
 // norm_i8.hip
 hipError_t launch_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
                           float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,

@@ -129,17 +129,18 @@ __global__ __launch_bounds__(NW == 1 ? kNormRows * WAVE : NW * WAVE) void norm_i
 
 template <bool NORM>
 static hipError_t launch_rows(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
-                              float eps, int T, int H, uint16_t* sum, uint16_t* y, int8_t* q,
+                              float eps, int T_all, int H, uint16_t* sum, uint16_t* y, int8_t* q,
                               float* q_scale, hipStream_t stream) {
     // Inputs that do not fit half of the Infinity Cache (256 MB) are not there any more,
     // wherever they come from; read without allocating in it they leave the codes there for
     // the next kernel.  8191 x 7168 with the residual: 90 us against 102, and reading the codes
     // back 28 against 38; 2048 x 2048, whose inputs are there: 11.4 against 8.3.
-    const bool big = (residual ? 4ll : 2ll) * T * H > (128ll << 20);
+    const bool big = (residual ? 4ll : 2ll) * T_all * H > (128ll << 20);
 #define MOE_NORM_S(NW, V, S)                                                                    \
     norm_i8_kernel<NW, V, NORM, S><<<NW == 1 ? (T + kNormRows - 1) / kNormRows : T,             \
                                      NW == 1 ? kNormRows * WAVE : NW * WAVE, 0, stream>>>(      \
-        x, residual, weight, eps, T, H, sum, y, q, q_scale)
+        x + t0 * H, at(residual, t0 * H), weight, eps, T, H, at(sum, t0 * H), at(y, t0 * H),    \
+        at(q, t0 * H), at(q_scale, t0))
 #define MOE_NORM(NW, V)                      \
     {                                        \
         if (big) MOE_NORM_S(NW, V, true);    \
@@ -148,15 +149,21 @@ static hipError_t launch_rows(const uint16_t* x, const uint16_t* residual, const
     // Wider rows by several waves, one or two pieces a lane: their loads and stores are the chain
     // of a call of few rows.  One row of 2048 by 4 waves 2.5 us, by one 3.9 (2048 rows 8.6, 9.2);
     // 64 rows of 7168 by 8 waves 4.3, by 4 4.9 (8191 rows 84, 90; by 16 88).
-    if (H <= 512) MOE_NORM(1, 1)
-    else if (H <= 1024) MOE_NORM(1, 2)
-    else if (H <= 2048) MOE_NORM(4, 1)
-    else if (H <= 4096) MOE_NORM(8, 1)
-    else if (H <= 8192) MOE_NORM(8, 2)
-    else MOE_NORM(16, 2)   // up to kMaxNormWidth
+    auto at = [](auto* p, size_t by) { return p ? p + by : p; };
+    for (size_t t0 = 0; t0 < (size_t)T_all; t0 += kItemsALaunch) {
+        const int T = (int)min((size_t)T_all - t0, (size_t)kItemsALaunch);
+        if (H <= 512) MOE_NORM(1, 1)
+        else if (H <= 1024) MOE_NORM(1, 2)
+        else if (H <= 2048) MOE_NORM(4, 1)
+        else if (H <= 4096) MOE_NORM(8, 1)
+        else if (H <= 8192) MOE_NORM(8, 2)
+        else MOE_NORM(16, 2)   // up to kMaxNormWidth
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
 #undef MOE_NORM
 #undef MOE_NORM_S
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 hipError_t launch_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,

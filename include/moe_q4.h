@@ -461,14 +461,14 @@ typedef struct {
  *   residual itself (the same address); no other outputs alias inputs.
  * H a multiple of 64 up to 16384, T >= 1, eps > 0 and finite; finite |v| and
  * |v * weight| below 1e17 (a row's squares are summed in fp32).
- * Enqueues one kernel. */
+ * Enqueues one kernel for each 2^21 rows. */
 int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
                 int T, int H, uint16_t* sum, uint16_t* y, int8_t* q, float* q_scale,
                 hipStream_t stream);
 
 /* Rows of bf16 [R, K] as codes int8 [R, K] and scales fp32 [R] (weights at load
  * time, activations that need no norm).  x and q 16-byte aligned, K a multiple
- * of 64 up to 16384.  Enqueues one kernel. */
+ * of 64 up to 16384.  Enqueues one kernel for each 2^21 rows. */
 int moe_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, hipStream_t stream);
 
 /* The way back: out = bf16(code * scale), [R, K] row-major, K a multiple of 64;

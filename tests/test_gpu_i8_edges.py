@@ -152,3 +152,39 @@ def test_layer_sums_its_experts_before_rounding(T, H, I, I_sh, E, k, block_rows)
     bq.moe_grouped_gemm_i8(dev(x, torch.int8), dev(sx, torch.float32), I, I_sh, E, k, block_rows, r, *mats, eo2, so2, ws)
     sync()
     assert torch.equal(eo2, got["expert_out"]) and (so2 is None or torch.equal(so2, got["shared_out"]))
+
+
+# ---- sizes beyond one launch (a grid dimension ends below 2^32 threads) ----
+
+@pytest.fixture
+def large():
+    require_gpu()
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
+# a wave a row, and four waves a row
+@pytest.mark.parametrize("R,K", [((1 << 26) + 5, 64), ((1 << 24) + 5, 1088)])
+def test_norm_and_quant_of_rows_beyond_one_launch(large, R, K):
+    announce(f"norm and quant R={R} K={K}")
+    x = torch.zeros((R, K), dtype=torch.bfloat16, device=DEV)
+    some = [0, (1 << 21) - 1, 1 << 21, R // 2, R - 1]
+    rows = dev(np.random.default_rng(K).normal(size=(len(some), K)), torch.bfloat16)
+    x[some] = rows
+    w = dev(1 + 0.3 * np.random.default_rng(1).normal(size=K), torch.bfloat16)
+    q, s = torch.full((R, K), 1, dtype=torch.int8, device=DEV), torch.full((R,), -1.0, device=DEV)
+    want = [torch.empty((len(some), K), dtype=torch.int8, device=DEV), torch.empty(len(some), device=DEV)]
+    for call, few in ((lambda: bq.moe_quant_i8(x, q, s), lambda: bq.moe_quant_i8(rows, *want)),
+                      (lambda: bq.moe_norm_i8(x, None, w, EPS, q=q, q_scale=s),
+                       lambda: bq.moe_norm_i8(rows, None, w, EPS, q=want[0], q_scale=want[1]))):
+        q.fill_(1)
+        s.fill_(-1.0)
+        call()
+        few()
+        sync()
+        assert torch.equal(q[some], want[0]) and torch.equal(s[some], want[1])
+        assert int((s != 0).sum()) == len(some)
+        s[some] = 0
+        q[some] = 0
+        assert not any(part.any() for part in q.split(1 << 22))
