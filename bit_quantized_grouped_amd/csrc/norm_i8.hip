@@ -212,10 +212,16 @@ __global__ __launch_bounds__(kDequantWaves * WAVE) void dequant_i8_kernel(
 hipError_t launch_dequant_i8(const int8_t* q, const float* scale, int R, int K, uint16_t* out,
                              hipStream_t stream) {
     const uint32_t parts = R < kDequantPartRows ? ((uint32_t)K + kDequantPart - 1) / kDequantPart : 1;
-    const long long waves = (long long)R * parts;
-    dequant_i8_kernel<<<(unsigned)((waves + kDequantWaves - 1) / kDequantWaves), kDequantWaves * WAVE, 0,
-                        stream>>>(q, scale, R, K, parts, out);
-    return hipGetLastError();
+    const int most = parts > 1 ? (int)(16u * kItemsALaunch / parts) : kItemsALaunch;   // parts are at most 2^21
+    for (size_t r0 = 0; r0 < (size_t)R; r0 += most) {
+        const int rows = R - (long long)r0 < most ? R - (int)r0 : most;
+        const long long waves = (long long)rows * parts;
+        dequant_i8_kernel<<<(unsigned)((waves + kDequantWaves - 1) / kDequantWaves), kDequantWaves * WAVE,
+                            0, stream>>>(q + r0 * K, scale + r0, rows, K, parts, out + r0 * K);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moeq4

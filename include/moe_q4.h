@@ -472,7 +472,8 @@ int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* wei
 int moe_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, hipStream_t stream);
 
 /* The way back: out = bf16(code * scale), [R, K] row-major, K a multiple of 64;
- * q and out 16-byte aligned.  Enqueues one kernel. */
+ * q and out 16-byte aligned.  Enqueues one kernel for each 2^21 rows, of fewer than 2048
+ * wide rows for each 2^25 parts of 1024 codes. */
 int moe_dequant_i8_bf16(const int8_t* q, const float* scale, int R, int K, uint16_t* out,
                         hipStream_t stream);
 

@@ -188,3 +188,31 @@ def test_norm_and_quant_of_rows_beyond_one_launch(large, R, K):
         s[some] = 0
         q[some] = 0
         assert not any(part.any() for part in q.split(1 << 22))
+
+
+def test_dequant_of_rows_beyond_one_launch(large):
+    R, K = (1 << 26) + 5, 64
+    announce(f"dequant R={R} K={K}")
+    q, s = torch.zeros((R, K), dtype=torch.int8, device=DEV), torch.ones(R, device=DEV)
+    some = [0, (1 << 21) - 1, 1 << 21, R // 2, R - 1]
+    q[some], s[some] = 100, torch.arange(1.0, 6.0, device=DEV)
+    out = torch.full((R, K), 3.0, dtype=torch.bfloat16, device=DEV)
+    bq.moe_dequant_i8_bf16(q, s, out)
+    sync()
+    assert torch.equal(out[some].float(), (100.0 * torch.arange(1.0, 6.0, device=DEV))[:, None].expand(5, K).bfloat16().float())
+    out[some] = 0
+    assert not any(part.any() for part in out.split(1 << 22))
+
+
+def test_dequant_of_few_rows_beyond_one_launch(large):
+    """2^21 parts of a row of 1024 codes: 16 rows a launch."""
+    R, K = 17, (1 << 31) - 64
+    announce(f"dequant R={R} K={K}")
+    q, s = torch.zeros((R, K), dtype=torch.int8, device=DEV), torch.ones(R, device=DEV)
+    q[:, 0], q[:, K - 1], q[15, 5], q[16, 1 << 30] = 1, 2, 3, 4
+    out = torch.full((R, K), 9.0, dtype=torch.bfloat16, device=DEV)
+    bq.moe_dequant_i8_bf16(q, s, out)
+    sync()
+    assert (out[:, 0] == 1).all() and (out[:, K - 1] == 2).all() and float(out[15, 5]) == 3 and float(out[16, 1 << 30]) == 4
+    out[:, 0], out[:, K - 1], out[15, 5], out[16, 1 << 30] = 0, 0, 0, 0
+    assert not any(part.any() for row in out for part in row.split(1 << 28))
