@@ -704,7 +704,7 @@ __global__ __launch_bounds__(kQuantWaves* WAVE) void quant_h_kernel(
 }
 
 // Rows to 16 x 64 tiles: piece (n, k / 16) of 16 bytes to its place.
-__global__ void prepack_i8_kernel(const i32x4_t* __restrict__ src, size_t pieces, int N, int K,
+__global__ void prepack_i8_kernel(const i32x4_t* __restrict__ src, size_t pieces, int K,
                                   i32x4_t* __restrict__ dst) {
     const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= pieces) return;
@@ -718,10 +718,18 @@ __global__ void prepack_i8_kernel(const i32x4_t* __restrict__ src, size_t pieces
 
 hipError_t launch_prepack_i8(const int8_t* src, int n_exp, int N, int K, int8_t* dst,
                              hipStream_t stream) {
+    // a row tile is K pieces, from one contiguous range to the other: whole tiles, up to 2^30
+    // pieces a launch (a grid of 2^32 threads would be cut without an error)
     const size_t pieces = (size_t)n_exp * N * K / 16;
-    prepack_i8_kernel<<<(unsigned)((pieces + 255) / 256), 256, 0, stream>>>(
-        (const i32x4_t*)src, pieces, N, K, (i32x4_t*)dst);
-    return hipGetLastError();
+    const size_t most = (size_t)K * (K < 1 << 30 ? (1 << 30) / K : 1);
+    for (size_t p0 = 0; p0 < pieces; p0 += most) {
+        const size_t n = pieces - p0 < most ? pieces - p0 : most;
+        prepack_i8_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>((const i32x4_t*)src + p0, n, K,
+                                                                           (i32x4_t*)dst + p0);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 size_t linear_i8_ws_bytes(int, int, int) { return 0; }

@@ -482,7 +482,7 @@ int moe_dequant_i8_bf16(const int8_t* q, const float* scale, int R, int K, uint1
  *   (n/16)*16*K + (k/64)*1024 + ((k%64)/16)*256 + (n%16)*16 + k%16,
  * so a tile is one contiguous kilobyte in the order in which a wave's lanes
  * hold it.  Distinct device buffers, 16-byte aligned; N a multiple of 16, K of
- * 64, n_exp*N*K < 2^40.  Enqueues one kernel. */
+ * 64, n_exp*N*K < 2^40.  Enqueues one kernel for each 2^34 codes. */
 int moe_i8_prepack(const int8_t* src, int n_exp, int N, int K, int8_t* dst, hipStream_t stream);
 
 /* out[m, n] = bf16(a_scale[m] * w_scale[n] * sum_k a[m, k] * w[n, k]).

@@ -216,3 +216,22 @@ def test_dequant_of_few_rows_beyond_one_launch(large):
     assert (out[:, 0] == 1).all() and (out[:, K - 1] == 2).all() and float(out[15, 5]) == 3 and float(out[16, 1 << 30]) == 4
     out[:, 0], out[:, K - 1], out[15, 5], out[16, 1 << 30] = 0, 0, 0, 0
     assert not any(part.any() for row in out for part in row.split(1 << 28))
+
+
+def test_prepack_beyond_one_launch(large):
+    """More than 2^32 pieces of 16 codes."""
+    E, N, K = 65, 16384, 65536
+    announce(f"prepack {E} x {N} x {K}")
+    src = torch.zeros((E, N, K), dtype=torch.int8, device=DEV)
+    dst = torch.full((E, N, K), 7, dtype=torch.int8, device=DEV)
+    some = (0, 15, 16, 33, 64)   # a launch takes 2^30 pieces, 16 matrices
+    for e in some:
+        src[e] = torch.randint(-128, 128, (N, K), dtype=torch.int8, device=DEV, generator=torch.Generator(DEV).manual_seed(e))
+    bq.moe_i8_prepack(src, dst)
+    sync()
+    for e in range(E):
+        if e in some:
+            want = src[e].view(N // 16, 16, K // 64, 4, 16).permute(0, 2, 3, 1, 4).reshape(N, K)
+            assert torch.equal(dst[e], want), e
+        else:
+            assert not dst[e].any(), e
