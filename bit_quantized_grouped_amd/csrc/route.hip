@@ -34,6 +34,8 @@ constexpr int kTopkWaves = 4;          // tokens per workgroup in the top-k kern
 constexpr int kGroupThreads = 1024;    // one grouping workgroup: 16 waves
 constexpr int kGroupWaves = kGroupThreads / WAVE;
 constexpr int kFusedMaxTokens = 64;    // T at or below this: one fused launch
+// Tokens of a selection launch at a wave each: a grid of 2^32 threads is cut without an error.
+constexpr int kTokensALaunch = 1 << 24;
 
 template <int EPL>
 __global__ __launch_bounds__(kTopkWaves * WAVE) void route_topk_kernel(
@@ -823,13 +825,18 @@ hipError_t launch_route_scored(const float* logits, const float* bias, const Sco
     if (const int tokens = seg_tokens_of(T, E, k)) {
         const int n_seg = (T + tokens - 1) / tokens, words = seg_words(E);
         const size_t smem = (size_t)(words + tokens * k) * sizeof(int);
+        // whole segments, up to 2^24 tokens a launch
+        for (size_t t0 = 0; t0 < (size_t)T; t0 += kTokensALaunch) {
+            const int Tc = T - (int)t0 < kTokensALaunch ? T - (int)t0 : kTokensALaunch;
 #define MOE_CALL(N)                                                                       \
-    route_scored_seg_kernel<N><<<n_seg, tokens * WAVE, smem, stream>>>(                   \
-        logits, bias, rule, T, E, k, r.topk_idx, r.topk_w, (uint32_t*)ws)
-        MOE_BY_EPL(MOE_CALL)
+    route_scored_seg_kernel<N><<<(Tc + tokens - 1) / tokens, tokens * WAVE, smem, stream>>>( \
+        logits + t0 * E, bias, rule, Tc, E, k, r.topk_idx + t0 * k, r.topk_w + t0 * k,        \
+        (uint32_t*)ws + t0 / tokens * words)
+            MOE_BY_EPL(MOE_CALL)
 #undef MOE_CALL
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+        }
         const int segs = kGroupThreads / (tokens * k);   // whole segments of 1024 assignments
         const int parts = kGroupThreads / words;
         const size_t smem_s = (size_t)(group_lds_ints(E) + parts * 2 * 4 * words) * sizeof(int);

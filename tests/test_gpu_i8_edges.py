@@ -235,3 +235,40 @@ def test_prepack_beyond_one_launch(large):
             assert torch.equal(dst[e], want), e
         else:
             assert not dst[e].any(), e
+
+
+def check_large_routing(T, E, k, seed):
+    """Scored routing of many tokens against a stable sort of its own choices, which are checked
+    against the logits' order (sigmoid keeps it but for ties, which go to the lower index)."""
+    announce(f"scored routing T={T} E={E} k={k}")
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    lg = torch.rand((T, E), device=DEV, generator=g) * 8 - 4
+    r = bq.DeviceRouting(T, E, k, 64, DEV)
+    for t in (r.topk_idx, r.counts, r.offsets, r.sorted_assign, r.assign_row, r.block_expert, r.block_row, r.n_blocks):
+        t.fill_(-7)
+    ws = torch.empty(max(256, bq.route_workspace_bytes(T, E, k, 64)), dtype=torch.uint8, device=DEV)
+    bq.moe_route_scored(lg, None, bq.ScoreRule("sigmoid"), k, 64, r, ws)
+    sync()
+    score = (1 / (1 + torch.exp(-lg.double()))).float()
+    best = torch.sort(score, dim=1, descending=True, stable=True)[1][:, :k]
+    assert torch.equal(r.topk_idx, best.int())
+    del lg, score, best
+    flat = r.topk_idx.view(-1)
+    counts = torch.bincount(flat, minlength=E)
+    assert torch.equal(r.counts, counts.int())
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64, device=DEV), counts.cumsum(0)])
+    assert torch.equal(r.offsets, offsets.int())
+    order = torch.sort(flat, stable=True)[1]
+    assert torch.equal(r.sorted_assign, order.int())
+    assert torch.equal(r.assign_row[order], torch.arange(T * k, device=DEV, dtype=torch.int32))
+    blocks = (counts + 63) // 64
+    n, start = int(blocks.sum()), blocks.cumsum(0) - blocks
+    assert int(r.n_blocks) == n
+    e = torch.repeat_interleave(torch.arange(E, device=DEV), blocks)
+    row = offsets[e] + 64 * (torch.arange(n, device=DEV) - start[e])
+    assert torch.equal(r.block_expert[:n], e.int()) and torch.equal(r.block_row[:n], row.int())
+    assert (r.block_expert[n:] == -1).all() and (r.block_row[n:] == -1).all()
+
+
+def test_scored_routing_of_tokens_beyond_one_launch(large):
+    check_large_routing((1 << 26) + 3, 2, 1, 0)
