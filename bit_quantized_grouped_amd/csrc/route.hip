@@ -501,19 +501,21 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int block_rows
     if (use_chunk_info(T, E, k)) {
         uint32_t* info = (uint32_t*)ws;
         const int tok = WAVE / k;
-        const int grid_c = (T + tok - 1) / tok;
 #define MOE_TOPK_CHUNK(N, KK)                                                                 \
-    route_topk_chunk_kernel<N, KK><<<grid_c, tok * WAVE, 0, stream>>>(logits, T, E, r.topk_idx, \
-                                                                       r.topk_w, info)
+    route_topk_chunk_kernel<N, KK><<<(Tc + tok - 1) / tok, tok * WAVE, 0, stream>>>(           \
+        logits + t0 * E, Tc, E, r.topk_idx + t0 * k, r.topk_w + t0 * k, info + t0 * k)
 #define MOE_TOPK_CHUNK_K(KK)                          \
         if (epl <= 1) MOE_TOPK_CHUNK(1, KK);          \
         else if (epl <= 2) MOE_TOPK_CHUNK(2, KK);     \
         else if (epl <= 4) MOE_TOPK_CHUNK(4, KK);     \
         else if (epl <= 8) MOE_TOPK_CHUNK(8, KK);     \
         else MOE_TOPK_CHUNK(16, KK);
-        if (k == 4) { MOE_TOPK_CHUNK_K(4) }
-        else if (k == 8) { MOE_TOPK_CHUNK_K(8) }
-        else { MOE_TOPK_CHUNK_K(16) }
+        for (size_t t0 = 0; t0 < (size_t)T; t0 += kTokensALaunch) {
+            const int Tc = T - (int)t0 < kTokensALaunch ? T - (int)t0 : kTokensALaunch;
+            if (k == 4) { MOE_TOPK_CHUNK_K(4) }
+            else if (k == 8) { MOE_TOPK_CHUNK_K(8) }
+            else { MOE_TOPK_CHUNK_K(16) }
+        }
 #undef MOE_TOPK_CHUNK_K
 #undef MOE_TOPK_CHUNK
         const bool stage = n <= kStageMaxAssign;
@@ -525,15 +527,17 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int block_rows
         return hipGetLastError();
     }
     const size_t smem_t = (size_t)kTopkWaves * 3 * k * sizeof(uint32_t);
-    const int grid = (T + kTopkWaves - 1) / kTopkWaves;
 #define MOE_TOPK(N)                                                                         \
-    route_topk_kernel<N><<<grid, kTopkWaves * WAVE, smem_t, stream>>>(logits, T, E, k,     \
-                                                                      r.topk_idx, r.topk_w)
-    if (epl <= 1) MOE_TOPK(1);
-    else if (epl <= 2) MOE_TOPK(2);
-    else if (epl <= 4) MOE_TOPK(4);
-    else if (epl <= 8) MOE_TOPK(8);
-    else MOE_TOPK(16);
+    route_topk_kernel<N><<<(Tc + kTopkWaves - 1) / kTopkWaves, kTopkWaves * WAVE, smem_t, stream>>>( \
+        logits + t0 * E, Tc, E, k, r.topk_idx + t0 * k, r.topk_w + t0 * k)
+    for (size_t t0 = 0; t0 < (size_t)T; t0 += kTokensALaunch) {
+        const int Tc = T - (int)t0 < kTokensALaunch ? T - (int)t0 : kTokensALaunch;
+        if (epl <= 1) MOE_TOPK(1);
+        else if (epl <= 2) MOE_TOPK(2);
+        else if (epl <= 4) MOE_TOPK(4);
+        else if (epl <= 8) MOE_TOPK(8);
+        else MOE_TOPK(16);
+    }
 #undef MOE_TOPK
     const bool stage = n <= kStageMaxAssign;
     const int stage_off = stage ? (int)(group_lds_bytes(E) / sizeof(int)) : 0;

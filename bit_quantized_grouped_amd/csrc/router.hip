@@ -100,9 +100,14 @@ static void launch_router_tiles(const uint16_t* x, int T, int H, const uint16_t*
                                 const uint16_t* w_gate, float* logits, float* gate,
                                 hipStream_t stream) {
     const int rows = E + (w_gate ? 1 : 0);
-    const dim3 grid((T + TM - 1) / TM, (rows + TN - 1) / TN);
-    router_kernel<TM, TN, WAVES, UNROLL><<<grid, WAVES * WAVE, 0, stream>>>(
-        x, T, H, w_router, E, w_gate, logits, gate);
+    // a grid of 2^32 threads in a dimension is cut without an error: up to 2^24 tokens a launch
+    constexpr int kTokens = 1 << 24;
+    for (size_t t0 = 0; t0 < (size_t)T; t0 += kTokens) {
+        const int Tc = T - (int)t0 < kTokens ? T - (int)t0 : kTokens;
+        const dim3 grid((Tc + TM - 1) / TM, (rows + TN - 1) / TN);
+        router_kernel<TM, TN, WAVES, UNROLL><<<grid, WAVES * WAVE, 0, stream>>>(
+            x + t0 * H, Tc, H, w_router, E, w_gate, logits + t0 * E, gate ? gate + t0 : nullptr);
+    }
 }
 
 hipError_t launch_router(const uint16_t* x, int T, int H, const uint16_t* w_router, int E,

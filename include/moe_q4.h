@@ -281,7 +281,7 @@ int moe_combine_gated(const uint16_t* expert_out, const uint16_t* shared_out,
  * x bf16 [T, H], w_router bf16 [E, H], w_gate bf16 [H] (each 16-byte aligned);
  * logits fp32 [T, E] row-major, gate fp32 [T] (4-byte aligned), caller-owned.
  * w_gate and gate are both given or both NULL.  H a multiple of 64,
- * 1 <= E <= 1000.  Enqueues one kernel. */
+ * 1 <= E <= 1000.  Enqueues one kernel for each 2^24 tokens. */
 int moe_router(const uint16_t* x, int T, int H, const uint16_t* w_router, int E,
                const uint16_t* w_gate, float* logits, float* gate, hipStream_t stream);
 

@@ -237,19 +237,22 @@ def test_prepack_beyond_one_launch(large):
             assert not dst[e].any(), e
 
 
-def check_large_routing(T, E, k, seed):
-    """Scored routing of many tokens against a stable sort of its own choices, which are checked
-    against the logits' order (sigmoid keeps it but for ties, which go to the lower index)."""
-    announce(f"scored routing T={T} E={E} k={k}")
+def check_large_routing(T, E, k, seed, scored=True):
+    """Routing of many tokens against a stable sort of its own choices, which are checked
+    against the scores' order (without a rule the logits'); ties go to the lower index."""
+    announce(f"routing T={T} E={E} k={k} scored={scored}")
     g = torch.Generator(device=DEV).manual_seed(seed)
     lg = torch.rand((T, E), device=DEV, generator=g) * 8 - 4
     r = bq.DeviceRouting(T, E, k, 64, DEV)
     for t in (r.topk_idx, r.counts, r.offsets, r.sorted_assign, r.assign_row, r.block_expert, r.block_row, r.n_blocks):
         t.fill_(-7)
     ws = torch.empty(max(256, bq.route_workspace_bytes(T, E, k, 64)), dtype=torch.uint8, device=DEV)
-    bq.moe_route_scored(lg, None, bq.ScoreRule("sigmoid"), k, 64, r, ws)
+    if scored:
+        bq.moe_route_scored(lg, None, bq.ScoreRule("sigmoid"), k, 64, r, ws)
+    else:
+        bq.moe_route(lg, k, 64, r, ws)
     sync()
-    score = (1 / (1 + torch.exp(-lg.double()))).float()
+    score = (1 / (1 + torch.exp(-lg.double()))).float() if scored else lg
     best = torch.sort(score, dim=1, descending=True, stable=True)[1][:, :k]
     assert torch.equal(r.topk_idx, best.int())
     del lg, score, best
@@ -272,3 +275,29 @@ def check_large_routing(T, E, k, seed):
 
 def test_scored_routing_of_tokens_beyond_one_launch(large):
     check_large_routing((1 << 26) + 3, 2, 1, 0)
+
+
+# the selection by waves alone, and with chunk information for the grouping
+@pytest.mark.parametrize("E,k", [(2, 1), (4, 4)])
+def test_routing_of_tokens_beyond_one_launch(large, E, k):
+    check_large_routing((1 << 26) + 3, E, k, 1, scored=False)
+
+
+def test_router_of_tokens_beyond_one_launch(large):
+    T, H = (1 << 28) + 40, 64
+    announce(f"router T={T}")
+    some = [0, (1 << 24) - 1, 1 << 24, T // 2, T - 1]
+    rows = dev(np.random.default_rng(0).normal(size=(len(some), H)), torch.bfloat16)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+    x[some] = rows
+    w, wg = dev(np.random.default_rng(1).normal(size=(1, H)), torch.bfloat16), torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    lg, gate = torch.full((T, 1), 9.0, device=DEV), torch.full((T,), 9.0, device=DEV)
+    bq.moe_router(x, w, lg, wg, gate)
+    sync()
+    want = f64(rows) @ f64(w).T
+    within(f64(lg[some]), want, H * 2.0 ** -23 * (np.abs(f64(rows)) @ np.abs(f64(w)).T), "logits")
+    # a sigmoid's slope is at most 1/4: a quarter of the sum's error, and of exp's (|z| < 32 steps of 2^-23)
+    z = f64(rows).sum(1)
+    within(f64(gate[some]), 1 / (1 + np.exp(-z)), H * 2.0 ** -23 * np.abs(f64(rows)).sum(1) + 2.0 ** -20, "gate")
+    lg[some], gate[some] = 0, 0.5
+    assert not lg.any() and (gate == 0.5).all()
