@@ -599,9 +599,9 @@ __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
 // the tokens are cut into segments of 8 or 16, a workgroup of the selection each, which
 // leaves its segment's counts, one byte per expert (a token takes an expert once, so a
 // count is at most 16), and a grouping workgroup takes whole segments and sums their
-// counts.  Then it scans the experts' totals and places its assignments: wave w owns
+// counts; above kScoredPrefixAssign a launch between the two sums them for all.  Then it scans the experts' totals and places its assignments: wave w owns
 // their 64-assignment chunk w, so rows follow assignment order and the sort is stable.
-// Every workgroup repeats the scan, which costs less than a third launch.  Bound by
+// Every workgroup repeats the scan, which costs less than a launch for it.  Bound by
 // instructions in the selection (about 650 a token) and by the chain of waits in the
 // grouping: 2048 tokens x 8 of 256 take 11.7 us (by segments 12.8), 8192 x 6 of 160 12 + 8
 // (one grouping workgroup: 87 for the latter's grouping).
@@ -636,15 +636,57 @@ __global__ __launch_bounds__(kGroupThreads) void route_scored_seg_kernel(
         seg_counts[(size_t)blockIdx.x * words + i] = (uint32_t)smem_i[i];
 }
 
-// The grouping; seg_counts NULL: counts from the indices, workgroups of `own` assignments.
+// The experts' counts before each grouping workgroup's segments, and at last over all, [n_wg + 1]
+// [4 * words]: a workgroup takes four experts (a word) over all workgroups, 1024 at a time.  Each
+// grouping workgroup summing all segments itself is work by the square of the tokens.
+__global__ __launch_bounds__(kGroupThreads) void route_seg_prefix_kernel(
+    const uint32_t* __restrict__ seg_counts, int words, int segs, int n_seg, int n_wg,
+    int32_t* __restrict__ base) {
+    __shared__ int s_wave[2 * (kGroupWaves + 1)];
+    const int pw = blockIdx.x;
+    int before[4] = {0, 0, 0, 0};
+    for (int g0 = 0; g0 < n_wg; g0 += kGroupThreads) {
+        const int g = g0 + (int)threadIdx.x;
+        // a workgroup's assignments to an expert are at most 1024: halves hold them
+        uint32_t even = 0, odd = 0;
+        if (g < n_wg) {
+            const int end = min(n_seg, (g + 1) * segs);
+            for (int s = g * segs; s < end; s += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = seg_counts[(size_t)min(s + i, end - 1) * words + pw];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t in = s + i < end ? w[i] : 0u;
+                    even += in & 0x00FF00FFu;
+                    odd += (in >> 8) & 0x00FF00FFu;
+                }
+            }
+        }
+        const int cnt[4] = {(int)(even & 0xFFFF), (int)(odd & 0xFFFF), (int)(even >> 16), (int)(odd >> 16)};
+        int ex[4], total[4];
+        block_exclusive_scan2(cnt[0], cnt[1], s_wave, &ex[0], &ex[1], &total[0], &total[1]);
+        block_exclusive_scan2(cnt[2], cnt[3], s_wave, &ex[2], &ex[3], &total[2], &total[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (g < n_wg) base[((size_t)g * words + pw) * 4 + i] = before[i] + ex[i];
+            before[i] += total[i];
+        }
+    }
+    if (threadIdx.x < 4) base[((size_t)n_wg * words + pw) * 4 + threadIdx.x] = before[threadIdx.x];
+}
+
+// The grouping; seg_counts NULL: counts from the indices, workgroups of `own` assignments;
+// base: from route_seg_prefix_kernel.
 __global__ __launch_bounds__(kGroupThreads) void route_seg_scatter_kernel(
-    const int32_t* __restrict__ topk_idx, const uint32_t* __restrict__ seg_counts, int n, int E,
-    int own, int segs, int n_seg, int block_rows, int max_blocks, RoutingDev r) {
+    const int32_t* __restrict__ topk_idx, const uint32_t* __restrict__ seg_counts,
+    const int32_t* __restrict__ base, int n, int E, int own, int segs, int n_seg, int block_rows,
+    int max_blocks, RoutingDev r) {
     extern __shared__ int s_hist[];   // [kGroupWaves][E], the scan's wave totals, [parts][2][4*words]
     int* s_wave = s_hist + kGroupWaves * E;
     int* s_sum = s_wave + 2 * (kGroupWaves + 1);
     const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
-    const int words = seg_words(E), parts = seg_counts ? kGroupThreads / words : 1;
+    const int words = seg_words(E), parts = seg_counts && !base ? kGroupThreads / words : 1;
     const int seg0 = blockIdx.x * segs;   // own: the assignments of its segments
     // this wave's chunk of the workgroup's assignments
     const int a = blockIdx.x * own + wave * WAVE + lane;
@@ -652,7 +694,12 @@ __global__ __launch_bounds__(kGroupThreads) void route_seg_scatter_kernel(
     const int mine = valid ? topk_idx[a] : 0;
     // four experts' counts before seg0 and in all, by parts of the segments
     const int part = tid / words, pw = tid - part * words;
-    if (!seg_counts) {
+    if (base) {
+        for (int i = tid; i < 4 * words; i += kGroupThreads) {
+            s_sum[i] = base[(size_t)blockIdx.x * 4 * words + i];
+            s_sum[4 * words + i] = base[(size_t)gridDim.x * 4 * words + i];
+        }
+    } else if (!seg_counts) {
         for (int i = tid; i < 8 * words; i += kGroupThreads) s_sum[i] = 0;
         __syncthreads();
         for (int i = tid; i < n; i += 8 * kGroupThreads) {   // eight loads in flight
@@ -786,16 +833,30 @@ static int seg_tokens_of(int T, int E, int k) {
 // take longer on one CU (10.0 against 8.4; 8 tokens 8.2 and 8.4).
 constexpr int kScoredFusedTokens = 8;
 
+// Whole segments that a grouping workgroup of 1024 assignments takes.
+static int group_segs(int tokens, int k) { return kGroupThreads / (tokens * k); }
+
+// Assignments above which the segments' counts are summed by a launch of its own (us of the call
+// without and with it, 256 experts, k 8: 65536 20.3 and 19.9, 131072 31.4 and 26.6, 1048576 332 and
+// 134, 4194304 3814 and 513; 60, k 4: 65536 14.7 and 17.0, 131072 21.1 and 20.9, 4194304 2100 and 392).
+constexpr long long kScoredPrefixAssign = 65536;
+static bool use_prefix(long long n) { return n > kScoredPrefixAssign; }
+
 size_t scored_ws_bytes(int T, int E, int k) {
     const int tokens = seg_tokens_of(T, E, k);
-    return tokens ? seg_bytes(T, E, tokens) : 0;
+    if (!tokens || tokens * k > kGroupThreads) return 0;   // k above kScoredMaxK is refused
+    const size_t counts = seg_bytes(T, E, tokens);
+    if (!use_prefix((long long)T * k)) return counts;
+    const int n_seg = (T + tokens - 1) / tokens, segs = group_segs(tokens, k);
+    const size_t n_wg = (n_seg + segs - 1) / segs;
+    return counts + align_up((n_wg + 1) * 4 * seg_words(E) * sizeof(int32_t), 256);
 }
 
 static hipError_t launch_count_scatter(int n, int E, int block_rows, int max_blocks, const RoutingDev& r,
                                        hipStream_t stream) {
     const size_t smem = (size_t)(group_lds_ints(E) + 8 * seg_words(E)) * sizeof(int);
     route_seg_scatter_kernel<<<(n + kGroupThreads - 1) / kGroupThreads, kGroupThreads, smem, stream>>>(
-        r.topk_idx, nullptr, n, E, kGroupThreads, 0, 0, block_rows, max_blocks, r);
+        r.topk_idx, nullptr, nullptr, n, E, kGroupThreads, 0, 0, block_rows, max_blocks, r);
     return hipGetLastError();
 }
 
@@ -841,11 +902,19 @@ hipError_t launch_route_scored(const float* logits, const float* bias, const Sco
             const hipError_t err = hipGetLastError();
             if (err != hipSuccess) return err;
         }
-        const int segs = kGroupThreads / (tokens * k);   // whole segments of 1024 assignments
-        const int parts = kGroupThreads / words;
+        const int segs = group_segs(tokens, k), n_wg = (n_seg + segs - 1) / segs;
+        int32_t* base = nullptr;
+        if (use_prefix(n)) {
+            base = (int32_t*)((char*)ws + seg_bytes(T, E, tokens));
+            route_seg_prefix_kernel<<<words, kGroupThreads, 0, stream>>>((const uint32_t*)ws, words, segs,
+                                                                         n_seg, n_wg, base);
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+        }
+        const int parts = base ? 1 : kGroupThreads / words;
         const size_t smem_s = (size_t)(group_lds_ints(E) + parts * 2 * 4 * words) * sizeof(int);
-        route_seg_scatter_kernel<<<(n_seg + segs - 1) / segs, kGroupThreads, smem_s, stream>>>(
-            r.topk_idx, (const uint32_t*)ws, n, E, segs * tokens * k, segs, n_seg, block_rows,
+        route_seg_scatter_kernel<<<n_wg, kGroupThreads, smem_s, stream>>>(
+            r.topk_idx, (const uint32_t*)ws, base, n, E, segs * tokens * k, segs, n_seg, block_rows,
             max_blocks, r);
         return hipGetLastError();
     }

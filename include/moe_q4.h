@@ -529,7 +529,7 @@ typedef struct {
  * logit shares the softmax with the row's other +inf.  A row of -inf alone has
  * score 0 everywhere: it keeps k experts, of weight 0.
  * k <= 64 and k <= topk_groups * (E / n_groups); otherwise arguments and workspace
- * (moe_route_workspace_bytes) are moe_route's.  One or two kernels, and one
+ * (moe_route_workspace_bytes) are moe_route's.  One to three kernels, and one
  * more for each 2^24 tokens. */
 int moe_route_scored(const float* logits, const float* bias, const moe_score_rule* rule, int T,
                      int E, int k, int block_rows, const moe_routing* out, void* ws,

@@ -301,3 +301,33 @@ def test_router_of_tokens_beyond_one_launch(large):
     within(f64(gate[some]), 1 / (1 + np.exp(-z)), H * 2.0 ** -23 * np.abs(f64(rows)).sum(1) + 2.0 ** -20, "gate")
     lg[some], gate[some] = 0, 0.5
     assert not lg.any() and (gate == 0.5).all()
+
+
+# ---- many tokens: work that grows with them ----
+
+# one round of the sums over workgroups and several, counts of one word and of many
+@pytest.mark.parametrize("T,E,k", [(8193, 256, 8), (65537, 2, 1), (33333, 40, 3), (70001, 1000, 8), (300000, 60, 4), (1100000, 1, 1),
+                                   (1 << 22, 64, 8)])
+def test_scored_routing_of_many_tokens(large, T, E, k):
+    check_large_routing(T, E, k, T)
+
+
+def test_scored_routings_time_follows_its_tokens(large):
+    """Sixteen times the tokens take about 15 times as long; where every grouping workgroup sums
+    all tokens' counts itself, 118 times."""
+    def best(T):
+        E, k = 256, 8
+        lg = torch.randn((T, E), device=DEV)
+        r = bq.DeviceRouting(T, E, k, 64, DEV)
+        ws = torch.empty(bq.route_workspace_bytes(T, E, k, 64), dtype=torch.uint8, device=DEV)
+        times = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                bq.moe_route_scored(lg, None, bq.ScoreRule("sigmoid"), k, 64, r, ws)
+            b.record()
+            sync()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    assert best(1 << 20) < 64 * best(1 << 16)
