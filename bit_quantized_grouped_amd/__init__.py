@@ -1205,6 +1205,10 @@ class MoeLayerI8:
         the block's residual "sum", the normed tokens "normed", their codes "q" and "q_scale",
         "logits" and the layer's "y"."""
         T, H = _x_of(x)
+        if H != self.H or x.get_device() != self._mats[0].codes.get_device():
+            raise ValueError(f"x: {(T, H)} on {x.device}, the layer is H={self.H} on "
+                             f"{self._mats[0].codes.device}")
+        _tensor(w_router, "w_router", BF16, (self.E, H))   # the norm is enqueued before the router checks
         b = self.buffers(T)
         if "sum" not in b:
             d = self.device

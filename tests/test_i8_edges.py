@@ -1,0 +1,34 @@
+"""Calls of the 8-bit layer object and binding that went wrong without an error, on the CPU (no GPU
+needed: every path ends at the device check or before)."""
+import pytest
+import torch
+
+import bit_quantized_grouped_amd as bq
+
+BF16, F32, I8 = torch.bfloat16, torch.float32, torch.int8
+T, H, I, E, k = 8, 256, 128, 16, 2
+
+
+def i8mat(n, N, K, device="cpu"):
+    return bq.DeviceI8Mat(torch.zeros((n, N, K), dtype=I8, device=device), torch.zeros((n, N), device=device))
+
+
+def layer(**kw):
+    mats = [i8mat(E, I, H), i8mat(E, I, H), i8mat(E, H, I)] + [None] * 3
+    return bq.MoeLayerI8(mats, H, I, 0, E, k, "cpu", **kw)
+
+
+def block(la, width=H, T=T):
+    return la.forward_block(torch.zeros((T, width), dtype=BF16), None, torch.zeros(width, dtype=BF16),
+                            torch.zeros((E, width), dtype=BF16))
+
+
+def test_a_block_of_another_width_leaves_no_buffers_behind():
+    la = layer()
+    with pytest.raises(ValueError, match="the layer is H=256"):
+        block(la, width=320)
+    with pytest.raises(ValueError, match="w_router: shape"):
+        la.forward_block(torch.zeros((T, H), dtype=BF16), None, torch.zeros(H, dtype=BF16), torch.zeros((E + 1, H), dtype=BF16))
+    with pytest.raises(ValueError, match="device tensors"):   # all of it fits: the CPU is refused last
+        block(la)
+    assert la.buffers(T)["sum"].shape == (T, H)
