@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections.abc import Mapping
+from types import MappingProxyType
 
 import torch
 
@@ -1155,7 +1157,12 @@ class MoeLayerI8:
         n = T * self.k
         return 16 if n < 8 * self.E else 32 if n < 32 * self.E else 64
 
-    def buffers(self, T: int) -> dict:
+    def buffers(self, T: int) -> Mapping:
+        """The buffers that calls for T tokens use, by name; made at the first use.  The mapping is
+        read-only: a call keeps the buffers' addresses."""
+        return MappingProxyType(self._buffers(T))
+
+    def _buffers(self, T: int) -> dict:
         if T not in self._bufs:
             rows = self.rows_for(T)
             d, bf = self.device, dict(dtype=torch.bfloat16, device=self.device)
@@ -1178,7 +1185,7 @@ class MoeLayerI8:
         stream then waits for the current one."""
         shape = T, H = _two_dims(x, "x", "[T, H]")
         d = x.get_device()
-        b = self.buffers(T)
+        b = self._buffers(T)
         y = b["y"] if out is None else out
         if T not in self._fixed:   # the arguments that belong to this object, checked once
             self._fixed[T] = (
@@ -1209,7 +1216,7 @@ class MoeLayerI8:
             raise ValueError(f"x: {(T, H)} on {x.device}, the layer is H={self.H} on "
                              f"{self._mats[0].codes.device}")
         _tensor(w_router, "w_router", BF16, (self.E, H))   # the norm is enqueued before the router checks
-        b = self.buffers(T)
+        b = self._buffers(T)
         if "sum" not in b:
             d = self.device
             b["sum"], b["normed"] = (torch.empty((T, H), dtype=torch.bfloat16, device=d)

@@ -32,3 +32,13 @@ def test_a_block_of_another_width_leaves_no_buffers_behind():
     with pytest.raises(ValueError, match="device tensors"):   # all of it fits: the CPU is refused last
         block(la)
     assert la.buffers(T)["sum"].shape == (T, H)
+
+
+def test_buffers_cannot_be_replaced():
+    """A call keeps their addresses: a replaced entry would leave it writing to freed memory."""
+    la = layer()
+    b = la.buffers(T)
+    with pytest.raises(TypeError, match="item assignment"):
+        b["expert_out"] = torch.zeros((T * k, H), dtype=BF16)
+    assert dict(b).keys() == {"routing", "route_ws", "gemm_ws", "expert_out", "shared_out", "y"}
+    assert la.buffers(T)["y"] is b["y"]
