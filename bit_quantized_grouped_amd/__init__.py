@@ -746,8 +746,18 @@ def _wait_for_allocations(stream, device):
         stream.wait_stream(torch.cuda.current_stream(device))
 
 
-class DeviceI8Mat:
-    """One set of 8-bit matrices [n_exp, N, K] resident on the device."""
+class _Fixed:
+    """An object whose C struct, its last attribute, is made once: no attribute changes after it."""
+
+    def __setattr__(self, name, value):
+        if "struct" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new {type(self).__name__}")
+        super().__setattr__(name, value)
+
+
+class DeviceI8Mat(_Fixed):
+    """One set of 8-bit matrices [n_exp, N, K] resident on the device.  Values may be written into
+    its tensors; another tensor takes another object."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, layout: int = LAYOUT_ROWS):
         """codes int8 [n_exp, N, K] (LAYOUT_TILES: the bytes moe_i8_prepack writes, in the same
@@ -797,9 +807,10 @@ class DeviceI8Mat:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-class ScoreRule:
+class ScoreRule(_Fixed):
     """Selection rule of moe_route_scored: score "softmax" or "sigmoid", groups of experts with
-    their worth "top2" or "max", weights renormalised or not, and a factor on them."""
+    their worth "top2" or "max", weights renormalised or not, and a factor on them.  Another rule
+    is another object."""
 
     def __init__(self, score: str = "softmax", n_groups: int = 1, topk_groups: int | None = None,
                  group_score: str = "top2", renormalise: bool = True, scale: float = 1.0):

@@ -42,3 +42,16 @@ def test_buffers_cannot_be_replaced():
         b["expert_out"] = torch.zeros((T * k, H), dtype=BF16)
     assert dict(b).keys() == {"routing", "route_ws", "gemm_ws", "expert_out", "shared_out", "y"}
     assert la.buffers(T)["y"] is b["y"]
+
+
+@pytest.mark.parametrize("make,name,value", [
+    (lambda: i8mat(E, I, H), "codes", torch.zeros((E, I, H), dtype=I8)), (lambda: i8mat(E, I, H), "scales", torch.ones(E, I)),
+    (lambda: i8mat(E, I, H), "layout", 1), (lambda: i8mat(E, I, H), "struct", None), (bq.ScoreRule, "scale", 2.0),
+    (bq.ScoreRule, "renormalise", False), (bq.ScoreRule, "n_groups", 4)])
+def test_what_a_struct_was_made_of_stays(make, name, value):
+    """The C call sees the struct alone: a new attribute would be ignored, or leave a freed address."""
+    obj = make()
+    before = getattr(obj, name)
+    with pytest.raises(AttributeError, match="is fixed"):
+        setattr(obj, name, value)
+    assert getattr(obj, name) is before
