@@ -1130,7 +1130,12 @@ class MoeLayer:
 
 
 class MoeLayerI8:
-    """Device-resident 8-bit weights of one layer plus per-call buffers for T tokens."""
+    """Device-resident 8-bit weights of one layer plus per-call buffers for T tokens.
+
+    Buffers are kept for every T that was called, since a captured graph replays on them: about
+    T * (k * (max(5 * I, I + H) + 2 * H) + 4 * H) bytes, and as much again for the shared
+    expert and forward_block (130 MB at 2048 tokens of H 2048, I 512, k 8).  A caller of many
+    lengths pads them to a few, or gives buffers back by release()."""
 
     def __init__(self, mats, H: int, I: int, I_sh: int, E: int, k: int, device,
                  block_rows: int | None = None, rule: ScoreRule | None = None, score_bias=None):
@@ -1172,6 +1177,16 @@ class MoeLayerI8:
         """The buffers that calls for T tokens use, by name; made at the first use.  The mapping is
         read-only: a call keeps the buffers' addresses."""
         return MappingProxyType(self._buffers(T))
+
+    def release(self, T: int | None = None):
+        """Gives the buffers for T tokens (None: for all) back to torch's allocator, when the work
+        on them has ended: the host waits for the device.  What calls returned must not be read
+        and a graph captured over them not be replayed afterwards; a later call makes new ones."""
+        if self._mats[0].codes.is_cuda:
+            torch.cuda.synchronize(self._mats[0].codes.device)
+        for t in list(self._bufs) if T is None else [T]:
+            self._fixed.pop(t, None)
+            self._bufs.pop(t, None)
 
     def _buffers(self, T: int) -> dict:
         if T not in self._bufs:

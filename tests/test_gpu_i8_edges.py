@@ -331,3 +331,26 @@ def test_scored_routings_time_follows_its_tokens(large):
             times.append(a.elapsed_time(b))
         return min(times)
     assert best(1 << 20) < 64 * best(1 << 16)
+
+
+# ---- the layer object's buffers ----
+
+def test_release_gives_the_memory_back(large):
+    H, I, I_sh, E, k = 256, 128, 64, 16, 2
+    g = np.random.default_rng(8)
+    mats = [i8mat(q, s, 1) for q, s in layer_weights(g, E, H, I, I_sh)]
+    layer = bq.MoeLayerI8(mats, H, I, I_sh, E, k, DEV)
+    x, sx = dev(codes(g, 4000, H), torch.int8), dev(g.random(4000), torch.float32) * 0.02
+    lg = dev(g.normal(size=(4000, E)), torch.float32)
+    run = lambda T, **kw: layer.forward(x[:T], sx[:T], lg[:T], **kw)["y"].clone()  # noqa: E731
+    want = run(70)
+    start = torch.cuda.memory_allocated()
+    run(4000)
+    run(4000, stream=torch.cuda.Stream())   # still on its way when the buffers go
+    assert torch.cuda.memory_allocated() - start > 8_000_000
+    layer.release(4000)
+    assert torch.cuda.memory_allocated() - start < 1_000_000
+    layer.release()
+    got = run(70)
+    sync()
+    assert torch.equal(got, want)

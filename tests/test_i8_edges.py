@@ -1,5 +1,7 @@
 """Calls of the 8-bit layer object and binding that went wrong without an error, on the CPU (no GPU
 needed: every path ends at the device check or before)."""
+import weakref
+
 import pytest
 import torch
 
@@ -55,3 +57,14 @@ def test_what_a_struct_was_made_of_stays(make, name, value):
     with pytest.raises(AttributeError, match="is fixed"):
         setattr(obj, name, value)
     assert getattr(obj, name) is before
+
+
+def test_released_buffers_are_freed_and_made_anew():
+    la = layer()
+    refs = {t: weakref.ref(la.buffers(t)["expert_out"]) for t in (3, T, 20)}
+    la.release(T)
+    assert refs[T]() is None and refs[3]() is not None and refs[20]() is not None
+    assert la.buffers(T)["y"].shape == (T, H)
+    la.release(7)   # never made
+    la.release()
+    assert all(r() is None for r in refs.values()) and la.buffers(3)["y"].shape == (3, H)
