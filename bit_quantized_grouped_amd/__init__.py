@@ -170,6 +170,9 @@ def _ptr(t):
 # any C call; they raise TypeError (dtype) or ValueError (everything else).
 # ---------------------------------------------------------------------------
 
+_INT_MAX = 2 ** 31 - 1   # ctypes passes the low 32 bits of a larger size without an error
+
+
 def _tensor(t, name, dtype=None, shape=None):
     """t must be a contiguous device tensor, of `dtype` and `shape` when given."""
     if not isinstance(t, torch.Tensor):
@@ -343,6 +346,8 @@ def abi_version() -> int:
 
 
 def route_max_blocks(T, E, k, block_rows) -> int:
+    if max(T, E, k, block_rows) > _INT_MAX:
+        raise ValueError(f"T={T} E={E} k={k} block_rows={block_rows}: a size passes 32 bits")
     v = lib().moe_route_max_blocks(T, E, k, block_rows)
     _check(min(v, 0), "moe_route_max_blocks")
     return v
@@ -711,6 +716,8 @@ def _two_dims(t, name, dims):
     try:
         shape = t.shape
         if len(shape) == 2:
+            if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+                raise ValueError(f"{name}: shape {tuple(shape)} passes 32-bit sizes")
             return shape
     except AttributeError:
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}") from None
@@ -765,6 +772,8 @@ class DeviceI8Mat(_Fixed):
         _tensor(codes, "codes", I8)
         if codes.dim() != 3:
             raise ValueError("codes: expected [n_exp, N, K]")
+        if max(codes.shape) > _INT_MAX:
+            raise ValueError(f"codes: shape {tuple(codes.shape)} passes 32-bit sizes")
         _tensor(scales, "scales", F32, codes.shape[:2])
         if layout not in (LAYOUT_ROWS, LAYOUT_TILES):
             raise ValueError("layout: expected LAYOUT_ROWS or LAYOUT_TILES")
@@ -888,6 +897,8 @@ def moe_i8_prepack(src: torch.Tensor, dst: torch.Tensor, stream=None):
     _tensor(src, "src", I8)
     if src.dim() != 3:
         raise ValueError("src: expected [n_exp, N, K]")
+    if max(src.shape) > _INT_MAX:
+        raise ValueError(f"src: shape {tuple(src.shape)} passes 32-bit sizes")
     d = src.get_device()
     _run(lib().moe_i8_prepack, "moe_i8_prepack", d, stream, src.data_ptr(), *src.shape,
          _arg(dst, "dst", I8, src.shape, d))

@@ -68,3 +68,26 @@ def test_released_buffers_are_freed_and_made_anew():
     la.release(7)   # never made
     la.release()
     assert all(r() is None for r in refs.values()) and la.buffers(3)["y"].shape == (3, H)
+
+
+def wide(rows, cols, dtype):
+    return torch.empty((rows, cols), dtype=dtype, device="meta")
+
+
+#: 2^32 and some: its low 32 bits are a valid size.
+BIG = (1 << 32) + 64
+
+
+@pytest.mark.parametrize("call", [
+    lambda: bq.moe_dequant_i8_bf16(wide(1, BIG, I8), torch.zeros(1), wide(1, BIG, BF16)),
+    lambda: bq.moe_quant_i8(wide(BIG, 64, BF16), wide(BIG, 64, I8), wide(1, BIG, F32)[0]),
+    lambda: bq.moe_norm_i8(wide(BIG, 64, BF16), None, torch.zeros(64, dtype=BF16), 1e-6, y=wide(BIG, 64, BF16)),
+    lambda: bq.moe_linear_i8(wide(BIG, 64, I8), wide(1, BIG, F32)[0], i8mat(1, 16, 64), wide(BIG, 16, BF16)),
+    lambda: bq.moe_route_scored(wide(BIG, 1, F32), None, bq.ScoreRule(), 1, 32, None, torch.zeros(256)),
+    lambda: i8mat(1, BIG, 64, "meta"),
+    lambda: bq.moe_i8_prepack(*[torch.empty((1, 16, BIG), dtype=I8, device="meta")] * 2),
+    lambda: bq.DeviceRouting(BIG, 1, 1, 32, "meta"), lambda: bq.DeviceRouting(1, BIG, 1, 32, "meta")])
+def test_sizes_past_32_bits_are_refused(call):
+    """ctypes would pass their low 32 bits, and the call work on a part of its tensors."""
+    with pytest.raises(ValueError, match="32"):
+        call()
