@@ -1249,18 +1249,22 @@ class MoeLayerI8:
         the block's residual "sum", the normed tokens "normed", their codes "q" and "q_scale",
         "logits" and the layer's "y"."""
         T, H = _x_of(x)
-        if H != self.H or x.get_device() != self._mats[0].codes.get_device():
+        d = x.get_device()
+        if H != self.H or d != self._mats[0].codes.get_device():
             raise ValueError(f"x: {(T, H)} on {x.device}, the layer is H={self.H} on "
                              f"{self._mats[0].codes.device}")
         _tensor(w_router, "w_router", BF16, (self.E, H))   # the norm is enqueued before the router checks
+        if d >= 0 and _current_device() != d:   # moe_router launches on the current device
+            with torch.cuda.device(d):
+                return self.forward_block(x, residual, norm_weight, w_router, eps, stream)
         b = self._buffers(T)
         if "sum" not in b:
-            d = self.device
-            b["sum"], b["normed"] = (torch.empty((T, H), dtype=torch.bfloat16, device=d)
+            on = self.device
+            b["sum"], b["normed"] = (torch.empty((T, H), dtype=torch.bfloat16, device=on)
                                      for _ in range(2))
-            b["q"] = torch.empty((T, H), dtype=I8, device=d)
-            b["q_scale"] = torch.empty(T, dtype=F32, device=d)
-            b["logits"] = torch.empty((T, self.E), dtype=F32, device=d)
+            b["q"] = torch.empty((T, H), dtype=I8, device=on)
+            b["q_scale"] = torch.empty(T, dtype=F32, device=on)
+            b["logits"] = torch.empty((T, self.E), dtype=F32, device=on)
             _wait_for_allocations(stream, x.device)
         moe_norm_i8(x, residual, norm_weight, eps, b["sum"], b["normed"], b["q"], b["q_scale"],
                     stream)

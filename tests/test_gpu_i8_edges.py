@@ -354,3 +354,39 @@ def test_release_gives_the_memory_back(large):
     got = run(70)
     sync()
     assert torch.equal(got, want)
+
+
+def test_block_runs_on_its_tensors_device(monkeypatch):
+    """Every launch of the block with the tensors' device as the current one (here the other device
+    is only claimed to be current: the test needs no second GPU)."""
+    require_gpu()
+    H, I, E, k, T = 256, 128, 16, 2, 5
+    g = np.random.default_rng(8)
+    mats = [i8mat(q, s, 1) for q, s in layer_weights(g, E, H, I, 0)] + [None] * 3
+    layer = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV)
+    x, r, w = norm_inputs(T, H, 0)
+    router = dev(g.normal(size=(E, H)) * H ** -0.5, torch.bfloat16)
+    want = layer.forward_block(x, r, w, router)["y"].clone()
+    current, seen, run_router = [1], [], bq.moe_router
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    def routed(*args, **kw):
+        seen.append(current[-1])
+        run_router(*args, **kw)
+
+    monkeypatch.setattr(bq.torch.cuda, "device", Device)
+    monkeypatch.setattr(bq, "_current_device", lambda: current[-1])
+    monkeypatch.setattr(bq, "moe_router", routed)
+    y = layer.forward_block(x, r, w, router)["y"]
+    monkeypatch.undo()
+    sync()
+    assert seen == [0] and current == [1] and torch.equal(y, want)
