@@ -390,3 +390,22 @@ def test_block_runs_on_its_tensors_device(monkeypatch):
     monkeypatch.undo()
     sync()
     assert seen == [0] and current == [1] and torch.equal(y, want)
+
+
+def test_one_tokens_rows_are_a_permutation_whatever_its_logits(large):
+    """NaN of all bits sorts as no expert at all: the selection then repeats the first, and a
+    product over the routing must still find a row for each of its assignments."""
+    H = I = 64
+    E, k = 8, 4
+    g = np.random.default_rng(4)
+    mats = [i8mat(q, s, 1) for q, s in layer_weights(g, E, H, I, 0)] + [None] * 3
+    layer = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV)
+    lg = torch.full((1, E), -1, dtype=torch.int32, device=DEV).view(torch.float32)
+    lg[0, 5] = 1.0
+    r = layer.buffers(1)["routing"]
+    r.sorted_assign.fill_(-7)
+    layer.forward(dev(codes(g, 1, H), torch.int8), torch.ones(1, device=DEV), lg)
+    sync()
+    assert int(r.topk_idx.min()) >= 0 and int(r.topk_idx.max()) < E
+    assert sorted(r.sorted_assign.tolist()) == list(range(k)) == sorted(r.assign_row.tolist())
+    assert [r.assign_row[a].item() for a in r.sorted_assign.tolist()] == list(range(k))
