@@ -226,8 +226,7 @@ __device__ __forceinline__ void score_topk_token(const float* __restrict__ row,
 
 // Routing arrays of one token from its k chosen experts and weights in LDS, by all
 // `threads` threads of a workgroup (the experts differ, so an assignment's row is
-// the number of chosen experts below its own; moe_route's selection repeats one where
-// logits are NaN of all bits, and the rows stay a permutation).
+// the number of chosen experts below its own).
 __device__ __forceinline__ void write_one_token(const RoutingDev& r, int E, int k, int max_blocks,
                                                 const int* s_idx, const float* s_w, int tid,
                                                 int threads) {
@@ -243,7 +242,7 @@ __device__ __forceinline__ void write_one_token(const RoutingDev& r, int E, int 
     for (int j = tid; j < k; j += threads) {
         const int e = s_idx[j];
         int row = 0;
-        for (int i = 0; i < k; ++i) row += s_idx[i] < e || (s_idx[i] == e && i < j) ? 1 : 0;
+        for (int i = 0; i < k; ++i) row += s_idx[i] < e ? 1 : 0;
         r.topk_idx[j] = e;
         r.topk_w[j] = s_w[j];
         r.sorted_assign[row] = j;

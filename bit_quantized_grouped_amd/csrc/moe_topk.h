@@ -11,10 +11,12 @@ namespace moeq4 {
 // 32-step radix select followed by an O(k^2) ranking.
 constexpr int kRoundsMaxK = 16;
 
-// Order-preserving map of a finite float to uint32 (-0.0 folded onto +0.0).
+// Order-preserving map of a finite float to uint32 (-0.0 folded onto +0.0).  Never 0, which
+// marks used and absent experts: NaN of all bits would give it, and its expert be chosen twice
+// or not at all.
 __device__ __forceinline__ uint32_t float_key(float v) {
     const uint32_t u = __builtin_bit_cast(uint32_t, v + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (u & 0x80000000u) ? max(~u, 1u) : (u | 0x80000000u);
 }
 
 __device__ __forceinline__ int wave_popc_ge(uint32_t key, uint32_t th, bool valid) {

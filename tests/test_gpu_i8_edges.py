@@ -409,3 +409,31 @@ def test_one_tokens_rows_are_a_permutation_whatever_its_logits(large):
     assert int(r.topk_idx.min()) >= 0 and int(r.topk_idx.max()) < E
     assert sorted(r.sorted_assign.tolist()) == list(range(k)) == sorted(r.assign_row.tolist())
     assert [r.assign_row[a].item() for a in r.sorted_assign.tolist()] == list(range(k))
+
+
+# one launch, chunk information and radix selection; with the layer's counted indices
+@pytest.mark.parametrize("T,k", [(1, 4), (3, 8), (70, 8), (70, 6), (20, 20), (70, 20)])
+@pytest.mark.parametrize("layer_call", [False, True])
+def test_no_expert_twice_whatever_the_logits(T, k, layer_call):
+    """Rows of NaN, of all bits and of others, with a few numbers: the chosen experts differ."""
+    require_gpu()
+    H = I = 64
+    E = 24
+    g = np.random.default_rng(T + k)
+    bits = g.choice(np.array([-1, -1, -1, 0x7FC00000, -0x400000, 0x7F800001], np.int32), (T, E))
+    bits[:, 7] = np.float32(1.5).view(np.int32)
+    bits[0] = -1
+    lg = dev(bits, torch.int32).view(torch.float32)
+    mats = [i8mat(q, s, 1) for q, s in layer_weights(g, E, H, I, 0)] + [None] * 3
+    layer = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV)
+    b = layer.buffers(T)
+    r = b["routing"]
+    r.sorted_assign.fill_(-7)
+    if layer_call:
+        layer.forward(dev(codes(g, T, H), torch.int8), torch.ones(T, device=DEV), lg)
+    else:
+        bq.moe_route(lg, k, r.block_rows, r, b["route_ws"])
+    sync()
+    idx = r.topk_idx.cpu().numpy()
+    assert idx.min() >= 0 and idx.max() < E and all(len(set(row)) == k for row in idx.tolist())
+    assert sorted(r.sorted_assign.tolist()) == list(range(T * k)) == sorted(r.assign_row.tolist())
