@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import bit_quantized_grouped_amd as bq
-from gpu_cases import DEV, announce, require_gpu
+from gpu_cases import DEV, announce, assert_routing_matches, require_gpu
 from oracle import i8_oracle as ref
 from test_gpu_i8 import (EPS, HALF, PROD_SHARE, check_norm, codes, dev, f64, i8mat, layer_weights, norm_inputs, sync,
                          within)
@@ -437,3 +437,36 @@ def test_no_expert_twice_whatever_the_logits(T, k, layer_call):
     idx = r.topk_idx.cpu().numpy()
     assert idx.min() >= 0 and idx.max() < E and all(len(set(row)) == k for row in idx.tolist())
     assert sorted(r.sorted_assign.tolist()) == list(range(T * k)) == sorted(r.assign_row.tolist())
+
+
+# ---- the layer's routing without a rule ----
+
+ROUTED = [  # T, E, k: one launch, counted indices, and above 32768 assignments; each count of experts a lane;
+    # k on both sides of the radix selection
+    (16, 256, 8), (17, 256, 8), (512, 256, 8), (4096, 256, 8), (4097, 256, 8), (300, 128, 6), (100, 500, 20), (40, 1000, 10),
+    (64, 1000, 64), (33, 64, 16), (33, 64, 17), (2048, 1, 1), (70, 3, 3), (2100, 130, 9), (4096, 600, 8), (32768, 32, 1),
+    (32769, 32, 1)]
+
+
+@pytest.mark.parametrize("T,E,k", ROUTED)
+@pytest.mark.parametrize("block_rows", [16, 32, 64])
+def test_layers_routing_without_a_rule(T, E, k, block_rows):
+    """moe_layer_i8's own routing arrays, with tied logits and tokens that all choose alike."""
+    require_gpu()
+    announce(f"layer routing T={T} E={E} k={k} rows={block_rows}")
+    H = I = 64
+    g = np.random.default_rng(T + E)
+    rnd = lambda *s: dev(codes(g, *s), torch.int8)  # noqa: E731
+    mats = [bq.DeviceI8Mat(rnd(E, 64, 64), torch.full((E, 64), 1e-3, device=DEV)) for _ in range(3)] + [None] * 3
+    layer = bq.MoeLayerI8(mats, H, I, 0, E, k, DEV, block_rows=block_rows)
+    x, sx = rnd(T, H), torch.full((T,), 0.02, device=DEV)
+    lg = g.normal(size=(T, E)).astype(np.float32)
+    alike = np.tile(lg[:1], (T, 1))
+    tied = np.round(lg)
+    ys = []
+    for values in (lg, tied, alike, lg):
+        got = layer.forward(x, sx, dev(values, torch.float32))
+        sync()
+        assert_routing_matches(got["routing"].to_host(), values, k, block_rows)
+        ys.append(got["y"].clone())
+    assert torch.equal(ys[0], ys[3])
