@@ -786,11 +786,15 @@ class DeviceI8Mat(_Fixed):
     @classmethod
     def from_bf16(cls, w: torch.Tensor, prepack: bool = True, stream=None) -> "DeviceI8Mat":
         """Load time: bf16 weights [n_exp, N, K] quantised by rows (one scale per output
-        channel), in tiles where N allows them and prepack is not False."""
+        channel), in tiles where N allows them and prepack is not False.  K a multiple of 64 up to
+        16384, moe_quant_i8's widest row; codes of wider rows, which the products take, come from
+        elsewhere (DeviceI8Mat(codes, scales).prepacked())."""
         _tensor(w, "w", BF16)
         if w.dim() != 3:
             raise ValueError("w: expected [n_exp, N, K]")
         n_exp, N, K = w.shape
+        if K < 64 or K % 64 or K > 16384:
+            raise ValueError(f"w: K = {K}, expected a multiple of 64 up to 16384")
         codes = torch.empty((n_exp, N, K), dtype=I8, device=w.device)
         scales = torch.empty((n_exp, N), dtype=F32, device=w.device)
         _wait_for_allocations(stream, w.device)
@@ -1170,7 +1174,8 @@ class MoeLayerI8:
     def from_bf16(cls, weights, H: int, I: int, I_sh: int, E: int, k: int, device,
                   **kw) -> "MoeLayerI8":
         """weights: bf16 device tensors gate, up [E, I, H], down [E, H, I] and the shared
-        expert's [1, ..] (None when I_sh is 0), quantised by rows and put into tiles."""
+        expert's [1, ..] (None when I_sh is 0), quantised by rows (H, I and I_sh up to 16384)
+        and put into tiles."""
         return cls([None if w is None else DeviceI8Mat.from_bf16(w) for w in weights], H, I, I_sh,
                    E, k, device, **kw)
 

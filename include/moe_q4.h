@@ -468,7 +468,7 @@ int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* wei
 
 /* Rows of bf16 [R, K] as codes int8 [R, K] and scales fp32 [R] (weights at load
  * time, activations that need no norm).  x and q 16-byte aligned, K a multiple
- * of 64 up to 16384.  Enqueues one kernel for each 2^21 rows. */
+ * of 64 up to 16384 (the products take wider rows, of codes made elsewhere).  Enqueues one kernel for each 2^21 rows. */
 int moe_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, hipStream_t stream);
 
 /* The way back: out = bf16(code * scale), [R, K] row-major, K a multiple of 64;

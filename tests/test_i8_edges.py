@@ -91,3 +91,13 @@ def test_sizes_past_32_bits_are_refused(call):
     """ctypes would pass their low 32 bits, and the call work on a part of its tensors."""
     with pytest.raises(ValueError, match="32"):
         call()
+
+
+@pytest.mark.parametrize("K", [96, 16448])
+def test_rows_that_cannot_be_quantised_are_named(K):
+    """Before anything is allocated or enqueued: a matrix of E = 16 experts of N = 64."""
+    w = torch.empty((E, 64, K), dtype=BF16)
+    with pytest.raises(ValueError, match=f"K = {K}, expected a multiple of 64 up to 16384"):
+        bq.DeviceI8Mat.from_bf16(w)
+    with pytest.raises(ValueError, match=f"K = {K}"):
+        bq.MoeLayerI8.from_bf16([w] * 3 + [None] * 3, K, 64, 0, E, k, "cpu")
