@@ -807,7 +807,7 @@ int moe_layer_chunked(const uint16_t* x, const float* logits, int T, int H, int 
 
 // ---- 8-bit operators ----
 
-// Sums of products of two 8-bit codes stay below 2^31 up to here (128 * 128 * K).
+// Sums of products of two 8-bit codes stay below 2^31 where K is less (128 * 128 * K).
 static constexpr int kMaxKI8 = 131072;
 
 static bool valid_k_i8(int K) { return K >= 64 && K % 64 == 0 && K < kMaxKI8; }

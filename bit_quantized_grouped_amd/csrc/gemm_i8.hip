@@ -1,6 +1,6 @@
 // Products of 8-bit codes with one scale per activation row and one per weight
 // row: out[m, n] = a_scale[m] * w_scale[n] * sum_k a[m, k] * w[n, k].  The sum
-// is a 32-bit integer and exact (K <= kMaxKI8), so its order does not matter;
+// is a 32-bit integer and exact (K < 131072), so its order does not matter;
 // the two scales are applied in fp32 and the result rounded once.
 //
 // moe_linear_i8 is the dense form.  The experts' FFNs run over the row blocks of
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
 // j ^ (r / 2 % (4 KS)), chosen on the source side (a load writes LDS in lane order), so
 // that neighbouring rows of a fragment read lie in different banks (with r / 4 half of
 // the LDS cycles were conflicts).  A workgroup requests its next tile's first stages
-// during the last products of a tile.  8192 x 4096 x 4096 takes 117 us (2350 TOP/s), MFMA
+// during the last products of a tile.  8192 x 4096 x 4096 takes 120 us (2290 TOP/s), MFMA
 // 56 % busy at 2.0 GHz; with codes of zero, at a higher clock, 92.  Where a CU has one tile
 // or few it is bound by what L2 gives a CU, 40 to 48 bytes a ns in every form here.
 // Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
@@ -450,8 +450,8 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 // waves: Q steps of 64 K at a time go straight into LDS, the next Q while these are
 // multiplied, laid out as in the tile kernel; small chunks leave room for three
 // workgroups on a CU, which cover each other's waits (Q = 8: two).  Bound by HBM: 541 MB
-// of gate and up weights of 256 experts in 94 us are 5.8 TB/s, of the 6.2 a plain read
-// reaches.
+// of gate and up weights of 256 experts (512 tokens) in 100 us are 5.4 TB/s, of the 6.2 a
+// plain read reaches.
 template <int MF, int NT, int D, int Q, bool GATEUP>
 __global__ __launch_bounds__(4 * WAVE, 2) void grouped_stream_kernel(ProductArgs p, uint32_t dense_rows,
                                                                      uint32_t routed_rows) {
@@ -844,7 +844,7 @@ hipError_t launch_grouped_i8(const GemmI8Problem& g, void* ws, bool want_low, hi
     // Rows / 16, weight rows of a wave / 16, steps ahead, steps of a chunk; us measured at H
     // 2048, I 512, 256 experts, k 8.  Gate/up: 64 tokens 1,2,4,4 76; 512 tokens 2,2,4,4 94
     // (2,4,4,4 103, 1,2,4,4 99, 4,4,2,2 105); 2048 tokens 4,4,2,2 120, skewed 90 (2,2,4,4 138
-    // and 115, 2,4,4,4 129 and 106, 4,4,2,8 132 and 104).  Down: 64 tokens 1,2,4,4 42; 512
+    // and 115, 2,4,4,4 129 and 106, 4,4,2,8 132 and 104).  Down, without low bytes: 64 tokens 1,2,4,4 42; 512
     // tokens 2,4,2,4 52 (1,2,4,4 54, 4,4,4,4 55); 2048 tokens 4,4,4,4 72, skewed 58 (2,4,2,4 76
     // and 63, 4,4,4,8 77 and 67).  Blocks of 32 rows that are mostly full take the wider waves.
     const bool full = n > 32 * g.E;

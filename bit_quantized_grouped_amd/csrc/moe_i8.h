@@ -13,7 +13,7 @@ namespace moeq4 {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-// Widest row of the norm and the row quantisation: 8 waves of 4 pieces of 8.
+// Widest row of the norm and the row quantisation: 16 waves of 2 pieces of 8 a lane.
 constexpr int kMaxNormWidth = 16384;
 
 struct I8MatDev {

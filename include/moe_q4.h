@@ -490,7 +490,7 @@ int moe_i8_prepack(const int8_t* src, int n_exp, int N, int K, int8_t* dst, hipS
  * a, out 16-byte aligned.  K a multiple of 64 below 131072 (the sum is exact in
  * 32 bits), M and N >= 1, M*K and N*K < 2^31, M*N < 2^40.  ws: device workspace of at least
  * moe_linear_i8_workspace_bytes() bytes, 256-byte aligned (may be NULL when
- * that is 0); two calls that may run at the same time need one each. */
+ * that is 0, as it is for every shape today); two calls that may run at the same time need one each. */
 size_t moe_linear_i8_workspace_bytes(int M, int N, int K);
 int moe_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
                   uint16_t* out, void* ws, size_t ws_bytes, hipStream_t stream);
@@ -535,7 +535,8 @@ int moe_route_scored(const float* logits, const float* bias, const moe_score_rul
                      int E, int k, int block_rows, const moe_routing* out, void* ws,
                      size_t ws_bytes, hipStream_t stream);
 
-/* Device workspace bytes moe_grouped_gemm_i8 needs (0 on bad shapes). */
+/* Device workspace bytes moe_grouped_gemm_i8 and moe_layer_i8 need (0 on bad shapes):
+ * h, its codes and scales, and the layer's further bits of the experts' outputs. */
 size_t moe_gemm_i8_workspace_bytes(int T, int H, int I, int I_sh, int E, int k, int block_rows);
 
 /* moe_grouped_gemm_q4 over 8-bit activations and weights:
