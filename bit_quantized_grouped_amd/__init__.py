@@ -983,7 +983,8 @@ def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, s
                  expert_out: torch.Tensor, shared_out, gemm_ws: torch.Tensor, y: torch.Tensor,
                  stream=None):
     """moe_route (rule None) or moe_route_scored, moe_grouped_gemm_i8 and moe_combine in one
-    call.  For at most 64 tokens expert_out and shared_out may stay unwritten."""
+    call, which sums the experts' outputs before their rounding to bf16.  For at most 64 tokens
+    expert_out and shared_out may stay unwritten."""
     shape = T, H = _two_dims(x, "x", "[T, H]")
     d = x.get_device()
     _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, _arg(x, "x", I8, shape, d),
@@ -1160,8 +1161,8 @@ class MoeLayerI8:
         self.H, self.I, self.I_sh, self.E, self.k = H, I, I_sh, E, k
         self.block_rows, self.device = block_rows, torch.device(device)
         self._mats = tuple(mats)
-        _expert_i8_mats(self._mats, E, H, I, I_sh, mats[0].codes.get_device()
-                        if isinstance(mats[0], DeviceI8Mat) else -1)
+        self._dev = mats[0].codes.get_device() if isinstance(mats[0], DeviceI8Mat) else -1
+        _expert_i8_mats(self._mats, E, H, I, I_sh, self._dev)
         self.rule, self.score_bias = rule, score_bias
         self._bufs, self._fixed = {}, {}
 
@@ -1227,24 +1228,26 @@ class MoeLayerI8:
         stream then waits for the current one."""
         shape = T, H = _two_dims(x, "x", "[T, H]")
         d = x.get_device()
+        if H != self.H or d != self._dev:
+            raise ValueError(f"x: {tuple(shape)} on {x.device}, the layer is H={self.H} on "
+                             f"{self._mats[0].codes.device}")
+        # what is refused makes no buffers
+        inputs = (_arg(x, "x", I8, shape, d), _arg(x_scale, "x_scale", F32, (T,), d),
+                  _arg(logits, "logits", F32, (T, self.E), d), *_rule_args(self.rule, self.score_bias, self.E, d))
         b = self._buffers(T)
         y = b["y"] if out is None else out
         if T not in self._fixed:   # the arguments that belong to this object, checked once
-            self._fixed[T] = (
-                [T, self.H, self.I, self.I_sh, self.E, self.k, self.rows_for(T),
-                 *_expert_i8_mats(self._mats, self.E, self.H, self.I, self.I_sh, d),
-                 _routing_arg(b["routing"], "routing", T, self.E, self.k, self.rows_for(T), d),
-                 *_ws_arg(b["route_ws"], "route_ws", d),
-                 _arg(b["expert_out"], "expert_out", BF16, (T * self.k, self.H), d),
-                 _shared_out_arg(b["shared_out"], self.I_sh, (T, self.H), d),
-                 *_ws_arg(b["gemm_ws"], "gemm_ws", d)], d)
+            self._fixed[T] = [
+                T, self.H, self.I, self.I_sh, self.E, self.k, self.rows_for(T),
+                *_expert_i8_mats(self._mats, self.E, self.H, self.I, self.I_sh, d),
+                _routing_arg(b["routing"], "routing", T, self.E, self.k, self.rows_for(T), d),
+                *_ws_arg(b["route_ws"], "route_ws", d),
+                _arg(b["expert_out"], "expert_out", BF16, (T * self.k, self.H), d),
+                _shared_out_arg(b["shared_out"], self.I_sh, (T, self.H), d),
+                *_ws_arg(b["gemm_ws"], "gemm_ws", d)]
             _wait_for_allocations(stream, x.device)
-        fixed, on = self._fixed[T]
-        if d != on or H != self.H:
-            raise ValueError(f"x: {tuple(shape)} on {x.device}, the layer is H={self.H} on cuda:{on}")
-        _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, _arg(x, "x", I8, shape, d),
-             _arg(x_scale, "x_scale", F32, (T,), d), _arg(logits, "logits", F32, (T, self.E), d),
-             *_rule_args(self.rule, self.score_bias, self.E, d), *fixed, _arg(y, "y", BF16, shape, d))
+        _run(lib().moe_layer_i8, "moe_layer_i8", d, stream, *inputs, *self._fixed[T],
+             _arg(y, "y", BF16, shape, d))
         return dict(b, y=y)
 
     def forward_block(self, x: torch.Tensor, residual, norm_weight: torch.Tensor,
@@ -1255,7 +1258,7 @@ class MoeLayerI8:
         "logits" and the layer's "y"."""
         T, H = _x_of(x)
         d = x.get_device()
-        if H != self.H or d != self._mats[0].codes.get_device():
+        if H != self.H or d != self._dev:
             raise ValueError(f"x: {(T, H)} on {x.device}, the layer is H={self.H} on "
                              f"{self._mats[0].codes.device}")
         _tensor(w_router, "w_router", BF16, (self.E, H))   # the norm is enqueued before the router checks

@@ -101,3 +101,15 @@ def test_rows_that_cannot_be_quantised_are_named(K):
         bq.DeviceI8Mat.from_bf16(w)
     with pytest.raises(ValueError, match=f"K = {K}"):
         bq.MoeLayerI8.from_bf16([w] * 3 + [None] * 3, K, 64, 0, E, k, "cpu")
+
+
+@pytest.mark.parametrize("x,x_scale,logits,msg", [
+    (torch.zeros((T, H + 64), dtype=I8), torch.zeros(T), torch.zeros(T, E), "the layer is H=256"),
+    (torch.zeros((T, H)), torch.zeros(T), torch.zeros(T, E), "x: dtype"),
+    (torch.zeros((T, H), dtype=I8), torch.zeros(T + 1), torch.zeros(T, E), "x_scale: shape"),
+    (torch.zeros((T, H), dtype=I8), torch.zeros(T), torch.zeros(T, E + 1), "logits: shape")])
+def test_a_refused_forward_keeps_no_buffers(x, x_scale, logits, msg):
+    la = layer()
+    with pytest.raises((TypeError, ValueError), match=msg):
+        la.forward(x, x_scale, logits)
+    assert not la._bufs
