@@ -754,10 +754,10 @@ def _wait_for_allocations(stream, device):
 
 
 class _Fixed:
-    """An object whose C struct, its last attribute, is made once: no attribute changes after it."""
+    """An object whose C struct is made once: what it had by then does not change after."""
 
     def __setattr__(self, name, value):
-        if "struct" in self.__dict__:
+        if "struct" in self.__dict__ and name in self.__dict__:
             raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new {type(self).__name__}")
         super().__setattr__(name, value)
 

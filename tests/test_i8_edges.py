@@ -57,6 +57,7 @@ def test_what_a_struct_was_made_of_stays(make, name, value):
     with pytest.raises(AttributeError, match="is fixed"):
         setattr(obj, name, value)
     assert getattr(obj, name) is before
+    obj.note = "gate of layer 3"   # one of the caller's own
 
 
 def test_released_buffers_are_freed_and_made_anew():
