@@ -133,8 +133,8 @@ static hipError_t launch_rows(const uint16_t* x, const uint16_t* residual, const
                               float* q_scale, hipStream_t stream) {
     // Inputs that do not fit half of the Infinity Cache (256 MB) are not there any more,
     // wherever they come from; read without allocating in it they leave the codes there for
-    // the next kernel.  8191 x 7168 with the residual (by 4 waves a row): 90 us against 102, and reading the
-    // codes back 28 against 38; 2048 x 2048, whose inputs are there: 11.4 against 8.3.
+    // the next kernel.  8191 x 7168 with the residual (by 4 waves a row): 90 us against 102, and
+    // reading the codes back 28 against 38; 2048 x 2048, whose inputs are there: 11.4 against 8.3.
     const bool big = (residual ? 4ll : 2ll) * T_all * H > (128ll << 20);
 #define MOE_NORM_S(NW, V, S)                                                                    \
     norm_i8_kernel<NW, V, NORM, S><<<NW == 1 ? (T + kNormRows - 1) / kNormRows : T,             \

@@ -599,8 +599,9 @@ __global__ __launch_bounds__(kOneThreads) void route_scored_one_kernel(
 // the tokens are cut into segments of 8 or 16, a workgroup of the selection each, which
 // leaves its segment's counts, one byte per expert (a token takes an expert once, so a
 // count is at most 16), and a grouping workgroup takes whole segments and sums their
-// counts; above kScoredPrefixAssign a launch between the two sums them for all.  Then it scans the experts' totals and places its assignments: wave w owns
-// their 64-assignment chunk w, so rows follow assignment order and the sort is stable.
+// counts; above kScoredPrefixAssign a launch between the two sums them for all.  Then it
+// scans the experts' totals and places its assignments: wave w owns their 64-assignment
+// chunk w, so rows follow assignment order and the sort is stable.
 // Every workgroup repeats the scan, which costs less than a launch for it.  Bound by
 // instructions in the selection (about 650 a token) and by the chain of waits in the
 // grouping: 2048 tokens x 8 of 256 take 11.7 us (by segments 12.8), 8192 x 6 of 160 12 + 8

@@ -31,7 +31,8 @@
  *     data (code words, scale values) is not validated.
  *   - Calls that enqueue more than one kernel (moe_route above its
  *     one-launch size, moe_grouped_gemm_q4, moe_layer_q4, moe_layer_chunked,
- *     moe_decode_q4 and its variants) check every argument before the first
+ *     moe_decode_q4 and its variants, and those whose description names
+ *     several kernels) check every argument before the first
  *     launch, but a launch itself can still fail (MOE_ERR_HIP, from
  *     hipGetLastError) after earlier kernels of the same call were enqueued.
  *     Those kernels then run; the call's outputs are undefined and the
@@ -468,7 +469,8 @@ int moe_norm_i8(const uint16_t* x, const uint16_t* residual, const uint16_t* wei
 
 /* Rows of bf16 [R, K] as codes int8 [R, K] and scales fp32 [R] (weights at load
  * time, activations that need no norm).  x and q 16-byte aligned, K a multiple
- * of 64 up to 16384 (the products take wider rows, of codes made elsewhere).  Enqueues one kernel for each 2^21 rows. */
+ * of 64 up to 16384 (the products take wider rows, of codes made elsewhere).
+ * Enqueues one kernel for each 2^21 rows. */
 int moe_quant_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, hipStream_t stream);
 
 /* The way back: out = bf16(code * scale), [R, K] row-major, K a multiple of 64;
@@ -490,7 +492,8 @@ int moe_i8_prepack(const int8_t* src, int n_exp, int N, int K, int8_t* dst, hipS
  * a, out 16-byte aligned.  K a multiple of 64 below 131072 (the sum is exact in
  * 32 bits), M and N >= 1, M*K and N*K < 2^31, M*N < 2^40.  ws: device workspace of at least
  * moe_linear_i8_workspace_bytes() bytes, 256-byte aligned (may be NULL when
- * that is 0, as it is for every shape today); two calls that may run at the same time need one each. */
+ * that is 0, as it is for every shape today); two calls that may run at the same
+ * time need one each. */
 size_t moe_linear_i8_workspace_bytes(int M, int N, int K);
 int moe_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
                   uint16_t* out, void* ws, size_t ws_bytes, hipStream_t stream);
@@ -544,8 +547,8 @@ size_t moe_gemm_i8_workspace_bytes(int T, int H, int I, int I_sh, int E, int k, 
  *   h = silu(x Wg^T) * (x Wu^T) in fp32, held as 8-bit codes with one scale per
  *   row;  expert_out / shared_out = bf16(h Wd^T)
  * Sums of products are exact 32-bit integers.  A NaN or infinite scale of x, gate
- * or up, or an h past fp32's range, makes the whole row of such an h NaN.  Shapes as for the 4-bit calls,
- * and H, I, I_sh below 131072, H*max(I, I_sh) < 2^31.  Other arguments, status
+ * or up, or an h past fp32's range, makes the whole row of such an h NaN.
+ * Shapes as for the 4-bit calls, and H, I, I_sh below 131072, H*max(I, I_sh) < 2^31.  Other arguments, status
  * codes and the order of rows as for moe_grouped_gemm_q4. */
 int moe_grouped_gemm_i8(const int8_t* x, const float* x_scale, int T, int H, int I, int I_sh, int E,
                         int k, int block_rows, const moe_routing* r, const moe_i8_mat* gate,
