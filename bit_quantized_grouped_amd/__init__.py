@@ -116,6 +116,9 @@ _SIGNATURES = {
     "moe_layer_i8": (_I, [_P, _P, _P, _P, ctypes.POINTER(MoeScoreRule), _I, _I, _I, _I, _I, _I, _I]
                      + [ctypes.POINTER(MoeI8Mat)] * 6
                      + [ctypes.POINTER(MoeRouting), _P, _S, _P, _P, _P, _S, _P, _P]),
+    "moe_decode_batch_workspace_bytes": (_S, [_I] * 6),
+    "moe_decode_batch_q4": (_I, [_P, _P, _P, ctypes.POINTER(MoeScoreRule), _P] + [_I] * 6
+                            + [ctypes.POINTER(MoeQ4Mat)] * 6 + [_P, _P, _P, _P, _S, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -998,6 +1001,72 @@ def moe_layer_i8(x: torch.Tensor, x_scale: torch.Tensor, logits: torch.Tensor, s
 
 
 # ---------------------------------------------------------------------------
+# Several requests at once: a few tokens through the 4-bit layer
+# ---------------------------------------------------------------------------
+
+MAX_BATCH_TOKENS = 64
+
+
+def decode_batch_workspace_bytes(T, H, I, I_sh, E, k) -> int:
+    return lib().moe_decode_batch_workspace_bytes(T, H, I, I_sh, E, k)
+
+
+def _q4mat(m, name, n_exp, N, K, dev, present=True):
+    """The argument of one 4-bit matrix set on device `dev` (None where it is not present)."""
+    if _qmat_for(m, name, n_exp, N, K, present) is None:
+        return None
+    packed = m.layout == LAYOUT_TILES_SB
+    for part, size in (("codes", 4), ("scales", 4 if packed else 2), ("biases", 2)):
+        t = getattr(m, part)
+        if t is None:
+            continue
+        if t.element_size() != size:
+            raise TypeError(f"{name}.{part}: dtype {t.dtype}, expected {8 * size} bits")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}.{part}: on {t.device}, the call's first tensor is elsewhere")
+        if t.data_ptr() != getattr(m.struct, part):
+            raise ValueError(f"{name}.{part}: another tensor than its DeviceQMat was made with")
+    return ctypes.byref(m.struct)
+
+
+def _expert_q4_mats(mats, E, H, I, I_sh, dev):
+    sh = I_sh > 0
+    return [_q4mat(m, name, *shape, dev, present=present) for m, name, shape, present in zip(
+        mats, ("gate", "up", "down", "sh_gate", "sh_up", "sh_down"),
+        ((E, I, H), (E, I, H), (E, H, I), (1, I_sh, H), (1, I_sh, H), (1, H, I_sh)),
+        (True, True, True, sh, sh, sh))]
+
+
+def _few_tokens(x, name="x"):
+    shape = _two_dims(x, name, "[T, H]")
+    if not 1 <= shape[0] <= MAX_BATCH_TOKENS:
+        raise ValueError(f"{name}: {shape[0]} tokens, expected 1 to {MAX_BATCH_TOKENS}")
+    return shape
+
+
+def moe_decode_batch_q4(x: torch.Tensor, logits: torch.Tensor, score_bias, rule, shared_gate, I: int,
+                        I_sh: int, k: int, gate, up, down, sh_gate, sh_up, sh_down, y: torch.Tensor,
+                        ws: torch.Tensor, topk_idx=None, topk_w=None, stream=None):
+    """1 to 64 tokens (x bf16 [T, H], logits fp32 [T, E]) through the whole 4-bit layer, each chosen
+    expert read once.  rule: a ScoreRule or None (moe_route's selection), score_bias fp32 [E] or
+    None, shared_gate fp32 [T] or None (a weight of 1).  topk_idx int32 and topk_w fp32 [T, k]
+    receive the selection when given.  ws: decode_batch_workspace_bytes(T, H, I, I_sh, E, k)."""
+    shape = T, H = _few_tokens(x)
+    d = x.get_device()
+    E = _two_dims(logits, "logits", "[T, E]")[1]
+    if (topk_idx is None) != (topk_w is None):
+        raise ValueError("topk_idx and topk_w: both or neither")
+    if shared_gate is not None and not I_sh:
+        raise ValueError("shared_gate: must be None here")
+    _run(lib().moe_decode_batch_q4, "moe_decode_batch_q4", d, stream, _arg(x, "x", BF16, shape, d),
+         _arg(logits, "logits", F32, (T, E), d), *_rule_args(rule, score_bias, E, d),
+         _opt_arg(shared_gate, "shared_gate", F32, (T,), d), T, H, I, I_sh, E, k,
+         *_expert_q4_mats((gate, up, down, sh_gate, sh_up, sh_down), E, H, I, I_sh, d),
+         _opt_arg(topk_idx, "topk_idx", I32, (T, k), d), _opt_arg(topk_w, "topk_w", F32, (T, k), d),
+         _arg(y, "y", BF16, shape, d), *_ws_arg(ws, "ws", d))
+
+
+# ---------------------------------------------------------------------------
 # Convenience: one layer's device weights and buffers, running the three calls
 # ---------------------------------------------------------------------------
 
@@ -1024,7 +1093,7 @@ class MoeLayer:
             (self.gate, self.up, self.down, self.sh_gate, self.sh_up,
              self.sh_down) = prepacked_mats(self.weight_mats(), pack_scales=prepack != "codes")
             torch.cuda.synchronize(self.device)
-        self._bufs = {}
+        self._bufs, self._batch_bufs, self._batch_mats = {}, {}, None
 
     @classmethod
     def from_device(cls, mats, H: int, I: int, I_sh: int, E: int, k: int, device,
@@ -1036,7 +1105,7 @@ class MoeLayer:
         layer.block_rows = block_rows
         layer.device = torch.device(device)
         (layer.gate, layer.up, layer.down, layer.sh_gate, layer.sh_up, layer.sh_down) = mats
-        layer._bufs = {}
+        layer._bufs, layer._batch_bufs, layer._batch_mats = {}, {}, None
         return layer
 
     def weight_mats(self):
@@ -1097,6 +1166,48 @@ class MoeLayer:
         moe_decode_q4(x, logits, self.I, self.I_sh, self.k, self.block_rows, *self.decode_mats(),
                       routing, y, ws, stream)
         return ws
+
+    def decode_batch(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None,
+                     rule: ScoreRule | None = None, score_bias=None, shared_gate=None,
+                     stream=None) -> dict:
+        """1 to 64 tokens through one moe_decode_batch_q4 call.  Returns y (out when given), the
+        selection topk_idx and topk_w, and the workspace ws.  These are this object's and the next
+        call's for as many tokens too: calls on several streams at once need an object each.  The
+        first call for a T makes them; its stream then waits for the current one."""
+        shape = T, H = _few_tokens(x)
+        d = x.get_device()
+        if H != self.H:
+            raise ValueError(f"x: {tuple(shape)}, the layer is H={self.H}")
+        # what is refused makes no buffers
+        inputs = (_arg(x, "x", BF16, shape, d), _arg(logits, "logits", F32, (T, self.E), d),
+                  *_rule_args(rule, score_bias, self.E, d),
+                  _opt_arg(shared_gate, "shared_gate", F32, (T,), d))
+        if shared_gate is not None and not self.I_sh:
+            raise ValueError("shared_gate: must be None here")
+        mats = self.weight_mats()
+        if self._batch_mats is None or self._batch_mats[0] != d or any(
+                a is not b for a, b in zip(mats, self._batch_mats[1])):
+            # checked once for these matrix sets; they stay alive with what was checked
+            args = _expert_q4_mats(mats, self.E, H, self.I, self.I_sh, d)
+            parts = [(m.codes, m.scales, m.biases) for m in mats if m is not None]
+            self._batch_mats = d, mats, args, parts
+        kept = self._batch_bufs.get((T, d))
+        if kept is None:
+            if d < 0:
+                raise ValueError("arguments must be device tensors (got tensors on the CPU)")
+            on = x.device
+            ws = _bytes_tensor(decode_batch_workspace_bytes(T, H, self.I, self.I_sh, self.E, self.k), on)
+            b = dict(y=torch.empty(shape, dtype=BF16, device=on),
+                     topk_idx=torch.empty((T, self.k), dtype=I32, device=on),
+                     topk_w=torch.empty((T, self.k), dtype=F32, device=on), ws=ws)
+            outs = b["topk_idx"].data_ptr(), b["topk_w"].data_ptr()
+            kept = self._batch_bufs[T, d] = b, outs, _ws_arg(ws, "ws", d)
+            _wait_for_allocations(stream, on)
+        b, outs, ws = kept
+        y = b["y"] if out is None else out
+        _run(lib().moe_decode_batch_q4, "moe_decode_batch_q4", d, stream, *inputs, T, H, self.I,
+             self.I_sh, self.E, self.k, *self._batch_mats[2], *outs, _arg(y, "y", BF16, shape, d), *ws)
+        return dict(b, y=y)
 
     def bf16_weights(self) -> dict:
         """Device buffers for the weights expanded to bf16 (allocated once, reused)."""

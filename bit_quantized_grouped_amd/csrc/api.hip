@@ -1053,4 +1053,72 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
     }
 }
 
+// ---- a few tokens through the 4-bit layer ----
+
+static int check_batch_shape(int T, int H, int I, int I_sh, int E, int k) {
+    if (T < 1 || T > kBatchMaxTokens || k > kScoredMaxK) return MOE_ERR_SHAPE;
+    return check_layer_shape(T, H, I, I_sh, E, k, 32);
+}
+
+size_t moe_decode_batch_workspace_bytes(int T, int H, int I, int I_sh, int E, int k) {
+    return check_batch_shape(T, H, I, I_sh, E, k) ? 0 : batch_ws_layout(T, I, I_sh, E, k).total;
+}
+
+int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* score_bias,
+                        const moe_score_rule* rule, const float* shared_gate, int T, int H, int I,
+                        int I_sh, int E, int k, const moe_q4_mat* gate, const moe_q4_mat* up,
+                        const moe_q4_mat* down, const moe_q4_mat* sh_gate, const moe_q4_mat* sh_up,
+                        const moe_q4_mat* sh_down, int32_t* topk_idx, float* topk_w, uint16_t* y,
+                        void* ws, size_t ws_bytes, hipStream_t stream) {
+    try {
+        int st = check_batch_shape(T, H, I, I_sh, E, k);
+        if (st) return st;
+        BatchArgs a{};
+        if (rule && (st = check_rule(rule, E, k, &a.rule))) return st;
+        if (score_bias && !rule) return MOE_ERR_SHAPE;
+        if (!x || !logits || !y || (topk_idx == nullptr) != (topk_w == nullptr)) return MOE_ERR_NULL;
+        if ((st = check_mat(gate)) || (st = check_mat(up)) || (st = check_mat(down))) return st;
+        if (I_sh) {
+            if ((st = check_mat(sh_gate)) || (st = check_mat(sh_up)) || (st = check_mat(sh_down)))
+                return st;
+        } else if (sh_gate || sh_up || sh_down || shared_gate) {
+            return MOE_ERR_SHAPE;
+        }
+        if ((st = check_layer_layouts(gate, up, down, sh_gate, sh_up, sh_down))) return st;
+        if (!aligned(x, 16) || !aligned(y, 16) || !aligned(logits, 4) || !aligned(score_bias, 4) ||
+            !aligned(shared_gate, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+            return MOE_ERR_ALIGN;
+        const BatchWs L = batch_ws_layout(T, I, I_sh, E, k);
+        if ((st = check_ws(ws, ws_bytes, L.total))) return st;
+        char* base = (char*)ws;
+        a.x = x;
+        a.logits = logits;
+        a.bias = score_bias;
+        a.scored = rule != nullptr;
+        a.shared_gate = shared_gate;
+        a.T = T;
+        a.H = H;
+        a.I = I;
+        a.I_sh = I_sh;
+        a.E = E;
+        a.k = k;
+        a.gate = to_dev(gate);
+        a.up = to_dev(up);
+        a.down = to_dev(down);
+        a.sh_gate = to_dev(sh_gate);
+        a.sh_up = to_dev(sh_up);
+        a.sh_down = to_dev(sh_down);
+        a.topk_idx = topk_idx ? topk_idx : (int32_t*)(base + L.idx);
+        a.topk_w = topk_w ? topk_w : (float*)(base + L.w);
+        a.h_hi = (uint16_t*)(base + L.h_hi);
+        a.h_lo = (uint16_t*)(base + L.h_lo);
+        a.list = (uint4*)(base + L.list);
+        a.n_list = (int*)(base + L.n_list);
+        a.y = y;
+        return launch_decode_batch(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
 }  // extern "C"

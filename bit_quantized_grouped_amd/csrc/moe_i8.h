@@ -137,4 +137,29 @@ bool decode_i8_fits(const GemmI8Problem& p);
 hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const float* bias,
                             const ScoreRule* rule, void* ws, uint16_t* y, hipStream_t stream);
 
+// decode_batch.hip: a few tokens through the 4-bit layer
+constexpr int kBatchMaxTokens = 64;   // a token's bit in a 64-bit mask
+struct BatchArgs {
+    const uint16_t* x;          // [T, H]
+    const float* logits;        // [T, E]
+    const float* bias;          // [E], scored selection only
+    ScoreRule rule;
+    int scored;                 // 0: moe_route's selection
+    const float* shared_gate;   // [T] or NULL
+    int T, H, I, I_sh, E, k;
+    QMatDev gate, up, down, sh_gate, sh_up, sh_down;
+    int32_t* topk_idx;          // [T, k], the caller's or the workspace's
+    float* topk_w;
+    uint16_t *h_hi, *h_lo;      // workspace: h of the routed rows by expert [T*k, I], then of the
+                                // shared expert [T, I_sh], weighted, as two bf16
+    uint4* list;                // workspace: the chosen experts (expert, first row, mask of tokens)
+    int* n_list;
+    uint16_t* y;                // [T, H]
+};
+struct BatchWs {
+    size_t h_hi, h_lo, list, n_list, idx, w, total;
+};
+BatchWs batch_ws_layout(int T, int I, int I_sh, int E, int k);
+hipError_t launch_decode_batch(const BatchArgs& args, hipStream_t stream);
+
 }  // namespace moeq4

@@ -571,6 +571,33 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
                  size_t route_ws_bytes, uint16_t* expert_out, uint16_t* shared_out, void* gemm_ws,
                  size_t gemm_ws_bytes, uint16_t* y, hipStream_t stream);
 
+/* ---- Several requests at once: a few tokens through the 4-bit layer. ---- */
+
+/* The whole 4-bit layer for a batch of 1 .. 64 tokens, each expert's weights read once for
+ * all of its tokens: two kernels, and a third in front for the selection of more than a few
+ * tokens.  [P3] "Decode is limited by bandwidth more than by compute".
+ *   selection  moe_route's (rule and score_bias NULL) or moe_route_scored's, with the same
+ *              experts and weights
+ *   y[t] = sum_j topk_w[t, j] * FFN_(topk_idx[t, j])(x[t]) + shared_gate[t] * FFN_shared(x[t])
+ *   x bf16 [T, H], y bf16 [T, H] (16-byte aligned), logits fp32 [T, E], score_bias fp32 [E]
+ *   or NULL, shared_gate fp32 [T] or NULL (a weight of 1; NULL without a shared expert)
+ *   topk_idx int32 [T, k], topk_w fp32 [T, k]: the selection, both or neither
+ * Weights are bf16 as in the grouped GEMM, sums fp32; h, with its weight, is kept to 16 bits,
+ * and y has one rounding, so y differs from the three-call path by that path's roundings of h
+ * and of the experts' outputs.  A token's y depends on no other token but through the
+ * order of its sums.  Deterministic: the same inputs give the same bits.
+ *   ws: moe_decode_batch_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned; need
+ *   not be cleared.
+ * Shapes and matrices as for moe_decode_q4, T <= 64, k <= 64; for a rule also
+ * moe_route_scored's limits. */
+size_t moe_decode_batch_workspace_bytes(int T, int H, int I, int I_sh, int E, int k);
+int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* score_bias,
+                        const moe_score_rule* rule, const float* shared_gate, int T, int H, int I,
+                        int I_sh, int E, int k, const moe_q4_mat* gate, const moe_q4_mat* up,
+                        const moe_q4_mat* down, const moe_q4_mat* sh_gate, const moe_q4_mat* sh_up,
+                        const moe_q4_mat* sh_down, int32_t* topk_idx, float* topk_w, uint16_t* y,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
