@@ -53,6 +53,11 @@ class MoeI8Mat(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("layout", ctypes.c_int32)]
 
 
+class MoeAdapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("n", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
 class MoeScoreRule(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_groups", "topk_groups", "group_score",
                                               "renormalise")] + [("scale", ctypes.c_float)]
@@ -119,6 +124,11 @@ _SIGNATURES = {
     "moe_decode_batch_workspace_bytes": (_S, [_I] * 6),
     "moe_decode_batch_q4": (_I, [_P, _P, _P, ctypes.POINTER(MoeScoreRule), _P] + [_I] * 6
                             + [ctypes.POINTER(MoeQ4Mat)] * 6 + [_P, _P, _P, _P, _S, _P]),
+    "moe_linear_lora_i8_workspace_bytes": (_S, [_I] * 4),
+    "moe_linear_lora_i8": (_I, [_P, _P, _I, _I, ctypes.POINTER(MoeI8Mat), _I, ctypes.POINTER(MoeAdapters),
+                                _P, _P, _P, _S, _P]),
+    "moe_logprobs_workspace_bytes": (_S, [_I] * 3),
+    "moe_logprobs": (_I, [_P, _I, ctypes.c_int64, _P, _I, _I, _I] + [_P] * 5 + [_S, _P]),
 }
 
 EXPORTED = tuple(_SIGNATURES)
@@ -1064,6 +1074,95 @@ def moe_decode_batch_q4(x: torch.Tensor, logits: torch.Tensor, score_bias, rule,
          *_expert_q4_mats((gate, up, down, sh_gate, sh_up, sh_down), E, H, I, I_sh, d),
          _opt_arg(topk_idx, "topk_idx", I32, (T, k), d), _opt_arg(topk_w, "topk_w", F32, (T, k), d),
          _arg(y, "y", BF16, shape, d), *_ws_arg(ws, "ws", d))
+
+
+# ---------------------------------------------------------------------------
+# Several requests at once: adapters beside a projection, log probabilities
+# ---------------------------------------------------------------------------
+
+class DeviceAdapters(_Fixed):
+    """A set of n low-rank adapters of one projection, resident on the device: a bf16 [n, rank, K],
+    b bf16 [n, N, rank], scales fp32 [n]; rank a multiple of 8 up to 128 (lower ranks padded with
+    zeros).  Values may be written into its tensors, an adapter exchanged for another; another
+    tensor takes another object."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor):
+        _tensor(a, "a", BF16)
+        _tensor(b, "b", BF16)
+        if a.dim() != 3 or b.dim() != 3:
+            raise ValueError("a, b: expected [n, rank, K] and [n, N, rank]")
+        n, rank, K = a.shape
+        N = b.shape[1]
+        if max(*a.shape, *b.shape) > _INT_MAX:
+            raise ValueError(f"a, b: shapes {tuple(a.shape)}, {tuple(b.shape)} pass 32-bit sizes")
+        _tensor(b, "b", BF16, (n, N, rank))
+        _tensor(scales, "scales", F32, (n,))
+        if n < 1 or rank < 8 or rank % 8 or rank > 128:
+            raise ValueError(f"a: {n} adapters of rank {rank}, expected one at least, of a multiple of 8 up to 128")
+        if not a.get_device() == b.get_device() == scales.get_device():
+            raise ValueError("a, b and scales: on different devices")
+        self.a, self.b, self.scales = a, b, scales
+        self.n, self.rank, self.K, self.N = n, rank, K, N
+        self.struct = MoeAdapters(a.data_ptr(), b.data_ptr(), scales.data_ptr(), n, rank)
+
+
+def linear_lora_i8_workspace_bytes(M, N, K, rank) -> int:
+    return lib().moe_linear_lora_i8_workspace_bytes(M, N, K, rank)
+
+
+def moe_linear_lora_i8(a: torch.Tensor, a_scale: torch.Tensor, w: DeviceI8Mat, adapters: DeviceAdapters,
+                       adapter: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None):
+    """moe_linear_i8 with row m's adapter number adapter[m] (int32 [M]; outside 0 .. n - 1: none)
+    beside it.  ws: linear_lora_i8_workspace_bytes(M, N, K, adapters.rank) bytes."""
+    shape = M, K = _two_dims(a, "a", "[M, K]")
+    if not isinstance(w, DeviceI8Mat):
+        raise TypeError("w: expected a DeviceI8Mat")
+    if not isinstance(adapters, DeviceAdapters):
+        raise TypeError("adapters: expected a DeviceAdapters")
+    d, N = a.get_device(), w.shape[1]
+    if (adapters.N, adapters.K) != (N, K):
+        raise ValueError(f"adapters: for [{adapters.N}, {adapters.K}], the matrix is [{N}, {K}]")
+    if adapters.a.get_device() != d:
+        raise ValueError(f"adapters: on {adapters.a.device}, the call's first tensor is elsewhere")
+    _run(lib().moe_linear_lora_i8, "moe_linear_lora_i8", d, stream, _arg(a, "a", I8, shape, d),
+         _arg(a_scale, "a_scale", F32, (M,), d), M, K, _i8mat(w, "w", 1, N, K, d), N,
+         ctypes.byref(adapters.struct), _arg(adapter, "adapter", I32, (M,), d),
+         _arg(out, "out", BF16, (M, N), d), *_ws_arg(ws, "ws", d))
+
+
+def logprobs_workspace_bytes(T, V, n_top) -> int:
+    return lib().moe_logprobs_workspace_bytes(T, V, n_top)
+
+
+def moe_logprobs(logits: torch.Tensor, targets=None, logprob=None, entropy=None, top_idx=None,
+                 top_logprob=None, ws=None, stream=None):
+    """Of rows of logits, bf16 or fp32 [T, V] (rows may lie apart): logprob fp32 [T] of the tokens
+    targets int32 [T] (0 for one outside the row), entropy fp32 [T] in nats, and the most probable
+    tokens top_idx int32 and their top_logprob fp32 [T, n], in order, ties to the lowest index.
+    Those outputs that are given are written.  ws: logprobs_workspace_bytes(T, V, n) bytes (None
+    where that is 0)."""
+    T, V = _two_dims(logits, "logits", "[T, V]")
+    if logits.dtype not in (BF16, F32):
+        raise TypeError(f"logits: dtype {logits.dtype}, expected {BF16} or {F32}")
+    stride = logits.stride(0) if T > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or stride < V:
+        raise ValueError(f"logits: strides {logits.stride()}, expected rows of values side by side")
+    if (targets is None) != (logprob is None):
+        raise ValueError("targets and logprob: both or neither")
+    d = logits.get_device()
+    shape = None
+    for t, name in ((top_idx, "top_idx"), (top_logprob, "top_logprob")):
+        if t is not None:
+            shape = _two_dims(t, name, "[T, n]") if shape is None else shape
+            if shape[1] < 1:
+                raise ValueError(f"{name}: no columns")
+    if logprob is None and entropy is None and shape is None:
+        raise ValueError("logprob, entropy, top_idx, top_logprob: at least one output")
+    n = 0 if shape is None else shape[1]
+    _run(lib().moe_logprobs, "moe_logprobs", d, stream, logits.data_ptr(), int(logits.dtype is F32), stride,
+         _opt_arg(targets, "targets", I32, (T,), d), T, V, n, _opt_arg(logprob, "logprob", F32, (T,), d),
+         _opt_arg(entropy, "entropy", F32, (T,), d), _opt_arg(top_idx, "top_idx", I32, (T, n), d),
+         _opt_arg(top_logprob, "top_logprob", F32, (T, n), d), *((None, 0) if ws is None else _ws_arg(ws, "ws", d)))
 
 
 # ---------------------------------------------------------------------------

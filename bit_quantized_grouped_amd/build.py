@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 SOURCES = ["api.hip", "route.hip", "gemm_q4.hip", "combine.hip", "decode.hip", "dequant.hip", "router.hip",
            "probe.hip", "norm_i8.hip", "gemm_i8.hip", "decode_i8.hip",
-           "decode_batch.hip"]
+           "decode_batch.hip", "lora_i8.hip", "logprobs.hip"]
 ARCH = "gfx950"
 
 

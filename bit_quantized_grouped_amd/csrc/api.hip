@@ -1121,4 +1121,77 @@ int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* sco
     }
 }
 
+// ---- adapters beside the linear's product ----
+
+static int check_lora_shape(int M, int N, int K, int rank) {
+    const int st = check_linear_shape(M, N, K);
+    if (st) return st;
+    return rank < 8 || rank > kLoraMaxRank || rank % 8 ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+size_t moe_linear_lora_i8_workspace_bytes(int M, int N, int K, int rank) {
+    return check_lora_shape(M, N, K, rank) ? 0 : linear_lora_ws_bytes(M, K, rank);
+}
+
+int moe_linear_lora_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
+                       const moe_adapters* adapters, const int32_t* adapter, uint16_t* out, void* ws,
+                       size_t ws_bytes, hipStream_t stream) {
+    try {
+        if (!adapters) return MOE_ERR_NULL;
+        int st = check_lora_shape(M, N, K, adapters->rank);
+        if (st) return st;
+        if (adapters->n < 1) return MOE_ERR_SHAPE;
+        if (!a || !a_scale || !out || !adapter || !adapters->a || !adapters->b || !adapters->scales)
+            return MOE_ERR_NULL;
+        if ((st = check_i8_mat(w, N))) return st;
+        if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(out, 16) || !aligned(adapter, 4) ||
+            !aligned(adapters->a, 16) || !aligned(adapters->b, 16) || !aligned(adapters->scales, 4))
+            return MOE_ERR_ALIGN;
+        if ((st = check_ws(ws, ws_bytes, linear_lora_ws_bytes(M, K, adapters->rank)))) return st;
+        LoraDev lora{};
+        lora.b = adapters->b;
+        hipError_t e = launch_lora_shrink(a, a_scale, M, K, adapters->a, adapters->scales, adapters->n,
+                                          adapters->rank, adapter, ws, &lora, stream);
+        if (e == hipSuccess) e = launch_linear_lora_i8(a, a_scale, M, K, i8_dev(w), N, lora, out, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
+// ---- log probabilities ----
+
+static int check_logprobs_shape(int T, int V, int n_top) {
+    return T < 1 || V < 1 || n_top < 0 || n_top > kLogprobsMaxTop || n_top > V ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+size_t moe_logprobs_workspace_bytes(int T, int V, int n_top) {
+    return check_logprobs_shape(T, V, n_top) ? 0 : logprobs_ws_bytes(T, V, n_top);
+}
+
+int moe_logprobs(const void* logits, int dtype, int64_t row_stride, const int32_t* targets, int T, int V,
+                 int n_top, float* logprob, float* entropy, int32_t* top_idx, float* top_logprob, void* ws,
+                 size_t ws_bytes, hipStream_t stream) {
+    try {
+        int st = check_logprobs_shape(T, V, n_top);
+        if (st) return st;
+        if (dtype != MOE_LOGITS_BF16 && dtype != MOE_LOGITS_F32) return MOE_ERR_SHAPE;
+        if ((T > 1 && row_stride < V) || row_stride >= (1ll << 40)) return MOE_ERR_SHAPE;
+        const bool top = top_idx || top_logprob;
+        if (!logits || (targets == nullptr) != (logprob == nullptr) || (!logprob && !entropy && !top))
+            return MOE_ERR_NULL;
+        if ((n_top > 0) != top) return MOE_ERR_SHAPE;
+        if (!aligned(logits, dtype == MOE_LOGITS_BF16 ? 2 : 4) || !aligned(targets, 4) || !aligned(logprob, 4) ||
+            !aligned(entropy, 4) || !aligned(top_idx, 4) || !aligned(top_logprob, 4))
+            return MOE_ERR_ALIGN;
+        const size_t need = logprobs_ws_bytes(T, V, n_top);
+        if (need && (st = check_ws(ws, ws_bytes, need))) return st;
+        const hipError_t e = launch_logprobs(logits, dtype == MOE_LOGITS_BF16, row_stride, targets, T, V, n_top,
+                                             logprob, entropy, top_idx, top_logprob, ws, stream);
+        return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    } catch (...) {
+        return MOE_ERR_HIP;
+    }
+}
+
 }  // extern "C"

@@ -14,6 +14,7 @@
 #include "moe_device.h"
 #include "moe_i8.h"
 #include "moe_lds.h"
+#include "moe_lora.h"
 
 namespace moeq4 {
 
@@ -53,10 +54,33 @@ __host__ __device__ constexpr int xcd_shares(int tiles) { return tiles == 2 || t
 // meet in LDS.  Bound by the latency of one round of loads.
 constexpr int kFewWaves = 8, kFewAhead = 8;
 
+// The adapters' part of MF x NF pieces by K-splitting waves: each takes every eighth of the
+// adapters among 16 rows, whose loads go out before the product's.
+template <int MF, int NF>
+__device__ __forceinline__ void few_lora(const LoraDev& l, int M, int N, int m0, int n0, int wave,
+                                         f32x4_t (&v)[MF][NF]) {
+    const int lane = __lane_id();
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+#pragma unroll
+        for (int n = 0; n < NF; ++n) v[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        const int of = lora_of(l, m0 + m * 16 + lane % 16, M);
+        unsigned long long left = __ballot(of >= 0);
+        for (int turn = 0; left; ++turn) {
+            const int j = __builtin_amdgcn_readlane(of, __builtin_ctzll(left));
+            left &= ~__ballot(of == j);
+            if (turn % kFewWaves == wave) lora_expand<NF>(l, j, of, N, m0 + m * 16, n0, v[m]);
+        }
+    }
+}
+
+// LORA: the rows' adapters are added in fp32, before the one rounding.
+template <bool LORA>
 __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
     const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
-    uint16_t* __restrict__ out) {
+    uint16_t* __restrict__ out, LoraDev lora) {
     __shared__ i32x4_t s_part[kFewWaves - 1][WAVE];
+    __shared__ f32x4_t s_lora[LORA ? kFewWaves : 1][WAVE];
     const int lane = threadIdx.x % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int n_tiles = (N + 15) / 16;
@@ -68,6 +92,11 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
                                 : (size_t)min(lane % 16, N - 1 - n0) * K + lane / 16 * 16);
     const int w_step = w.tiles ? 1024 : 64;
     const int steps = K / 64, s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
+    if constexpr (LORA) {
+        f32x4_t v[1][1];
+        few_lora<1, 1>(lora, M, N, m0, n0, wave, v);
+        s_lora[wave][lane] = v[0][0];
+    }
     i32x4_t acc = {0, 0, 0, 0};
     for (int s = s0; s < s1; s += kFewAhead) {
         i32x4_t va[kFewAhead], vw[kFewAhead];
@@ -92,6 +121,13 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * as * w.scales[min(c + i, N - 1)];
+    if constexpr (LORA) {
+        f32x4_t t = s_lora[0][lane];
+#pragma unroll
+        for (int i = 1; i < kFewWaves; ++i) t += s_lora[i][lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += t[i];
+    }
     uint16_t* o = out + (size_t)r * N + c;
     if (N % 4 == 0) {
         *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -108,14 +144,15 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
 // time, D of them ahead: the two halves of an activation row's cache line are requested one
 // after the other, while the line is in L1 (64 K at a time and deeper 128x2048x7168 took
 // 11.6 us, this 10.5; with contiguous rows it would take 7.8).  Bound by those half lines.
-template <int MF, int NF, int D>
+template <int MF, int NF, int D, bool LORA>
 __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
     const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
-    uint16_t* __restrict__ out, int n_tiles) {
+    uint16_t* __restrict__ out, int n_tiles, LoraDev lora) {
     constexpr int W = kFewWaves, P = MF * NF, ROUND = P < W ? P : W;   // pieces of 16 x 16, and those joined at a time
     static_assert(P % ROUND == 0, "whole rounds");
     constexpr uint32_t kPast = 0xC0000000u;   // past every buffer (both are below 2^31 bytes)
     __shared__ i32x4_t s_part[W][ROUND][WAVE];
+    __shared__ f32x4_t s_lora[LORA ? W : 1][LORA ? P : 1][WAVE];
     const int lane = threadIdx.x % WAVE, fr = lane % 16, fp = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int m0 = (int)(blockIdx.x / n_tiles) * MF * 16, n0 = (int)(blockIdx.x % n_tiles) * NF * 16;
@@ -149,6 +186,12 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
             va[slot][1][m] = __builtin_bit_cast(i32x4_t, buf_load16_u(ra, oa[m] | past1, (uint32_t)s * 128u + 64u));
         }
     };
+    if constexpr (LORA) {
+        f32x4_t v[MF][NF];
+        few_lora<MF, NF>(lora, M, N, m0, n0, wave, v);
+#pragma unroll
+        for (int p = 0; p < P; ++p) s_lora[wave][p][lane] = v[p % MF][p / MF];
+    }
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d, s0 + d);
     i32x4_t acc[NF][MF];
@@ -184,6 +227,13 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * as * w.scales[min(c + i, N - 1)];
+                if constexpr (LORA) {
+                    f32x4_t t = s_lora[0][p][lane];
+#pragma unroll
+                    for (int i = 1; i < W; ++i) t += s_lora[i][p][lane];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += t[i];
+                }
                 uint16_t* o = out + (size_t)r * N + c;
                 if (N % 4 == 0) {
                     *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -214,10 +264,10 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
 // or few it is bound by what L2 gives a CU, 40 to 48 bytes a ns in every form here.
 // Waits count this wave's own loads (KS * (LA + LB) a stage): the kernel must not spill,
 // which the build checks.
-template <int WM, int MF, int WN, int NF, int ST, int KS>
+template <int WM, int MF, int WN, int NF, int ST, int KS, bool LORA>
 __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, I8MatDev w, int N,
-    uint16_t* __restrict__ out, int m_tiles, int n_tiles) {
+    uint16_t* __restrict__ out, int m_tiles, int n_tiles, LoraDev lora) {
     constexpr int BM = WM * MF * 16, BN = WN * NF * 16, WAVES = WM * WN;
     constexpr int LA = BM / 16 / WAVES, LB = BN / 16 / WAVES;   // 1 KB loads per wave and block
     static_assert(BM / 16 % WAVES == 0 && BN / 16 % WAVES == 0, "whole loads per wave");
@@ -399,13 +449,24 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
             for (int mi = 0; mi < kRows / 16; ++mi) {
                 const int m = mb + mi, r = m0 + (wm * MF + m) * 16 + fr;
+                f32x4_t val[NF];
+#pragma unroll
+                for (int n = 0; n < NF; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) val[n][i] = (float)acc[n][m][i] * as[m] * ws[n][i];
+                if constexpr (LORA) {
+                    const int of = lora_of(lora, r, M);
+                    unsigned long long left = __ballot(of >= 0);
+                    while (left) {
+                        const int j = __builtin_amdgcn_readlane(of, __builtin_ctzll(left));
+                        left &= ~__ballot(of == j);
+                        lora_expand<NF>(lora, j, of, N, m0 + (wm * MF + m) * 16, n0 + wn * NF * 16, val);
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < NF; ++n) {
                     const int c = n0 + (wn * NF + n) * 16 + fp * 4;
-                    float v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = (float)acc[n][m][i] * as[m] * ws[n][i];
+                    const f32x4_t v = val[n];
                     const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                     if (wide) {
                         *(u32x2_t*)(s_o + (mi * 16 + fr) * kLdc + n * 16 + fp * 4) = o;
@@ -436,6 +497,12 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
         // The staging place is the next request's.  Stores still in flight only make the
         // counted waits of the next tile stricter.
         bare_barrier_i8();
+        if constexpr (LORA) {   // read again, so that the adapters' products have their registers
+#pragma unroll
+            for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, 0, n);
+#pragma unroll
+            for (int m = 0; m < FA; ++m) fa[0][m] = read_a(0, 0, m);
+        }
     }
     wait_loads<0>();
 }
@@ -755,15 +822,16 @@ static void launch_grouped_stream(ProductArgs& p, int routed_blocks, int T, int 
         <<<grid, 4 * WAVE, 0, stream>>>(p, (uint32_t)T, (uint32_t)(GATEUP ? T : n));
 }
 
-hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
-                            int N, uint16_t* out, void*, hipStream_t stream) {
+template <bool LORA>
+static hipError_t launch_linear(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
+                                int N, uint16_t* out, const LoraDev& lora, hipStream_t stream) {
 #define MOE_TILES(WM, MF, WN, NF, ST, KS)                                                         \
     {                                                                                         \
         const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
         const int lds = (WM * MF + WN * NF) * 1024 * ST * KS, most = kCUs * (kLdsBytes / lds);     \
         const int grid = mt * nt < most ? (mt * nt + 7) / 8 * 8 : most;                       \
-        linear_tiles_kernel<WM, MF, WN, NF, ST, KS><<<grid, WM * WN * WAVE, 0, stream>>>(         \
-            a, a_scale, M, K, w, N, out, mt, nt);                                             \
+        linear_tiles_kernel<WM, MF, WN, NF, ST, KS, LORA><<<grid, WM * WN * WAVE, 0, stream>>>(   \
+            a, a_scale, M, K, w, N, out, mt, nt, lora);                                       \
     }
     // The smallest tile that still makes no more than one round of the CUs (the larger ones
     // read less but leave CUs idle; us measured, small against next larger).  K over 8 waves:
@@ -783,10 +851,12 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
     auto rounds = [&](int bm, int bn) { return (tiles(bm, bn) + kCUs - 1) / kCUs; };
     const long long c128 = 2 * rounds(128, 128), c192 = 3 * rounds(256, 128), c256 = 5 * rounds(256, 256);
 #define MOE_SPLIT(MF, NF, D)                                                                  \
-    linear_split_kernel<MF, NF, D><<<(unsigned)tiles(MF * 16, NF * 16), kFewWaves * WAVE, 0, stream>>>( \
-        a, a_scale, M, K, w, N, out, cdiv(N, NF * 16))
+    linear_split_kernel<MF, NF, D, LORA>                                                      \
+        <<<(unsigned)tiles(MF * 16, NF * 16), kFewWaves * WAVE, 0, stream>>>(                 \
+            a, a_scale, M, K, w, N, out, cdiv(N, NF * 16), lora)
     if (M <= 16 || tiles(16, 16) <= kCUs)
-        linear_few_kernel<<<(unsigned)tiles(16, 16), kFewWaves * WAVE, 0, stream>>>(a, a_scale, M, K, w, N, out);
+        linear_few_kernel<LORA>
+            <<<(unsigned)tiles(16, 16), kFewWaves * WAVE, 0, stream>>>(a, a_scale, M, K, w, N, out, lora);
     else if (tiles(16, 32) <= kCUs) MOE_SPLIT(1, 2, 2);
     else if (w.tiles && tiles(32, 32) <= kCUs) MOE_SPLIT(2, 2, 1);
     else if (w.tiles && tiles(32, 64) <= kCUs) MOE_SPLIT(2, 4, 1);
@@ -799,6 +869,16 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
 #undef MOE_SPLIT
 #undef MOE_TILES
     return hipGetLastError();
+}
+
+hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
+                            int N, uint16_t* out, void*, hipStream_t stream) {
+    return launch_linear<false>(a, a_scale, M, K, w, N, out, LoraDev{}, stream);
+}
+
+hipError_t launch_linear_lora_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
+                                 int N, const LoraDev& lora, uint16_t* out, hipStream_t stream) {
+    return launch_linear<true>(a, a_scale, M, K, w, N, out, lora, stream);
 }
 
 GemmI8Ws gemm_i8_ws_layout(int T, int H, int I, int I_sh, int k) {

@@ -108,6 +108,22 @@ hipError_t launch_prepack_i8(const int8_t* src, int n_exp, int N, int K, int8_t*
 size_t linear_i8_ws_bytes(int M, int N, int K);
 hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
                             int N, uint16_t* out, void* ws, hipStream_t stream);
+// Low-rank adapters beside the linear's product (lora_i8.hip, moe_lora.h)
+struct LoraDev {
+    const float* u;        // [parts][M][rank]: the adapters' first product of each row, scaled
+    const uint16_t* b;     // bf16 [n, N, rank]
+    const int32_t* of;     // [M]: a row's adapter, none outside 0 .. n - 1
+    int n, rank, parts;
+    size_t part;           // M * rank
+};
+constexpr int kLoraMaxRank = 128;
+size_t linear_lora_ws_bytes(int M, int K, int rank);
+// u into ws; fills *out but for b
+hipError_t launch_lora_shrink(const int8_t* a, const float* a_scale, int M, int K, const uint16_t* A,
+                              const float* scales, int n, int rank, const int32_t* adapter, void* ws,
+                              LoraDev* out, hipStream_t stream);
+hipError_t launch_linear_lora_i8(const int8_t* a, const float* a_scale, int M, int K, const I8MatDev& w,
+                                 int N, const LoraDev& lora, uint16_t* out, hipStream_t stream);
 struct GemmI8Problem {
     const int8_t* x;          // [T, H]
     const float* x_scale;     // [T]
@@ -136,6 +152,13 @@ hipError_t launch_combine_low(const uint16_t* expert_out, const int8_t* low, con
 bool decode_i8_fits(const GemmI8Problem& p);
 hipError_t launch_decode_i8(const GemmI8Problem& p, const float* logits, const float* bias,
                             const ScoreRule* rule, void* ws, uint16_t* y, hipStream_t stream);
+
+// logprobs.hip
+constexpr int kLogprobsMaxTop = 64;
+size_t logprobs_ws_bytes(int T, int V, int n);
+hipError_t launch_logprobs(const void* logits, bool bf16, long long ld, const int32_t* target, int T, int V,
+                           int n, float* logprob, float* entropy, int32_t* top_idx, float* top_logprob,
+                           void* ws, hipStream_t stream);
 
 // decode_batch.hip: a few tokens through the 4-bit layer
 constexpr int kBatchMaxTokens = 64;   // a token's bit in a 64-bit mask

@@ -598,6 +598,52 @@ int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* sco
                         const moe_q4_mat* sh_down, int32_t* topk_idx, float* topk_w, uint16_t* y,
                         void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- Several requests at once: each row's low-rank adapter beside a projection. ----
+ * A set of n adapters of one rank:
+ *   a bf16 [n, rank, K], b bf16 [n, N, rank] (16-byte aligned), scales fp32 [n]
+ * rank a multiple of 8, 8 .. 128; an adapter of a lower rank is padded with zeros. */
+typedef struct {
+    const uint16_t* a;
+    const uint16_t* b;
+    const float*    scales;
+    int32_t n;
+    int32_t rank;
+} moe_adapters;
+
+/* moe_linear_i8 with an adapter for each row, j = adapter[m]:
+ *   out[m, n] = bf16(a_scale[m] * (w_scale[n] * sum_k a[m, k] * w[n, k]
+ *                    + scales[j] * sum_r b[j, n, r] * (sum_k a[j, r, k] * a[m, k])))
+ * adapter int32 [M]; a row whose adapter lies outside 0 .. n - 1 has none, and moe_linear_i8's
+ * values.  The adapters' sums are fp32, the first product's result counts to 16 bits, and out
+ * has one rounding.  An adapter's values reach its own rows only, infinities and NaN too.
+ *   ws: moe_linear_lora_i8_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned
+ * Sizes as for moe_linear_i8.  Enqueues two kernels. */
+size_t moe_linear_lora_i8_workspace_bytes(int M, int N, int K, int rank);
+int moe_linear_lora_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
+                       const moe_adapters* adapters, const int32_t* adapter, uint16_t* out, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
+
+/* ---- Log probabilities of rows of logits, such as moe_linear_i8 gives as a model's head. ----
+ *   logits  bf16 or fp32 (dtype) [T, V], row t at logits + t * row_stride values, row_stride >= V
+ *           (not read for one row); aligned to its values only
+ *   logprob[t] = z[target] - log(sum_i exp(z[i])), targets int32 [T]; a target outside 0 .. V - 1
+ *           gives 0.  Both or neither NULL.
+ *   entropy[t] = - sum_i p[i] log p[i], in nats
+ *   top_idx int32, top_logprob fp32 [T, n_top]: the n_top largest logits' tokens in order and
+ *           their log probabilities, ties to the lowest index; n_top 0 .. 64, at most V
+ * Outputs may be NULL, not all of them (n_top is 0 where both of the top's are, and only then).
+ * Sums are fp32.  -inf has probability 0.  A row of -inf alone has entropy 0 and log probabilities
+ * -inf; one with a NaN or +inf has NaN for all of them, and its top_idx by value, NaN as -inf.
+ *   ws: moe_logprobs_workspace_bytes() bytes (0 on bad shapes, and for many rows), 256-byte
+ *   aligned; two calls that may run at the same time need one each
+ * Enqueues one kernel, two for few rows; for each 2^21 rows. */
+#define MOE_LOGITS_BF16 0
+#define MOE_LOGITS_F32  1
+size_t moe_logprobs_workspace_bytes(int T, int V, int n_top);
+int moe_logprobs(const void* logits, int dtype, int64_t row_stride, const int32_t* targets, int T, int V,
+                 int n_top, float* logprob, float* entropy, int32_t* top_idx, float* top_logprob, void* ws,
+                 size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
