@@ -54,22 +54,58 @@ __host__ __device__ constexpr int xcd_shares(int tiles) { return tiles == 2 || t
 // meet in LDS.  Bound by the latency of one round of loads.
 constexpr int kFewWaves = 8, kFewAhead = 8;
 
-// The adapters' part of MF x NF pieces by K-splitting waves: each takes every eighth of the
-// adapters among 16 rows, whose loads go out before the product's.
+// The adapters' part of MF x NF pieces by K-splitting waves, before the product's loads: each wave
+// takes every eighth step of ranks of every adapter among 16 rows, two of them at a time.
 template <int MF, int NF>
 __device__ __forceinline__ void few_lora(const LoraDev& l, int M, int N, int m0, int n0, int wave,
                                          f32x4_t (&v)[MF][NF]) {
     const int lane = __lane_id();
+    int of[MF];
+    unsigned long long left[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
 #pragma unroll
         for (int n = 0; n < NF; ++n) v[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        const int of = lora_of(l, m0 + m * 16 + lane % 16, M);
-        unsigned long long left = __ballot(of >= 0);
-        for (int turn = 0; left; ++turn) {
-            const int j = __builtin_amdgcn_readlane(of, __builtin_ctzll(left));
-            left &= ~__ballot(of == j);
-            if (turn % kFewWaves == wave) lora_expand<NF>(l, j, of, N, m0 + m * 16, n0, v[m]);
+        of[m] = lora_of(l, m0 + m * 16 + lane % 16, M);
+        left[m] = __ballot(of[m] >= 0);
+    }
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        int j = 0, step = l.steps, turn = 0;   // the item at hand: a step of adapter j
+        // this wave's next item, false when there is none
+        auto next = [&](int& at_j, int& at_step) {
+            for (;;) {
+                if (step == l.steps) {
+                    if (!left[m]) return false;
+                    j = __builtin_amdgcn_readlane(of[m], __builtin_ctzll(left[m]));
+                    left[m] &= ~__ballot(of[m] == j);
+                    step = 0;
+                }
+                at_j = j;
+                at_step = step++;
+                if (turn++ % kFewWaves == wave) return true;
+            }
+        };
+        for (;;) {
+            int j0 = 0, j1 = 0, t0 = 0, t1 = 0;
+            if (!next(j0, t0)) break;
+            const bool two = next(j1, t1);
+            if (!two) {
+                j1 = j0;
+                t1 = t0;
+            }
+            const u32x4_t u0 = lora_u(l, m0 / 16 + m, t0, lane), u1 = lora_u(l, m0 / 16 + m, t1, lane);
+            u32x4_t b0[NF], b1[NF];
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                b0[n] = lora_b(l, j0, N, n0 + n * 16, t0, lane);
+                b1[n] = lora_b(l, j1, N, n0 + n * 16, t1, lane);
+            }
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                lora_add(b0[n], u0, of[m] == j0, v[m][n]);
+                lora_add(b1[n], u1, two && of[m] == j1, v[m][n]);
+            }
         }
     }
 }
@@ -387,7 +423,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
             for (int m = 0; m < MF; ++m) acc[n][m] = i32x4_t{0, 0, 0, 0};
         in += stride;
-        const bool more = in < mine;
+        const bool more = !LORA && in < mine;   // with adapters a workgroup has one tile
         if (more) corner(in, m1, n1);
         for (int round = 0; round < rounds; ++round) {
             int s = round * ST + ST - 1;   // stage that the step requests
@@ -444,29 +480,114 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 ws[n][i] = w.scales[min(n0 + (wn * NF + n) * 16 + fp * 4 + i, N - 1)];
+        // the tile's values, in the sums' registers
+        auto value = [&](int n, int m) { return __builtin_bit_cast(f32x4_t, acc[n][m]); };
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                f32x4_t v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = (float)acc[n][m][i] * as[m] * ws[n][i];
+                acc[n][m] = __builtin_bit_cast(i32x4_t, v);
+            }
+        if constexpr (LORA) {
+            // One adapter after another among the tile's rows, ST steps of ranks at a time: its
+            // columns, and once the rows' u, go through LDS, where the product's stages were.
+            constexpr int QL = (BM + WAVE - 1) / WAVE;
+            int here = lane;   // nothing of this is computed before the product's loop, which needs the registers
+            asm volatile("" : "+v"(here));
+            const int tiles_in = min(BM / 16, (M - m0 + 15) / 16), cols_in = min(BN, N - n0);
+            const buf_rsrc_t ru = make_buf(lora.u + (size_t)(m0 / 16) * lora.steps * (WAVE * 8),
+                                           (uint32_t)(tiles_in * lora.steps) * 1024u);
+            int all[QL], of[MF];
+            unsigned long long left[QL];
+#pragma unroll
+            for (int q = 0; q < QL; ++q) {
+                const int j = lora_of(lora, m0 + q * WAVE + here, M);
+                all[q] = q * WAVE + here < BM ? j : -1;
+            }
+#pragma unroll
+            for (int m = 0; m < MF; ++m) of[m] = lora_of(lora, m0 + (wm * MF + m) * 16 + here % 16, M);
+            for (int base = 0; base < lora.steps; base += ST) {
+#pragma unroll
+                for (int q = 0; q < QL; ++q) left[q] = __ballot(all[q] >= 0);
+                bool first = true;
+                for (;;) {
+                    int j = -1;
+#pragma unroll
+                    for (int q = QL - 1; q >= 0; --q)
+                        if (left[q]) j = __builtin_amdgcn_readlane(all[q], __builtin_ctzll(left[q]));
+                    if (j < 0) break;
+#pragma unroll
+                    for (int q = 0; q < QL; ++q) left[q] &= ~__ballot(all[q] == j);
+                    wait_loads<0>();
+                    __syncthreads();   // what the stages held has been read
+                    if (first) {
+#pragma unroll
+                        for (int st = 0; st < ST; ++st)
+                            for (int t = wave; t < BM / 16; t += WAVES)
+                                if (base + st < lora.steps)
+                                    buf_to_lds16(ru, s_a(st) + t * 1024, here * 16u,
+                                                 (uint32_t)(t * lora.steps + base + st) * 1024u);
+                        first = false;
+                    }
+                    const buf_rsrc_t rl = make_buf(lora.b + ((size_t)j * N + n0) * lora.rank,
+                                                   (uint32_t)(cols_in * lora.rank) * 2u);
+#pragma unroll
+                    for (int st = 0; st < ST; ++st)
+                        for (int t = wave; t < BN / 32; t += WAVES) {   // 32 columns of 16 ranks
+                            const int rr = (base + st) * 16 + here / 16 % 2 * 8;
+                            const uint32_t c = t * 32 + here / 32 * 16 + here % 16;
+                            if (base + st < lora.steps)
+                                buf_to_lds16(rl, s_b(st) + t * 1024, rr < lora.rank ? (c * lora.rank + rr) * 2u : kPast, 0);
+                        }
+                    wait_loads<0>();
+                    __syncthreads();
+#pragma unroll
+                    for (int st = 0; st < ST; ++st) {
+                        if (base + st >= lora.steps) break;
+                        u32x4_t b[NF], u[MF];
+#pragma unroll
+                        for (int n = 0; n < NF; ++n)
+                            b[n] = *(const u32x4_t*)(s_b(st) + (wn * NF + n) * 512 + here % 32 * 16);
+#pragma unroll
+                        for (int m = 0; m < MF; ++m)
+                            u[m] = *(const u32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + here * 16);
+                        bool bad = false;
+#pragma unroll
+                        for (int n = 0; n < NF; ++n) bad |= !lora_finite(b[n]);
+                        // 0 times an infinity would reach other rows: such columns count as zeros, and u as NaN
+                        if (__ballot(bad)) {
+#pragma unroll
+                            for (int n = 0; n < NF; ++n) b[n] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+                            for (int m = 0; m < MF; ++m) u[m][0] = 0x7FC07FC0u;
+                        }
+#pragma unroll
+                        for (int m = 0; m < MF; ++m) {
+                            const bf16x8_t um = lora_only(of[m] == j, u[m]);
+#pragma unroll
+                            for (int n = 0; n < NF; ++n)
+                                acc[n][m] = __builtin_bit_cast(
+                                    i32x4_t, mfma_16x16x32(__builtin_bit_cast(bf16x8_t, b[n]), um, value(n, m)));
+                        }
+                    }
+                }
+            }
+        }
+        if constexpr (LORA) __syncthreads();   // the stores go through a stage
+        // the stores' places are not those of the scales above: kept over the adapters they need registers
+        if constexpr (LORA) asm volatile("" : "+s"(m0), "+s"(n0));
 #pragma unroll
         for (int mb = 0; mb < MF; mb += kRows / 16) {
 #pragma unroll
             for (int mi = 0; mi < kRows / 16; ++mi) {
                 const int m = mb + mi, r = m0 + (wm * MF + m) * 16 + fr;
-                f32x4_t val[NF];
-#pragma unroll
-                for (int n = 0; n < NF; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) val[n][i] = (float)acc[n][m][i] * as[m] * ws[n][i];
-                if constexpr (LORA) {
-                    const int of = lora_of(lora, r, M);
-                    unsigned long long left = __ballot(of >= 0);
-                    while (left) {
-                        const int j = __builtin_amdgcn_readlane(of, __builtin_ctzll(left));
-                        left &= ~__ballot(of == j);
-                        lora_expand<NF>(lora, j, of, N, m0 + (wm * MF + m) * 16, n0 + wn * NF * 16, val);
-                    }
-                }
 #pragma unroll
                 for (int n = 0; n < NF; ++n) {
                     const int c = n0 + (wn * NF + n) * 16 + fp * 4;
-                    const f32x4_t v = val[n];
+                    const f32x4_t v = value(n, m);
                     const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                     if (wide) {
                         *(u32x2_t*)(s_o + (mi * 16 + fr) * kLdc + n * 16 + fp * 4) = o;
@@ -497,12 +618,6 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
         // The staging place is the next request's.  Stores still in flight only make the
         // counted waits of the next tile stricter.
         bare_barrier_i8();
-        if constexpr (LORA) {   // read again, so that the adapters' products have their registers
-#pragma unroll
-            for (int n = 0; n < NF; ++n) fb[0][n] = read_b(0, 0, n);
-#pragma unroll
-            for (int m = 0; m < FA; ++m) fa[0][m] = read_a(0, 0, m);
-        }
     }
     wait_loads<0>();
 }
@@ -829,7 +944,7 @@ static hipError_t launch_linear(const int8_t* a, const float* a_scale, int M, in
     {                                                                                         \
         const int mt = cdiv(M, WM * MF * 16), nt = cdiv(N, WN * NF * 16);                     \
         const int lds = (WM * MF + WN * NF) * 1024 * ST * KS, most = kCUs * (kLdsBytes / lds);     \
-        const int grid = mt * nt < most ? (mt * nt + 7) / 8 * 8 : most;                       \
+        const int grid = LORA || mt * nt < most ? (mt * nt + 7) / 8 * 8 : most;                       \
         linear_tiles_kernel<WM, MF, WN, NF, ST, KS, LORA><<<grid, WM * WN * WAVE, 0, stream>>>(   \
             a, a_scale, M, K, w, N, out, mt, nt, lora);                                       \
     }

@@ -1,17 +1,18 @@
 // The adapters' first product: u[m, r] = scale_j * a_scale[m] * sum_k A_j[r, k] a[m, k] for the
 // rows m that have an adapter j = adapter[m] (codes a as bf16, which holds them exactly;
-// products exact, sums fp32).
+// products exact, sums fp32), written as two bf16 in the order of the second product's operand
+// (moe_lora.h).
 //
-// A workgroup takes 16 MT rows, every gridDim.y-th of the adapters among them, and a part of
-// K, which its 8 waves split once more; their sums meet in LDS.  Rows of other adapters are
-// zeros in the products.  Bound by reading A, once for each tile of rows that has the adapter.
+// A workgroup multiplies 16 RT ranks of one adapter by up to 16 MT rows that have it, its waves
+// splitting K; their sums meet in LDS.  Bound by reading A, once for each such set of rows, so
+// where tiles of 16 rows as they come could read more than kDirectBytes (rows of many adapters,
+// or many rows), a kernel in front puts the rows in order of their adapters.  Otherwise a
+// workgroup finds the adapters of its 16 rows itself, and rows of others are zeros.
 #include "moe_device.h"
 #include "moe_i8.h"
 #include "moe_lora.h"
 
 namespace moeq4 {
-
-constexpr int kLsWaves = 8;
 
 // Eight codes as bf16.
 __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t lo, uint32_t hi) {
@@ -24,136 +25,250 @@ __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t lo, uint32_t hi) {
     return r;
 }
 
-// RT: tiles of 16 ranks.
-template <int MT, int RT>
-__global__ __launch_bounds__(kLsWaves* WAVE) void lora_shrink_kernel(
-    const int8_t* __restrict__ a, const float* __restrict__ a_scale, int M, int K, const uint16_t* __restrict__ A,
-    const float* __restrict__ scales, const int32_t* __restrict__ adapter, int n, int R,
-    float* __restrict__ u) {
-    __shared__ f32x4_t s_part[kLsWaves][RT][WAVE];
+struct ShrinkArgs {
+    const int8_t* a;
+    const float* a_scale;
+    const uint16_t* A;
+    const float* scales;
+    const int32_t* adapter;
+    uint16_t* u;
+    int M, K, n, rank, steps;      // steps of 16 ranks
+    const int32_t* order;          // grouped: rows by adapter, and the blocks of up to 64 of them
+    const int4* blocks;            // (adapter, first place in order, rows, -)
+    const int* n_blocks;
+};
+
+// One adapter's product with the rows row[m] (below 0: none) of the lanes; W waves.
+template <int MT, int RT, int W, int AHEAD>
+__device__ __forceinline__ void shrink_rows(const ShrinkArgs& p, int j, int t0, const int (&row)[MT],
+                                            f32x4_t (*s_part)[RT][WAVE]) {
     const int lane = threadIdx.x % WAVE, fr = lane % 16, fp = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int m0 = blockIdx.x * 16 * MT;
-    const int steps = K / 64, share = kLsWaves * gridDim.z, at = blockIdx.z * kLsWaves + wave;
-    const int s0 = (int)((long long)steps * at / share), s1 = (int)((long long)steps * (at + 1) / share);
-    int of[MT];
-    unsigned long long left[MT];
+    const int steps = p.K / 64, s0 = steps * wave / W, s1 = steps * (wave + 1) / W;
+    const uint16_t* Aj = p.A + ((size_t)j * p.rank + t0 * 16 + fr) * p.K + fp * 16;
+    f32x4_t acc[MT][RT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = m0 + m * 16 + fr;
-        const int j = r < M ? adapter[r] : -1;
-        of[m] = j >= 0 && j < n ? j : -1;
-        left[m] = __ballot(of[m] >= 0) & 0xFFFF;
-    }
-    for (int turn = 0;; ++turn) {
-        // the next adapter among the rows
-        int j = -1;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int m = MT - 1; m >= 0; --m)
-            if (left[m]) j = __builtin_amdgcn_readlane(of[m], __builtin_ctzll(left[m]));
-        if (j < 0) break;
-        bool mine[MT];
+        for (int t = 0; t < RT; ++t) acc[m][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    u32x4_t w[AHEAD][RT][2], c[AHEAD][MT];
+    auto load = [&](int q, int s) {
+        const bool in = s < s1;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            mine[m] = of[m] == j;
-            left[m] &= ~__ballot(mine[m]);
-        }
-        if (turn % (int)gridDim.y != (int)blockIdx.y) continue;
-        f32x4_t acc[MT][RT];
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[q][t][i] = in && (t0 + t) * 16 + fr < p.rank
+                                 ? *(const u32x4_t*)(Aj + (size_t)t * 16 * p.K + s * 64 + 8 * i)
+                                 : u32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int m = 0; m < MT; ++m)
+            c[q][m] = in && row[m] >= 0 ? *(const u32x4_t*)(p.a + (size_t)row[m] * p.K + s * 64 + fp * 16)
+                                        : u32x4_t{0, 0, 0, 0};
+    };
 #pragma unroll
-            for (int t = 0; t < RT; ++t) acc[m][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        const uint16_t* Aj = A + (size_t)j * R * K;
-        for (int s = s0; s < s1; ++s) {
-            const int kb = s * 64 + fp * 16;
-            u32x4_t w[RT][2], c[MT];
+    for (int q = 0; q < AHEAD; ++q) load(q, s0 + q);
+    for (int s = s0; s < s1; s += AHEAD) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const int r = t * 16 + fr;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    w[t][i] = r < R ? *(const u32x4_t*)(Aj + (size_t)r * K + kb + 8 * i) : u32x4_t{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                c[m] = mine[m] ? *(const u32x4_t*)(a + (size_t)(m0 + m * 16 + fr) * K + kb) : u32x4_t{0, 0, 0, 0};
+        for (int q = 0; q < AHEAD; ++q) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const bf16x8_t b = codes_bf16(c[m][2 * i], c[m][2 * i + 1]);
+                    const bf16x8_t b = codes_bf16(c[q][m][2 * i], c[q][m][2 * i + 1]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
-                        acc[m][t] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, w[t][i]), b, acc[m][t]);
+                        acc[m][t] = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, w[q][t][i]), b, acc[m][t]);
                 }
+            load(q, s + q + AHEAD);
         }
-        const float scale = scales[j];
+    }
+    const float scale = p.scales[j];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (!__ballot(mine[m])) continue;
-            __syncthreads();
+    for (int m = 0; m < MT; ++m) {
+        if (!__ballot(row[m] >= 0)) continue;
+        __syncthreads();
 #pragma unroll
-            for (int t = 0; t < RT; ++t) s_part[wave][t][lane] = acc[m][t];
-            __syncthreads();
-            for (int t = wave; t < RT; t += kLsWaves) {
-                f32x4_t v = s_part[0][t][lane];
+        for (int t = 0; t < RT; ++t) s_part[wave][t][lane] = acc[m][t];
+        __syncthreads();
+        for (int t = wave; t < RT; t += W) {
+            if (t0 + t >= p.steps) break;
+            f32x4_t v = s_part[0][t][lane];
 #pragma unroll
-                for (int w = 1; w < kLsWaves; ++w) v += s_part[w][t][lane];
-                const int row = m0 + m * 16 + fr, r = t * 16 + fp * 4;
-                if (mine[m] && r < R)
-                    *(f32x4_t*)(u + ((size_t)blockIdx.z * M + row) * R + r) = v * (a_scale[row] * scale);
+            for (int i = 1; i < W; ++i) v += s_part[i][t][lane];
+            const int r = row[m];
+            if (r >= 0) {
+                v *= p.a_scale[r] * scale;
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+                    lo[i] = pack_bf16x2(v[2 * i] - __builtin_bit_cast(float, hi[i] << 16),
+                                        v[2 * i + 1] - __builtin_bit_cast(float, hi[i] & 0xFFFF0000u));
+                }
+                // ranks 4 fp .. + 3: half of what lane r % 16 + 16 (fp / 2) of the operand holds
+                uint16_t* o = p.u + (((size_t)(r / 16) * p.steps + t0 + t) * WAVE + r % 16 + fp / 2 * 16) * 8 + fp % 2 * 4;
+                *(u32x2_t*)o = u32x2_t{hi[0], hi[1]};
+                *(u32x2_t*)(o + 32 * 8) = u32x2_t{lo[0], lo[1]};
             }
         }
     }
 }
 
-static int lora_row_tiles(int M) { return M >= 1024 ? 4 : 1; }
-
-// Parts of K, so that a few rows still reach many compute units.
-static int lora_parts(int M, int K) {
-    const int tiles = (M + 15) / 16;
-    int parts = M >= 1024 ? 2 : 32 / tiles;
-    const int most = K / 512 > 0 ? K / 512 : 1;
-    parts = parts < 1 ? 1 : parts;
-    parts = parts < most ? parts : most;
-    return parts < 8 ? parts : 8;
+// 16 rows as they come, every gridDim.y-th of their adapters, one step of ranks.
+constexpr int kSdWaves = 16;
+__global__ __launch_bounds__(kSdWaves* WAVE) void lora_shrink_kernel(ShrinkArgs p) {
+    __shared__ f32x4_t s_part[kSdWaves][1][WAVE];
+    const int r = blockIdx.x * 16 + threadIdx.x % 16;
+    int of = r < p.M ? p.adapter[r] : -1;
+    of = of >= 0 && of < p.n ? of : -1;
+    unsigned long long left = __ballot(of >= 0) & 0xFFFF;
+    for (int turn = 0; left; ++turn) {
+        const int j = __builtin_amdgcn_readlane(of, __builtin_ctzll(left));
+        left &= ~__ballot(of == j);
+        if (turn % (int)gridDim.y != (int)blockIdx.y) continue;
+        const int row[1] = {of == j ? r : -1};
+        shrink_rows<1, 1, kSdWaves, 4>(p, j, blockIdx.z, row, s_part);
+    }
 }
 
-size_t linear_lora_ws_bytes(int M, int K, int rank) {
-    return align_up((size_t)lora_parts(M, K) * M * rank * 4, 256);
+// A block of rows of one adapter, RT steps of ranks.
+constexpr int kSgWaves = 8, kSgRows = 64;
+template <int RT>
+__global__ __launch_bounds__(kSgWaves* WAVE) void lora_shrink_grouped_kernel(ShrinkArgs p) {
+    __shared__ f32x4_t s_part[kSgWaves][RT][WAVE];
+    if ((int)blockIdx.x >= *p.n_blocks) return;
+    const int4 b = p.blocks[blockIdx.x];
+    int row[kSgRows / 16];
+#pragma unroll
+    for (int m = 0; m < kSgRows / 16; ++m) {
+        const int at = m * 16 + threadIdx.x % 16;
+        row[m] = at < b.z ? p.order[b.y + at] : -1;
+    }
+    shrink_rows<kSgRows / 16, RT, kSgWaves, 3>(p, b.x, blockIdx.y * RT, row, s_part);
 }
 
-template <int MT>
-static void launch_shrink(dim3 grid, const int8_t* a, const float* a_scale, int M, int K, const uint16_t* A,
-                          const float* scales, const int32_t* of, int n, int R, float* u, hipStream_t stream) {
-#define MOE_SHRINK(RT) \
-    lora_shrink_kernel<MT, RT><<<grid, kLsWaves * WAVE, 0, stream>>>(a, a_scale, M, K, A, scales, of, n, R, u)
-    if (R <= 16) MOE_SHRINK(1);
-    else if (R <= 32) MOE_SHRINK(2);
-    else if (R <= 64) MOE_SHRINK(4);
-    else MOE_SHRINK(8);
-#undef MOE_SHRINK
+// Rows in order of their adapters, in blocks, by one workgroup: counts, a scan over the
+// adapters, places.  The order inside an adapter is any: a row's product does not depend on it.
+constexpr int kGroupThreads = 1024, kGroupMax = 4096;   // adapters whose counts fit LDS
+__global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(const int32_t* adapter, int M, int n,
+                                                                   int32_t* order, int4* blocks, int* n_blocks) {
+    __shared__ int s_at[kGroupMax];
+    __shared__ int2 s_wave[kGroupThreads / WAVE];
+    const int tid = threadIdx.x, lane = tid % WAVE;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    for (int j = tid; j < n; j += kGroupThreads) s_at[j] = 0;
+    __syncthreads();
+    // rows of one adapter lie together mostly: a wave's rows of one count at once
+    for (int m0 = 0; m0 < M; m0 += kGroupThreads) {
+        const int m = m0 + tid, j = adapter[min(m, M - 1)];
+        const bool on = m < M && j >= 0 && j < n;
+        if (__ballot(on && j == __builtin_amdgcn_readfirstlane(j)) == ~0ull) {
+            if (lane == 0) atomicAdd(&s_at[j], WAVE);
+        } else if (on) {
+            atomicAdd(&s_at[j], 1);
+        }
+    }
+    __syncthreads();
+    int2 base = {0, 0};   // rows and blocks of the adapters before
+    for (int j0 = 0; j0 < n; j0 += kGroupThreads) {
+        const int j = j0 + tid, count = j < n ? s_at[j] : 0;
+        int2 upto = {count, (count + kSgRows - 1) / kSgRows};
+#pragma unroll
+        for (int off = 1; off < WAVE; off <<= 1) {
+            const int2 o = {__shfl_up(upto.x, off, WAVE), __shfl_up(upto.y, off, WAVE)};
+            if (lane >= off) upto = {upto.x + o.x, upto.y + o.y};
+        }
+        if (lane == WAVE - 1) s_wave[wave] = upto;
+        __syncthreads();
+        int2 at = base;
+        for (int w = 0; w < kGroupThreads / WAVE; ++w) {
+            const int2 v = s_wave[w];
+            if (w < wave) at = {at.x + v.x, at.y + v.y};
+            base = {base.x + v.x, base.y + v.y};
+        }
+        const int first = at.x + upto.x - count;
+        int b = at.y + upto.y - (count + kSgRows - 1) / kSgRows;
+        for (int done = 0; done < count; done += kSgRows, ++b)
+            blocks[b] = int4{j, first + done, min(kSgRows, count - done), 0};
+        if (j < n) s_at[j] = first;
+        __syncthreads();
+    }
+    if (tid == 0) *n_blocks = base.y;
+    for (int m0 = 0; m0 < M; m0 += kGroupThreads) {
+        const int m = m0 + tid, j = adapter[min(m, M - 1)];
+        const bool on = m < M && j >= 0 && j < n;
+        if (__ballot(on && j == __builtin_amdgcn_readfirstlane(j)) == ~0ull) {
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&s_at[j], WAVE);
+            order[__builtin_amdgcn_readfirstlane(at) + lane] = m;
+        } else if (on) {
+            order[atomicAdd(&s_at[j], 1)] = m;
+        }
+    }
 }
+
+// Bytes of A that workgroups of 16 rows may read at most before the rows are put in order.
+constexpr double kDirectBytes = 64e6;
+
+static bool lora_grouped(int M, int K, int n, int rank) {
+    if (n > kGroupMax) return false;
+    const int most = n < 16 ? n : 16;
+    return (double)((M + 15) / 16) * most * rank * K * 2 > kDirectBytes;
+}
+
+struct LoraWs {
+    size_t u, order, blocks, n_blocks, total;
+};
+
+// Room for either form: the workspace's size does not depend on the number of adapters.
+static LoraWs lora_ws(int M, int rank) {
+    LoraWs w{};
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += align_up(bytes, 256);
+        return at;
+    };
+    const size_t tiles = ((size_t)M + 15) / 16;
+    w.u = take(tiles * ((rank + 15) / 16) * 1024);
+    w.order = take((size_t)M * 4);
+    w.blocks = take(((size_t)M / kSgRows + (M < kGroupMax ? M : kGroupMax) + 1) * 16);
+    w.n_blocks = take(4);
+    w.total = o;
+    return w;
+}
+
+size_t linear_lora_ws_bytes(int M, int, int rank) { return lora_ws(M, rank).total; }
 
 hipError_t launch_lora_shrink(const int8_t* a, const float* a_scale, int M, int K, const uint16_t* A,
                               const float* scales, int n, int rank, const int32_t* adapter, void* ws,
                               LoraDev* out, hipStream_t stream) {
-    const int mt = lora_row_tiles(M), tiles = (M + 16 * mt - 1) / (16 * mt), parts = lora_parts(M, K);
-    int turns = 1024 / (tiles * parts);
-    turns = turns < 1 ? 1 : turns;
-    const int rows = 16 * mt < M ? 16 * mt : M, most = rows < n ? rows : n;
-    turns = turns < most ? turns : most;
-    float* u = (float*)ws;
-    const dim3 grid(tiles, turns, parts);
-    if (mt == 1) launch_shrink<1>(grid, a, a_scale, M, K, A, scales, adapter, n, rank, u, stream);
-    else launch_shrink<4>(grid, a, a_scale, M, K, A, scales, adapter, n, rank, u, stream);
-    out->u = u;
+    const LoraWs L = lora_ws(M, rank);
+    char* base = (char*)ws;
+    const int steps = (rank + 15) / 16;
+    ShrinkArgs p = {a, a_scale, A, scales, adapter, (uint16_t*)(base + L.u), M, K, n, rank, steps,
+                    (const int32_t*)(base + L.order), (const int4*)(base + L.blocks),
+                    (const int*)(base + L.n_blocks)};
+    if (lora_grouped(M, K, n, rank)) {
+        lora_group_kernel<<<1, kGroupThreads, 0, stream>>>(adapter, M, n, (int32_t*)(base + L.order),
+                                                           (int4*)(base + L.blocks), (int*)(base + L.n_blocks));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const unsigned blocks = M / kSgRows + (M < n ? M : n);
+        if (steps <= 1) lora_shrink_grouped_kernel<1><<<dim3(blocks), kSgWaves * WAVE, 0, stream>>>(p);
+        else lora_shrink_grouped_kernel<2><<<dim3(blocks, (steps + 1) / 2), kSgWaves * WAVE, 0, stream>>>(p);
+    } else {
+        const int tiles = (M + 15) / 16, rows = M < 16 ? M : 16, most = rows < n ? rows : n;
+        int turns = 2048 / (tiles * steps);
+        turns = turns < 1 ? 1 : turns < most ? turns : most;
+        lora_shrink_kernel<<<dim3(tiles, turns, steps), kSdWaves * WAVE, 0, stream>>>(p);
+    }
+    out->u = p.u;
     out->of = adapter;
     out->n = n;
     out->rank = rank;
-    out->parts = parts;
-    out->part = (size_t)M * rank;
+    out->steps = steps;
     return hipGetLastError();
 }
 

@@ -110,11 +110,10 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
                             int N, uint16_t* out, void* ws, hipStream_t stream);
 // Low-rank adapters beside the linear's product (lora_i8.hip, moe_lora.h)
 struct LoraDev {
-    const float* u;        // [parts][M][rank]: the adapters' first product of each row, scaled
+    const uint16_t* u;     // the adapters' first product of each row, scaled, as operands (moe_lora.h)
     const uint16_t* b;     // bf16 [n, N, rank]
     const int32_t* of;     // [M]: a row's adapter, none outside 0 .. n - 1
-    int n, rank, parts;
-    size_t part;           // M * rank
+    int n, rank, steps;    // steps of 16 ranks
 };
 constexpr int kLoraMaxRank = 128;
 size_t linear_lora_ws_bytes(int M, int K, int rank);

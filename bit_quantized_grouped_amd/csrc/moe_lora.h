@@ -1,11 +1,11 @@
 // Low-rank adapters beside the dense product of 8-bit codes: what the product's kernels add.
 //
 // u[m] = scale_j * a_scale[m] * (A_j a[m]), j = adapter[m], comes from the shrink kernel
-// (lora_i8.hip) in fp32, in `parts` pieces of K that are added here.  The expansion B_j u is a
-// matrix product of bf16: 16 columns of out are the rows of its A operand (B_j as it is), 16
-// rows of out its columns, and a step of its K of 32 holds 16 ranks twice: with u rounded to
-// bf16, and with what that rounding left, so that u counts to 16 bits.  Rows of another
-// adapter have zeros, and keep their sums whatever the adapter holds.
+// (lora_i8.hip).  The expansion B_j u is a matrix product of bf16: 16 columns of out are the
+// rows of its A operand (B_j as it is), 16 rows of out its columns, and a step of its K of
+// 32 holds 16 ranks twice: with u rounded to bf16, and with what that rounding left, so that u
+// counts to 16 bits.  u lies in that operand's order, a kilobyte for 16 rows and 16 ranks.
+// Rows of another adapter have zeros there, and keep their sums whatever the adapter holds.
 #pragma once
 
 #include "moe_device.h"
@@ -13,59 +13,47 @@
 
 namespace moeq4 {
 
-// Ranks rr .. rr + 7 of a row's u as bf16, or the rest of their rounding.
-__device__ __forceinline__ bf16x8_t lora_u(const LoraDev& l, size_t row, int rr, bool on, bool rest) {
-    f32x4_t v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    if (on) {
-        const float* u = l.u + row * l.rank + rr;
-        for (int i = 0; i < l.parts; ++i, u += l.part) {
-            v[0] += *(const f32x4_t*)u;
-            v[1] += *(const f32x4_t*)(u + 4);
-        }
-    }
-    bf16x8_t r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = v[i / 4][i % 4];
-        const __bf16 h = (__bf16)x;
-        r[i] = rest ? (__bf16)(x - (float)h) : h;
-    }
-    return r;
+// 16 ranks of the rows of a tile of 16, as they lie.
+__device__ __forceinline__ u32x4_t lora_u(const LoraDev& l, int m_tile, int step, int lane) {
+    return *(const u32x4_t*)(l.u + (((size_t)m_tile * l.steps + step) * WAVE + lane) * 8);
 }
 
-// Ranks rr .. rr + 7 of column n of adapter j.
-__device__ __forceinline__ bf16x8_t lora_b(const LoraDev& l, int j, int N, int n, int rr) {
+__device__ __forceinline__ bf16x8_t lora_only(bool mine, const u32x4_t& u) {
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mine ? u[i] : 0u;
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// The same 16 ranks of 16 columns of adapter j, from column n0 on.
+__device__ __forceinline__ u32x4_t lora_b(const LoraDev& l, int j, int N, int n0, int step,
+                                           int lane) {
+    const int n = n0 + lane % 16, rr = step * 16 + lane / 16 % 2 * 8;
     u32x4_t v = {0, 0, 0, 0};
     if (n < N && rr < l.rank) v = *(const u32x4_t*)(l.b + ((size_t)j * N + n) * l.rank + rr);
-    return __builtin_bit_cast(bf16x8_t, v);
+    return v;
 }
 
 // Adapter of row r, or -1.
 __device__ __forceinline__ int lora_of(const LoraDev& l, int r, int M) {
-    const int j = r < M ? l.of[r] : -1;
-    return j >= 0 && j < l.n ? j : -1;
+    const int j = l.of[min(r, M - 1)];
+    return r < M && j >= 0 && j < l.n ? j : -1;
 }
 
-// One adapter's part of the pieces at rows m0 .. +15 and columns n0 + 16 i: v[i] is D of the
-// 16 x 16 product, column n0 + 16 i + 4 (lane / 16) + 0..3, row m0 + lane % 16.  j: the adapter,
-// `of`: the one of this lane's row.
-template <int NF>
-__device__ __forceinline__ void lora_expand(const LoraDev& l, int j, int of, int N, int m0, int n0,
-                                            f32x4_t (&v)[NF]) {
-    const int lane = __lane_id(), fr = lane % 16, fp = lane / 16;
-    const bool mine = of == j;
+// No infinity or NaN among eight bf16.
+__device__ __forceinline__ bool lora_finite(const u32x4_t& v) {
+    bool ok = true;
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-        f32x4_t t = v[i];
-        for (int r0 = 0; r0 < l.rank; r0 += 16) {
-            const int rr = r0 + fp % 2 * 8;
-            const bf16x8_t b = lora_b(l, j, N, n0 + i * 16 + fr, rr);
-            const bf16x8_t u = lora_u(l, (size_t)(m0 + fr), rr, mine && rr < l.rank, fp >= 2);
-            t = mfma_16x16x32(b, u, t);
-        }
+    for (int i = 0; i < 4; ++i)
+        ok = ok && (v[i] & 0x7F80u) != 0x7F80u && (v[i] & 0x7F800000u) != 0x7F800000u;
+    return ok;
+}
+
+// v += b u in the rows that are `mine`.
+__device__ __forceinline__ void lora_add(const u32x4_t& b, const u32x4_t& u, bool mine, f32x4_t& v) {
+    const f32x4_t t = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, b), lora_only(mine, u), v);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[i][q] = mine ? t[q] : v[i][q];
-    }
+    for (int q = 0; q < 4; ++q) v[q] = mine ? t[q] : v[q];
 }
 
 }  // namespace moeq4
