@@ -122,7 +122,8 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
     const int n_tiles = (N + 15) / 16;
     const int m0 = blockIdx.x / n_tiles * 16, n0 = blockIdx.x % n_tiles * 16;
     // rows behind the last read the last; their results go nowhere
-    const int8_t* pa = a + (size_t)min(m0 + lane % 16, M - 1) * K + lane / 16 * 16;
+    const int row = row_at<LORA>(lora, m0 + lane % 16, M);
+    const int8_t* pa = a + (size_t)row * K + lane / 16 * 16;
     const int8_t* pw = w.codes + (size_t)n0 * K +
                        (w.tiles ? (size_t)lane * 16
                                 : (size_t)min(lane % 16, N - 1 - n0) * K + lane / 16 * 16);
@@ -151,9 +152,9 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
     if (wave) return;
 #pragma unroll
     for (int i = 0; i < kFewWaves - 1; ++i) acc += s_part[i][lane];
-    const int r = m0 + lane % 16, c = n0 + lane / 16 * 4;
-    if (r >= M || c >= N) return;
-    const float as = a_scale[r];
+    const int c = n0 + lane / 16 * 4;
+    if (m0 + lane % 16 >= M || c >= N) return;
+    const float as = a_scale[row];
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * as * w.scales[min(c + i, N - 1)];
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += t[i];
     }
-    uint16_t* o = out + (size_t)r * N + c;
+    uint16_t* o = out + (size_t)row * N + c;
     if (N % 4 == 0) {
         *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     } else {
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
 #pragma unroll
     for (int m = 0; m < MF; ++m) {
         const uint32_t r = m0 + m * 16 + fr;
-        oa[m] = r < (uint32_t)M ? r * (uint32_t)K + fp * 16 : kPast;
+        oa[m] = r < (uint32_t)M ? (uint32_t)row_at<LORA>(lora, r, M) * (uint32_t)K + fp * 16 : kPast;
     }
 #pragma unroll
     for (int n = 0; n < NF; ++n) {
@@ -259,7 +260,8 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
             for (int i = 1; i < W; ++i) sum += s_part[i][wave][lane];
             const int p = p0 + wave, r = m0 + p % MF * 16 + fr, c = n0 + p / MF * 16 + fp * 4;
             if (r < M && c < N) {
-                const float as = a_scale[r];
+                const int row = row_at<LORA>(lora, r, M);
+                const float as = a_scale[row];
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = (float)sum[i] * as * w.scales[min(c + i, N - 1)];
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] += t[i];
                 }
-                uint16_t* o = out + (size_t)r * N + c;
+                uint16_t* o = out + (size_t)row * N + c;
                 if (N % 4 == 0) {
                     *(u32x2_t*)o = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 } else {
@@ -358,7 +360,9 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
                 const uint32_t r = m0 + (i * WAVES + wave) * 16 + lr + j * 8;
-                va[i][j] = r < (uint32_t)M ? r * (uint32_t)K + (piece ^ j * 4) * 16 : kPast;
+                va[i][j] = r < (uint32_t)M
+                               ? (uint32_t)row_at<LORA>(lora, r, M) * (uint32_t)K + (piece ^ j * 4) * 16
+                               : kPast;
             }
 #pragma unroll
         for (int i = 0; i < LB; ++i)
@@ -407,6 +411,18 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
     i32x4_t fb[2][NF], fa[2][FA];
     int m0, n0, m1 = 0, n1 = 0;
     corner(in, m0, n0);
+    // the adapters of the tile's rows, and of this wave's row tiles
+    constexpr int QL = (BM + WAVE - 1) / WAVE;
+    int all[LORA ? QL : 1], of[LORA ? MF : 1];
+    if constexpr (LORA) {
+#pragma unroll
+        for (int q = 0; q < QL; ++q) {
+            const int j = lora_of(lora, m0 + q * WAVE + lane, M);
+            all[q] = q * WAVE + lane < BM ? j : -1;
+        }
+#pragma unroll
+        for (int m = 0; m < MF; ++m) of[m] = lora_of(lora, m0 + (wm * MF + m) * 16 + fr, M);
+    }
     sources(m0, n0);
 #pragma unroll
     for (int st = 0; st < ST - 1; ++st) load(st, st);
@@ -472,9 +488,13 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
         static_assert(kRows * kLdc * 2 <= (BM < BN ? BM : BN) * 64 * KS / kHalf && kRows * NF * 2 % WAVE == 0,
                       "a wave's staged rows fit its share");
         const bool wide = N % 8 == 0;
+        int rows[MF];
         float as[MF], ws[NF][4];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) as[m] = a_scale[min(m0 + (wm * MF + m) * 16 + fr, M - 1)];
+        for (int m = 0; m < MF; ++m) {
+            rows[m] = row_at<LORA>(lora, m0 + (wm * MF + m) * 16 + fr, M);
+            as[m] = a_scale[rows[m]];
+        }
 #pragma unroll
         for (int n = 0; n < NF; ++n)
 #pragma unroll
@@ -494,21 +514,12 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
         if constexpr (LORA) {
             // One adapter after another among the tile's rows, ST steps of ranks at a time: its
             // columns, and once the rows' u, go through LDS, where the product's stages were.
-            constexpr int QL = (BM + WAVE - 1) / WAVE;
             int here = lane;   // nothing of this is computed before the product's loop, which needs the registers
             asm volatile("" : "+v"(here));
             const int tiles_in = min(BM / 16, (M - m0 + 15) / 16), cols_in = min(BN, N - n0);
             const buf_rsrc_t ru = make_buf(lora.u + (size_t)(m0 / 16) * lora.steps * (WAVE * 8),
                                            (uint32_t)(tiles_in * lora.steps) * 1024u);
-            int all[QL], of[MF];
             unsigned long long left[QL];
-#pragma unroll
-            for (int q = 0; q < QL; ++q) {
-                const int j = lora_of(lora, m0 + q * WAVE + here, M);
-                all[q] = q * WAVE + here < BM ? j : -1;
-            }
-#pragma unroll
-            for (int m = 0; m < MF; ++m) of[m] = lora_of(lora, m0 + (wm * MF + m) * 16 + here % 16, M);
             for (int base = 0; base < lora.steps; base += ST) {
 #pragma unroll
                 for (int q = 0; q < QL; ++q) left[q] = __ballot(all[q] >= 0);
@@ -594,7 +605,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
                     } else if (r < M) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (c + i < N) out[(size_t)r * N + c + i] = (uint16_t)(o[i / 2] >> 16 * (i % 2));
+                            if (c + i < N) out[(size_t)rows[m] * N + c + i] = (uint16_t)(o[i / 2] >> 16 * (i % 2));
                     }
                 }
             }
@@ -605,8 +616,9 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
                 for (int i = 0; i < kRows * NF * 2 / WAVE; ++i) {
                     const int p = i * WAVE + lane, row = p / (NF * 2), c8 = p % (NF * 2) * 8;
                     const int r = m0 + (wm * MF + mb) * 16 + row, c = n0 + wn * NF * 16 + c8;
+                    const int at = LORA ? __shfl(rows[mb], row, WAVE) : r;   // one row tile: kRows 16
                     if (r < M && c < N)
-                        *(u32x4_t*)(out + (size_t)r * N + c) = *(const u32x4_t*)(s_o + row * kLdc + c8);
+                        *(u32x4_t*)(out + (size_t)at * N + c) = *(const u32x4_t*)(s_o + row * kLdc + c8);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();

@@ -33,15 +33,16 @@ struct ShrinkArgs {
     const int32_t* adapter;
     uint16_t* u;
     int M, K, n, rank, steps;      // steps of 16 ranks
-    const int32_t* order;          // grouped: rows by adapter, and the blocks of up to 64 of them
+    const int32_t* order;          // grouped: rows by adapter, and the blocks of kSgRows of them
     const int4* blocks;            // (adapter, first place in order, rows, -)
     const int* n_blocks;
 };
 
-// One adapter's product with the rows row[m] (below 0: none) of the lanes; W waves.
+// One adapter's product with the rows row[m] (below 0: none) of the lanes, whose u goes to
+// place[m]; W waves.
 template <int MT, int RT, int W, int AHEAD>
 __device__ __forceinline__ void shrink_rows(const ShrinkArgs& p, int j, int t0, const int (&row)[MT],
-                                            f32x4_t (*s_part)[RT][WAVE]) {
+                                            const int (&place)[MT], f32x4_t (*s_part)[RT][WAVE]) {
     const int lane = threadIdx.x % WAVE, fr = lane % 16, fp = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int steps = p.K / 64, s0 = steps * wave / W, s1 = steps * (wave + 1) / W;
@@ -96,9 +97,9 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs& p, int j, int t0, 
             f32x4_t v = s_part[0][t][lane];
 #pragma unroll
             for (int i = 1; i < W; ++i) v += s_part[i][t][lane];
-            const int r = row[m];
-            if (r >= 0) {
-                v *= p.a_scale[r] * scale;
+            const int r = place[m];
+            if (row[m] >= 0) {
+                v *= p.a_scale[row[m]] * scale;
                 uint32_t hi[2], lo[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -128,52 +129,81 @@ __global__ __launch_bounds__(kSdWaves* WAVE) void lora_shrink_kernel(ShrinkArgs 
         left &= ~__ballot(of == j);
         if (turn % (int)gridDim.y != (int)blockIdx.y) continue;
         const int row[1] = {of == j ? r : -1};
-        shrink_rows<1, 1, kSdWaves, 4>(p, j, blockIdx.z, row, s_part);
+        shrink_rows<1, 1, kSdWaves, 4>(p, j, blockIdx.z, row, row, s_part);
     }
 }
 
 // A block of rows of one adapter, RT steps of ranks.
-constexpr int kSgWaves = 8, kSgRows = 64;
+constexpr int kSgWaves = 8, kSgRows = 32;
 template <int RT>
 __global__ __launch_bounds__(kSgWaves* WAVE) void lora_shrink_grouped_kernel(ShrinkArgs p) {
     __shared__ f32x4_t s_part[kSgWaves][RT][WAVE];
     if ((int)blockIdx.x >= *p.n_blocks) return;
     const int4 b = p.blocks[blockIdx.x];
-    int row[kSgRows / 16];
+    int row[kSgRows / 16], place[kSgRows / 16];
 #pragma unroll
     for (int m = 0; m < kSgRows / 16; ++m) {
         const int at = m * 16 + threadIdx.x % 16;
-        row[m] = at < b.z ? p.order[b.y + at] : -1;
+        place[m] = b.y + at;
+        row[m] = at < b.z ? p.order[place[m]] : -1;
     }
-    shrink_rows<kSgRows / 16, RT, kSgWaves, 3>(p, b.x, blockIdx.y * RT, row, s_part);
+    shrink_rows<kSgRows / 16, RT, kSgWaves, 1>(p, b.x, blockIdx.y * RT, row, place, s_part);
 }
 
-// Rows in order of their adapters, in blocks, by one workgroup: counts, a scan over the
-// adapters, places.  The order inside an adapter is any: a row's product does not depend on it.
+// Rows in order of their adapters, those without one last, and the adapters' rows in blocks, by
+// one workgroup: counts, a scan over the adapters, places.  The order inside an adapter is any:
+// what a row gets does not depend on it.
 constexpr int kGroupThreads = 1024, kGroupMax = 4096;   // adapters whose counts fit LDS
+constexpr int kGroupRows = 8;                           // rows of a thread that it holds together
+
 __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(const int32_t* adapter, int M, int n,
-                                                                   int32_t* order, int4* blocks, int* n_blocks) {
-    __shared__ int s_at[kGroupMax];
+                                                                   int32_t* order, int32_t* of, int4* blocks,
+                                                                   int* n_blocks) {
+    __shared__ int s_at[kGroupMax + 1];      // counts, then the next place of each adapter's rows
+    __shared__ int s_block[kGroupMax + 1];   // blocks up to and with each adapter
+    __shared__ int s_first[kGroupMax + 1];
     __shared__ int2 s_wave[kGroupThreads / WAVE];
     const int tid = threadIdx.x, lane = tid % WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
-    for (int j = tid; j < n; j += kGroupThreads) s_at[j] = 0;
-    __syncthreads();
-    // rows of one adapter lie together mostly: a wave's rows of one count at once
-    for (int m0 = 0; m0 < M; m0 += kGroupThreads) {
-        const int m = m0 + tid, j = adapter[min(m, M - 1)];
-        const bool on = m < M && j >= 0 && j < n;
-        if (__ballot(on && j == __builtin_amdgcn_readfirstlane(j)) == ~0ull) {
-            if (lane == 0) atomicAdd(&s_at[j], WAVE);
-        } else if (on) {
-            atomicAdd(&s_at[j], 1);
+    for (int j = tid; j <= n; j += kGroupThreads) s_at[j] = 0;
+    int id[kGroupRows];
+    auto read = [&](int m0) {
+#pragma unroll
+        for (int i = 0; i < kGroupRows; ++i) {
+            const int j = adapter[min(m0 + i * kGroupThreads + tid, M - 1)];
+            id[i] = j >= 0 && j < n ? j : n;
         }
+    };
+    // `use` for a wave's 64 rows at a time: they are of one adapter mostly, and move the count at once
+    auto each = [&](int m0, auto use) {
+#pragma unroll
+        for (int i = 0; i < kGroupRows; ++i) {
+            const int m = m0 + i * kGroupThreads + tid;
+            if (m - lane >= M) break;
+            const bool on = m < M;
+            int at = 0;
+            if (__ballot(on && id[i] == __builtin_amdgcn_readfirstlane(id[i])) == ~0ull) {
+                if (lane == 0) at = atomicAdd(&s_at[id[i]], WAVE);
+                at = __builtin_amdgcn_readfirstlane(at) + lane;
+            } else if (on) {
+                at = atomicAdd(&s_at[id[i]], 1);
+            }
+            if (on) use(m, at, id[i]);
+        }
+    };
+    constexpr int kChunk = kGroupRows * kGroupThreads;
+    read(0);
+    __syncthreads();
+    for (int m0 = 0; m0 < M; m0 += kChunk) {
+        if (m0) read(m0);
+        each(m0, [](int, int, int) {});
     }
     __syncthreads();
     int2 base = {0, 0};   // rows and blocks of the adapters before
-    for (int j0 = 0; j0 < n; j0 += kGroupThreads) {
-        const int j = j0 + tid, count = j < n ? s_at[j] : 0;
-        int2 upto = {count, (count + kSgRows - 1) / kSgRows};
+    for (int j0 = 0; j0 <= n; j0 += kGroupThreads) {
+        const int j = j0 + tid, count = j <= n ? s_at[j] : 0;
+        const int mine = j < n ? (count + kSgRows - 1) / kSgRows : 0;
+        int2 upto = {count, mine};
 #pragma unroll
         for (int off = 1; off < WAVE; off <<= 1) {
             const int2 o = {__shfl_up(upto.x, off, WAVE), __shfl_up(upto.y, off, WAVE)};
@@ -187,24 +217,29 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(const int32_t
             if (w < wave) at = {at.x + v.x, at.y + v.y};
             base = {base.x + v.x, base.y + v.y};
         }
-        const int first = at.x + upto.x - count;
-        int b = at.y + upto.y - (count + kSgRows - 1) / kSgRows;
-        for (int done = 0; done < count; done += kSgRows, ++b)
-            blocks[b] = int4{j, first + done, min(kSgRows, count - done), 0};
-        if (j < n) s_at[j] = first;
+        if (j <= n) {
+            s_at[j] = s_first[j] = at.x + upto.x - count;
+            s_block[j] = at.y + upto.y;
+        }
         __syncthreads();
     }
     if (tid == 0) *n_blocks = base.y;
-    for (int m0 = 0; m0 < M; m0 += kGroupThreads) {
-        const int m = m0 + tid, j = adapter[min(m, M - 1)];
-        const bool on = m < M && j >= 0 && j < n;
-        if (__ballot(on && j == __builtin_amdgcn_readfirstlane(j)) == ~0ull) {
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&s_at[j], WAVE);
-            order[__builtin_amdgcn_readfirstlane(at) + lane] = m;
-        } else if (on) {
-            order[atomicAdd(&s_at[j], 1)] = m;
+    for (int b = tid; b < base.y; b += kGroupThreads) {
+        int lo = 0, hi = n - 1;   // the first adapter whose blocks reach past b
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (s_block[mid] > b) hi = mid;
+            else lo = mid + 1;
         }
+        const int first = s_first[lo] + (b - (lo ? s_block[lo - 1] : 0)) * kSgRows;
+        blocks[b] = int4{lo, first, min(kSgRows, s_first[lo + 1] - first), 0};
+    }
+    for (int m0 = 0; m0 < M; m0 += kChunk) {
+        if (M > kChunk) read(m0);
+        each(m0, [&](int m, int at, int j) {
+            order[at] = m;
+            of[at] = j;
+        });
     }
 }
 
@@ -218,7 +253,7 @@ static bool lora_grouped(int M, int K, int n, int rank) {
 }
 
 struct LoraWs {
-    size_t u, order, blocks, n_blocks, total;
+    size_t u, order, of, blocks, n_blocks, total;
 };
 
 // Room for either form: the workspace's size does not depend on the number of adapters.
@@ -233,6 +268,7 @@ static LoraWs lora_ws(int M, int rank) {
     const size_t tiles = ((size_t)M + 15) / 16;
     w.u = take(tiles * ((rank + 15) / 16) * 1024);
     w.order = take((size_t)M * 4);
+    w.of = take((size_t)M * 4);
     w.blocks = take(((size_t)M / kSgRows + (M < kGroupMax ? M : kGroupMax) + 1) * 16);
     w.n_blocks = take(4);
     w.total = o;
@@ -252,12 +288,13 @@ hipError_t launch_lora_shrink(const int8_t* a, const float* a_scale, int M, int 
                     (const int*)(base + L.n_blocks)};
     if (lora_grouped(M, K, n, rank)) {
         lora_group_kernel<<<1, kGroupThreads, 0, stream>>>(adapter, M, n, (int32_t*)(base + L.order),
-                                                           (int4*)(base + L.blocks), (int*)(base + L.n_blocks));
+                                                           (int32_t*)(base + L.of), (int4*)(base + L.blocks), (int*)(base + L.n_blocks));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const unsigned blocks = M / kSgRows + (M < n ? M : n);
         if (steps <= 1) lora_shrink_grouped_kernel<1><<<dim3(blocks), kSgWaves * WAVE, 0, stream>>>(p);
-        else lora_shrink_grouped_kernel<2><<<dim3(blocks, (steps + 1) / 2), kSgWaves * WAVE, 0, stream>>>(p);
+        else if (steps <= 2) lora_shrink_grouped_kernel<2><<<dim3(blocks), kSgWaves * WAVE, 0, stream>>>(p);
+        else lora_shrink_grouped_kernel<4><<<dim3(blocks, (steps + 3) / 4), kSgWaves * WAVE, 0, stream>>>(p);
     } else {
         const int tiles = (M + 15) / 16, rows = M < 16 ? M : 16, most = rows < n ? rows : n;
         int turns = 2048 / (tiles * steps);
@@ -265,7 +302,9 @@ hipError_t launch_lora_shrink(const int8_t* a, const float* a_scale, int M, int 
         lora_shrink_kernel<<<dim3(tiles, turns, steps), kSdWaves * WAVE, 0, stream>>>(p);
     }
     out->u = p.u;
-    out->of = adapter;
+    const bool grouped = lora_grouped(M, K, n, rank);
+    out->order = grouped ? p.order : nullptr;
+    out->of = grouped ? (const int32_t*)(base + L.of) : adapter;
     out->n = n;
     out->rank = rank;
     out->steps = steps;

@@ -112,7 +112,8 @@ hipError_t launch_linear_i8(const int8_t* a, const float* a_scale, int M, int K,
 struct LoraDev {
     const uint16_t* u;     // the adapters' first product of each row, scaled, as operands (moe_lora.h)
     const uint16_t* b;     // bf16 [n, N, rank]
-    const int32_t* of;     // [M]: a row's adapter, none outside 0 .. n - 1
+    const int32_t* order;  // [M]: the rows by adapter, in which order the product goes; NULL: as they come
+    const int32_t* of;     // [M]: in that order, a row's adapter, none outside 0 .. n - 1
     int n, rank, steps;    // steps of 16 ranks
 };
 constexpr int kLoraMaxRank = 128;

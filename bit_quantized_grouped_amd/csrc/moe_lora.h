@@ -34,7 +34,15 @@ __device__ __forceinline__ u32x4_t lora_b(const LoraDev& l, int j, int N, int n0
     return v;
 }
 
-// Adapter of row r, or -1.
+// Row at place r of the product's order; places behind the last have the last row.
+template <bool LORA>
+__device__ __forceinline__ int row_at(const LoraDev& l, int r, int M) {
+    r = min(r, M - 1);
+    if constexpr (LORA) return l.order ? l.order[r] : r;
+    return r;
+}
+
+// Adapter of the row at place r, or -1.
 __device__ __forceinline__ int lora_of(const LoraDev& l, int r, int M) {
     const int j = l.of[min(r, M - 1)];
     return r < M && j >= 0 && j < l.n ? j : -1;
