@@ -1061,7 +1061,7 @@ static int check_batch_shape(int T, int H, int I, int I_sh, int E, int k) {
 }
 
 size_t moe_decode_batch_workspace_bytes(int T, int H, int I, int I_sh, int E, int k) {
-    return check_batch_shape(T, H, I, I_sh, E, k) ? 0 : batch_ws_layout(T, I, I_sh, E, k).total;
+    return check_batch_shape(T, H, I, I_sh, E, k) ? 0 : batch_ws_layout(T, H, I, I_sh, E, k).total;
 }
 
 int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* score_bias,
@@ -1088,7 +1088,7 @@ int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* sco
         if (!aligned(x, 16) || !aligned(y, 16) || !aligned(logits, 4) || !aligned(score_bias, 4) ||
             !aligned(shared_gate, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
             return MOE_ERR_ALIGN;
-        const BatchWs L = batch_ws_layout(T, I, I_sh, E, k);
+        const BatchWs L = batch_ws_layout(T, H, I, I_sh, E, k);
         if ((st = check_ws(ws, ws_bytes, L.total))) return st;
         char* base = (char*)ws;
         a.x = x;
@@ -1114,6 +1114,7 @@ int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* sco
         a.h_lo = (uint16_t*)(base + L.h_lo);
         a.list = (uint4*)(base + L.list);
         a.n_list = (int*)(base + L.n_list);
+        a.y_part = (float*)(base + L.y_part);
         a.y = y;
         return launch_decode_batch(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
     } catch (...) {

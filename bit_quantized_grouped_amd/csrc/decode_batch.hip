@@ -26,6 +26,7 @@ namespace moeq4 {
 
 constexpr int kBgWaves = 8;              // waves of a gate/up workgroup
 constexpr int kBgThreads = kBgWaves * WAVE;
+constexpr int kBgResident = 512;        // workgroups that the chip holds, two a compute unit
 constexpr int kBgAhead = 2;              // 128-K chunks of a wave in flight
 constexpr int kBdWaves = 16;             // waves of a down workgroup
 constexpr int kBdAhead = 2;
@@ -68,10 +69,11 @@ __device__ __forceinline__ int wave_incl_sum_i32(int v, int lane) {
     return v;
 }
 
-// EPL 0: the experts are chosen already.  NT: tiles of 16 tokens.  rt: row tiles of 16 that a
-// workgroup's waves take side by side (1, 2 or 4); 8 / rt waves split K.
-template <int EPL, int NT, bool SB>
-__global__ __launch_bounds__(kBgThreads) void batch_gateup_kernel(BatchArgs p, int rt_log) {
+// EPL 0: the experts are chosen already.  rt: row tiles of 16 that a workgroup's waves take side
+// by side (1, 2 or 4); 8 / rt waves split K.  More than 16 tokens of an expert take its rows again
+// from the caches for each 16: the shared expert mostly, whose rows are few beside the others'.
+template <int EPL, bool SB>
+__global__ __launch_bounds__(kBgThreads, 4) void batch_gateup_kernel(BatchArgs p, int rt_log) {
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
     __shared__ f32x4_t s_part[kBgWaves][2][WAVE];
     __shared__ uint32_t s_scr[EPL ? kBgWaves : 1][3 * kScoredMaxK];
@@ -162,86 +164,61 @@ __global__ __launch_bounds__(kBgThreads) void batch_gateup_kernel(BatchArgs p, i
         if (mask >> lane & 1) s_tok[wave][__popcll(mask & lanemask_lt())] = lane;
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        u32x4_t wg[kBgAhead], wu[kBgAhead], xv[kBgAhead][4];
-        float sg[kBgAhead], bg[kBgAhead], su[kBgAhead], bu[kBgAhead];
-        const uint16_t* x0 = p.x + (size_t)(c < cnt ? s_tok[wave][c] : 0) * H;
-        auto load_x = [&](const uint16_t* x, bool on, u32x4_t (&v)[4]) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = on ? *(const u32x4_t*)(x + 8 * i) : u32x4_t{0, 0, 0, 0};
-        };
-        auto load = [&](int s, int q) {
-            const int kb = q * 128 + g * 32;
-            const bool in = q < q1 && kb < H;
-            wg[s] = in ? *(const u32x4_t*)(gc + (size_t)q * w_step) : u32x4_t{0, 0, 0, 0};
-            wu[s] = in ? *(const u32x4_t*)(uc + (size_t)q * w_step) : u32x4_t{0, 0, 0, 0};
-            if constexpr (SB) {
-                const uint32_t a = in ? ((const uint32_t*)mg.scales)[s_at + (size_t)q * 128] : 0u;
-                const uint32_t b = in ? ((const uint32_t*)mu.scales)[s_at + (size_t)q * 128] : 0u;
-                sg[s] = bf16_to_f32((uint16_t)a);
-                bg[s] = bf16_to_f32((uint16_t)(a >> 16));
-                su[s] = bf16_to_f32((uint16_t)b);
-                bu[s] = bf16_to_f32((uint16_t)(b >> 16));
-            } else {
-                sg[s] = in ? bf16_to_f32(mg.scales[s_at + q * 2]) : 0.f;
-                bg[s] = in ? bf16_to_f32(mg.biases[s_at + q * 2]) : 0.f;
-                su[s] = in ? bf16_to_f32(mu.scales[s_at + q * 2]) : 0.f;
-                bu[s] = in ? bf16_to_f32(mu.biases[s_at + q * 2]) : 0.f;
-            }
-            load_x(x0 + kb, in && c < cnt, xv[s]);
-        };
-        f32x4_t acc[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < kBgAhead; ++s) load(s, q0 + s);
-        for (int q = q0; q < q1; q += kBgAhead) {
-#pragma unroll
-            for (int s = 0; s < kBgAhead; ++s) {
-                bf16x8_t ag[4], au[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ag[i] = dequant_word(wg[s][i], sg[s] * unit_inv, bg[s]);
-                    au[i] = dequant_word(wu[s][i], su[s] * unit_inv, bu[s]);
+        for (int t0 = 0; t0 < cnt; t0 += 16) {
+            const int at = t0 + c;
+            const bool mine = at < cnt;
+            const int t = mine ? s_tok[wave][at] : 0;
+            const uint16_t* x0 = p.x + (size_t)t * H;
+            u32x4_t wg[kBgAhead], wu[kBgAhead], xv[kBgAhead][4];
+            float sg[kBgAhead], bg[kBgAhead], su[kBgAhead], bu[kBgAhead];
+            auto load = [&](int s, int q) {
+                const int kb = q * 128 + g * 32;
+                const bool in = q < q1 && kb < H;
+                wg[s] = in ? *(const u32x4_t*)(gc + (size_t)q * w_step) : u32x4_t{0, 0, 0, 0};
+                wu[s] = in ? *(const u32x4_t*)(uc + (size_t)q * w_step) : u32x4_t{0, 0, 0, 0};
+                if constexpr (SB) {
+                    const uint32_t a = in ? ((const uint32_t*)mg.scales)[s_at + (size_t)q * 128] : 0u;
+                    const uint32_t b = in ? ((const uint32_t*)mu.scales)[s_at + (size_t)q * 128] : 0u;
+                    sg[s] = bf16_to_f32((uint16_t)a);
+                    bg[s] = bf16_to_f32((uint16_t)(a >> 16));
+                    su[s] = bf16_to_f32((uint16_t)b);
+                    bu[s] = bf16_to_f32((uint16_t)(b >> 16));
+                } else {
+                    sg[s] = in ? bf16_to_f32(mg.scales[s_at + q * 2]) : 0.f;
+                    bg[s] = in ? bf16_to_f32(mg.biases[s_at + q * 2]) : 0.f;
+                    su[s] = in ? bf16_to_f32(mu.scales[s_at + q * 2]) : 0.f;
+                    bu[s] = in ? bf16_to_f32(mu.biases[s_at + q * 2]) : 0.f;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf16x8_t b = __builtin_bit_cast(bf16x8_t, xv[s][i]);
-                    acc[0][0] = mfma_16x16x32(ag[i], b, acc[0][0]);
-                    acc[0][1] = mfma_16x16x32(au[i], b, acc[0][1]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    xv[s][i] = in && mine ? *(const u32x4_t*)(x0 + kb + 8 * i) : u32x4_t{0, 0, 0, 0};
+            };
+            f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-                for (int nt = 1; nt < NT; ++nt) {
-                    if (nt * 16 >= cnt) break;
-                    const int kb = (q + s) * 128 + g * 32, at = nt * 16 + c;
-                    const bool on = q + s < q1 && kb < H && at < cnt;
-                    u32x4_t v[4];
-                    load_x(p.x + (size_t)(at < cnt ? s_tok[wave][at] : 0) * H + kb, on, v);
+            for (int s = 0; s < kBgAhead; ++s) load(s, q0 + s);
+            for (int q = q0; q < q1; q += kBgAhead) {
+#pragma unroll
+                for (int s = 0; s < kBgAhead; ++s) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, v[i]);
-                        acc[nt][0] = mfma_16x16x32(ag[i], b, acc[nt][0]);
-                        acc[nt][1] = mfma_16x16x32(au[i], b, acc[nt][1]);
+                        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, xv[s][i]);
+                        acc[0] = mfma_16x16x32(dequant_word(wg[s][i], sg[s] * unit_inv, bg[s]), b, acc[0]);
+                        acc[1] = mfma_16x16x32(dequant_word(wu[s][i], su[s] * unit_inv, bu[s]), b, acc[1]);
                     }
+                    load(s, q + s + kBgAhead);
                 }
-                load(s, q + s + kBgAhead);
             }
-        }
-        // the waves' sums over K in order; 4 rows of one token a lane
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (nt * 16 >= cnt) break;
+            // the waves' sums over K in order; 4 rows of one token a lane
             __syncthreads();
-            s_part[wave][0][lane] = acc[nt][0];
-            s_part[wave][1][lane] = acc[nt][1];
+            s_part[wave][0][lane] = acc[0];
+            s_part[wave][1][lane] = acc[1];
             __syncthreads();
-            const int at = nt * 16 + c;
-            if (ks == 0 && at < cnt) {
+            if (ks == 0 && mine) {
                 f32x4_t gs = s_part[rt][0][lane], us = s_part[rt][1][lane];
                 for (int i = 1; i < KS; ++i) {
                     gs += s_part[rt + i * RT][0][lane];
                     us += s_part[rt + i * RT][1][lane];
                 }
-                const int t = s_tok[wave][at];
                 float wt = 1.f;
                 if (sh) {
                     if (p.shared_gate) wt = p.shared_gate[t];
@@ -252,8 +229,7 @@ __global__ __launch_bounds__(kBgThreads) void batch_gateup_kernel(BatchArgs p, i
                 uint16_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split_bf16(wt * (silu_f32(gs[i]) * us[i]), &hi[i], &lo[i]);
-                const size_t at_h = (sh ? (size_t)n * p.I + (size_t)t * N
-                                        : (size_t)(ent.y + at) * N) + row0 + g * 4;
+                const size_t at_h = (sh ? (size_t)n * p.I + (size_t)t * N : (size_t)(ent.y + at) * N) + row0 + g * 4;
                 *(u32x2_t*)(p.h_hi + at_h) = u32x2_t{(uint32_t)hi[0] | (uint32_t)hi[1] << 16,
                                                      (uint32_t)hi[2] | (uint32_t)hi[3] << 16};
                 *(u32x2_t*)(p.h_lo + at_h) = u32x2_t{(uint32_t)lo[0] | (uint32_t)lo[1] << 16,
@@ -347,10 +323,174 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
     }
 }
 
+// ---- Down for more tokens: a workgroup owns 64 columns and a share of the experts, so that h is
+// read by H / 64 workgroups instead of H / 8.  A wave takes 128 K of an expert at a time: the
+// 64 columns' codes are two runs of 2 KB (tiles), and the product's columns are the expert's
+// tokens one after another, whose sums then go to the tokens' rows in the wave's part of
+// LDS.  The workgroups' sums meet in batch_join_kernel.
+constexpr int kBpWaves = 8, kBpAhead = 3;
+
+// An entry of the list of chosen experts, through scalar loads: the list is another kernel's.
+struct BatchEntry {
+    uint32_t expert, row;
+    unsigned long long mask;   // its tokens
+    bool shared;
+};
+__device__ __forceinline__ BatchEntry batch_entry(const uint4* list, int u) {
+    typedef const __attribute__((address_space(4))) u32x4_t* scalar_t;
+    const u32x4_t v = ((scalar_t)(uintptr_t)list)[u];
+    return BatchEntry{v[0], v[1], (unsigned long long)v[3] << 32 | v[2], false};
+}
+
+// VEC: K a multiple of 128, so that the two scales of a row and step are one load.
+template <bool VEC>
+__global__ __launch_bounds__(kBpWaves* WAVE) void batch_down_split_kernel(BatchArgs p, int splits) {
+    extern __shared__ __attribute__((aligned(16))) float s_y[];   // [waves][T][64 + 4]
+    __shared__ int s_tok[kBpWaves][WAVE];
+    constexpr int LDY = 68;
+    const int tid = threadIdx.x, lane = tid % WAVE, g = lane / 16, c = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int T = p.T, H = p.H, I = p.I, I_sh = p.I_sh;
+    const int cols = H / 64, cg = blockIdx.x % cols, split = blockIdx.x / cols;
+    const int per = (I + 127) / 128, per_sh = (I_sh + 127) / 128;
+    const float unit_inv = 1.0f / fp8_unit();
+    const size_t sh_h = (size_t)T * p.k * I;
+    const int routed = *p.n_list * per, steps = routed + per_sh;
+    // this wave's steps lie together, so that an expert's sums stay in registers
+    const int share = splits * kBpWaves, mine = split * kBpWaves + wave;
+    const int first = (int)((long long)steps * mine / share), last = (int)((long long)steps * (mine + 1) / share);
+    float* y = s_y + wave * T * LDY;
+    for (int i = lane; i < T * LDY; i += WAVE) y[i] = 0.f;
+    u32x4_t wv[kBpAhead][4], hi[kBpAhead][4], lo[kBpAhead][4];
+    uint32_t sc[kBpAhead][4], bi[kBpAhead][4];
+    BatchEntry ent[kBpAhead];
+    int block[kBpAhead], K[kBpAhead];   // uniform over the wave, as the entry
+    auto load_h = [&](int s, int at, bool on, u32x4_t (&h)[4], u32x4_t (&l)[4]) {
+        const int kb = block[s] * 128 + g * 32;
+        // a routed expert's rows lie in order, the shared one's by token
+        const size_t from = (ent[s].shared ? sh_h : (size_t)ent[s].row * I) + (size_t)at * K[s] + kb;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = on && kb < K[s] ? *(const u32x4_t*)(p.h_hi + from + 8 * i) : u32x4_t{0, 0, 0, 0};
+            l[i] = on && kb < K[s] ? *(const u32x4_t*)(p.h_lo + from + 8 * i) : u32x4_t{0, 0, 0, 0};
+        }
+    };
+    auto load = [&](int s, int step) {
+        const bool on = step < last, sh = step >= routed;
+        const int u = on && !sh ? step / per : 0;
+        const int d = sh ? step - routed : step - u * per;
+        ent[s] = batch_entry(p.list, u);
+        if (sh) ent[s] = BatchEntry{0, 0, ~0ull >> (64 - T), true};
+        if (!on) ent[s].mask = 0;
+        K[s] = sh ? I_sh : I;
+        block[s] = d;
+        const QMatDev& m = sh ? p.sh_down : p.down;
+        const uint32_t* codes = m.codes + (size_t)ent[s].expert * H * (K[s] / 8);
+        const bool in = on && d * 128 + g * 32 < K[s];
+        // four column tiles of 16: 512 bytes apart in tiles, 2 K words in rows
+        const uint32_t at0 = code_word(m.layout, cg * 64 + c, d * 16 + g * 4, K[s]);
+        const uint32_t t_step = m.layout ? 128u : 2u * K[s];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            wv[s][t] = in ? *(const u32x4_t*)(codes + (at0 + t * t_step)) : u32x4_t{0, 0, 0, 0};
+        const uint32_t groups = K[s] / 64;
+        const size_t s0 = ((size_t)ent[s].expert * H + cg * 64) * groups + d * 2;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t at = (t * 16 + c) * groups;
+            if constexpr (VEC) {   // the groups of both halves of the wave
+                sc[s][t] = on ? *(const uint32_t*)(m.scales + s0 + at) : 0u;
+                bi[s][t] = on ? *(const uint32_t*)(m.biases + s0 + at) : 0u;
+            } else {               // this lane's
+                sc[s][t] = in ? m.scales[s0 + at + g / 2] : 0u;
+                bi[s][t] = in ? m.biases[s0 + at + g / 2] : 0u;
+            }
+        }
+        load_h(s, c, c < __popcll(ent[s].mask), hi[s], lo[s]);
+    };
+    f32x4_t acc[4];
+    auto multiply = [&](int s, const u32x4_t (&h)[4], const u32x4_t (&l)[4]) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float sv = VEC ? __builtin_bit_cast(float, g < 2 ? sc[s][t] << 16 : sc[s][t] & 0xFFFF0000u)
+                                 : bf16_to_f32((uint16_t)sc[s][t]);
+            const float bv = VEC ? __builtin_bit_cast(float, g < 2 ? bi[s][t] << 16 : bi[s][t] & 0xFFFF0000u)
+                                 : bf16_to_f32((uint16_t)bi[s][t]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bf16x8_t w = dequant_word(wv[s][t][i], sv * unit_inv, bv);
+                acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, h[i]), acc[t]);
+                acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, l[i]), acc[t]);
+            }
+        }
+    };
+    // the sums of the expert's tokens t0 .. + 15 to the tokens' rows: the lanes have different places
+    auto flush = [&](unsigned long long mask, int t0) {
+        if (mask >> lane & 1) s_tok[wave][__popcll(mask & lanemask_lt())] = lane;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (t0 + c < __popcll(mask)) {
+            float* o = y + s_tok[wave][t0 + c] * LDY + g * 4;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) *(f32x4_t*)(o + t * 16) = *(const f32x4_t*)(o + t * 16) + acc[t];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();   // the next expert's tokens take these ones' place
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    };
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kBpAhead; ++s) load(s, first + s);
+    for (int step = first; step < last; step += kBpAhead) {
+#pragma unroll
+        for (int s = 0; s < kBpAhead; ++s) {
+            if (step + s >= last) break;
+            const unsigned long long mask = ent[s].mask;
+            const int cnt = __popcll(mask);
+            multiply(s, hi[s], lo[s]);
+            // the expert's last block of this wave, or more tokens than one product's columns
+            if (cnt > 16 || step + s + 1 == last || (block[s] + 1) * 128 >= K[s]) flush(mask, 0);
+            for (int t0 = 16; t0 < cnt; t0 += 16) {
+                u32x4_t h[4], l[4];
+                load_h(s, t0 + c, t0 + c < cnt, h, l);
+                multiply(s, h, l);
+                flush(mask, t0);
+            }
+            load(s, step + s + kBpAhead);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < T * 64; i += kBpWaves * WAVE) {
+        const int t = i / 64, n = i % 64;
+        float v = s_y[t * LDY + n];
+#pragma unroll
+        for (int w = 1; w < kBpWaves; ++w) v += s_y[(w * T + t) * LDY + n];
+        p.y_part[((size_t)split * T + t) * H + cg * 64 + n] = v;
+    }
+}
+
+// The shares' sums, in order, rounded once.
+__global__ __launch_bounds__(256) void batch_join_kernel(const float* part, int splits, size_t n, uint16_t* y) {
+    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    f32x4_t v = *(const f32x4_t*)(part + i);
+    for (int s = 1; s < splits; ++s) v += *(const f32x4_t*)(part + s * n + i);
+    *(u32x2_t*)(y + i) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// Shares of the experts: a workgroup for each compute unit.
+static int batch_splits(int H) {
+    const int s = 256 / (H / 64);
+    return s < 1 ? 1 : s < 16 ? s : 16;
+}
+
 // Tokens whose selection every gate/up workgroup repeats, one or two a wave.
 constexpr int kBatchOwnSelect = 8;
+constexpr int kBatchColumns = 8;
 
-BatchWs batch_ws_layout(int T, int I, int I_sh, int E, int k) {
+BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k) {
     BatchWs w{};
     const size_t n = (size_t)T * k, slots = (size_t)E < n ? E : n;
     size_t o = 0;
@@ -364,18 +504,19 @@ BatchWs batch_ws_layout(int T, int I, int I_sh, int E, int k) {
     w.h_lo = take(values * 2);
     w.list = take(slots * 16);
     w.n_list = take(4);
+    w.y_part = take((size_t)batch_splits(H) * T * H * 4);
     w.idx = take(n * 4);
     w.w = take(n * 4);
     w.total = o;
     return w;
 }
 
-template <int EPL, int NT>
+template <int EPL>
 static void launch_batch_gateup(const BatchArgs& a, int grid, size_t lds, int rt_log, hipStream_t stream) {
     if (a.gate.layout == 2)
-        batch_gateup_kernel<EPL, NT, true><<<grid, kBgThreads, lds, stream>>>(a, rt_log);
+        batch_gateup_kernel<EPL, true><<<grid, kBgThreads, lds, stream>>>(a, rt_log);
     else
-        batch_gateup_kernel<EPL, NT, false><<<grid, kBgThreads, lds, stream>>>(a, rt_log);
+        batch_gateup_kernel<EPL, false><<<grid, kBgThreads, lds, stream>>>(a, rt_log);
 }
 
 hipError_t launch_decode_batch(const BatchArgs& a, hipStream_t stream) {
@@ -394,20 +535,43 @@ hipError_t launch_decode_batch(const BatchArgs& a, hipStream_t stream) {
 #undef MOE_SEL
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
-    const int rt_log = slots <= 32 ? 0 : slots <= 128 ? 1 : 2;
-    const int most = (a.I_sh + slots * a.I) >> (4 + rt_log);
-    const int grid = most < 1024 ? most : 1024;
+    // Rows of a task: few tasks a workgroup leave compute units idle in the last round, tasks of few
+    // rows split K over more waves, each of which waits for its loads once: kStart chunks' time.
+    constexpr int kStart = 4;
+    int rt_log = 0, grid = 0;
+    long long best = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int tasks = (a.I_sh + slots * a.I) >> (4 + i), rounds = (tasks + kBgResident - 1) / kBgResident;
+        const long long cost = (long long)rounds * (8 * kStart + (((a.H + 127) / 128) << i));
+        if (i == 0 || cost < best) {
+            best = cost;
+            rt_log = i;
+            grid = tasks < kBgResident ? tasks : kBgResident;
+        }
+    }
     const size_t lds = (size_t)slots * 16 + (size_t)a.E * 8 + (size_t)n * (own ? 8 : 4);
     if (own) {
-        if (epl <= 1) launch_batch_gateup<1, 1>(a, grid, lds, rt_log, stream);
-        else if (epl <= 2) launch_batch_gateup<2, 1>(a, grid, lds, rt_log, stream);
-        else if (epl <= 4) launch_batch_gateup<4, 1>(a, grid, lds, rt_log, stream);
-        else if (epl <= 8) launch_batch_gateup<8, 1>(a, grid, lds, rt_log, stream);
-        else launch_batch_gateup<16, 1>(a, grid, lds, rt_log, stream);
-    } else if (a.T <= 16) launch_batch_gateup<0, 1>(a, grid, lds, rt_log, stream);
-    else if (a.T <= 32) launch_batch_gateup<0, 2>(a, grid, lds, rt_log, stream);
-    else launch_batch_gateup<0, 4>(a, grid, lds, rt_log, stream);
+        if (epl <= 1) launch_batch_gateup<1>(a, grid, lds, rt_log, stream);
+        else if (epl <= 2) launch_batch_gateup<2>(a, grid, lds, rt_log, stream);
+        else if (epl <= 4) launch_batch_gateup<4>(a, grid, lds, rt_log, stream);
+        else if (epl <= 8) launch_batch_gateup<8>(a, grid, lds, rt_log, stream);
+        else launch_batch_gateup<16>(a, grid, lds, rt_log, stream);
+    } else launch_batch_gateup<0>(a, grid, lds, rt_log, stream);
     if ((err = hipGetLastError()) != hipSuccess) return err;
+    if (a.T > kBatchColumns) {
+        const int splits = batch_splits(a.H), grid2 = a.H / 64 * splits;
+        const size_t lds2 = (size_t)kBpWaves * a.T * 68 * 4;
+        // pairs of scales as one load: even rows, and arrays that start at 4 bytes
+        auto even = [](const QMatDev& m) { return ((uintptr_t)m.scales | (uintptr_t)m.biases) % 4 == 0; };
+        if (a.I % 128 == 0 && a.I_sh % 128 == 0 && even(a.down) && even(a.sh_down))
+            batch_down_split_kernel<true><<<grid2, kBpWaves * WAVE, lds2, stream>>>(a, splits);
+        else
+            batch_down_split_kernel<false><<<grid2, kBpWaves * WAVE, lds2, stream>>>(a, splits);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+        const size_t n_y = (size_t)a.T * a.H;
+        batch_join_kernel<<<(unsigned)((n_y / 4 + 255) / 256), 256, 0, stream>>>(a.y_part, splits, n_y, a.y);
+        return hipGetLastError();
+    }
     const int cols = a.H / 8;
     if (a.T <= 8) batch_down_kernel<1><<<cols, kBdWaves * WAVE, 0, stream>>>(a);
     else if (a.T <= 16) batch_down_kernel<2><<<cols, kBdWaves * WAVE, 0, stream>>>(a);

@@ -54,7 +54,7 @@ __host__ __device__ constexpr int xcd_shares(int tiles) { return tiles == 2 || t
 // meet in LDS.  Bound by the latency of one round of loads.
 constexpr int kFewWaves = 8, kFewAhead = 8;
 
-// The adapters' part of MF x NF pieces by K-splitting waves, before the product's loads: each wave
+// The adapters' part of MF x NF pieces by K-splitting waves, behind the product's first loads: each wave
 // takes every eighth step of ranks of every adapter among 16 rows, two of them at a time.
 template <int MF, int NF>
 __device__ __forceinline__ void few_lora(const LoraDev& l, int M, int N, int m0, int n0, int wave,
@@ -129,11 +129,13 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
                                 : (size_t)min(lane % 16, N - 1 - n0) * K + lane / 16 * 16);
     const int w_step = w.tiles ? 1024 : 64;
     const int steps = K / 64, s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
-    if constexpr (LORA) {
+    auto add_lora = [&]() {
         f32x4_t v[1][1];
         few_lora<1, 1>(lora, M, N, m0, n0, wave, v);
         s_lora[wave][lane] = v[0][0];
-    }
+    };
+    if constexpr (LORA)
+        if (s0 == s1) add_lora();   // fewer steps than waves
     i32x4_t acc = {0, 0, 0, 0};
     for (int s = s0; s < s1; s += kFewAhead) {
         i32x4_t va[kFewAhead], vw[kFewAhead];
@@ -143,6 +145,8 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_few_kernel(
                 vw[i] = *(const i32x4_t*)(pw + (size_t)(s + i) * w_step);
                 va[i] = *(const i32x4_t*)(pa + (size_t)(s + i) * 64);
             }
+        if constexpr (LORA)
+            if (s == s0) add_lora();   // while the first loads are in flight
 #pragma unroll
         for (int i = 0; i < kFewAhead; ++i)
             if (s + i < s1) acc = mfma_i8(vw[i], va[i], acc);
@@ -223,14 +227,14 @@ __global__ __launch_bounds__(kFewWaves* WAVE) void linear_split_kernel(
             va[slot][1][m] = __builtin_bit_cast(i32x4_t, buf_load16_u(ra, oa[m] | past1, (uint32_t)s * 128u + 64u));
         }
     };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, s0 + d);
     if constexpr (LORA) {
         f32x4_t v[MF][NF];
         few_lora<MF, NF>(lora, M, N, m0, n0, wave, v);
 #pragma unroll
         for (int p = 0; p < P; ++p) s_lora[wave][p][lane] = v[p % MF][p / MF];
     }
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(d, s0 + d);
     i32x4_t acc[NF][MF];
 #pragma unroll
     for (int n = 0; n < NF; ++n)

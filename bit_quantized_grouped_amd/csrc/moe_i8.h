@@ -177,12 +177,13 @@ struct BatchArgs {
                                 // shared expert [T, I_sh], weighted, as two bf16
     uint4* list;                // workspace: the chosen experts (expert, first row, mask of tokens)
     int* n_list;
+    float* y_part;              // workspace: sums of shares of the experts [shares, T, H]
     uint16_t* y;                // [T, H]
 };
 struct BatchWs {
-    size_t h_hi, h_lo, list, n_list, idx, w, total;
+    size_t h_hi, h_lo, list, n_list, y_part, idx, w, total;
 };
-BatchWs batch_ws_layout(int T, int I, int I_sh, int E, int k);
+BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k);
 hipError_t launch_decode_batch(const BatchArgs& args, hipStream_t stream);
 
 }  // namespace moeq4
