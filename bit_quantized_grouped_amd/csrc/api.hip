@@ -1112,6 +1112,8 @@ int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* sco
         a.topk_w = topk_w ? topk_w : (float*)(base + L.w);
         a.h_hi = (uint16_t*)(base + L.h_hi);
         a.h_lo = (uint16_t*)(base + L.h_lo);
+        a.sh_h = L.sh_h;
+        a.tiles = L.tiles;
         a.list = (uint4*)(base + L.list);
         a.n_list = (int*)(base + L.n_list);
         a.y_part = (float*)(base + L.y_part);

@@ -18,16 +18,15 @@
 //     experts: the products' columns are the tokens, so the sum over experts stays in the
 //     accumulators.  The 16 x 16 product is used as two of 8 x 8: rows and columns 8 .. 15
 //     hold the same 8 columns of y and tokens at a K 128 further on.
+#include <type_traits>
+
 #include "moe_device.h"
 #include "moe_i8.h"
+#include "moe_lds.h"
 #include "moe_score.h"
 
 namespace moeq4 {
 
-constexpr int kBgWaves = 8;              // waves of a gate/up workgroup
-constexpr int kBgThreads = kBgWaves * WAVE;
-constexpr int kBgResident = 512;        // workgroups that the chip holds, two a compute unit
-constexpr int kBgAhead = 2;              // 128-K chunks of a wave in flight
 constexpr int kBdWaves = 16;             // waves of a down workgroup
 constexpr int kBdAhead = 2;
 
@@ -69,179 +68,334 @@ __device__ __forceinline__ int wave_incl_sum_i32(int v, int lane) {
     return v;
 }
 
-// EPL 0: the experts are chosen already.  rt: row tiles of 16 that a workgroup's waves take side
-// by side (1, 2 or 4); 8 / rt waves split K.  More than 16 tokens of an expert take its rows again
-// from the caches for each 16: the shared expert mostly, whose rows are few beside the others'.
+// The lowest 16 set bits of m, which has more than 16.
+__device__ __forceinline__ unsigned long long lowest_16(unsigned long long m) {
+    int bits = 0;
+#pragma unroll
+    for (int b = 32; b; b >>= 1)
+        if (__popcll(m & ((1ull << (bits + b)) - 1)) <= 16) bits += b;
+    return m & ((1ull << bits) - 1);
+}
+
+// Entries: an expert with up to 16 of its tokens, which are the columns of its products.  Up to
+// kBatchDense tokens every entry's columns are the tokens as they come; of more, an entry's own
+// tokens in order, and an expert of more than 16 has several entries.
+constexpr int kBatchDense = 16;
+__device__ __forceinline__ unsigned long long shared_mask(int T, int v) {
+    const unsigned long long all = ~0ull >> (64 - T);
+    return T <= kBatchDense ? all : all & (0xFFFFull << 16 * v);
+}
+__device__ __forceinline__ void list_tokens(unsigned long long mask, uint8_t* tok, int lane) {
+    if (mask >> lane & 1) tok[__popcll(mask & lanemask_lt())] = (uint8_t)lane;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Where rows row .. + 3 (row a multiple of 4) of column c lie in an entry's h: for each 128 rows the B
+// operands of the down products, four of 1 KB, lane after lane, so that a load of one is contiguous.
+__device__ __forceinline__ size_t h_place(int row, int c) {
+    return (size_t)(row / 128) * 2048 + ((row % 32) / 8 * 64 + (row % 128) / 32 * 16 + c) * 8 + row % 8;
+}
+
+// EPL > 0: selects too, for at most 8 tokens.  x_kb: LDS for x, in pieces of 4 tokens by 128 K.
+// rt_log: a task is 16 << rt_log rows of an entry, 16 a wave, and the other waves split K.  A
+// workgroup's tasks lie together, so that x changes seldom, and the waves fetch the next task's
+// weights before they are done with this one's.
 template <int EPL, bool SB>
-__global__ __launch_bounds__(kBgThreads, 4) void batch_gateup_kernel(BatchArgs p, int rt_log) {
+__global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(BatchArgs p, int x_kb, int rt_log) {
+    constexpr int NW = EPL ? 8 : 16, THREADS = NW * WAVE;
+    typedef typename std::conditional<(EPL > 0), int32_t, uint16_t>::type idx_t;
     extern __shared__ __attribute__((aligned(16))) char s_dyn[];
-    __shared__ f32x4_t s_part[kBgWaves][2][WAVE];
-    __shared__ uint32_t s_scr[EPL ? kBgWaves : 1][3 * kScoredMaxK];
-    __shared__ int s_tok[kBgWaves][WAVE];
-    __shared__ int s_total[kBgWaves];
+    __shared__ uint8_t s_tok[NW][WAVE];
+    __shared__ int s_total[NW];
     const int T = p.T, E = p.E, k = p.k, n = T * k, H = p.H;
-    const int slots = E < n ? E : n;
-    uint4* s_list = (uint4*)s_dyn;                             // expert, first row, mask of tokens
-    unsigned long long* s_mask = (unsigned long long*)(s_list + slots);
-    int* s_idx = (int*)(s_mask + E);
-    float* s_w = (float*)(s_idx + n);                          // EPL > 0 only
-    const float* wts = EPL ? s_w : p.topk_w;
-    const int tid = threadIdx.x, lane = tid % WAVE;
+    const bool dense = T <= kBatchDense;
+    char* s_x = s_dyn;
+    f32x4_t* s_part = (f32x4_t*)(s_x + x_kb * 1024);                 // [2][NW][2][WAVE]
+    uint4* s_list = (uint4*)(s_part + 2 * NW * 2 * WAVE);            // expert, -, mask of tokens
+    float* s_w = (float*)(s_list + p.tiles);                         // EPL > 0 only
+    idx_t* s_idx = (idx_t*)(s_w + (EPL ? n : 0));
+    unsigned long long* s_mask = (unsigned long long*)s_part;        // [E], before the products
+    const int tid = threadIdx.x, lane = tid % WAVE, g = lane / 16, c = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int chunks = (H + 127) / 128;
+    const buf_rsrc_t rx = make_buf(p.x, (uint32_t)T * H * 2);
+
+    // x of the entry's `rows` tokens, chunks c0 .. + len: 16 bytes of token r, piece j of a chunk lie at
+    // place j ^ r, so that the 16 tokens' pieces that a product reads at once are in different banks
+    auto stage_x = [&](int rows, int c0, int len) {
+        const int nq = (rows + 3) / 4;
+        for (int i = wave; i < len * nq; i += NW) {
+            const int q = i / nq, r = (i - q * nq) * 4 + g;
+            const int kk = (c0 + q) * 128 + (c ^ r) * 8;
+            const int t = dense ? r : s_tok[wave][r];
+            const bool in = r < rows && kk < H;
+            buf_to_lds16(rx, s_x + i * 1024, in ? ((uint32_t)t * H + kk) * 2 : 0xFFFFFFF0u, 0);
+        }
+    };
+    int staged = -1;   // entry and segment of x in LDS
+    if (dense) {
+        const int s = x_kb / ((T + 3) / 4);
+        stage_x(T, 0, s < chunks ? s : chunks);
+        staged = 0;
+    }
 
     // ---- selection and grouping ----
-    for (int e = tid; e < E; e += kBgThreads) s_mask[e] = 0;
+    for (int e = tid; e < E; e += THREADS) s_mask[e] = 0;
     if constexpr (EPL > 0) {
-        for (int t = wave; t < T; t += kBgWaves)
-            batch_select_token<EPL>(p, t, s_idx + t * k, s_w + t * k, s_scr[wave]);
+        static_assert(NW * 4096 >= 1024 * 8 + NW * 3 * kScoredMaxK * 4, "scratch behind the masks");
+        if (wave < T)
+            batch_select_token<EPL>(p, wave, s_idx + wave * k, s_w + wave * k,
+                                    (uint32_t*)(s_mask + E) + wave * 3 * kScoredMaxK);
     } else {
-        for (int a = tid; a < n; a += kBgThreads) s_idx[a] = p.topk_idx[a];
+        for (int a = tid; a < n; a += THREADS) s_idx[a] = (uint16_t)p.topk_idx[a];
     }
     __syncthreads();
-    for (int a = tid; a < n; a += kBgThreads) atomicOr(&s_mask[s_idx[a]], 1ull << (a / k));
+    for (int a = tid; a < n; a += THREADS) atomicOr(&s_mask[s_idx[a]], 1ull << (a / k));
     __syncthreads();
-    int used = 0, rows = 0;
-    for (int e0 = 0; e0 < E; e0 += kBgThreads) {
+    int used = 0;
+    for (int e0 = 0; e0 < E; e0 += THREADS) {
         const int e = e0 + tid;
-        const unsigned long long m = e < E ? s_mask[e] : 0ull;
-        const int mine = m ? 1 << 16 | __popcll(m) : 0;   // experts and rows, both below 2^16
+        unsigned long long m = e < E ? s_mask[e] : 0ull;
+        const int mine = !m ? 0 : dense ? 1 : (__popcll(m) + 15) / 16;
         const int upto = wave_incl_sum_i32(mine, lane);
         if (lane == WAVE - 1) s_total[wave] = upto;
         __syncthreads();
         int before = upto - mine, all = 0;
 #pragma unroll
-        for (int w = 0; w < kBgWaves; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const int v = s_total[w];
             before += w < wave ? v : 0;
             all += v;
         }
-        if (m)
-            s_list[used + (before >> 16)] =
-                uint4{(uint32_t)e, (uint32_t)(rows + (before & 0xFFFF)), (uint32_t)m, (uint32_t)(m >> 32)};
-        used += all >> 16;
-        rows += all & 0xFFFF;
+        for (int i = 0; i < mine; ++i) {
+            const unsigned long long part = i + 1 < mine ? lowest_16(m) : m;
+            s_list[used + before + i] = uint4{(uint32_t)e, 0, (uint32_t)part, (uint32_t)(part >> 32)};
+            m &= ~part;
+        }
+        used += all;
         __syncthreads();
     }
     if (blockIdx.x == 0) {
-        for (int u = tid; u < used; u += kBgThreads) p.list[u] = s_list[u];
+        for (int u = tid; u < used; u += THREADS) p.list[u] = s_list[u];
         if (tid == 0) *p.n_list = used;
         if constexpr (EPL > 0)
-            for (int a = tid; a < n; a += kBgThreads) {
+            for (int a = tid; a < n; a += THREADS) {
                 p.topk_idx[a] = s_idx[a];
                 p.topk_w[a] = s_w[a];
             }
     }
 
-    // ---- row tiles: the shared expert's, then those of the experts in turn ----
-    const int RT = 1 << rt_log, KS = kBgWaves >> rt_log;
-    const int rt = wave & (RT - 1), ks = wave >> rt_log;
-    const int g = lane / 16, c = lane % 16;
+    // ---- tasks: row tiles of the shared expert's entries, then of the list's ----
+    const int KS = NW >> rt_log, rt = wave & ((1 << rt_log) - 1), ks = wave >> rt_log;
+    const int ks_log = 31 - __builtin_clz(KS);
+    const int sh_n = !p.I_sh ? 0 : dense ? 1 : (T + 15) / 16;
     const int sh_tiles = p.I_sh >> (4 + rt_log), tiles = p.I >> (4 + rt_log);
-    const int tasks = sh_tiles + used * tiles;
-    const int chunks = (H + 127) / 128, q0 = chunks * ks / KS, q1 = chunks * (ks + 1) / KS;
+    const int tasks = sh_n * sh_tiles + used * tiles;
+    const int last = (int)((long long)tasks * (blockIdx.x + 1) / gridDim.x);
+    const int G = H / 64;
     const float unit_inv = 1.0f / fp8_unit();
-    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const bool sh = task < sh_tiles;
-        const int u = sh ? 0 : (task - sh_tiles) / tiles;
-        const int tile = sh ? task : task - sh_tiles - u * tiles;
-        const int N = sh ? p.I_sh : p.I;
-        const uint4 ent = s_list[u];
-        const int e = sh ? 0 : __builtin_amdgcn_readfirstlane((int)ent.x);
-        unsigned long long mask = (unsigned long long)(uint32_t)__builtin_amdgcn_readfirstlane((int)ent.w) << 32 |
-                                  (uint32_t)__builtin_amdgcn_readfirstlane((int)ent.z);
-        if (sh) mask = ~0ull >> (64 - T);
-        const int cnt = __popcll(mask);
-        const QMatDev& mg = sh ? p.sh_gate : p.gate;
-        const QMatDev& mu = sh ? p.sh_up : p.up;
-        const int row0 = ((tile << rt_log) + rt) * 16;
-        const size_t grow = (size_t)e * N + row0 + c;
-        const size_t ebase = (size_t)e * N * (H / 8);
-        const uint32_t w_at = code_word(mg.layout, row0 + c, g * 4, H), w_step = mg.layout ? 1024u : 16u;
-        const uint32_t *gc = mg.codes + ebase + w_at, *uc = mu.codes + ebase + w_at;
-        const int G = H / 64;
-        const size_t s_at = SB ? ((grow / 64) * G + g / 2) * 64 + grow % 64 : grow * G + g / 2;
-        // the expert's tokens, in order: the wave's own list
-        if (mask >> lane & 1) s_tok[wave][__popcll(mask & lanemask_lt())] = lane;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        for (int t0 = 0; t0 < cnt; t0 += 16) {
-            const int at = t0 + c;
-            const bool mine = at < cnt;
-            const int t = mine ? s_tok[wave][at] : 0;
-            const uint16_t* x0 = p.x + (size_t)t * H;
-            u32x4_t wg[kBgAhead], wu[kBgAhead], xv[kBgAhead][4];
-            float sg[kBgAhead], bg[kBgAhead], su[kBgAhead], bu[kBgAhead];
-            auto load = [&](int s, int q) {
-                const int kb = q * 128 + g * 32;
-                const bool in = q < q1 && kb < H;
-                wg[s] = in ? *(const u32x4_t*)(gc + (size_t)q * w_step) : u32x4_t{0, 0, 0, 0};
-                wu[s] = in ? *(const u32x4_t*)(uc + (size_t)q * w_step) : u32x4_t{0, 0, 0, 0};
-                if constexpr (SB) {
-                    const uint32_t a = in ? ((const uint32_t*)mg.scales)[s_at + (size_t)q * 128] : 0u;
-                    const uint32_t b = in ? ((const uint32_t*)mu.scales)[s_at + (size_t)q * 128] : 0u;
-                    sg[s] = bf16_to_f32((uint16_t)a);
-                    bg[s] = bf16_to_f32((uint16_t)(a >> 16));
-                    su[s] = bf16_to_f32((uint16_t)b);
-                    bu[s] = bf16_to_f32((uint16_t)(b >> 16));
-                } else {
-                    sg[s] = in ? bf16_to_f32(mg.scales[s_at + q * 2]) : 0.f;
-                    bg[s] = in ? bf16_to_f32(mg.biases[s_at + q * 2]) : 0.f;
-                    su[s] = in ? bf16_to_f32(mu.scales[s_at + q * 2]) : 0.f;
-                    bu[s] = in ? bf16_to_f32(mu.biases[s_at + q * 2]) : 0.f;
+    const bool half_chunk = H % 128 != 0;   // the last chunk's groups g >= 2 lie behind K
+    int task = (int)((long long)tasks * blockIdx.x / gridDim.x);
+    int v = 0, tile = 0;
+    if (task < last) {
+        const int r = task - sh_n * sh_tiles;
+        v = r < 0 ? task / sh_tiles : sh_n + r / tiles;
+        tile = r < 0 ? task - v * sh_tiles : r - (v - sh_n) * tiles;
+    }
+    struct Entry {
+        int expert, rows, nq, per_seg;   // nq: pieces of 4 tokens; per_seg: chunks of x in LDS
+        unsigned long long mask;
+    };
+    auto entry = [&](int v) {
+        Entry o;
+        if (v < sh_n) {
+            o.expert = 0;
+            o.mask = shared_mask(T, v);
+        } else {
+            const uint4 ent = s_list[v - sh_n];
+            o.expert = __builtin_amdgcn_readfirstlane((int)ent.x);
+            o.mask = (unsigned long long)(uint32_t)__builtin_amdgcn_readfirstlane((int)ent.w) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)ent.z);
+        }
+        o.rows = dense ? T : __popcll(o.mask);
+        o.nq = (o.rows + 3) / 4;
+        o.per_seg = o.nq == 1 ? x_kb : o.nq == 2 ? x_kb / 2 : o.nq == 3 ? x_kb / 3 : x_kb / 4;
+        return o;
+    };
+
+    // ---- the wave's weights: a sequence of chunks of its rows and K, from task to task ----
+    struct Chunk {
+        u32x4_t wg, wu;
+        uint32_t sg, su, bg, bu;      // SB: scale and bias in sg, su
+    };
+    int l_task = task, l_v = v, l_tile = tile, l_seg = 0, l_q = 0, l_qb = 0;
+    bool l_new = true;
+    Entry l_ent;
+    const char *gc = nullptr, *uc = nullptr, *gs = nullptr, *us = nullptr, *gb = nullptr, *ub = nullptr;
+    uint32_t w_at = 0, s_at = 0;      // of the chunk, within the expert
+    const int layout = p.gate.layout;
+    const uint32_t w_step = layout ? 4096u : 64u, s_step = SB ? 512u : 4u;
+    const uint32_t w_lane = code_word(layout, c, g * 4, H) * 4, s_lane = SB ? (g / 2 * 64 + c) * 4 : (c * G + g / 2) * 2;
+    const uint32_t w_half = g >= 2 ? (layout ? 2048u : 32u) : 0u, s_half = g >= 2 ? (SB ? 256u : 2u) : 0u;
+    auto fetch = [&](Chunk& o) {
+        while (l_q >= l_qb) {         // the next segment, task or entry
+            if (l_task >= last) return;
+            const bool sh = l_v < sh_n;
+            if (l_new) {
+                l_ent = entry(l_v);
+                l_new = false;
+                const QMatDev& mg = sh ? p.sh_gate : p.gate;
+                const QMatDev& mu = sh ? p.sh_up : p.up;
+                const size_t row = (size_t)l_ent.expert * (sh ? p.I_sh : p.I);
+                const size_t ce = row * (H / 2), se = row * G * (SB ? 4 : 2);
+                gc = (const char*)mg.codes + ce;
+                uc = (const char*)mu.codes + ce;
+                gs = (const char*)mg.scales + se;
+                us = (const char*)mu.scales + se;
+                gb = (const char*)mg.biases + se;
+                ub = (const char*)mu.biases + se;
+            }
+            const int c0 = l_seg * l_ent.per_seg, len = min(l_ent.per_seg, chunks - c0);
+            l_q = c0 + (len * ks >> ks_log);
+            l_qb = c0 + (len * (ks + 1) >> ks_log);
+            const uint32_t stripe = (l_tile << rt_log) + rt, block = stripe / 4;   // 16 and 64 rows
+            w_at = block * H * 32 + stripe % 4 * (layout ? 512u : H * 8) + l_q * w_step;
+            s_at = SB ? (block * G * 64 + stripe % 4 * 16) * 4 + l_q * s_step : stripe * G * 32 + l_q * s_step;
+            if (c0 + len < chunks) {
+                ++l_seg;
+            } else {
+                l_seg = 0;
+                ++l_task;
+                if (++l_tile == (sh ? sh_tiles : tiles)) {
+                    l_tile = 0;
+                    ++l_v;
+                    l_new = true;
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    xv[s][i] = in && mine ? *(const u32x4_t*)(x0 + kb + 8 * i) : u32x4_t{0, 0, 0, 0};
-            };
-            f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-            for (int s = 0; s < kBgAhead; ++s) load(s, q0 + s);
-            for (int q = q0; q < q1; q += kBgAhead) {
-#pragma unroll
-                for (int s = 0; s < kBgAhead; ++s) {
+            }
+        }
+        uint32_t w = w_at + w_lane, s = s_at + s_lane;
+        if (half_chunk && l_q == chunks - 1) {   // an address of the row, whose weights are not used
+            w -= w_half;
+            s -= s_half;
+        }
+        o.wg = *(const u32x4_t*)(gc + w);
+        o.wu = *(const u32x4_t*)(uc + w);
+        if constexpr (SB) {
+            o.sg = *(const uint32_t*)(gs + s);
+            o.su = *(const uint32_t*)(us + s);
+        } else {
+            o.sg = *(const uint16_t*)(gs + s);
+            o.su = *(const uint16_t*)(us + s);
+            o.bg = *(const uint16_t*)(gb + s);
+            o.bu = *(const uint16_t*)(ub + s);
+        }
+        ++l_q;
+        w_at += w_step;
+        s_at += s_step;
+    };
+    Chunk w0 = {}, w1 = {};
+    fetch(w0);
+    fetch(w1);
+    if (dense) {
+        wait_loads<0>();
+        __syncthreads();
+    }
+    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    int turn = 0;   // the task's number here: the waves that join its sums, where these lie
+    for (; task < last; ++v, tile = 0) {
+        const Entry ent = entry(v);
+        const bool sh = v < sh_n;
+        // columns behind the last token read any one's x
+        const int cx = c < ent.nq * 4 ? c : 0;
+        const char* x_lane = s_x + cx / 4 * 1024 + cx % 4 * 256 + (g * 4 ^ (cx & 12)) * 16;
+        const int x_low = (cx & 3) * 16;
+        for (const int n_tiles = sh ? sh_tiles : tiles; tile < n_tiles && task < last; ++tile, ++task, ++turn) {
+            const bool joins = ks == (turn & (KS - 1));
+            float wt = 1.f;   // the weight of the column's token
+            bool on = false;
+            for (int c0 = 0; c0 < chunks; c0 += ent.per_seg) {
+                const int len = min(ent.per_seg, chunks - c0), want = (dense ? 0 : v) * chunks + c0;
+                if (want != staged) {
+                    __syncthreads();
+                    if (!dense) list_tokens(ent.mask, s_tok[wave], lane);
+                    stage_x(ent.rows, c0, len);
+                    staged = want;
+                    wait_loads<0>();
+                    __syncthreads();
+                }
+                if (joins && c0 == 0) {
+                    on = dense ? ent.mask >> c & 1 : c < ent.rows;
+                    const int t = !on ? 0 : dense ? c : s_tok[wave][c];
+                    if (sh) {
+                        if (p.shared_gate) wt = p.shared_gate[t];
+                    } else {
+                        int a = -1;   // the lanes of a column share the search
+#pragma unroll 2
+                        for (int j = g; j < k; j += 4)
+                            if (s_idx[t * k + j] == ent.expert) a = t * k + j;
+                        a = max(a, __shfl_xor(a, 16));
+                        a = max(a, __shfl_xor(a, 32));
+                        wt = on ? EPL ? s_w[a] : p.topk_w[a] : 0.f;
+                    }
+                }
+                const int q1 = c0 + (len * (ks + 1) >> ks_log);
+                for (int q = c0 + (len * ks >> ks_log); q < q1; ++q) {
+                    Chunk w2 = w1;
+                    fetch(w2);
+                    const char* xq = x_lane + (q - c0) * ent.nq * 1024;
+                    float sg = bf16_to_f32((uint16_t)w0.sg) * unit_inv, su = bf16_to_f32((uint16_t)w0.su) * unit_inv;
+                    float bg = bf16_to_f32((uint16_t)(SB ? w0.sg >> 16 : w0.bg));
+                    float bu = bf16_to_f32((uint16_t)(SB ? w0.su >> 16 : w0.bu));
+                    if (half_chunk && q == chunks - 1) {
+                        sg = g >= 2 ? 0.f : sg;
+                        su = g >= 2 ? 0.f : su;
+                        bg = g >= 2 ? 0.f : bg;
+                        bu = g >= 2 ? 0.f : bu;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, xv[s][i]);
-                        acc[0] = mfma_16x16x32(dequant_word(wg[s][i], sg[s] * unit_inv, bg[s]), b, acc[0]);
-                        acc[1] = mfma_16x16x32(dequant_word(wu[s][i], su[s] * unit_inv, bu[s]), b, acc[1]);
+                        const bf16x8_t b = *(const bf16x8_t*)(xq + (x_low ^ i * 16));
+                        acc[0] = mfma_16x16x32(dequant_word(w0.wg[i], sg, bg), b, acc[0]);
+                        acc[1] = mfma_16x16x32(dequant_word(w0.wu[i], su, bu), b, acc[1]);
                     }
-                    load(s, q + s + kBgAhead);
+                    w0 = w1;
+                    w1 = w2;
                 }
             }
             // the waves' sums over K in order; 4 rows of one token a lane
-            __syncthreads();
-            s_part[wave][0][lane] = acc[0];
-            s_part[wave][1][lane] = acc[1];
-            __syncthreads();
-            if (ks == 0 && mine) {
-                f32x4_t gs = s_part[rt][0][lane], us = s_part[rt][1][lane];
-                for (int i = 1; i < KS; ++i) {
-                    gs += s_part[rt + i * RT][0][lane];
-                    us += s_part[rt + i * RT][1][lane];
-                }
-                float wt = 1.f;
-                if (sh) {
-                    if (p.shared_gate) wt = p.shared_gate[t];
-                } else {
-                    for (int j = 0; j < k; ++j)
-                        if (s_idx[t * k + j] == e) wt = wts[t * k + j];
+            f32x4_t* part = s_part + (turn & 1) * NW * 2 * WAVE;
+            part[(wave * 2 + 0) * WAVE + lane] = acc[0];
+            part[(wave * 2 + 1) * WAVE + lane] = acc[1];
+            acc[0] = acc[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            wait_lds();
+            bare_barrier_i8();
+            if (joins && on) {
+                f32x4_t gsum = {0.f, 0.f, 0.f, 0.f}, usum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+                for (int i = 0; i < KS; ++i) {
+                    const int w = rt + (i << rt_log);
+                    gsum += part[(w * 2 + 0) * WAVE + lane];
+                    usum += part[(w * 2 + 1) * WAVE + lane];
                 }
                 uint16_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split_bf16(wt * (silu_f32(gs[i]) * us[i]), &hi[i], &lo[i]);
-                const size_t at_h = (sh ? (size_t)n * p.I + (size_t)t * N : (size_t)(ent.y + at) * N) + row0 + g * 4;
+                for (int i = 0; i < 4; ++i) split_bf16(wt * (silu_f32(gsum[i]) * usum[i]), &hi[i], &lo[i]);
+                const int row0 = ((tile << rt_log) + rt) * 16;
+                const size_t at_h = (sh ? p.sh_h + (size_t)v * ((p.I_sh + 127) / 128) * 2048
+                                        : (size_t)(v - sh_n) * ((p.I + 127) / 128) * 2048) +
+                                    h_place(row0 + g * 4, c);
                 *(u32x2_t*)(p.h_hi + at_h) = u32x2_t{(uint32_t)hi[0] | (uint32_t)hi[1] << 16,
                                                      (uint32_t)hi[2] | (uint32_t)hi[3] << 16};
                 *(u32x2_t*)(p.h_lo + at_h) = u32x2_t{(uint32_t)lo[0] | (uint32_t)lo[1] << 16,
                                                      (uint32_t)lo[2] | (uint32_t)lo[3] << 16};
             }
         }
-        __syncthreads();
     }
 }
 
-// NT: tiles of 8 tokens.
-template <int NT>
+// A workgroup owns 8 columns of y; its waves take 256 K of an entry at a time, whose columns are the
+// tokens (kBatchDense), so the sum over the entries stays in the accumulators.
 __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p) {
     __shared__ f32x4_t s_part[kBdWaves][WAVE];
     const int tid = threadIdx.x, lane = tid % WAVE;
@@ -252,149 +406,128 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
     const int per = (I + 255) / 256, per_sh = (I_sh + 255) / 256;
     const int routed = *p.n_list * per, steps = routed + per_sh;
     const float unit_inv = 1.0f / fp8_unit();
-    const size_t sh_h = (size_t)T * p.k * I;
     u32x4_t wv[kBdAhead];
     float sc[kBdAhead], bi[kBdAhead];
-    unsigned long long mask[kBdAhead];
-    size_t h_at[kBdAhead];   // the lane's place in h's first row of the expert
-    int K[kBdAhead], kb[kBdAhead];
+    bool on[kBdAhead];         // the lane's token is the entry's, and its K in range
+    size_t h_at[kBdAhead];
     auto load = [&](int s, int step) {
-        const bool on = step < steps, sh = step >= routed;
-        const int u = on && !sh ? step / per : 0;
+        const bool in = step < steps, sh = step >= routed;
+        const int u = in && !sh ? step / per : 0;
         const int d = sh ? step - routed : step - u * per;
-        uint4 ent = {0, 0, 0, 0};
-        if (on && !sh) ent = p.list[u];
-        mask[s] = !on ? 0ull : sh ? ~0ull >> (64 - T) : (unsigned long long)ent.w << 32 | ent.z;
-        K[s] = sh ? I_sh : I;
-        kb[s] = d * 256 + half * 128 + g * 32;
-        h_at[s] = (sh ? sh_h : (size_t)ent.y * I) + kb[s];
+        uint4 ent = {0, 0, 0xFF, 0};
+        if (in && !sh) ent = p.list[u];
+        const int K = sh ? I_sh : I, kb = d * 256 + half * 128 + g * 32;
+        on[s] = in && kb < K && c < T && (ent.z >> c & 1);
+        h_at[s] = (sh ? p.sh_h : (size_t)u * ((I + 127) / 128) * 2048) + (size_t)(d * 2 + half) * 2048 +
+                  (g * 16 + c) * 8;
         const QMatDev& m = sh ? p.sh_down : p.down;
-        const bool in = on && kb[s] < K[s];
         const size_t row = (size_t)ent.x * H + col;
-        wv[s] = in ? *(const u32x4_t*)(m.codes + (size_t)ent.x * H * (K[s] / 8) +
-                                       code_word(m.layout, col, kb[s] / 8, K[s]))
-                   : u32x4_t{0, 0, 0, 0};
-        sc[s] = in ? bf16_to_f32(m.scales[row * (K[s] / 64) + kb[s] / 64]) : 0.f;
-        bi[s] = in ? bf16_to_f32(m.biases[row * (K[s] / 64) + kb[s] / 64]) : 0.f;
+        wv[s] = in && kb < K ? *(const u32x4_t*)(m.codes + (size_t)ent.x * H * (K / 8) +
+                                                 code_word(m.layout, col, kb / 8, K))
+                             : u32x4_t{0, 0, 0, 0};
+        sc[s] = in && kb < K ? bf16_to_f32(m.scales[row * (K / 64) + kb / 64]) : 0.f;
+        bi[s] = in && kb < K ? bf16_to_f32(m.biases[row * (K / 64) + kb / 64]) : 0.f;
     };
-    f32x4_t acc[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < kBdAhead; ++s) load(s, wave + s * kBdWaves);
     for (int step = wave; step < steps; step += kBdAhead * kBdWaves) {
 #pragma unroll
         for (int s = 0; s < kBdAhead; ++s) {
-            bf16x8_t a[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = dequant_word(wv[s][i], sc[s] * unit_inv, bi[s]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (!(mask[s] >> (nt * 8) & 0xFF)) continue;
-                const int t = nt * 8 + c;
-                const bool on = (mask[s] >> t & 1) && kb[s] < K[s];
-                const size_t at = h_at[s] + (size_t)__popcll(mask[s] & ((1ull << t) - 1)) * K[s];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32x4_t hi = on ? *(const u32x4_t*)(p.h_hi + at + 8 * i) : u32x4_t{0, 0, 0, 0};
-                    const u32x4_t lo = on ? *(const u32x4_t*)(p.h_lo + at + 8 * i) : u32x4_t{0, 0, 0, 0};
-                    acc[nt] = mfma_16x16x32(a[i], __builtin_bit_cast(bf16x8_t, hi), acc[nt]);
-                    acc[nt] = mfma_16x16x32(a[i], __builtin_bit_cast(bf16x8_t, lo), acc[nt]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const u32x4_t hi = on[s] ? *(const u32x4_t*)(p.h_hi + h_at[s] + i * 512) : u32x4_t{0, 0, 0, 0};
+                const u32x4_t lo = on[s] ? *(const u32x4_t*)(p.h_lo + h_at[s] + i * 512) : u32x4_t{0, 0, 0, 0};
+                const bf16x8_t w = dequant_word(wv[s][i], sc[s] * unit_inv, bi[s]);
+                acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, hi), acc);
+                acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, lo), acc);
             }
             load(s, step + (s + kBdAhead) * kBdWaves);
         }
     }
     // the waves' sums in order; rows and columns 0 .. 7 and 8 .. 15 hold two parts of K
+    s_part[wave][lane] = acc;
+    __syncthreads();
+    if (tid < 64) {
+        const int r = tid % 8, t = tid / 8;
+        float y = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        __syncthreads();
-        s_part[wave][lane] = acc[nt];
-        __syncthreads();
-        if (tid < 64) {
-            const int r = tid % 8, t = tid / 8;
-            float y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kBdWaves; ++w)
-                y += s_part[w][r / 4 * 16 + t][r % 4] + s_part[w][(r + 8) / 4 * 16 + 8 + t][r % 4];
-            if (nt * 8 + t < T)
-                p.y[(size_t)(nt * 8 + t) * H + blockIdx.x * 8 + r] = (uint16_t)pack_bf16x2(y, 0.f);
-        }
+        for (int w = 0; w < kBdWaves; ++w)
+            y += s_part[w][r / 4 * 16 + t][r % 4] + s_part[w][(r + 8) / 4 * 16 + 8 + t][r % 4];
+        if (t < T) p.y[(size_t)t * H + blockIdx.x * 8 + r] = (uint16_t)pack_bf16x2(y, 0.f);
     }
 }
 
-// ---- Down for more tokens: a workgroup owns 64 columns and a share of the experts, so that h is
-// read by H / 64 workgroups instead of H / 8.  A wave takes 128 K of an expert at a time: the
-// 64 columns' codes are two runs of 2 KB (tiles), and the product's columns are the expert's
-// tokens one after another, whose sums then go to the tokens' rows in the wave's part of
-// LDS.  The workgroups' sums meet in batch_join_kernel.
-constexpr int kBpWaves = 8, kBpAhead = 3;
+// ---- Down for more tokens: a workgroup owns 64 columns and a share of the entries' 128-K blocks, so
+// that h is read by H / 64 workgroups instead of H / 8.  The 64 columns' codes of a block are two
+// runs of 2 KB (tiles), its h four contiguous KB twice; a wave's blocks lie together, and an entry's sums go to
+// the tokens' rows in the wave's part of LDS.  The workgroups' sums meet in batch_join_kernel.
+constexpr int kBpWaves = 8;
 
-// An entry of the list of chosen experts, through scalar loads: the list is another kernel's.
-struct BatchEntry {
-    uint32_t expert, row;
-    unsigned long long mask;   // its tokens
-    bool shared;
-};
-__device__ __forceinline__ BatchEntry batch_entry(const uint4* list, int u) {
-    typedef const __attribute__((address_space(4))) u32x4_t* scalar_t;
-    const u32x4_t v = ((scalar_t)(uintptr_t)list)[u];
-    return BatchEntry{v[0], v[1], (unsigned long long)v[3] << 32 | v[2], false};
-}
-
-// VEC: K a multiple of 128, so that the two scales of a row and step are one load.
+// VEC: K a multiple of 128, so that the two scales of a row and block are one load.
 template <bool VEC>
 __global__ __launch_bounds__(kBpWaves* WAVE) void batch_down_split_kernel(BatchArgs p, int splits) {
     extern __shared__ __attribute__((aligned(16))) float s_y[];   // [waves][T][64 + 4]
-    __shared__ int s_tok[kBpWaves][WAVE];
+    __shared__ uint8_t s_tok[kBpWaves][WAVE];
     constexpr int LDY = 68;
     const int tid = threadIdx.x, lane = tid % WAVE, g = lane / 16, c = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int T = p.T, H = p.H, I = p.I, I_sh = p.I_sh;
+    const bool dense = T <= kBatchDense;
     const int cols = H / 64, cg = blockIdx.x % cols, split = blockIdx.x / cols;
     const int per = (I + 127) / 128, per_sh = (I_sh + 127) / 128;
     const float unit_inv = 1.0f / fp8_unit();
-    const size_t sh_h = (size_t)T * p.k * I;
-    const int routed = *p.n_list * per, steps = routed + per_sh;
-    // this wave's steps lie together, so that an expert's sums stay in registers
+    const int sh_steps = !I_sh ? 0 : (dense ? 1 : (T + 15) / 16) * per_sh;
+    const int steps = sh_steps + *p.n_list * per;
     const int share = splits * kBpWaves, mine = split * kBpWaves + wave;
     const int first = (int)((long long)steps * mine / share), last = (int)((long long)steps * (mine + 1) / share);
     float* y = s_y + wave * T * LDY;
-    for (int i = lane; i < T * LDY; i += WAVE) y[i] = 0.f;
-    u32x4_t wv[kBpAhead][4], hi[kBpAhead][4], lo[kBpAhead][4];
-    uint32_t sc[kBpAhead][4], bi[kBpAhead][4];
-    BatchEntry ent[kBpAhead];
-    int block[kBpAhead], K[kBpAhead];   // uniform over the wave, as the entry
-    auto load_h = [&](int s, int at, bool on, u32x4_t (&h)[4], u32x4_t (&l)[4]) {
-        const int kb = block[s] * 128 + g * 32;
-        // a routed expert's rows lie in order, the shared one's by token
-        const size_t from = (ent[s].shared ? sh_h : (size_t)ent[s].row * I) + (size_t)at * K[s] + kb;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = on && kb < K[s] ? *(const u32x4_t*)(p.h_hi + from + 8 * i) : u32x4_t{0, 0, 0, 0};
-            l[i] = on && kb < K[s] ? *(const u32x4_t*)(p.h_lo + from + 8 * i) : u32x4_t{0, 0, 0, 0};
-        }
+    // the next block to fetch: block d of entry u, the shared expert's below 0
+    int step = first, u, d;
+    if (first < sh_steps) {
+        u = first / per_sh;
+        d = first - u * per_sh;
+        u -= sh_steps / per_sh;
+    } else {
+        u = (first - sh_steps) / per;
+        d = first - sh_steps - u * per;
+    }
+    // the list 64 entries at a time, one a lane
+    int list0 = u < 0 ? 0 : u;
+    auto fetch_list = [&]() {
+        return list0 + lane < p.tiles ? p.list[list0 + lane] : uint4{0, 0, 0, 0};
     };
-    auto load = [&](int s, int step) {
-        const bool on = step < last, sh = step >= routed;
-        const int u = on && !sh ? step / per : 0;
-        const int d = sh ? step - routed : step - u * per;
-        ent[s] = batch_entry(p.list, u);
-        if (sh) ent[s] = BatchEntry{0, 0, ~0ull >> (64 - T), true};
-        if (!on) ent[s].mask = 0;
-        K[s] = sh ? I_sh : I;
-        block[s] = d;
+    uint4 window = first < last ? fetch_list() : uint4{0, 0, 0, 0};
+    u32x4_t wv[2][4], hi[2][4], lo[2][4];
+    uint32_t sc[2][4], bi[2][4];
+    unsigned long long mask[2];
+    bool valid[2], ends[2];       // a block is there; it is the entry's last of this wave
+    auto load = [&](int s) {
+        const bool on = step < last, sh = u < 0;
+        const int K = sh ? I_sh : I;
+        uint32_t e = 0;
+        if (sh) {
+            mask[s] = shared_mask(T, u + (dense ? 1 : (T + 15) / 16));
+        } else {
+            if (u >= list0 + WAVE && on) {
+                list0 = u;
+                window = fetch_list();
+            }
+            e = __builtin_amdgcn_readlane(window.x, u - list0);
+            mask[s] = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane(window.w, u - list0) << 32 |
+                      (uint32_t)__builtin_amdgcn_readlane(window.z, u - list0);
+        }
         const QMatDev& m = sh ? p.sh_down : p.down;
-        const uint32_t* codes = m.codes + (size_t)ent[s].expert * H * (K[s] / 8);
-        const bool in = on && d * 128 + g * 32 < K[s];
+        const bool in = on && d * 128 + g * 32 < K;
         // four column tiles of 16: 512 bytes apart in tiles, 2 K words in rows
-        const uint32_t at0 = code_word(m.layout, cg * 64 + c, d * 16 + g * 4, K[s]);
-        const uint32_t t_step = m.layout ? 128u : 2u * K[s];
+        const uint32_t* codes = m.codes + (size_t)e * H * (K / 8) + code_word(m.layout, cg * 64, d * 16, K);
+        const uint32_t w_lane = code_word(m.layout, c, g * 4, K);
+        const uint32_t t_step = m.layout ? 128u : 2u * K;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            wv[s][t] = in ? *(const u32x4_t*)(codes + (at0 + t * t_step)) : u32x4_t{0, 0, 0, 0};
-        const uint32_t groups = K[s] / 64;
-        const size_t s0 = ((size_t)ent[s].expert * H + cg * 64) * groups + d * 2;
+            wv[s][t] = in ? *(const u32x4_t*)(codes + (w_lane + t * t_step)) : u32x4_t{0, 0, 0, 0};
+        const uint32_t groups = K / 64;
+        const size_t s0 = ((size_t)e * H + cg * 64) * groups + d * 2;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const uint32_t at = (t * 16 + c) * groups;
@@ -402,65 +535,71 @@ __global__ __launch_bounds__(kBpWaves* WAVE) void batch_down_split_kernel(BatchA
                 sc[s][t] = on ? *(const uint32_t*)(m.scales + s0 + at) : 0u;
                 bi[s][t] = on ? *(const uint32_t*)(m.biases + s0 + at) : 0u;
             } else {               // this lane's
-                sc[s][t] = in ? m.scales[s0 + at + g / 2] : 0u;
-                bi[s][t] = in ? m.biases[s0 + at + g / 2] : 0u;
+                sc[s][t] = in ? (m.scales + s0)[at + g / 2] : 0u;
+                bi[s][t] = in ? (m.biases + s0)[at + g / 2] : 0u;
             }
         }
-        load_h(s, c, c < __popcll(ent[s].mask), hi[s], lo[s]);
+        const size_t h0 = (sh ? p.sh_h + (size_t)(u + (dense ? 1 : (T + 15) / 16)) * per_sh * 2048
+                              : (size_t)u * per * 2048) + (size_t)d * 2048;
+        const bool col = in && (dense ? mask[s] >> c & 1 : c < __popcll(mask[s]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[s][i] = col ? *(const u32x4_t*)(p.h_hi + h0 + (i * 512 + lane * 8)) : u32x4_t{0, 0, 0, 0};
+            lo[s][i] = col ? *(const u32x4_t*)(p.h_lo + h0 + (i * 512 + lane * 8)) : u32x4_t{0, 0, 0, 0};
+        }
+        valid[s] = on;
+        ++step;
+        ++d;
+        ends[s] = step >= last || d == (sh ? per_sh : per);
+        if (d == (sh ? per_sh : per)) {
+            d = 0;
+            ++u;
+        }
     };
     f32x4_t acc[4];
-    auto multiply = [&](int s, const u32x4_t (&h)[4], const u32x4_t (&l)[4]) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float sv = VEC ? __builtin_bit_cast(float, g < 2 ? sc[s][t] << 16 : sc[s][t] & 0xFFFF0000u)
-                                 : bf16_to_f32((uint16_t)sc[s][t]);
-            const float bv = VEC ? __builtin_bit_cast(float, g < 2 ? bi[s][t] << 16 : bi[s][t] & 0xFFFF0000u)
-                                 : bf16_to_f32((uint16_t)bi[s][t]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bf16x8_t w = dequant_word(wv[s][t][i], sv * unit_inv, bv);
-                acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, h[i]), acc[t]);
-                acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, l[i]), acc[t]);
-            }
-        }
-    };
-    // the sums of the expert's tokens t0 .. + 15 to the tokens' rows: the lanes have different places
-    auto flush = [&](unsigned long long mask, int t0) {
-        if (mask >> lane & 1) s_tok[wave][__popcll(mask & lanemask_lt())] = lane;
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (t0 + c < __popcll(mask)) {
-            float* o = y + s_tok[wave][t0 + c] * LDY + g * 4;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) *(f32x4_t*)(o + t * 16) = *(const f32x4_t*)(o + t * 16) + acc[t];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();   // the next expert's tokens take these ones' place
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    };
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i = lane; i < T * LDY / 4; i += WAVE) ((f32x4_t*)y)[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // two slots, each fetched before the other's products: the first round's first slot holds nothing
+    valid[0] = false;
+    do {
 #pragma unroll
-    for (int s = 0; s < kBpAhead; ++s) load(s, first + s);
-    for (int step = first; step < last; step += kBpAhead) {
+        for (int s = 0; s < 2; ++s) {
+            load(1 - s);
+            if (!valid[s]) continue;
 #pragma unroll
-        for (int s = 0; s < kBpAhead; ++s) {
-            if (step + s >= last) break;
-            const unsigned long long mask = ent[s].mask;
-            const int cnt = __popcll(mask);
-            multiply(s, hi[s], lo[s]);
-            // the expert's last block of this wave, or more tokens than one product's columns
-            if (cnt > 16 || step + s + 1 == last || (block[s] + 1) * 128 >= K[s]) flush(mask, 0);
-            for (int t0 = 16; t0 < cnt; t0 += 16) {
-                u32x4_t h[4], l[4];
-                load_h(s, t0 + c, t0 + c < cnt, h, l);
-                multiply(s, h, l);
-                flush(mask, t0);
+            for (int t = 0; t < 4; ++t) {
+                const float sv = VEC ? __builtin_bit_cast(float, g < 2 ? sc[s][t] << 16 : sc[s][t] & 0xFFFF0000u)
+                                     : bf16_to_f32((uint16_t)sc[s][t]);
+                const float bv = VEC ? __builtin_bit_cast(float, g < 2 ? bi[s][t] << 16 : bi[s][t] & 0xFFFF0000u)
+                                     : bf16_to_f32((uint16_t)bi[s][t]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bf16x8_t w = dequant_word(wv[s][t][i], sv * unit_inv, bv);
+                    acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, hi[s][i]), acc[t]);
+                    acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, lo[s][i]), acc[t]);
+                }
             }
-            load(s, step + s + kBpAhead);
+            if (ends[s]) {   // to the tokens' rows: the lanes have different places
+                int row = c;
+                bool col = mask[s] >> c & 1;
+                if (!dense) {
+                    list_tokens(mask[s], s_tok[wave], lane);
+                    col = c < __popcll(mask[s]);
+                    row = col ? s_tok[wave][c] : 0;
+                }
+                if (col) {
+                    float* o = y + row * LDY + g * 4;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) *(f32x4_t*)(o + t * 16) = *(const f32x4_t*)(o + t * 16) + acc[t];
+                }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();   // the next entry's tokens take these ones' place
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
         }
-    }
+    } while (valid[0]);
     __syncthreads();
     for (int i = tid; i < T * 64; i += kBpWaves * WAVE) {
         const int t = i / 64, n = i % 64;
@@ -476,6 +615,7 @@ __global__ __launch_bounds__(256) void batch_join_kernel(const float* part, int 
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= n) return;
     f32x4_t v = *(const f32x4_t*)(part + i);
+#pragma unroll 8
     for (int s = 1; s < splits; ++s) v += *(const f32x4_t*)(part + s * n + i);
     *(u32x2_t*)(y + i) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
@@ -486,23 +626,31 @@ static int batch_splits(int H) {
     return s < 1 ? 1 : s < 16 ? s : 16;
 }
 
-// Tokens whose selection every gate/up workgroup repeats, one or two a wave.
+// Tokens whose selection every gate/up workgroup repeats, one a wave.
 constexpr int kBatchOwnSelect = 8;
+// Tokens whose down products keep the sum over the experts in the accumulators.
 constexpr int kBatchColumns = 8;
+
+static int batch_tiles(int T, int E, int k) {   // entries of the list at most
+    const int n = T * k, slots = E < n ? E : n;
+    return slots + (T > kBatchDense ? n / 16 : 0);
+}
 
 BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k) {
     BatchWs w{};
-    const size_t n = (size_t)T * k, slots = (size_t)E < n ? E : n;
+    const size_t n = (size_t)T * k;
+    w.tiles = batch_tiles(T, E, k);
+    w.sh_h = (size_t)w.tiles * ((I + 127) / 128) * 2048;
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
         o += align_up(bytes, 256);
         return at;
     };
-    const size_t values = n * I + (size_t)T * I_sh;
+    const size_t values = w.sh_h + (size_t)((T + 15) / 16) * ((I_sh + 127) / 128) * 2048;
     w.h_hi = take(values * 2);
     w.h_lo = take(values * 2);
-    w.list = take(slots * 16);
+    w.list = take((size_t)w.tiles * 16);
     w.n_list = take(4);
     w.y_part = take((size_t)batch_splits(H) * T * H * 4);
     w.idx = take(n * 4);
@@ -512,19 +660,27 @@ BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k) {
 }
 
 template <int EPL>
-static void launch_batch_gateup(const BatchArgs& a, int grid, size_t lds, int rt_log, hipStream_t stream) {
+static void launch_batch_gateup(const BatchArgs& a, hipStream_t stream) {
+    constexpr int NW = EPL ? 8 : 16;
+    const int chunks = (a.H + 127) / 128;
+    // a wave takes two chunks of K or more, where there are so many
+    const int rt_log = (chunks >= 8 ? 0 : chunks >= 4 ? 1 : 2) + (EPL || chunks < 8 ? 0 : 1);
+    const int want = (a.T < 16 ? (a.T + 3) / 4 : 4) * chunks, most = EPL ? 32 : 64;
+    const int x_kb = want < most ? want : most;
+    const int sh_n = a.T > kBatchDense ? (a.T + 15) / 16 : 1;
+    const int tasks = (sh_n * a.I_sh + a.tiles * a.I) >> (4 + rt_log), resident = EPL ? 512 : 256;
+    const int grid = tasks < resident ? tasks : resident;
+    const size_t lds = (size_t)x_kb * 1024 + NW * 4096 + (size_t)a.tiles * 16 + (size_t)a.T * a.k * (EPL ? 8 : 2);
     if (a.gate.layout == 2)
-        batch_gateup_kernel<EPL, true><<<grid, kBgThreads, lds, stream>>>(a, rt_log);
+        batch_gateup_kernel<EPL, true><<<grid, NW * WAVE, lds, stream>>>(a, x_kb, rt_log);
     else
-        batch_gateup_kernel<EPL, false><<<grid, kBgThreads, lds, stream>>>(a, rt_log);
+        batch_gateup_kernel<EPL, false><<<grid, NW * WAVE, lds, stream>>>(a, x_kb, rt_log);
 }
 
 hipError_t launch_decode_batch(const BatchArgs& a, hipStream_t stream) {
-    const int n = a.T * a.k, slots = a.E < n ? a.E : n;
     const int epl = (a.E + WAVE - 1) / WAVE;
-    const bool own = a.T <= kBatchOwnSelect;
     hipError_t err;
-    if (!own) {
+    if (a.T > kBatchOwnSelect) {
         const int grid = (a.T + kBsWaves - 1) / kBsWaves;
 #define MOE_SEL(N) batch_select_kernel<N><<<grid, kBsWaves * WAVE, 0, stream>>>(a)
         if (epl <= 1) MOE_SEL(1);
@@ -534,29 +690,12 @@ hipError_t launch_decode_batch(const BatchArgs& a, hipStream_t stream) {
         else MOE_SEL(16);
 #undef MOE_SEL
         if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
-    // Rows of a task: few tasks a workgroup leave compute units idle in the last round, tasks of few
-    // rows split K over more waves, each of which waits for its loads once: kStart chunks' time.
-    constexpr int kStart = 4;
-    int rt_log = 0, grid = 0;
-    long long best = 0;
-    for (int i = 0; i < 3; ++i) {
-        const int tasks = (a.I_sh + slots * a.I) >> (4 + i), rounds = (tasks + kBgResident - 1) / kBgResident;
-        const long long cost = (long long)rounds * (8 * kStart + (((a.H + 127) / 128) << i));
-        if (i == 0 || cost < best) {
-            best = cost;
-            rt_log = i;
-            grid = tasks < kBgResident ? tasks : kBgResident;
-        }
-    }
-    const size_t lds = (size_t)slots * 16 + (size_t)a.E * 8 + (size_t)n * (own ? 8 : 4);
-    if (own) {
-        if (epl <= 1) launch_batch_gateup<1>(a, grid, lds, rt_log, stream);
-        else if (epl <= 2) launch_batch_gateup<2>(a, grid, lds, rt_log, stream);
-        else if (epl <= 4) launch_batch_gateup<4>(a, grid, lds, rt_log, stream);
-        else if (epl <= 8) launch_batch_gateup<8>(a, grid, lds, rt_log, stream);
-        else launch_batch_gateup<16>(a, grid, lds, rt_log, stream);
-    } else launch_batch_gateup<0>(a, grid, lds, rt_log, stream);
+        launch_batch_gateup<0>(a, stream);
+    } else if (epl <= 1) launch_batch_gateup<1>(a, stream);
+    else if (epl <= 2) launch_batch_gateup<2>(a, stream);
+    else if (epl <= 4) launch_batch_gateup<4>(a, stream);
+    else if (epl <= 8) launch_batch_gateup<8>(a, stream);
+    else launch_batch_gateup<16>(a, stream);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (a.T > kBatchColumns) {
         const int splits = batch_splits(a.H), grid2 = a.H / 64 * splits;
@@ -572,11 +711,7 @@ hipError_t launch_decode_batch(const BatchArgs& a, hipStream_t stream) {
         batch_join_kernel<<<(unsigned)((n_y / 4 + 255) / 256), 256, 0, stream>>>(a.y_part, splits, n_y, a.y);
         return hipGetLastError();
     }
-    const int cols = a.H / 8;
-    if (a.T <= 8) batch_down_kernel<1><<<cols, kBdWaves * WAVE, 0, stream>>>(a);
-    else if (a.T <= 16) batch_down_kernel<2><<<cols, kBdWaves * WAVE, 0, stream>>>(a);
-    else if (a.T <= 32) batch_down_kernel<4><<<cols, kBdWaves * WAVE, 0, stream>>>(a);
-    else batch_down_kernel<8><<<cols, kBdWaves * WAVE, 0, stream>>>(a);
+    batch_down_kernel<<<a.H / 8, kBdWaves * WAVE, 0, stream>>>(a);
     return hipGetLastError();
 }
 

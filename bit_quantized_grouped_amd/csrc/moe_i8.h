@@ -173,15 +173,19 @@ struct BatchArgs {
     QMatDev gate, up, down, sh_gate, sh_up, sh_down;
     int32_t* topk_idx;          // [T, k], the caller's or the workspace's
     float* topk_w;
-    uint16_t *h_hi, *h_lo;      // workspace: h of the routed rows by expert [T*k, I], then of the
-                                // shared expert [T, I_sh], weighted, as two bf16
-    uint4* list;                // workspace: the chosen experts (expert, first row, mask of tokens)
+    uint16_t *h_hi, *h_lo;      // workspace: h of 16 tokens for each entry of the list, at sh_h the
+                                // shared expert's, weighted, as two bf16
+    size_t sh_h;
+    int tiles;                  // the list's capacity
+    uint4* list;                // workspace: the chosen experts (expert, -, mask of tokens)
     int* n_list;
     float* y_part;              // workspace: sums of shares of the experts [shares, T, H]
     uint16_t* y;                // [T, H]
 };
 struct BatchWs {
     size_t h_hi, h_lo, list, n_list, y_part, idx, w, total;
+    size_t sh_h;   // the shared expert's place in h, in values
+    int tiles;
 };
 BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k);
 hipError_t launch_decode_batch(const BatchArgs& args, hipStream_t stream);

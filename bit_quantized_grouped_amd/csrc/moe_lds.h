@@ -36,6 +36,11 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
+// Waits for this wave's accesses of LDS.
+__device__ __forceinline__ void wait_lds() {
+    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));
+}
+
 // Workgroup barrier without a memory fence, which would wait for every load still in
 // flight: the caller has waited for what the other waves must see.  Nothing moves
 // across it.
