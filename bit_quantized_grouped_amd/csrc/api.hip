@@ -1116,7 +1116,8 @@ int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* sco
         a.tiles = L.tiles;
         a.list = (uint4*)(base + L.list);
         a.n_list = (int*)(base + L.n_list);
-        a.y_part = (float*)(base + L.y_part);
+        a.assign = (int*)(base + L.assign);
+        a.rows = (float*)(base + L.rows);
         a.y = y;
         return launch_decode_batch(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
     } catch (...) {

@@ -18,8 +18,6 @@
 //     experts: the products' columns are the tokens, so the sum over experts stays in the
 //     accumulators.  The 16 x 16 product is used as two of 8 x 8: rows and columns 8 .. 15
 //     hold the same 8 columns of y and tokens at a K 128 further on.
-#include <type_traits>
-
 #include "moe_device.h"
 #include "moe_i8.h"
 #include "moe_lds.h"
@@ -97,67 +95,54 @@ __device__ __forceinline__ size_t h_place(int row, int c) {
     return (size_t)(row / 128) * 2048 + ((row % 32) / 8 * 64 + (row % 128) / 32 * 16 + c) * 8 + row % 8;
 }
 
-// EPL > 0: selects too, for at most 8 tokens.  x_kb: LDS for x, in pieces of 4 tokens by 128 K.
-// rt_log: a task is 16 << rt_log rows of an entry, 16 a wave, and the other waves split K.  A
-// workgroup's tasks lie together, so that x changes seldom, and the waves fetch the next task's
-// weights before they are done with this one's.
-template <int EPL, bool SB>
-__global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(BatchArgs p, int x_kb, int rt_log) {
-    constexpr int NW = EPL ? 8 : 16, THREADS = NW * WAVE;
-    typedef typename std::conditional<(EPL > 0), int32_t, uint16_t>::type idx_t;
-    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
-    __shared__ uint8_t s_tok[NW][WAVE];
-    __shared__ int s_total[NW];
-    const int T = p.T, E = p.E, k = p.k, n = T * k, H = p.H;
-    const bool dense = T <= kBatchDense;
-    char* s_x = s_dyn;
-    f32x4_t* s_part = (f32x4_t*)(s_x + x_kb * 1024);                 // [2][NW][2][WAVE]
-    uint4* s_list = (uint4*)(s_part + 2 * NW * 2 * WAVE);            // expert, -, mask of tokens
-    float* s_w = (float*)(s_list + p.tiles);                         // EPL > 0 only
-    idx_t* s_idx = (idx_t*)(s_w + (EPL ? n : 0));
-    unsigned long long* s_mask = (unsigned long long*)s_part;        // [E], before the products
-    const int tid = threadIdx.x, lane = tid % WAVE, g = lane / 16, c = lane % 16;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
-    const int chunks = (H + 127) / 128;
-    const buf_rsrc_t rx = make_buf(p.x, (uint32_t)T * H * 2);
+// dequant_word's weights from a code read as a subnormal fp16, q 2^-24 or, 4 bits up, q 2^-20: 17
+// instructions, and 30.5 ns for a word in each lane of a SIMD's wave where the fp8 conversions take
+// 35.3.  s: the scale times 2^24 and 2^20, which is exact below 2^103.
+__device__ __forceinline__ bf16x8_t dequant_half(uint32_t w, f32x2_t s, float b) {
+    typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+    const uint32_t w8 = w >> 8;
+    const f16x2_t q04 = __builtin_bit_cast(f16x2_t, w & 0x000F000Fu), q15 = __builtin_bit_cast(f16x2_t, w & 0x00F000F0u);
+    const f16x2_t q26 = __builtin_bit_cast(f16x2_t, w8 & 0x000F000Fu), q37 = __builtin_bit_cast(f16x2_t, w8 & 0x00F000F0u);
+    u32x4_t r;
+    r[0] = pack_bf16x2(__builtin_fmaf((float)q04[0], s[0], b), __builtin_fmaf((float)q15[0], s[1], b));
+    r[1] = pack_bf16x2(__builtin_fmaf((float)q26[0], s[0], b), __builtin_fmaf((float)q37[0], s[1], b));
+    r[2] = pack_bf16x2(__builtin_fmaf((float)q04[1], s[0], b), __builtin_fmaf((float)q15[1], s[1], b));
+    r[3] = pack_bf16x2(__builtin_fmaf((float)q26[1], s[0], b), __builtin_fmaf((float)q37[1], s[1], b));
+    return __builtin_bit_cast(bf16x8_t, r);
+}
 
-    // x of the entry's `rows` tokens, chunks c0 .. + len: 16 bytes of token r, piece j of a chunk lie at
-    // place j ^ r, so that the 16 tokens' pieces that a product reads at once are in different banks
-    auto stage_x = [&](int rows, int c0, int len) {
-        const int nq = (rows + 3) / 4;
-        for (int i = wave; i < len * nq; i += NW) {
-            const int q = i / nq, r = (i - q * nq) * 4 + g;
-            const int kk = (c0 + q) * 128 + (c ^ r) * 8;
-            const int t = dense ? r : s_tok[wave][r];
-            const bool in = r < rows && kk < H;
-            buf_to_lds16(rx, s_x + i * 1024, in ? ((uint32_t)t * H + kk) * 2 : 0xFFFFFFF0u, 0);
-        }
-    };
-    int staged = -1;   // entry and segment of x in LDS
-    if (dense) {
-        const int s = x_kb / ((T + 3) / 4);
-        stage_x(T, 0, s < chunks ? s : chunks);
-        staged = 0;
+// x of `rows` tokens (their numbers in tok, or `dense`), chunks c0 .. + len of 128 K, to LDS: 1 KB for 4
+// tokens of a chunk.  16 bytes of token r, piece j of a chunk lie at place j ^ r, so that the 16
+// tokens' pieces that a product reads at once are in different banks.
+__device__ __forceinline__ void stage_x(buf_rsrc_t rx, bool dense, const uint8_t* tok, int rows, int H, char* to,
+                                        int c0, int len, int wave, int waves, int lane) {
+    const int nq = (rows + 3) / 4, g = lane / 16, c = lane % 16;
+    for (int i = wave; i < len * nq; i += waves) {
+        const int q = i / nq, r = (i - q * nq) * 4 + g;
+        const int kk = (c0 + q) * 128 + (c ^ r) * 8;
+        const int t = dense ? r : tok[r];
+        const bool in = r < rows && kk < H;
+        buf_to_lds16(rx, to + i * 1024, in ? ((uint32_t)t * H + kk) * 2 : 0xFFFFFFF0u, 0);
     }
+}
 
-    // ---- selection and grouping ----
-    for (int e = tid; e < E; e += THREADS) s_mask[e] = 0;
-    if constexpr (EPL > 0) {
-        static_assert(NW * 4096 >= 1024 * 8 + NW * 3 * kScoredMaxK * 4, "scratch behind the masks");
-        if (wave < T)
-            batch_select_token<EPL>(p, wave, s_idx + wave * k, s_w + wave * k,
-                                    (uint32_t*)(s_mask + E) + wave * 3 * kScoredMaxK);
-    } else {
-        for (int a = tid; a < n; a += THREADS) s_idx[a] = (uint16_t)p.topk_idx[a];
-    }
+// The list of entries from the tokens' experts, in LDS; returns their number.  Begins and ends with a
+// barrier.
+template <int NW, typename Idx>
+__device__ __forceinline__ int group_tokens(const BatchArgs& p, const Idx* s_idx, unsigned long long* s_mask,
+                                            int* s_total, uint4* s_list) {
+    constexpr int THREADS = NW * WAVE;
+    const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int n = p.T * p.k;
+    for (int e = tid; e < p.E; e += THREADS) s_mask[e] = 0;
     __syncthreads();
-    for (int a = tid; a < n; a += THREADS) atomicOr(&s_mask[s_idx[a]], 1ull << (a / k));
+    for (int a = tid; a < n; a += THREADS) atomicOr(&s_mask[s_idx[a]], 1ull << (a / p.k));
     __syncthreads();
     int used = 0;
-    for (int e0 = 0; e0 < E; e0 += THREADS) {
+    for (int e0 = 0; e0 < p.E; e0 += THREADS) {
         const int e = e0 + tid;
-        unsigned long long m = e < E ? s_mask[e] : 0ull;
-        const int mine = !m ? 0 : dense ? 1 : (__popcll(m) + 15) / 16;
+        unsigned long long m = e < p.E ? s_mask[e] : 0ull;
+        const int mine = !m ? 0 : p.T <= kBatchDense ? 1 : (__popcll(m) + 15) / 16;
         const int upto = wave_incl_sum_i32(mine, lane);
         if (lane == WAVE - 1) s_total[wave] = upto;
         __syncthreads();
@@ -176,25 +161,61 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
         used += all;
         __syncthreads();
     }
+    return used;
+}
+
+// ---- up to kBatchColumns tokens ----
+//
+// Selects too.  x_kb: LDS for x, in pieces of 4 tokens by 128 K; T tokens' pieces of per_seg chunks fit.
+// rt_log: a task is 16 << rt_log rows of an entry, 16 a wave, and the other waves split K.  A
+// workgroup's tasks lie together, and the waves fetch the next task's weights before they are done
+// with this one's.
+constexpr int kBgWaves = 8;
+
+template <int EPL, bool SB>
+__global__ __launch_bounds__(kBgWaves* WAVE, 4) void batch_gateup_kernel(BatchArgs p, int x_kb, int rt_log) {
+    constexpr int NW = kBgWaves, THREADS = NW * WAVE;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    __shared__ int s_total[NW];
+    const int T = p.T, k = p.k, n = T * k, H = p.H;
+    char* s_x = s_dyn;
+    f32x4_t* s_part = (f32x4_t*)(s_x + x_kb * 1024);                 // [2][NW][2][WAVE]
+    uint4* s_list = (uint4*)(s_part + 2 * NW * 2 * WAVE);
+    float* s_w = (float*)(s_list + p.tiles);
+    int32_t* s_idx = (int32_t*)(s_w + n);
+    const int tid = threadIdx.x, lane = tid % WAVE, g = lane / 16, c = lane % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int chunks = (H + 127) / 128, nq = (T + 3) / 4, per_seg = x_kb / nq;
+    const buf_rsrc_t rx = make_buf(p.x, (uint32_t)T * H * 2);
+    auto stage = [&](int c0) {
+        stage_x(rx, true, nullptr, T, H, s_x, c0, min(per_seg, chunks - c0), wave, NW, lane);
+    };
+    stage(0);
+    int staged = 0;   // first chunk of x in LDS
+
+    // ---- selection and grouping, whose masks and scratch lie where the waves' sums will ----
+    static_assert(NW * 4096 >= 1024 * 8 + NW * 3 * kScoredMaxK * 4, "scratch behind the masks");
+    if (wave < T)
+        batch_select_token<EPL>(p, wave, s_idx + wave * k, s_w + wave * k,
+                                (uint32_t*)((unsigned long long*)s_part + p.E) + wave * 3 * kScoredMaxK);
+    const int used = group_tokens<NW>(p, s_idx, (unsigned long long*)s_part, s_total, s_list);
     if (blockIdx.x == 0) {
         for (int u = tid; u < used; u += THREADS) p.list[u] = s_list[u];
         if (tid == 0) *p.n_list = used;
-        if constexpr (EPL > 0)
-            for (int a = tid; a < n; a += THREADS) {
-                p.topk_idx[a] = s_idx[a];
-                p.topk_w[a] = s_w[a];
-            }
+        for (int a = tid; a < n; a += THREADS) {
+            p.topk_idx[a] = s_idx[a];
+            p.topk_w[a] = s_w[a];
+        }
     }
 
     // ---- tasks: row tiles of the shared expert's entries, then of the list's ----
     const int KS = NW >> rt_log, rt = wave & ((1 << rt_log) - 1), ks = wave >> rt_log;
     const int ks_log = 31 - __builtin_clz(KS);
-    const int sh_n = !p.I_sh ? 0 : dense ? 1 : (T + 15) / 16;
+    const int sh_n = p.I_sh ? 1 : 0;
     const int sh_tiles = p.I_sh >> (4 + rt_log), tiles = p.I >> (4 + rt_log);
     const int tasks = sh_n * sh_tiles + used * tiles;
     const int last = (int)((long long)tasks * (blockIdx.x + 1) / gridDim.x);
     const int G = H / 64;
-    const float unit_inv = 1.0f / fp8_unit();
     const bool half_chunk = H % 128 != 0;   // the last chunk's groups g >= 2 lie behind K
     int task = (int)((long long)tasks * blockIdx.x / gridDim.x);
     int v = 0, tile = 0;
@@ -204,23 +225,16 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
         tile = r < 0 ? task - v * sh_tiles : r - (v - sh_n) * tiles;
     }
     struct Entry {
-        int expert, rows, nq, per_seg;   // nq: pieces of 4 tokens; per_seg: chunks of x in LDS
-        unsigned long long mask;
+        int expert;
+        uint32_t mask;
     };
     auto entry = [&](int v) {
-        Entry o;
-        if (v < sh_n) {
-            o.expert = 0;
-            o.mask = shared_mask(T, v);
-        } else {
+        Entry o{0, 0xFFu >> (8 - T)};
+        if (v >= sh_n) {
             const uint4 ent = s_list[v - sh_n];
             o.expert = __builtin_amdgcn_readfirstlane((int)ent.x);
-            o.mask = (unsigned long long)(uint32_t)__builtin_amdgcn_readfirstlane((int)ent.w) << 32 |
-                     (uint32_t)__builtin_amdgcn_readfirstlane((int)ent.z);
+            o.mask = (uint32_t)__builtin_amdgcn_readfirstlane((int)ent.z);
         }
-        o.rows = dense ? T : __popcll(o.mask);
-        o.nq = (o.rows + 3) / 4;
-        o.per_seg = o.nq == 1 ? x_kb : o.nq == 2 ? x_kb / 2 : o.nq == 3 ? x_kb / 3 : x_kb / 4;
         return o;
     };
 
@@ -256,7 +270,7 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
                 gb = (const char*)mg.biases + se;
                 ub = (const char*)mu.biases + se;
             }
-            const int c0 = l_seg * l_ent.per_seg, len = min(l_ent.per_seg, chunks - c0);
+            const int c0 = l_seg * per_seg, len = min(per_seg, chunks - c0);
             l_q = c0 + (len * ks >> ks_log);
             l_qb = c0 + (len * (ks + 1) >> ks_log);
             const uint32_t stripe = (l_tile << rt_log) + rt, block = stripe / 4;   // 16 and 64 rows
@@ -297,36 +311,32 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
     Chunk w0 = {}, w1 = {};
     fetch(w0);
     fetch(w1);
-    if (dense) {
-        wait_loads<0>();
-        __syncthreads();
-    }
+    wait_loads<0>();
+    __syncthreads();
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     int turn = 0;   // the task's number here: the waves that join its sums, where these lie
+    // columns behind the last token read any one's x
+    const int cx = c < nq * 4 ? c : 0, x_low = (cx & 3) * 16;
+    const char* x_lane = s_x + cx / 4 * 1024 + cx % 4 * 256 + (g * 4 ^ (cx & 12)) * 16;
     for (; task < last; ++v, tile = 0) {
         const Entry ent = entry(v);
         const bool sh = v < sh_n;
-        // columns behind the last token read any one's x
-        const int cx = c < ent.nq * 4 ? c : 0;
-        const char* x_lane = s_x + cx / 4 * 1024 + cx % 4 * 256 + (g * 4 ^ (cx & 12)) * 16;
-        const int x_low = (cx & 3) * 16;
         for (const int n_tiles = sh ? sh_tiles : tiles; tile < n_tiles && task < last; ++tile, ++task, ++turn) {
             const bool joins = ks == (turn & (KS - 1));
             float wt = 1.f;   // the weight of the column's token
             bool on = false;
-            for (int c0 = 0; c0 < chunks; c0 += ent.per_seg) {
-                const int len = min(ent.per_seg, chunks - c0), want = (dense ? 0 : v) * chunks + c0;
-                if (want != staged) {
+            for (int c0 = 0; c0 < chunks; c0 += per_seg) {
+                const int len = min(per_seg, chunks - c0);
+                if (c0 != staged) {
                     __syncthreads();
-                    if (!dense) list_tokens(ent.mask, s_tok[wave], lane);
-                    stage_x(ent.rows, c0, len);
-                    staged = want;
+                    stage(c0);
+                    staged = c0;
                     wait_loads<0>();
                     __syncthreads();
                 }
                 if (joins && c0 == 0) {
-                    on = dense ? ent.mask >> c & 1 : c < ent.rows;
-                    const int t = !on ? 0 : dense ? c : s_tok[wave][c];
+                    on = ent.mask >> c & 1;
+                    const int t = on ? c : 0;
                     if (sh) {
                         if (p.shared_gate) wt = p.shared_gate[t];
                     } else {
@@ -336,15 +346,15 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
                             if (s_idx[t * k + j] == ent.expert) a = t * k + j;
                         a = max(a, __shfl_xor(a, 16));
                         a = max(a, __shfl_xor(a, 32));
-                        wt = on ? EPL ? s_w[a] : p.topk_w[a] : 0.f;
+                        wt = on ? s_w[a] : 0.f;
                     }
                 }
                 const int q1 = c0 + (len * (ks + 1) >> ks_log);
                 for (int q = c0 + (len * ks >> ks_log); q < q1; ++q) {
                     Chunk w2 = w1;
                     fetch(w2);
-                    const char* xq = x_lane + (q - c0) * ent.nq * 1024;
-                    float sg = bf16_to_f32((uint16_t)w0.sg) * unit_inv, su = bf16_to_f32((uint16_t)w0.su) * unit_inv;
+                    const char* xq = x_lane + (q - c0) * nq * 1024;
+                    float sg = bf16_to_f32((uint16_t)w0.sg), su = bf16_to_f32((uint16_t)w0.su);
                     float bg = bf16_to_f32((uint16_t)(SB ? w0.sg >> 16 : w0.bg));
                     float bu = bf16_to_f32((uint16_t)(SB ? w0.su >> 16 : w0.bu));
                     if (half_chunk && q == chunks - 1) {
@@ -353,11 +363,12 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
                         bg = g >= 2 ? 0.f : bg;
                         bu = g >= 2 ? 0.f : bu;
                     }
+                    const f32x2_t dg = {sg * 0x1p24f, sg * 0x1p20f}, du = {su * 0x1p24f, su * 0x1p20f};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const bf16x8_t b = *(const bf16x8_t*)(xq + (x_low ^ i * 16));
-                        acc[0] = mfma_16x16x32(dequant_word(w0.wg[i], sg, bg), b, acc[0]);
-                        acc[1] = mfma_16x16x32(dequant_word(w0.wu[i], su, bu), b, acc[1]);
+                        acc[0] = mfma_16x16x32(dequant_half(w0.wg[i], dg, bg), b, acc[0]);
+                        acc[1] = mfma_16x16x32(dequant_half(w0.wu[i], du, bu), b, acc[1]);
                     }
                     w0 = w1;
                     w1 = w2;
@@ -382,8 +393,7 @@ __global__ __launch_bounds__(EPL ? 512 : 1024, 4) void batch_gateup_kernel(Batch
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split_bf16(wt * (silu_f32(gsum[i]) * usum[i]), &hi[i], &lo[i]);
                 const int row0 = ((tile << rt_log) + rt) * 16;
-                const size_t at_h = (sh ? p.sh_h + (size_t)v * ((p.I_sh + 127) / 128) * 2048
-                                        : (size_t)(v - sh_n) * ((p.I + 127) / 128) * 2048) +
+                const size_t at_h = (sh ? p.sh_h : (size_t)(v - sh_n) * ((p.I + 127) / 128) * 2048) +
                                     h_place(row0 + g * 4, c);
                 *(u32x2_t*)(p.h_hi + at_h) = u32x2_t{(uint32_t)hi[0] | (uint32_t)hi[1] << 16,
                                                      (uint32_t)hi[2] | (uint32_t)hi[3] << 16};
@@ -405,7 +415,6 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
     const int col = blockIdx.x * 8 + c;
     const int per = (I + 255) / 256, per_sh = (I_sh + 255) / 256;
     const int routed = *p.n_list * per, steps = routed + per_sh;
-    const float unit_inv = 1.0f / fp8_unit();
     u32x4_t wv[kBdAhead];
     float sc[kBdAhead], bi[kBdAhead];
     bool on[kBdAhead];         // the lane's token is the entry's, and its K in range
@@ -434,11 +443,12 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
     for (int step = wave; step < steps; step += kBdAhead * kBdWaves) {
 #pragma unroll
         for (int s = 0; s < kBdAhead; ++s) {
+            const f32x2_t d = {sc[s] * 0x1p24f, sc[s] * 0x1p20f};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const u32x4_t hi = on[s] ? *(const u32x4_t*)(p.h_hi + h_at[s] + i * 512) : u32x4_t{0, 0, 0, 0};
                 const u32x4_t lo = on[s] ? *(const u32x4_t*)(p.h_lo + h_at[s] + i * 512) : u32x4_t{0, 0, 0, 0};
-                const bf16x8_t w = dequant_word(wv[s][i], sc[s] * unit_inv, bi[s]);
+                const bf16x8_t w = dequant_half(wv[s][i], d, bi[s]);
                 acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, hi), acc);
                 acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, lo), acc);
             }
@@ -458,177 +468,280 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
     }
 }
 
-// ---- Down for more tokens: a workgroup owns 64 columns and a share of the entries' 128-K blocks, so
-// that h is read by H / 64 workgroups instead of H / 8.  The 64 columns' codes of a block are two
-// runs of 2 KB (tiles), its h four contiguous KB twice; a wave's blocks lie together, and an entry's sums go to
-// the tokens' rows in the wave's part of LDS.  The workgroups' sums meet in batch_join_kernel.
-constexpr int kBpWaves = 8;
+// ---- more tokens: gate/up (DOWN 0) and down (DOWN 1), whose work is a list of tiles ----
+//
+// A tile is one wave's: 16 rows of an entry's gate and up, or 32 of its down, times the whole K, so
+// that nothing is joined and waves do not wait for each other.  A workgroup takes a run of tiles,
+// which belong to one or two entries, whose B operands (x, or h as written) lie in LDS for all of
+// its waves.  kBmAhead chunks of a wave's weights are in flight, 2 KB each.
+constexpr int kBmWaves = 12, kBmAhead = 4;
 
-// VEC: K a multiple of 128, so that the two scales of a row and block are one load.
-template <bool VEC>
-__global__ __launch_bounds__(kBpWaves* WAVE) void batch_down_split_kernel(BatchArgs p, int splits) {
-    extern __shared__ __attribute__((aligned(16))) float s_y[];   // [waves][T][64 + 4]
-    __shared__ uint8_t s_tok[kBpWaves][WAVE];
-    constexpr int LDY = 68;
+template <bool DOWN, bool SB>
+__global__ __launch_bounds__(kBmWaves* WAVE) void batch_tiles_kernel(BatchArgs p, int x_kb) {
+    constexpr int NW = kBmWaves, THREADS = NW * WAVE, ROWS = DOWN ? 32 : 16;
+    extern __shared__ __attribute__((aligned(16))) char s_dyn[];
+    __shared__ uint8_t s_tok[NW][WAVE];
+    __shared__ int s_total[NW];
+    const int T = p.T, E = p.E, k = p.k, n = T * k, H = p.H;
+    const bool dense = T <= kBatchDense;
+    char* s_x = s_dyn;
+    uint4* s_list = (uint4*)(s_x + x_kb * 1024);
+    uint16_t* s_idx = (uint16_t*)(s_list + p.tiles);
     const int tid = threadIdx.x, lane = tid % WAVE, g = lane / 16, c = lane % 16;
     const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
-    const int T = p.T, H = p.H, I = p.I, I_sh = p.I_sh;
-    const bool dense = T <= kBatchDense;
-    const int cols = H / 64, cg = blockIdx.x % cols, split = blockIdx.x / cols;
-    const int per = (I + 127) / 128, per_sh = (I_sh + 127) / 128;
-    const float unit_inv = 1.0f / fp8_unit();
-    const int sh_steps = !I_sh ? 0 : (dense ? 1 : (T + 15) / 16) * per_sh;
-    const int steps = sh_steps + *p.n_list * per;
-    const int share = splits * kBpWaves, mine = split * kBpWaves + wave;
-    const int first = (int)((long long)steps * mine / share), last = (int)((long long)steps * (mine + 1) / share);
-    float* y = s_y + wave * T * LDY;
-    // the next block to fetch: block d of entry u, the shared expert's below 0
-    int step = first, u, d;
-    if (first < sh_steps) {
-        u = first / per_sh;
-        d = first - u * per_sh;
-        u -= sh_steps / per_sh;
+    int used;
+    if constexpr (DOWN) {
+        used = *p.n_list;
     } else {
-        u = (first - sh_steps) / per;
-        d = first - sh_steps - u * per;
+        for (int a = tid; a < n; a += THREADS) s_idx[a] = (uint16_t)p.topk_idx[a];
+        used = group_tokens<NW>(p, s_idx, (unsigned long long*)s_x, s_total, s_list);
+        if (blockIdx.x == 0) {
+            for (int u = tid; u < used; u += THREADS) p.list[u] = s_list[u];
+            if (tid == 0) *p.n_list = used;
+        }
     }
-    // the list 64 entries at a time, one a lane
-    int list0 = u < 0 ? 0 : u;
-    auto fetch_list = [&]() {
-        return list0 + lane < p.tiles ? p.list[list0 + lane] : uint4{0, 0, 0, 0};
-    };
-    uint4 window = first < last ? fetch_list() : uint4{0, 0, 0, 0};
-    u32x4_t wv[2][4], hi[2][4], lo[2][4];
-    uint32_t sc[2][4], bi[2][4];
-    unsigned long long mask[2];
-    bool valid[2], ends[2];       // a block is there; it is the entry's last of this wave
-    auto load = [&](int s) {
-        const bool on = step < last, sh = u < 0;
-        const int K = sh ? I_sh : I;
-        uint32_t e = 0;
-        if (sh) {
-            mask[s] = shared_mask(T, u + (dense ? 1 : (T + 15) / 16));
+    const int sh_n = !p.I_sh ? 0 : dense ? 1 : (T + 15) / 16;
+    // of an entry v, the shared expert's first: tiles, chunks of K, its B operand's size in LDS
+    auto tiles_of = [&](int v) { return (DOWN ? H : v < sh_n ? p.I_sh : p.I) / ROWS; };
+    auto k_of = [&](int v) { return !DOWN ? H : v < sh_n ? p.I_sh : p.I; };
+    auto mask_of = [&](int v) {
+        if (v < sh_n) return shared_mask(T, v);
+        u32x4_t ent;
+        if constexpr (DOWN) {   // another kernel's: through scalar loads
+            typedef const __attribute__((address_space(4))) u32x4_t* scalar_t;
+            ent = ((scalar_t)(uintptr_t)p.list)[v - sh_n];
         } else {
-            if (u >= list0 + WAVE && on) {
-                list0 = u;
-                window = fetch_list();
-            }
-            e = __builtin_amdgcn_readlane(window.x, u - list0);
-            mask[s] = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane(window.w, u - list0) << 32 |
-                      (uint32_t)__builtin_amdgcn_readlane(window.z, u - list0);
+            ent = *(const u32x4_t*)(s_list + (v - sh_n));
         }
-        const QMatDev& m = sh ? p.sh_down : p.down;
-        const bool in = on && d * 128 + g * 32 < K;
-        // four column tiles of 16: 512 bytes apart in tiles, 2 K words in rows
-        const uint32_t* codes = m.codes + (size_t)e * H * (K / 8) + code_word(m.layout, cg * 64, d * 16, K);
-        const uint32_t w_lane = code_word(m.layout, c, g * 4, K);
-        const uint32_t t_step = m.layout ? 128u : 2u * K;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            wv[s][t] = in ? *(const u32x4_t*)(codes + (w_lane + t * t_step)) : u32x4_t{0, 0, 0, 0};
-        const uint32_t groups = K / 64;
-        const size_t s0 = ((size_t)e * H + cg * 64) * groups + d * 2;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint32_t at = (t * 16 + c) * groups;
-            if constexpr (VEC) {   // the groups of both halves of the wave
-                sc[s][t] = on ? *(const uint32_t*)(m.scales + s0 + at) : 0u;
-                bi[s][t] = on ? *(const uint32_t*)(m.biases + s0 + at) : 0u;
-            } else {               // this lane's
-                sc[s][t] = in ? (m.scales + s0)[at + g / 2] : 0u;
-                bi[s][t] = in ? (m.biases + s0)[at + g / 2] : 0u;
-            }
-        }
-        const size_t h0 = (sh ? p.sh_h + (size_t)(u + (dense ? 1 : (T + 15) / 16)) * per_sh * 2048
-                              : (size_t)u * per * 2048) + (size_t)d * 2048;
-        const bool col = in && (dense ? mask[s] >> c & 1 : c < __popcll(mask[s]));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            hi[s][i] = col ? *(const u32x4_t*)(p.h_hi + h0 + (i * 512 + lane * 8)) : u32x4_t{0, 0, 0, 0};
-            lo[s][i] = col ? *(const u32x4_t*)(p.h_lo + h0 + (i * 512 + lane * 8)) : u32x4_t{0, 0, 0, 0};
-        }
-        valid[s] = on;
-        ++step;
-        ++d;
-        ends[s] = step >= last || d == (sh ? per_sh : per);
-        if (d == (sh ? per_sh : per)) {
-            d = 0;
-            ++u;
+        return (unsigned long long)(uint32_t)__builtin_amdgcn_readfirstlane(ent[3]) << 32 |
+               (uint32_t)__builtin_amdgcn_readfirstlane(ent[2]);
+    };
+    auto expert_of = [&](int v) {
+        if (v < sh_n) return 0;
+        if constexpr (DOWN) {
+            typedef const __attribute__((address_space(4))) u32x4_t* scalar_t;
+            return (int)((scalar_t)(uintptr_t)p.list)[v - sh_n][0];
+        } else {
+            return __builtin_amdgcn_readfirstlane((int)s_list[v - sh_n].x);
         }
     };
-    f32x4_t acc[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int i = lane; i < T * LDY / 4; i += WAVE) ((f32x4_t*)y)[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // two slots, each fetched before the other's products: the first round's first slot holds nothing
-    valid[0] = false;
-    do {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            load(1 - s);
-            if (!valid[s]) continue;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float sv = VEC ? __builtin_bit_cast(float, g < 2 ? sc[s][t] << 16 : sc[s][t] & 0xFFFF0000u)
-                                     : bf16_to_f32((uint16_t)sc[s][t]);
-                const float bv = VEC ? __builtin_bit_cast(float, g < 2 ? bi[s][t] << 16 : bi[s][t] & 0xFFFF0000u)
-                                     : bf16_to_f32((uint16_t)bi[s][t]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf16x8_t w = dequant_word(wv[s][t][i], sv * unit_inv, bv);
-                    acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, hi[s][i]), acc[t]);
-                    acc[t] = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, lo[s][i]), acc[t]);
-                }
+    auto piece_of = [&](unsigned long long mask) {   // KB of a chunk
+        return DOWN ? 8 : ((dense ? T : __popcll(mask)) + 3) / 4;
+    };
+    const buf_rsrc_t rx = make_buf(p.x, (uint32_t)T * H * 2);
+    // the B operand of entry v, chunks c0 .. + len, to `at`
+    auto stage = [&](int v, unsigned long long mask, char* at, int c0, int len) {
+        if constexpr (DOWN) {   // as it lies: for each chunk the four KB of h's upper parts, then the lower
+            const size_t h0 = v < sh_n ? p.sh_h + (size_t)v * ((p.I_sh + 127) / 128) * 2048
+                                       : (size_t)(v - sh_n) * ((p.I + 127) / 128) * 2048;
+            const bool on = dense ? mask >> c & 1 : c < __popcll(mask);
+            const int K = k_of(v);
+            const buf_rsrc_t rh = make_buf(p.h_hi + h0, ((K + 127) / 128) * 4096);
+            const buf_rsrc_t rl = make_buf(p.h_lo + h0, ((K + 127) / 128) * 4096);
+            for (int i = wave; i < len * 8; i += NW) {
+                const int q = c0 + i / 8;
+                const bool in = on && q * 128 + g * 32 < K;
+                buf_to_lds16(i & 4 ? rl : rh, at + i * 1024, in ? (q * 4 + i % 4) * 1024 + lane * 16 : 0xFFFFFFF0u, 0);
             }
-            if (ends[s]) {   // to the tokens' rows: the lanes have different places
-                int row = c;
-                bool col = mask[s] >> c & 1;
-                if (!dense) {
-                    list_tokens(mask[s], s_tok[wave], lane);
-                    col = c < __popcll(mask[s]);
-                    row = col ? s_tok[wave][c] : 0;
+        } else {
+            if (!dense) list_tokens(mask, s_tok[wave], lane);
+            stage_x(rx, dense, s_tok[wave], dense ? T : __popcll(mask), H, at, c0, len, wave, NW, lane);
+        }
+    };
+    const int total = sh_n * ((DOWN ? H : p.I_sh) / ROWS) + used * ((DOWN ? H : p.I) / ROWS);
+    int pos = (int)((long long)total * blockIdx.x / gridDim.x);
+    const int last = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+    int v, tile;
+    {
+        const int sh_all = sh_n * ((DOWN ? H : p.I_sh) / ROWS), r = pos - sh_all, per = (DOWN ? H : p.I) / ROWS;
+        v = r < 0 ? pos / ((DOWN ? H : p.I_sh) / ROWS) : sh_n + r / per;
+        tile = r < 0 ? pos % ((DOWN ? H : p.I_sh) / ROWS) : r % per;
+    }
+    while (pos < last) {
+        // ---- as many tiles as the B operands that fit into LDS have ----
+        __syncthreads();
+        int count = 0, per_seg = 1 << 30;
+        {
+            int room = x_kb, vv = v, from = tile;
+            while (count < last - pos) {
+                const unsigned long long mask = mask_of(vv);
+                const int piece = piece_of(mask), chunks = (k_of(vv) + 127) / 128;
+                const int here = min(tiles_of(vv) - from, last - pos - count);
+                if (piece * chunks > room) {
+                    if (count) break;
+                    per_seg = x_kb / piece / kBmAhead * kBmAhead;   // one entry's, a part of K after another
+                    count = min(here, NW);
+                    break;
                 }
-                if (col) {
-                    float* o = y + row * LDY + g * 4;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) *(f32x4_t*)(o + t * 16) = *(const f32x4_t*)(o + t * 16) + acc[t];
-                }
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();   // the next entry's tokens take these ones' place
-#pragma unroll
-                for (int t = 0; t < 4; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                stage(vv, mask, s_x + (x_kb - room) * 1024, 0, chunks);
+                room -= piece * chunks;
+                count += here;
+                ++vv;
+                from = 0;
             }
         }
-    } while (valid[0]);
-    __syncthreads();
-    for (int i = tid; i < T * 64; i += kBpWaves * WAVE) {
-        const int t = i / 64, n = i % 64;
-        float v = s_y[t * LDY + n];
+        for (int i0 = 0; i0 < count; i0 += NW) {
+            const bool mine = i0 + wave < count;
+            // this wave's tile
+            int vv = v, tl = tile + min(i0 + wave, count - 1);
+            const char* xb = s_x;
+            unsigned long long mask = mask_of(vv);
+            while (tl >= tiles_of(vv)) {
+                tl -= tiles_of(vv);
+                xb += piece_of(mask) * ((k_of(vv) + 127) / 128) * 1024;
+                mask = mask_of(++vv);
+            }
+            const bool sh = vv < sh_n;
+            const int K = k_of(vv), N = DOWN ? H : sh ? p.I_sh : p.I, chunks = (K + 127) / 128, G = K / 64;
+            const int row0 = tl * ROWS, piece = piece_of(mask), expert = expert_of(vv);
+            const size_t row = (size_t)expert * N;
+            const QMatDev& m0 = DOWN ? (sh ? p.sh_down : p.down) : (sh ? p.sh_gate : p.gate);
+            const QMatDev& m1 = DOWN ? m0 : (sh ? p.sh_up : p.up);
+            const int layout = m0.layout;
+            const size_t w0 = row * (K / 2) + (size_t)code_word(layout, row0, 0, K) * 4;
+            const size_t w1 = DOWN ? row * (K / 2) + (size_t)code_word(layout, row0 + 16, 0, K) * 4 : w0;
+            const size_t sc0 = SB ? ((row + row0) / 64 * G * 64 + row0 % 64) * 4 : (row + row0) * G * 2;
+            const size_t sc1 = DOWN ? sc0 + 32 * G : sc0;
+            const char *c0p = (const char*)m0.codes + w0, *c1p = (const char*)m1.codes + w1;
+            const char *s0p = (const char*)m0.scales + sc0, *s1p = (const char*)m1.scales + sc1;
+            const char *b0p = (const char*)m0.biases + sc0, *b1p = (const char*)m1.biases + sc1;
+            const uint32_t w_step = layout ? 4096u : 64u, s_step = SB ? 512u : 4u;
+            const uint32_t w_lane = code_word(layout, c, g * 4, K) * 4;
+            const uint32_t s_lane = SB ? (g / 2 * 64 + c) * 4 : (c * G + g / 2) * 2;
+            const bool half = K % 128 != 0;   // the last chunk's groups g >= 2 lie behind K
+            u32x4_t wa[kBmAhead], wb[kBmAhead];
+            uint32_t sa[kBmAhead], sb[kBmAhead], ba[kBmAhead], bb[kBmAhead];
+            auto fetch = [&](int s, int q) {
+                if (q >= chunks) return;
+                uint32_t w = w_lane + q * w_step, a = s_lane + q * s_step;
+                if (half && q == chunks - 1 && g >= 2) {   // an address of the row: not used
+                    w -= layout ? 2048u : 32u;
+                    a -= SB ? 256u : 2u;
+                }
+                wa[s] = *(const u32x4_t*)(c0p + w);
+                wb[s] = *(const u32x4_t*)(c1p + w);
+                if constexpr (SB) {
+                    sa[s] = *(const uint32_t*)(s0p + a);
+                    sb[s] = *(const uint32_t*)(s1p + a);
+                } else {
+                    sa[s] = *(const uint16_t*)(s0p + a);
+                    sb[s] = *(const uint16_t*)(s1p + a);
+                    ba[s] = *(const uint16_t*)(b0p + a);
+                    bb[s] = *(const uint16_t*)(b1p + a);
+                }
+            };
+            if (mine) {
+                fetch(0, 0);
+                fetch(1, 1);
+            }
+            // the token of this lane's column
+            bool on = mine && (dense ? mask >> c & 1 : c < __popcll(mask));
+            int t = c, at = 0;
+            if (!dense) {
+                list_tokens(mask, s_tok[wave], lane);
+                t = on ? s_tok[wave][c] : 0;
+            }
+            float wt = 1.f;
+            if constexpr (DOWN) {
+                if (!sh && on) at = p.assign[(vv - sh_n) * 16 + c];
+            } else if (sh) {
+                if (on && p.shared_gate) wt = p.shared_gate[t];
+            } else {
+                at = -1;   // its place among the token's experts: the lanes of a column share the search
+#pragma unroll 2
+                for (int j = g; j < k && on; j += 4)
+                    if (s_idx[t * k + j] == expert) at = t * k + j;
+                at = max(at, __shfl_xor(at, 16));
+                at = max(at, __shfl_xor(at, 32));
+                if (on) wt = p.topk_w[at];
+                if (on && tl == 0 && g == 0) p.assign[(vv - sh_n) * 16 + c] = at;
+            }
+            f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const int cx = DOWN || c < piece * 4 ? c : 0;   // columns behind the last token read any one's x
+            const uint32_t x_lane = DOWN ? lane * 16 : cx / 4 * 1024 + cx % 4 * 256 + (g * 4 ^ (cx & 12)) * 16;
+            const uint32_t x_low = DOWN ? 0 : (cx & 3) * 16;
+            for (int k0 = 0; k0 < chunks; k0 += per_seg) {
+                const int k1 = per_seg < chunks - k0 ? k0 + per_seg : chunks;
+                if (per_seg < chunks) {   // the same for all waves
+                    __syncthreads();
+                    stage(v, mask, s_x, k0, k1 - k0);
+                }
+                if (i0 == 0) {
+                    wait_loads<0>();
+                    __syncthreads();
+                }
+                if (!mine) continue;
+                if (k0 == 0) {
+                    fetch(2, 2);
+                    fetch(3, 3);
+                }
+                // slots by chunk: a segment's first chunk is a multiple of kBmAhead
+                for (int q0 = k0; q0 < k1; q0 += kBmAhead) {
 #pragma unroll
-        for (int w = 1; w < kBpWaves; ++w) v += s_y[(w * T + t) * LDY + n];
-        p.y_part[((size_t)split * T + t) * H + cg * 64 + n] = v;
+                    for (int s = 0; s < kBmAhead; ++s) {
+                        if (q0 + s >= k1) break;
+                        const char* xq = xb + (q0 + s - k0) * piece * 1024 + x_lane;
+                        float f0 = bf16_to_f32((uint16_t)sa[s]), f1 = bf16_to_f32((uint16_t)sb[s]);
+                        float e0 = bf16_to_f32((uint16_t)(SB ? sa[s] >> 16 : ba[s]));
+                        float e1 = bf16_to_f32((uint16_t)(SB ? sb[s] >> 16 : bb[s]));
+                        if (half && q0 + s == chunks - 1 && g >= 2) f0 = f1 = e0 = e1 = 0.f;
+                        const f32x2_t d0 = {f0 * 0x1p24f, f0 * 0x1p20f}, d1 = {f1 * 0x1p24f, f1 * 0x1p20f};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bf16x8_t a0 = dequant_half(wa[s][i], d0, e0), a1 = dequant_half(wb[s][i], d1, e1);
+                            const bf16x8_t b = *(const bf16x8_t*)(xq + (DOWN ? i * 1024 : (int)(x_low ^ i * 16)));
+                            acc[0] = mfma_16x16x32(a0, b, acc[0]);
+                            acc[1] = mfma_16x16x32(a1, b, acc[1]);
+                            if constexpr (DOWN) {
+                                const bf16x8_t l = *(const bf16x8_t*)(xq + 4096 + i * 1024);
+                                acc[0] = mfma_16x16x32(a0, l, acc[0]);
+                                acc[1] = mfma_16x16x32(a1, l, acc[1]);
+                            }
+                        }
+                        fetch(s, q0 + s + kBmAhead);
+                    }
+                }
+            }
+            if (on) {
+                if constexpr (DOWN) {   // fp32 rows: of the token's expert, or the token's shared expert
+                    float* o = p.rows + (size_t)(sh ? n + t : at) * H + row0 + g * 4;
+                    *(f32x4_t*)o = acc[0];
+                    *(f32x4_t*)(o + 16) = acc[1];
+                } else {
+                    uint16_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split_bf16(wt * (silu_f32(acc[0][i]) * acc[1][i]), &hi[i], &lo[i]);
+                    const size_t at_h = (sh ? p.sh_h + (size_t)vv * ((p.I_sh + 127) / 128) * 2048
+                                            : (size_t)(vv - sh_n) * ((p.I + 127) / 128) * 2048) +
+                                        h_place(row0 + g * 4, c);
+                    *(u32x2_t*)(p.h_hi + at_h) = u32x2_t{(uint32_t)hi[0] | (uint32_t)hi[1] << 16,
+                                                         (uint32_t)hi[2] | (uint32_t)hi[3] << 16};
+                    *(u32x2_t*)(p.h_lo + at_h) = u32x2_t{(uint32_t)lo[0] | (uint32_t)lo[1] << 16,
+                                                         (uint32_t)lo[2] | (uint32_t)lo[3] << 16};
+                }
+            }
+        }
+        pos += count;
+        tile += count;
+        while (pos < last && tile >= tiles_of(v)) tile -= tiles_of(v++);
     }
 }
 
-// The shares' sums, in order, rounded once.
-__global__ __launch_bounds__(256) void batch_join_kernel(const float* part, int splits, size_t n, uint16_t* y) {
+// y = the sum of a token's rows, the shared expert's last, rounded once.
+__global__ __launch_bounds__(256) void batch_join_kernel(const float* rows, int T, int k, int H, int shared, uint16_t* y) {
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
-    f32x4_t v = *(const f32x4_t*)(part + i);
+    if (i >= (size_t)T * H) return;
+    const int t = (int)(i / H), h = (int)(i - (size_t)t * H);
+    const float* row = rows + (size_t)t * k * H + h;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (shared) v = *(const f32x4_t*)(rows + ((size_t)T * k + t) * H + h);
 #pragma unroll 8
-    for (int s = 1; s < splits; ++s) v += *(const f32x4_t*)(part + s * n + i);
+    for (int j = 0; j < k; ++j) v += *(const f32x4_t*)(row + (size_t)j * H);
     *(u32x2_t*)(y + i) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// Shares of the experts: a workgroup for each compute unit.
-static int batch_splits(int H) {
-    const int s = 256 / (H / 64);
-    return s < 1 ? 1 : s < 16 ? s : 16;
-}
-
-// Tokens whose selection every gate/up workgroup repeats, one a wave.
-constexpr int kBatchOwnSelect = 8;
-// Tokens whose down products keep the sum over the experts in the accumulators.
+// Tokens whose gate/up workgroups each repeat the selection, a wave for each, and whose down products
+// keep the sum over the experts in the accumulators.
 constexpr int kBatchColumns = 8;
 
 static int batch_tiles(int T, int E, int k) {   // entries of the list at most
@@ -652,7 +765,8 @@ BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k) {
     w.h_lo = take(values * 2);
     w.list = take((size_t)w.tiles * 16);
     w.n_list = take(4);
-    w.y_part = take((size_t)batch_splits(H) * T * H * 4);
+    w.assign = take((size_t)w.tiles * 16 * 4);
+    w.rows = take(T > kBatchColumns ? (n + T) * H * 4 : 0);
     w.idx = take(n * 4);
     w.w = take(n * 4);
     w.total = o;
@@ -661,57 +775,53 @@ BatchWs batch_ws_layout(int T, int H, int I, int I_sh, int E, int k) {
 
 template <int EPL>
 static void launch_batch_gateup(const BatchArgs& a, hipStream_t stream) {
-    constexpr int NW = EPL ? 8 : 16;
     const int chunks = (a.H + 127) / 128;
     // a wave takes two chunks of K or more, where there are so many
-    const int rt_log = (chunks >= 8 ? 0 : chunks >= 4 ? 1 : 2) + (EPL || chunks < 8 ? 0 : 1);
-    const int want = (a.T < 16 ? (a.T + 3) / 4 : 4) * chunks, most = EPL ? 32 : 64;
-    const int x_kb = want < most ? want : most;
-    const int sh_n = a.T > kBatchDense ? (a.T + 15) / 16 : 1;
-    const int tasks = (sh_n * a.I_sh + a.tiles * a.I) >> (4 + rt_log), resident = EPL ? 512 : 256;
-    const int grid = tasks < resident ? tasks : resident;
-    const size_t lds = (size_t)x_kb * 1024 + NW * 4096 + (size_t)a.tiles * 16 + (size_t)a.T * a.k * (EPL ? 8 : 2);
+    const int rt_log = chunks >= 8 ? 0 : chunks >= 4 ? 1 : 2;
+    const int x_all = (a.T + 3) / 4 * chunks, x_kb = x_all < 32 ? x_all : 32;
+    const int tasks = (a.I_sh + a.tiles * a.I) >> (4 + rt_log);
+    const int grid = tasks < 512 ? tasks : 512;   // two workgroups a compute unit
+    const size_t lds = (size_t)x_kb * 1024 + kBgWaves * 4096 + (size_t)a.tiles * 16 + (size_t)a.T * a.k * 8;
     if (a.gate.layout == 2)
-        batch_gateup_kernel<EPL, true><<<grid, NW * WAVE, lds, stream>>>(a, x_kb, rt_log);
+        batch_gateup_kernel<EPL, true><<<grid, kBgWaves * WAVE, lds, stream>>>(a, x_kb, rt_log);
     else
-        batch_gateup_kernel<EPL, false><<<grid, NW * WAVE, lds, stream>>>(a, x_kb, rt_log);
+        batch_gateup_kernel<EPL, false><<<grid, kBgWaves * WAVE, lds, stream>>>(a, x_kb, rt_log);
 }
 
 hipError_t launch_decode_batch(const BatchArgs& a, hipStream_t stream) {
     const int epl = (a.E + WAVE - 1) / WAVE;
     hipError_t err;
-    if (a.T > kBatchOwnSelect) {
-        const int grid = (a.T + kBsWaves - 1) / kBsWaves;
-#define MOE_SEL(N) batch_select_kernel<N><<<grid, kBsWaves * WAVE, 0, stream>>>(a)
-        if (epl <= 1) MOE_SEL(1);
-        else if (epl <= 2) MOE_SEL(2);
-        else if (epl <= 4) MOE_SEL(4);
-        else if (epl <= 8) MOE_SEL(8);
-        else MOE_SEL(16);
-#undef MOE_SEL
+    if (a.T <= kBatchColumns) {
+        if (epl <= 1) launch_batch_gateup<1>(a, stream);
+        else if (epl <= 2) launch_batch_gateup<2>(a, stream);
+        else if (epl <= 4) launch_batch_gateup<4>(a, stream);
+        else if (epl <= 8) launch_batch_gateup<8>(a, stream);
+        else launch_batch_gateup<16>(a, stream);
         if ((err = hipGetLastError()) != hipSuccess) return err;
-        launch_batch_gateup<0>(a, stream);
-    } else if (epl <= 1) launch_batch_gateup<1>(a, stream);
-    else if (epl <= 2) launch_batch_gateup<2>(a, stream);
-    else if (epl <= 4) launch_batch_gateup<4>(a, stream);
-    else if (epl <= 8) launch_batch_gateup<8>(a, stream);
-    else launch_batch_gateup<16>(a, stream);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
-    if (a.T > kBatchColumns) {
-        const int splits = batch_splits(a.H), grid2 = a.H / 64 * splits;
-        const size_t lds2 = (size_t)kBpWaves * a.T * 68 * 4;
-        // pairs of scales as one load: even rows, and arrays that start at 4 bytes
-        auto even = [](const QMatDev& m) { return ((uintptr_t)m.scales | (uintptr_t)m.biases) % 4 == 0; };
-        if (a.I % 128 == 0 && a.I_sh % 128 == 0 && even(a.down) && even(a.sh_down))
-            batch_down_split_kernel<true><<<grid2, kBpWaves * WAVE, lds2, stream>>>(a, splits);
-        else
-            batch_down_split_kernel<false><<<grid2, kBpWaves * WAVE, lds2, stream>>>(a, splits);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-        const size_t n_y = (size_t)a.T * a.H;
-        batch_join_kernel<<<(unsigned)((n_y / 4 + 255) / 256), 256, 0, stream>>>(a.y_part, splits, n_y, a.y);
+        batch_down_kernel<<<a.H / 8, kBdWaves * WAVE, 0, stream>>>(a);
         return hipGetLastError();
     }
-    batch_down_kernel<<<a.H / 8, kBdWaves * WAVE, 0, stream>>>(a);
+    const int sel = (a.T + kBsWaves - 1) / kBsWaves;
+    if (epl <= 1) batch_select_kernel<1><<<sel, kBsWaves * WAVE, 0, stream>>>(a);
+    else if (epl <= 2) batch_select_kernel<2><<<sel, kBsWaves * WAVE, 0, stream>>>(a);
+    else if (epl <= 4) batch_select_kernel<4><<<sel, kBsWaves * WAVE, 0, stream>>>(a);
+    else if (epl <= 8) batch_select_kernel<8><<<sel, kBsWaves * WAVE, 0, stream>>>(a);
+    else batch_select_kernel<16><<<sel, kBsWaves * WAVE, 0, stream>>>(a);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    // a workgroup for each compute unit; 160 KB of LDS less the lists
+    constexpr int kGrid = 256, kLds = 156 * 1024;
+    const size_t lists = (size_t)a.tiles * 16 + (size_t)a.T * a.k * 2;
+    const int x_kb = (int)((kLds - lists) / 1024) < 128 ? (int)((kLds - lists) / 1024) : 128;
+    const size_t lds = (size_t)x_kb * 1024 + lists;
+    if (a.gate.layout == 2)
+        batch_tiles_kernel<false, true><<<kGrid, kBmWaves * WAVE, lds, stream>>>(a, x_kb);
+    else
+        batch_tiles_kernel<false, false><<<kGrid, kBmWaves * WAVE, lds, stream>>>(a, x_kb);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    batch_tiles_kernel<true, false><<<kGrid, kBmWaves * WAVE, 128 * 1024, stream>>>(a, 128);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    const unsigned blocks = (unsigned)(((size_t)a.T * a.H / 4 + 255) / 256);
+    batch_join_kernel<<<blocks, 256, 0, stream>>>(a.rows, a.T, a.k, a.H, a.I_sh > 0, a.y);
     return hipGetLastError();
 }
 

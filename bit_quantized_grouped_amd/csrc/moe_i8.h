@@ -179,11 +179,12 @@ struct BatchArgs {
     int tiles;                  // the list's capacity
     uint4* list;                // workspace: the chosen experts (expert, -, mask of tokens)
     int* n_list;
-    float* y_part;              // workspace: sums of shares of the experts [shares, T, H]
+    int* assign;                // workspace: of an entry's columns, the places in topk_idx [tiles, 16]
+    float* rows;                // workspace: the experts' rows of y [T*k, H], the shared one's [T, H]
     uint16_t* y;                // [T, H]
 };
 struct BatchWs {
-    size_t h_hi, h_lo, list, n_list, y_part, idx, w, total;
+    size_t h_hi, h_lo, list, n_list, assign, rows, idx, w, total;
     size_t sh_h;   // the shared expert's place in h, in values
     int tiles;
 };
