@@ -417,8 +417,7 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
     const int routed = *p.n_list * per, steps = routed + per_sh;
     u32x4_t wv[kBdAhead];
     float sc[kBdAhead], bi[kBdAhead];
-    bool on[kBdAhead];         // the lane's token is the entry's, and its K in range
-    size_t h_at[kBdAhead];
+    u32x4_t hi[kBdAhead][4], lo[kBdAhead][4];
     auto load = [&](int s, int step) {
         const bool in = step < steps, sh = step >= routed;
         const int u = in && !sh ? step / per : 0;
@@ -426,8 +425,8 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
         uint4 ent = {0, 0, 0xFF, 0};
         if (in && !sh) ent = p.list[u];
         const int K = sh ? I_sh : I, kb = d * 256 + half * 128 + g * 32;
-        on[s] = in && kb < K && c < T && (ent.z >> c & 1);
-        h_at[s] = (sh ? p.sh_h : (size_t)u * ((I + 127) / 128) * 2048) + (size_t)(d * 2 + half) * 2048 +
+        const bool on = in && kb < K && c < T && (ent.z >> c & 1);   // the entry's token
+        const size_t h_at = (sh ? p.sh_h : (size_t)u * ((I + 127) / 128) * 2048) + (size_t)(d * 2 + half) * 2048 +
                   (g * 16 + c) * 8;
         const QMatDev& m = sh ? p.sh_down : p.down;
         const size_t row = (size_t)ent.x * H + col;
@@ -436,6 +435,11 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
                              : u32x4_t{0, 0, 0, 0};
         sc[s] = in && kb < K ? bf16_to_f32(m.scales[row * (K / 64) + kb / 64]) : 0.f;
         bi[s] = in && kb < K ? bf16_to_f32(m.biases[row * (K / 64) + kb / 64]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[s][i] = on ? *(const u32x4_t*)(p.h_hi + h_at + i * 512) : u32x4_t{0, 0, 0, 0};
+            lo[s][i] = on ? *(const u32x4_t*)(p.h_lo + h_at + i * 512) : u32x4_t{0, 0, 0, 0};
+        }
     };
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -446,11 +450,9 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
             const f32x2_t d = {sc[s] * 0x1p24f, sc[s] * 0x1p20f};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const u32x4_t hi = on[s] ? *(const u32x4_t*)(p.h_hi + h_at[s] + i * 512) : u32x4_t{0, 0, 0, 0};
-                const u32x4_t lo = on[s] ? *(const u32x4_t*)(p.h_lo + h_at[s] + i * 512) : u32x4_t{0, 0, 0, 0};
                 const bf16x8_t w = dequant_half(wv[s][i], d, bi[s]);
-                acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, hi), acc);
-                acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, lo), acc);
+                acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, hi[s][i]), acc);
+                acc = mfma_16x16x32(w, __builtin_bit_cast(bf16x8_t, lo[s][i]), acc);
             }
             load(s, step + (s + kBdAhead) * kBdWaves);
         }
