@@ -13,8 +13,11 @@
 // neither ties nor sorted rows change the amount of work much.
 //
 // Few rows are split over workgroups, whose results a second kernel joins.
-// Bound by the bytes of the logits, and for bf16 nearly as much by vector instructions: about
-// 10 a value, the exponential counting four.
+// Bound by vector instructions for bf16, about 14 a value with the exponential as four, which 2048
+// rows of 131072 need 90 us for where their bytes need 85: 132 us in all.  Few rows are bound by
+// latency: one of 131072 takes 8.9 us, 1.6 of them for its values, and 3.5 for the join.
+// The next pieces' loads before the present ones' sums, 1024 threads and 256 a workgroup were tried: 150, 191
+// and 135 us, 192 rows of 150001 in 21.1, 21.7 and 30.1 where 512 threads take 22.0.
 #include "moe_i8.h"
 #include "moe_score.h"
 
@@ -35,17 +38,52 @@ struct LpSums {
     float m, s, d;
 };
 
-// b joins a.  A part without a number has m = -inf and sums 0, or NaN if it held one.
-__device__ __forceinline__ LpSums lp_join(const LpSums& a, const LpSums& b) {
-    const float ninf = -__builtin_huge_valf();
-    if (b.m == ninf) return LpSums{a.m, a.s + b.s, a.d + b.d};
-    if (a.m == ninf) return LpSums{b.m, a.s + b.s, a.d + b.d};
-    const float m = fmaxf(a.m, b.m);
-    const float ta = (a.m - m) * kLog2e, tb = (b.m - m) * kLog2e;   // +inf: NaN from here on
-    const float fa = __builtin_amdgcn_exp2f(ta), fb = __builtin_amdgcn_exp2f(tb);
-    // a factor of 0 leaves nothing, however far below its part lies
-    return LpSums{m, fa * a.s + fb * b.s, (fa == 0.f ? 0.f * a.s : fa * (a.d + ta * a.s)) +
-                                              (fb == 0.f ? 0.f * b.s : fb * (b.d + tb * b.s))};
+// a's sums for the maximum m >= a.m.  A part without a number has m = -inf and sums 0, or NaN if it
+// held one.  A factor of 0 leaves nothing, however far below m the part lies; m = +inf: NaN.
+__device__ __forceinline__ LpSums lp_scaled(const LpSums& a, float m) {
+    if (m == -__builtin_huge_valf()) return a;
+    const float t = (a.m - m) * kLog2e, f = __builtin_amdgcn_exp2f(t);
+    return LpSums{m, f * a.s, f == 0.f ? 0.f * a.s : f * (a.d + t * a.s)};
+}
+
+// Sum over the wave, in one order.
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#define MOE_DPP_ADD(ctrl) \
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, 0xf, 0xf, true))
+    MOE_DPP_ADD(0x111);   // row_shr:1
+    MOE_DPP_ADD(0x112);   // row_shr:2
+    MOE_DPP_ADD(0x114);   // row_shr:4
+    MOE_DPP_ADD(0x118);   // row_shr:8
+    MOE_DPP_ADD(0x142);   // row_bcast:15
+    MOE_DPP_ADD(0x143);   // row_bcast:31
+#undef MOE_DPP_ADD
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// The lanes' sums together: one exponential a lane, for the maximum of all.
+__device__ __forceinline__ LpSums lp_wave(const LpSums& a) {
+    const float m = key_float(wave_max_u32(choice_key(a.m)));
+    const LpSums o = lp_scaled(a, m);
+    return LpSums{m, wave_sum_f32(o.s), wave_sum_f32(o.d)};
+}
+
+// Keys above `mine` among `lists` lists of n in descending order.
+__device__ __forceinline__ int keys_above(const uint64_t* keys, int lists, int n, uint64_t mine) {
+    int above = 0;
+    const int top = 1 << (31 - __builtin_clz(n));
+    for (int l = 0; l < lists; l += 8) {   // eight searches at a time: each waits for LDS at every step
+        int at[8] = {};
+        for (int step = top; step; step >>= 1) {
+            uint64_t key[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) key[i] = keys[min(l + i, lists - 1) * n + min(at[i] + step, n) - 1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) at[i] += (key[i] > mine) & (at[i] + step <= n) & (l + i < lists) ? step : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) above += at[i];
+    }
+    return above;
 }
 
 // Four or eight values of a 16-byte piece.
@@ -122,10 +160,20 @@ struct LpArgs {
     uint64_t* keys;    // workspace [T, splits, n], each list in order, 0 behind its end
 };
 
+// The target's logit, in thread 0, fetched before it is needed.
+template <bool BF16>
+__device__ __forceinline__ float lp_target(const LpArgs& p, int row, int tid) {
+    if (tid || !p.logprob) return 0.f;
+    const int t = p.target[row];
+    if (t < 0 || t >= p.V) return 0.f;
+    const size_t at = (size_t)row * p.ld + t;
+    return BF16 ? bf16_to_f32(((const uint16_t*)p.logits)[at]) : ((const float*)p.logits)[at];
+}
+
 // The row's results from its sums and the n best keys in order.
 template <bool BF16>
 __device__ __forceinline__ void lp_write(const LpArgs& p, int row, const LpSums& all, const uint64_t* best,
-                                         int tid) {
+                                         float z_target, int tid) {
     const float ninf = -__builtin_huge_valf();
     const bool none = all.m == ninf && all.s == 0.f;   // -inf alone
     const float log_s = __builtin_logf(all.s);
@@ -140,12 +188,7 @@ __device__ __forceinline__ void lp_write(const LpArgs& p, int row, const LpSums&
         if (p.entropy) p.entropy[row] = none ? 0.f : log_s - kLn2 * (all.d / all.s);
         if (p.logprob) {
             const int t = p.target[row];
-            float v = 0.f;
-            if (t >= 0 && t < p.V) {
-                const size_t at = (size_t)row * p.ld + t;
-                v = lp(BF16 ? bf16_to_f32(((const uint16_t*)p.logits)[at]) : ((const float*)p.logits)[at]);
-            }
-            p.logprob[row] = v;
+            p.logprob[row] = t >= 0 && t < p.V ? lp(z_target) : 0.f;
         }
     }
 }
@@ -246,12 +289,10 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs p) {
         take_best(v, extra, piece_max(v));
     }
 
+    const float z_target = p.splits == 1 ? lp_target<BF16>(p, row, tid) : 0.f;
+
     // ---- the sums of the workgroup, in a fixed order ----
-#pragma unroll
-    for (int off = 1; off < WAVE; off <<= 1) {
-        const LpSums o = {shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.d, off)};
-        a = lane & off ? lp_join(o, a) : lp_join(a, o);
-    }
+    a = lp_wave(a);
     if (lane == 0) s_sums[wave] = a;
 
     // ---- the n best: threads' maxima, then the values of the best n threads ----
@@ -278,8 +319,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs p) {
         const int all = kLpWaves * p.n;
         if (tid < all) {
             const uint64_t mine = s_lists[tid];
-            int rank = 0;
-            for (int i = 0; i < all; ++i) rank += s_lists[i] > mine ? 1 : 0;
+            const int rank = keys_above(s_lists, kLpWaves, p.n, mine);
             if (mine && rank < p.n) {
                 // the thread of this maximum
                 const uint32_t index = 0xFFFFFFFFu - (uint32_t)mine;
@@ -354,10 +394,17 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LpArgs p) {
         }
     }
     __syncthreads();
-    LpSums total = s_sums[0];
-    for (int w = 1; w < kLpWaves; ++w) total = lp_join(total, s_sums[w]);
+    LpSums total = {s_sums[0].m, 0.f, 0.f};
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) total.m = fmaxf(total.m, s_sums[w].m);
+#pragma unroll
+    for (int w = 0; w < kLpWaves; ++w) {
+        const LpSums o = lp_scaled(s_sums[w], total.m);
+        total.s += o.s;
+        total.d += o.d;
+    }
     if (p.splits == 1) {
-        lp_write<BF16>(p, row, total, s_best, tid);
+        lp_write<BF16>(p, row, total, s_best, z_target, tid);
         return;
     }
     if (tid == 0) p.sums[blockIdx.x] = total;
@@ -369,26 +416,30 @@ template <bool BF16>
 __global__ __launch_bounds__(kLpThreads) void logprobs_join_kernel(LpArgs p) {
     __shared__ uint64_t s_keys[kLpCands];
     __shared__ uint64_t s_best[kLogprobsMaxTop];
-    const int row = blockIdx.x, tid = threadIdx.x;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid % WAVE;
     const int all = p.splits * p.n;
+    const float ninf = -__builtin_huge_valf(), z_target = lp_target<BF16>(p, row, tid);
+    // every wave joins the sums, a part a lane
+    const LpSums total = lp_wave(lane < p.splits ? p.sums[(size_t)row * p.splits + lane] : LpSums{ninf, 0.f, 0.f});
     for (int i = tid; i < all; i += kLpThreads) s_keys[i] = p.keys[(size_t)row * all + i];
     __syncthreads();
     for (int c = tid; c < all; c += kLpThreads) {
         const uint64_t mine = s_keys[c];
-        int rank = 0;
-        for (int i = 0; i < all; ++i) rank += s_keys[i] > mine ? 1 : 0;
-        if (mine && rank < p.n) s_best[rank] = mine;
+        if (!mine) continue;
+        const int rank = keys_above(s_keys, p.splits, p.n, mine);
+        if (rank < p.n) s_best[rank] = mine;
     }
-    LpSums total = p.sums[(size_t)row * p.splits];
-    for (int i = 1; i < p.splits; ++i) total = lp_join(total, p.sums[(size_t)row * p.splits + i]);
     __syncthreads();
-    lp_write<BF16>(p, row, total, s_best, tid);
+    lp_write<BF16>(p, row, total, s_best, z_target, tid);
 }
 
-// Workgroups a row is split over: about four for each compute unit, of 4096 values at least.
+// Workgroups a row is split over: as many as give each compute unit at most one, of 16384 values at
+// least.  What a workgroup does behind its values (5 us where they are read in 4) costs more than
+// idle compute units: 48 rows of 100003 fp32 take 12.8 us with 5 parts and 14.1 with 6, 96 rows of
+// 150001 bf16 15.3 with 2 and 17.2 with 3, and one row of 131072 8.9 + 3.5 with 8 and 9.4 + 6.0 with 32.
 static int lp_splits(int T, int V, int n) {
-    int s = (1024 + T - 1) / T;
-    const int most = V / 4096 > 0 ? V / 4096 : 1, room = n ? kLpCands / n : kLpCands;
+    int s = T < 256 ? 256 / T : 1;
+    const int most = V / 16384 > 0 ? V / 16384 : 1, room = n ? kLpCands / n : kLpCands;
     s = s < most ? s : most;
     s = s < room ? s : room;
     return s < 64 ? s : 64;
