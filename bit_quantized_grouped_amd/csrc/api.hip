@@ -1056,7 +1056,7 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
 // ---- a few tokens through the 4-bit layer ----
 
 static int check_batch_shape(int T, int H, int I, int I_sh, int E, int k) {
-    if (T < 1 || T > kBatchMaxTokens || k > kScoredMaxK) return MOE_ERR_SHAPE;
+    if (T < 1 || T > kBatchMaxTokens || k > kScoredMaxK || H >= 1 << 24) return MOE_ERR_SHAPE;
     return check_layer_shape(T, H, I, I_sh, E, k, 32);
 }
 

@@ -35,6 +35,7 @@ def with_mat(i, m):
 
 @pytest.mark.parametrize("kw,st", [
     (dict(T=0), SHAPE), (dict(T=65), SHAPE), (dict(H=96), SHAPE), (dict(I=0), SHAPE), (dict(I_sh=-64), SHAPE),
+    (dict(H=1 << 24, I=64, I_sh=64), SHAPE),
     (dict(E=0), SHAPE), (dict(E=1001), SHAPE), (dict(k=17), SHAPE), (dict(k=0), SHAPE),
     (dict(k=65, E=100), SHAPE), (dict(x=None), NULL), (dict(lg=None), NULL), (dict(y=None), NULL),
     (dict(ws=None), NULL), (dict(idx=None), NULL), (dict(w=None), NULL), (dict(bias=F), SHAPE),
