@@ -216,6 +216,59 @@ def test_captured_replayed_and_on_another_stream(T):
     assert all(torch.equal(side[k], want[1][k]) for k in side)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_special_rows_in_parts(dtype):
+    """Rows that are split over workgroups and joined, also where they start inside a piece."""
+    require_gpu()
+    announce(f"logprobs special rows in parts {dtype}")
+    V = 70011
+    rows = special_rows(V)
+    wide = torch.full((len(rows), V + 6), float("inf"), dtype=dtype, device=DEV)
+    z = wide[:, 3:3 + V]
+    z.copy_(torch.from_numpy(np.stack(list(rows.values())).astype(np.float32)))
+    t = torch.full((len(z),), V // 3, dtype=torch.int32, device=DEV)
+    for n in (1, 20, 64):
+        check(call(z, t, n), z, t, n, "special in parts")
+    # the best tokens all in one part, and at its ends
+    g = np.random.default_rng(12)
+    z = rows_of(g, 5, 200003, dtype, 1.0)
+    z[0, :40] += 30
+    z[1, -40:] += 30
+    z[2, 100000:100040] += 30
+    z[3, ::4001] += 30
+    t = targets_of(g, 5, 200003)
+    check(call(z, t, 30), z, t, 30, "parts")
+
+
+def test_parts_captured_and_on_two_streams():
+    require_gpu()
+    announce("logprobs in parts, captured and on two streams")
+    T, V, n = 3, 80001, 9
+    g = np.random.default_rng(3)
+    sets = [(rows_of(g, T, V, BF16), targets_of(g, T, V)) for _ in range(2)]
+    want = [call(*s, n) for s in sets]
+    z, t, o = sets[0][0].clone(), sets[0][1].clone(), outputs(T, n)
+    wss = [torch.zeros(bq.logprobs_workspace_bytes(T, V, n), dtype=torch.uint8, device=DEV) for _ in range(3)]
+    assert wss[0].numel()
+    sync()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bq.moe_logprobs(z, t, ws=wss[0], **o)
+    for i in (1, 0, 1):
+        z.copy_(sets[i][0])
+        t.copy_(sets[i][1])
+        graph.replay()
+        mine = call(*sets[1 - i], n)
+        assert all(torch.equal(o[k], want[i][k]) and torch.equal(mine[k], want[1 - i][k]) for k in o)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [outputs(T, n) for _ in range(12)]
+    sync()
+    for i, out in enumerate(outs):
+        bq.moe_logprobs(*sets[i % 2], ws=wss[1 + i % 2], **out, stream=streams[i % 2])
+    sync()
+    assert all(torch.equal(out[k], want[i % 2][k]) for i, out in enumerate(outs) for k in out)
+
+
 def test_rows_far_into_a_large_tensor():
     """Rows whose offsets pass 2^32 bytes."""
     require_gpu()

@@ -190,6 +190,29 @@ def test_captured_replayed_and_on_another_stream(M):
     assert torch.equal(o, want[2])
 
 
+@pytest.mark.parametrize("M", [2, 60, 1300])
+def test_two_streams_with_a_workspace_each(M):
+    """The same adapters and weights from two streams at once."""
+    require_gpu()
+    announce(f"lora on two streams M={M}")
+    N, K, R, n = 300, 512, 16, 9
+    g = np.random.default_rng(M)
+    h, args = make(g, M, N, K, R, n, pattern(g, M, n, "rows"), False)
+    calls = [args, dict(args, adapter=dev(pattern(g, M, n, "runs"), torch.int32))]
+    wss = [workspace(M, N, K, R) for _ in calls]
+    want = [torch.empty((M, N), dtype=torch.bfloat16, device=DEV) for _ in calls]
+    for c, o, ws in zip(calls, want, wss):
+        bq.moe_linear_lora_i8(**c, out=o, ws=ws)
+    sync()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [torch.empty_like(want[0]) for _ in range(16)]
+    sync()
+    for i, o in enumerate(outs):
+        bq.moe_linear_lora_i8(**calls[i % 2], out=o, ws=wss[i % 2], stream=streams[i % 2])
+    sync()
+    assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(outs))
+
+
 def test_an_adapter_is_exchanged_in_place():
     require_gpu()
     g = np.random.default_rng(0)
