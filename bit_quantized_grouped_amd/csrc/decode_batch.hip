@@ -3,21 +3,27 @@
 //
 //   y_t = sum_j w_tj FFN_e(t,j)(x_t) + g_t FFN_shared(x_t),  FFN(x) = (silu(x Wg^T) * x Wu^T) Wd^T
 //
-// Each chosen expert's weights are read once, whatever number of its tokens: a weight tile
-// is the A operand of the matrix instruction, 16 rows by 32 K, and the expert's tokens are
-// the 16 columns of B.  So a weight costs its dequantization, 19 instructions for 8, and the
-// number of tokens nothing; both sides of the sum are bf16 exactly as the format says
-// (w = bf16(q * s + b), x), products and sums in fp32.
+// A weight tile is the A operand of the matrix instruction, 16 rows by 32 K, and up to 16 tokens of
+// an expert are the columns of B.  So a weight costs its read and its dequantization, 17
+// instructions for 8, for 16 tokens as for one; both sides of the sums are bf16 exactly as the
+// format says (w = bf16(q * s + b), x), products and sums fp32.  h already holds the token's
+// weight, and is kept as two bf16 (16 bits), so that y has the one rounding of its own.
 //
-//   batch_gateup_kernel: every workgroup groups the T * k assignments by expert in LDS (a
-//     64-bit mask of tokens for each expert, a scan over the experts), then takes row tiles
-//     of the experts in turn, its waves splitting rows and K, and writes h = w * silu(g) * u.
-//     h already holds the token's weight, and is kept as two bf16 (16 bits), so that y
-//     has the one rounding of its own.  Workgroup 0 also writes the grouping for down.
-//   batch_down_kernel: a workgroup owns 8 columns of y for all tokens and sums over all
-//     experts: the products' columns are the tokens, so the sum over experts stays in the
-//     accumulators.  The 16 x 16 product is used as two of 8 x 8: rows and columns 8 .. 15
-//     hold the same 8 columns of y and tokens at a K 128 further on.
+// Up to 8 tokens, two launches (2048 wide, 256 experts of 512 and a shared one, scales packed, 8 a token):
+//   batch_gateup_kernel: every workgroup selects and groups for itself, then its waves split K.
+//   batch_down_kernel: a workgroup owns 8 columns of y for all tokens, and the products' columns are
+//     the tokens, so the sum over the experts stays in the accumulators.  The 16 x 16 product is
+//     used as two of 8 x 8: rows and columns 8 .. 15 hold the same columns of y and tokens at a
+//     K 128 further on.
+//   1, 2, 4, 8 tokens 13.0 + 6.6, 15.4 + 8.2, 17.9 + 11.2 and 26.5 + 20.4 us, for weights that 6.2
+//   TB/s read in 2.6, 4.8, 9.2 and 16.5; in the form below 18.2 + 9.9 for 2, 18.1 + 10.9 for 4, 23.9 +
+//   16.6 for 8, each with 7 to 9 us of selection and join.
+// More tokens, four launches: batch_select_kernel (4.7 us), batch_tiles_kernel for gate/up and for down,
+//   batch_join_kernel (4.6).  16 tokens 30.3 + 19.5 us (floor 14.5 + 7.2), 32 tokens 52.8 + 32.6 (31 +
+//   16), 64 tokens of skewed experts 29.5 + 19.6 (10 + 5).
+// What bounds them: 5 us of a launch are its own, 6 to 8 pass before a workgroup's first product (list, tile,
+// operands, first weights, each a trip to memory), then dequantization (34 ns a word and wave on a
+// SIMD) and the 24 bytes a ns that a compute unit gets from memory take about as long as each other.
 #include "moe_device.h"
 #include "moe_i8.h"
 #include "moe_lds.h"
@@ -166,7 +172,8 @@ __device__ __forceinline__ int group_tokens(const BatchArgs& p, const Idx* s_idx
 
 // ---- up to kBatchColumns tokens ----
 //
-// Selects too.  x_kb: LDS for x, in pieces of 4 tokens by 128 K; T tokens' pieces of per_seg chunks fit.
+// Selects too; x of all tokens is in LDS, read in the order of the B operand, where lanes that fetched
+// their 16 bytes of 16 rows from memory held up the weights' loads.  x_kb: LDS for x, in pieces of 4 tokens by 128 K; T tokens' pieces of per_seg chunks fit.
 // rt_log: a task is 16 << rt_log rows of an entry, 16 a wave, and the other waves split K.  A
 // workgroup's tasks lie together, and the waves fetch the next task's weights before they are done
 // with this one's.
@@ -475,9 +482,12 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
 // ---- more tokens: gate/up (DOWN 0) and down (DOWN 1), whose work is a list of tiles ----
 //
 // A tile is one wave's: 16 rows of an entry's gate and up, or 32 of its down, times the whole K, so
-// that nothing is joined and waves do not wait for each other.  A workgroup takes a run of tiles,
-// which belong to one or two entries, whose B operands (x, or h as written) lie in LDS for all of
-// its waves.  kBmAhead chunks of a wave's weights are in flight, 2 KB each.
+// that nothing is joined and waves do not wait for each other (K over 8 waves, a barrier a task:
+// 32 tokens 56 + 38 us instead of 52 + 32).  A workgroup takes a run of tiles, which belong to one
+// or two entries, whose B operands (x, or h as written) lie in LDS for all of its waves; where an
+// entry's do not fit, a part of K after another.  kBmAhead chunks of a wave's weights are in flight,
+// 2 KB each.  A compute unit has 9 to 10 tiles of 16 tokens' 8 experts, so 12 waves; 16 take as
+// long, and the next tile's weights before this one's end gained nothing.
 constexpr int kBmWaves = 12, kBmAhead = 4;
 
 template <bool DOWN, bool SB>

@@ -574,8 +574,7 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
 /* ---- Several requests at once: a few tokens through the 4-bit layer. ---- */
 
 /* The whole 4-bit layer for a batch of 1 .. 64 tokens, each expert's weights read once for
- * all of its tokens: two kernels, and a third in front for the selection of more than a few
- * tokens.  [P3] "Decode is limited by bandwidth more than by compute".
+ * every 16 of its tokens: two kernels for up to 8 tokens, four for more.  [P3] "Decode is limited by bandwidth more than by compute".
  *   selection  moe_route's (rule and score_bias NULL) or moe_route_scored's, with the same
  *              experts and weights
  *   y[t] = sum_j topk_w[t, j] * FFN_(topk_idx[t, j])(x[t]) + shared_gate[t] * FFN_shared(x[t])
@@ -588,8 +587,8 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
  * order of its sums.  Deterministic: the same inputs give the same bits.
  *   ws: moe_decode_batch_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned; need
  *   not be cleared.
- * Shapes and matrices as for moe_decode_q4, T <= 64, k <= 64; for a rule also
- * moe_route_scored's limits. */
+ * Shapes and matrices as for moe_decode_q4, T <= 64, k <= 64, H < 2^24; for a rule also
+ * moe_route_scored's limits.  Scales are finite and below 2^103 in magnitude. */
 size_t moe_decode_batch_workspace_bytes(int T, int H, int I, int I_sh, int E, int k);
 int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* score_bias,
                         const moe_score_rule* rule, const float* shared_gate, int T, int H, int I,
@@ -615,9 +614,10 @@ typedef struct {
  *                    + scales[j] * sum_r b[j, n, r] * (sum_k a[j, r, k] * a[m, k])))
  * adapter int32 [M]; a row whose adapter lies outside 0 .. n - 1 has none, and moe_linear_i8's
  * values.  The adapters' sums are fp32, the first product's result counts to 16 bits, and out
- * has one rounding.  An adapter's values reach its own rows only, infinities and NaN too.
+ * has one rounding.  An adapter's values reach its own rows only, infinities and NaN too (of its b:
+ * NaN in those rows then, also in other columns).
  *   ws: moe_linear_lora_i8_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned
- * Sizes as for moe_linear_i8.  Enqueues two kernels. */
+ * Sizes as for moe_linear_i8.  Enqueues two kernels, three where the rows are put in order of their adapters first. */
 size_t moe_linear_lora_i8_workspace_bytes(int M, int N, int K, int rank);
 int moe_linear_lora_i8(const int8_t* a, const float* a_scale, int M, int K, const moe_i8_mat* w, int N,
                        const moe_adapters* adapters, const int32_t* adapter, uint16_t* out, void* ws,

@@ -190,6 +190,40 @@ def test_captured_replayed_and_on_another_stream(M):
     assert torch.equal(o, want[2])
 
 
+@pytest.mark.parametrize("M,N,K,R,n,kind", [
+    (2100, 256, 512, 64, 40, "rows"), (2100, 256, 512, 64, 40, "runs"), (2100, 80, 512, 64, 40, "one"),
+    (2100, 45, 512, 64, 40, "none"), (9001, 64, 128, 64, 30, "rows"), (9001, 33, 128, 72, 3000, "rows"),
+    (2050, 64, 512, 64, 5000, "rows")])
+def test_rows_in_order_of_their_adapters(M, N, K, R, n, kind):
+    """Enough rows and adapters that rows are put in order first, more adapters than that takes, more
+    rows than one round of it, no row with an adapter; captured, with other adapters at each replay."""
+    require_gpu()
+    what = f"lora in order M={M} N={N} K={K} R={R} n={n} {kind}"
+    announce(what)
+    g = np.random.default_rng(M + n)
+    of = np.full(M, -1) if kind == "none" else pattern(g, M, n, kind)
+    h, args = make(g, M, N, K, R, n, of, N % 16 == 0)
+    out = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = workspace(M, N, K, R)
+    bq.moe_linear_lora_i8(**args, out=out[:M], ws=ws)
+    sync()
+    check(out[:M], h, what)
+    assert (out[M:] == 7).all()
+    first = out[:M].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bq.moe_linear_lora_i8(**args, out=out[:M], ws=ws)
+    other = dev(pattern(g, M, n, "rows"), torch.int32)
+    want = torch.empty_like(first)
+    bq.moe_linear_lora_i8(**dict(args, adapter=other), out=want, ws=workspace(M, N, K, R))
+    mine = args["adapter"].clone()
+    for a, w in ((other, want), (mine, first), (other, want)):
+        args["adapter"].copy_(a)
+        graph.replay()
+        sync()
+        assert torch.equal(out[:M], w)
+
+
 @pytest.mark.parametrize("M", [2, 60, 1300])
 def test_two_streams_with_a_workspace_each(M):
     """The same adapters and weights from two streams at once."""
