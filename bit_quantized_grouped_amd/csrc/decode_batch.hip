@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kBgWaves* WAVE, bg_per_simd(EPL, SB)) void batch_ga
             }
         }
         uint32_t w = w_at + w_lane, s = s_at + s_lane;
-        if (half_chunk && l_q == chunks - 1) {   // an address of the row, whose weights are not used
+        if (half_chunk && l_q == chunks - 1) {   // weights of the row again: they meet zeros in LDS
             w -= w_half;
             s -= s_half;
         }
@@ -363,15 +363,9 @@ __global__ __launch_bounds__(kBgWaves* WAVE, bg_per_simd(EPL, SB)) void batch_ga
                     Chunk w2 = w1;
                     fetch(w2);
                     const char* xq = x_lane + (q - c0) * nq * 1024;
-                    float sg = bf16_to_f32((uint16_t)w0.sg), su = bf16_to_f32((uint16_t)w0.su);
-                    float bg = bf16_to_f32((uint16_t)(SB ? w0.sg >> 16 : w0.bg));
-                    float bu = bf16_to_f32((uint16_t)(SB ? w0.su >> 16 : w0.bu));
-                    if (half_chunk && q == chunks - 1) {
-                        sg = g >= 2 ? 0.f : sg;
-                        su = g >= 2 ? 0.f : su;
-                        bg = g >= 2 ? 0.f : bg;
-                        bu = g >= 2 ? 0.f : bu;
-                    }
+                    const float sg = bf16_to_f32((uint16_t)w0.sg), su = bf16_to_f32((uint16_t)w0.su);
+                    const float bg = bf16_to_f32((uint16_t)(SB ? w0.sg >> 16 : w0.bg));
+                    const float bu = bf16_to_f32((uint16_t)(SB ? w0.su >> 16 : w0.bu));
                     const f32x2_t dg = {sg * 0x1p24f, sg * 0x1p20f}, du = {su * 0x1p24f, su * 0x1p20f};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -488,7 +482,7 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
 // entry's do not fit, a part of K after another.  kBmAhead chunks of a wave's weights are in flight,
 // 2 KB each.  A compute unit has 9 to 10 tiles of 16 tokens' 8 experts, so 12 waves; 16 take as
 // long, and the next tile's weights before this one's end gained nothing.
-constexpr int kBmWaves = 12, kBmAhead = 4;
+constexpr int kBmWaves = 16, kBmAhead = 2;
 
 template <bool DOWN, bool SB>
 __global__ __launch_bounds__(kBmWaves* WAVE) void batch_tiles_kernel(BatchArgs p, int x_kb) {
@@ -628,7 +622,7 @@ __global__ __launch_bounds__(kBmWaves* WAVE) void batch_tiles_kernel(BatchArgs p
             auto fetch = [&](int s, int q) {
                 if (q >= chunks) return;
                 uint32_t w = w_lane + q * w_step, a = s_lane + q * s_step;
-                if (half && q == chunks - 1 && g >= 2) {   // an address of the row: not used
+                if (half && q == chunks - 1 && g >= 2) {   // weights of the row again: they meet zeros in LDS
                     w -= layout ? 2048u : 32u;
                     a -= SB ? 256u : 2u;
                 }
@@ -685,20 +679,15 @@ __global__ __launch_bounds__(kBmWaves* WAVE) void batch_tiles_kernel(BatchArgs p
                     __syncthreads();
                 }
                 if (!mine) continue;
-                if (k0 == 0) {
-                    fetch(2, 2);
-                    fetch(3, 3);
-                }
                 // slots by chunk: a segment's first chunk is a multiple of kBmAhead
                 for (int q0 = k0; q0 < k1; q0 += kBmAhead) {
 #pragma unroll
                     for (int s = 0; s < kBmAhead; ++s) {
                         if (q0 + s >= k1) break;
                         const char* xq = xb + (q0 + s - k0) * piece * 1024 + x_lane;
-                        float f0 = bf16_to_f32((uint16_t)sa[s]), f1 = bf16_to_f32((uint16_t)sb[s]);
-                        float e0 = bf16_to_f32((uint16_t)(SB ? sa[s] >> 16 : ba[s]));
-                        float e1 = bf16_to_f32((uint16_t)(SB ? sb[s] >> 16 : bb[s]));
-                        if (half && q0 + s == chunks - 1 && g >= 2) f0 = f1 = e0 = e1 = 0.f;
+                        const float f0 = bf16_to_f32((uint16_t)sa[s]), f1 = bf16_to_f32((uint16_t)sb[s]);
+                        const float e0 = bf16_to_f32((uint16_t)(SB ? sa[s] >> 16 : ba[s]));
+                        const float e1 = bf16_to_f32((uint16_t)(SB ? sb[s] >> 16 : bb[s]));
                         const f32x2_t d0 = {f0 * 0x1p24f, f0 * 0x1p20f}, d1 = {f1 * 0x1p24f, f1 * 0x1p20f};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {

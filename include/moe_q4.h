@@ -588,7 +588,7 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
  *   ws: moe_decode_batch_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned; need
  *   not be cleared.
  * Shapes and matrices as for moe_decode_q4, T <= 64, k <= 64, H < 2^24; for a rule also
- * moe_route_scored's limits.  Scales are finite and below 2^103 in magnitude. */
+ * moe_route_scored's limits.  Scales and biases are finite, scales below 2^103 in magnitude. */
 size_t moe_decode_batch_workspace_bytes(int T, int H, int I, int I_sh, int E, int k);
 int moe_decode_batch_q4(const uint16_t* x, const float* logits, const float* score_bias,
                         const moe_score_rule* rule, const float* shared_gate, int T, int H, int I,
