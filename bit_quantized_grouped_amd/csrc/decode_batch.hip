@@ -19,8 +19,8 @@
 //   TB/s read in 2.6, 4.8, 9.2 and 16.5; in the form below 18.2 + 9.9 for 2, 18.1 + 10.9 for 4, 23.9 +
 //   16.6 for 8, each with 7 to 9 us of selection and join.
 // More tokens, four launches: batch_select_kernel (4.7 us), batch_tiles_kernel for gate/up and for down,
-//   batch_join_kernel (4.6).  16 tokens 30.3 + 19.5 us (floor 14.5 + 7.2), 32 tokens 52.8 + 32.6 (31 +
-//   16), 64 tokens of skewed experts 29.5 + 19.6 (10 + 5).
+//   batch_join_kernel (4.6).  16 tokens 30.7 + 17.8 us (floor 14.5 + 7.2), 32 tokens 48.0 + 29.3 (31 +
+//   16), 64 tokens of skewed experts 29.4 + 18.1 (10 + 5).
 // What bounds them: 5 us of a launch are its own, 6 to 8 pass before a workgroup's first product (list, tile,
 // operands, first weights, each a trip to memory), then dequantization (34 ns a word and wave on a
 // SIMD) and the 24 bytes a ns that a compute unit gets from memory take about as long as each other.
@@ -480,8 +480,9 @@ __global__ __launch_bounds__(kBdWaves* WAVE) void batch_down_kernel(BatchArgs p)
 // 32 tokens 56 + 38 us instead of 52 + 32).  A workgroup takes a run of tiles, which belong to one
 // or two entries, whose B operands (x, or h as written) lie in LDS for all of its waves; where an
 // entry's do not fit, a part of K after another.  kBmAhead chunks of a wave's weights are in flight,
-// 2 KB each.  A compute unit has 9 to 10 tiles of 16 tokens' 8 experts, so 12 waves; 16 take as
-// long, and the next tile's weights before this one's end gained nothing.
+// 2 KB each: 32 tokens 49 + 30 us, with 12 waves 52 + 31, with four chunks and 12 waves 53 + 32; 16
+// tokens take 30 + 18 in each but the last, 30 + 19.  The next tile's weights before this one's end
+// gained nothing.
 constexpr int kBmWaves = 16, kBmAhead = 2;
 
 template <bool DOWN, bool SB>
