@@ -783,7 +783,7 @@ static void launch_batch_gateup(const BatchArgs& a, hipStream_t stream) {
     // a wave takes two chunks of K or more, where there are so many
     const int rt_log = chunks >= 8 ? 0 : chunks >= 4 ? 1 : 2;
     const int x_all = (a.T + 3) / 4 * chunks, x_kb = x_all < 32 ? x_all : 32;
-    const int tasks = (a.I_sh + a.tiles * a.I) >> (4 + rt_log);
+    const int tasks = (a.I_sh >> (4 + rt_log)) + a.tiles * (a.I >> (4 + rt_log));
     const size_t lds = (size_t)x_kb * 1024 + kBgWaves * 4096 + (size_t)a.tiles * 16 + (size_t)a.T * a.k * 8;
     const bool packed = a.gate.layout == 2;
     // a task each for as many workgroups as the chip holds (160 KB of LDS a compute unit), else runs of
