@@ -1058,9 +1058,10 @@ def moe_decode_batch_q4(x: torch.Tensor, logits: torch.Tensor, score_bias, rule,
                         I_sh: int, k: int, gate, up, down, sh_gate, sh_up, sh_down, y: torch.Tensor,
                         ws: torch.Tensor, topk_idx=None, topk_w=None, stream=None):
     """1 to 64 tokens (x bf16 [T, H], logits fp32 [T, E]) through the whole 4-bit layer, each chosen
-    expert read once for every 16 of its tokens.  rule: a ScoreRule or None (moe_route's selection), score_bias fp32 [E] or
-    None, shared_gate fp32 [T] or None (a weight of 1).  topk_idx int32 and topk_w fp32 [T, k]
-    receive the selection when given.  ws: decode_batch_workspace_bytes(T, H, I, I_sh, E, k)."""
+    expert read once for every 16 of its tokens.  rule: a ScoreRule or None (moe_route's
+    selection), score_bias fp32 [E] or None, shared_gate fp32 [T] or None (a weight of 1).
+    topk_idx int32 and topk_w fp32 [T, k] receive the selection when given.
+    ws: decode_batch_workspace_bytes(T, H, I, I_sh, E, k)."""
     shape = T, H = _few_tokens(x)
     d = x.get_device()
     E = _two_dims(logits, "logits", "[T, E]")[1]
