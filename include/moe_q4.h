@@ -574,7 +574,8 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
 /* ---- Several requests at once: a few tokens through the 4-bit layer. ---- */
 
 /* The whole 4-bit layer for a batch of 1 .. 64 tokens, each expert's weights read once for
- * every 16 of its tokens: two kernels for up to 8 tokens, four for more.  [P3] "Decode is limited by bandwidth more than by compute".
+ * every 16 of its tokens: two kernels for up to 8 tokens, four for more.  [P3] "Decode is
+ * limited by bandwidth more than by compute".
  *   selection  moe_route's (rule and score_bias NULL) or moe_route_scored's, with the same
  *              experts and weights
  *   y[t] = sum_j topk_w[t, j] * FFN_(topk_idx[t, j])(x[t]) + shared_gate[t] * FFN_shared(x[t])
