@@ -1036,7 +1036,25 @@ def _q4mat(m, name, n_exp, N, K, dev, present=True):
             raise ValueError(f"{name}.{part}: on {t.device}, the call's first tensor is elsewhere")
         if t.data_ptr() != getattr(m.struct, part):
             raise ValueError(f"{name}.{part}: another tensor than its DeviceQMat was made with")
+    if m.layout != m.struct.layout:
+        raise ValueError(f"{name}.layout: another layout than its DeviceQMat was made with")
     return ctypes.byref(m.struct)
+
+
+def _q4_parts(m):
+    return (m, m.struct, m.codes, m.scales, m.biases) if isinstance(m, DeviceQMat) else (m,)
+
+
+def _q4_state(mats):
+    """Numbers that change when a matrix set, a tensor of it or a tensor's place does, as long as
+    what they were taken of is alive."""
+    state = []
+    for m in mats:
+        parts = _q4_parts(m)
+        state += map(id, parts)
+        if m is not None and len(parts) > 1:
+            state += m.layout, m.codes.data_ptr(), m.scales.data_ptr(), m.biases is not None and m.biases.data_ptr()
+    return state
 
 
 def _expert_q4_mats(mats, E, H, I, I_sh, dev):
@@ -1284,14 +1302,13 @@ class MoeLayer:
                   _opt_arg(shared_gate, "shared_gate", F32, (T,), d))
         if shared_gate is not None and not self.I_sh:
             raise ValueError("shared_gate: must be None here")
-        mats = self.weight_mats()
-        if self._batch_mats is None or self._batch_mats[0] != d or any(
-                a is not b for a, b in zip(mats, self._batch_mats[1])):
-            # checked once for these matrix sets; they stay alive with what was checked
+        mats, sizes = self.weight_mats(), (d, H, self.I, self.I_sh, self.E, self.k)
+        state = _q4_state(mats)
+        if self._batch_mats is None or self._batch_mats[0] != sizes or self._batch_mats[1] != state:
+            # checked once for what these matrix sets hold, which stays alive with them
             args = _expert_q4_mats(mats, self.E, H, self.I, self.I_sh, d)
-            parts = [(m.codes, m.scales, m.biases) for m in mats if m is not None]
-            self._batch_mats = d, mats, args, parts
-        kept = self._batch_bufs.get((T, d))
+            self._batch_mats = sizes, state, args, [_q4_parts(m) for m in mats]
+        kept = self._batch_bufs.get((T, sizes))
         if kept is None:
             if d < 0:
                 raise ValueError("arguments must be device tensors (got tensors on the CPU)")
@@ -1301,7 +1318,7 @@ class MoeLayer:
                      topk_idx=torch.empty((T, self.k), dtype=I32, device=on),
                      topk_w=torch.empty((T, self.k), dtype=F32, device=on), ws=ws)
             outs = b["topk_idx"].data_ptr(), b["topk_w"].data_ptr()
-            kept = self._batch_bufs[T, d] = b, outs, _ws_arg(ws, "ws", d)
+            kept = self._batch_bufs[T, sizes] = b, outs, _ws_arg(ws, "ws", d)
             _wait_for_allocations(stream, on)
         b, outs, ws = kept
         y = b["y"] if out is None else out

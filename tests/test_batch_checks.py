@@ -106,6 +106,43 @@ def test_matrix_sets_are_checked():
         m.decode_batch(X, LG)
 
 
+def replaced(m, part):
+    t = getattr(m.gate, part)
+    setattr(m.gate, part, t + 1 if part == "layout" else t.clone())
+
+
+def moved(m, part):
+    getattr(m.down, part).set_(getattr(m.down, part).clone())   # the same tensor, elsewhere
+
+
+@pytest.mark.parametrize("change,part,match", [
+    (replaced, "codes", "gate.codes: another"), (replaced, "scales", "gate.scales: another"),
+    (replaced, "biases", "gate.biases: another"), (replaced, "layout", "gate.layout: another"),
+    (moved, "codes", "down.codes: another"), (moved, "biases", "down.biases: another")])
+def test_matrix_sets_are_checked_again_when_they_change(change, part, match):
+    """A set is checked at the object's first call; one whose tensors are replaced afterwards is
+    refused as it is before it, and not used with the tensors of then."""
+    m = layer()
+    for _ in range(2):
+        with pytest.raises(ValueError, match="device tensors"):   # the sets are as they should be
+            m.decode_batch(X, LG)
+    change(m, part)
+    for _ in range(2):
+        with pytest.raises(ValueError, match=match):
+            m.decode_batch(X, LG)
+
+
+def test_sizes_that_change_are_taken_up():
+    """Matrix sets that no longer hold the layer's sizes are refused after its first call too."""
+    for name, value in (("E", 16), ("I", 128), ("I_sh", 128), ("I_sh", 0)):
+        m = layer()
+        with pytest.raises(ValueError, match="device tensors"):
+            m.decode_batch(X, LG)
+        setattr(m, name, value)
+        with pytest.raises(ValueError, match="do not hold|must be None"):
+            m.decode_batch(X, torch.zeros((4, m.E)))
+
+
 def test_binding_refusals():
     m = layer().weight_mats()
     ws, y = torch.zeros(1 << 16, dtype=torch.uint8), torch.zeros_like(X)
