@@ -1041,20 +1041,29 @@ def _q4mat(m, name, n_exp, N, K, dev, present=True):
     return ctypes.byref(m.struct)
 
 
-def _q4_parts(m):
-    return (m, m.struct, m.codes, m.scales, m.biases) if isinstance(m, DeviceQMat) else (m,)
+def _held(m):
+    """What a checked matrix set holds, kept alive, and its tensors' places (by bound methods: they
+    are compared at every call)."""
+    if m is None:
+        return None, None, None, None, None, None, ()
+    return (m, m.struct, m.layout, m.codes, m.scales, m.biases,
+            [(t.data_ptr, t.data_ptr()) for t in (m.codes, m.scales, m.biases) if t is not None])
 
 
-def _q4_state(mats):
-    """Numbers that change when a matrix set, a tensor of it or a tensor's place does, as long as
-    what they were taken of is alive."""
-    state = []
-    for m in mats:
-        parts = _q4_parts(m)
-        state += map(id, parts)
-        if m is not None and len(parts) > 1:
-            state += m.layout, m.codes.data_ptr(), m.scales.data_ptr(), m.biases is not None and m.biases.data_ptr()
-    return state
+def _holds(held, mats):
+    """Whether matrix sets hold what they did when `held` was taken of them."""
+    for (one, struct, layout, codes, scales, biases, places), m in zip(held, mats):
+        if m is not one:
+            return False
+        if m is None:
+            continue
+        if (m.codes is not codes or m.scales is not scales or m.biases is not biases or m.struct is not struct
+                or m.layout != layout):
+            return False
+        for place, at in places:
+            if place() != at:
+                return False
+    return True
 
 
 def _expert_q4_mats(mats, E, H, I, I_sh, dev):
@@ -1303,11 +1312,10 @@ class MoeLayer:
         if shared_gate is not None and not self.I_sh:
             raise ValueError("shared_gate: must be None here")
         mats, sizes = self.weight_mats(), (d, H, self.I, self.I_sh, self.E, self.k)
-        state = _q4_state(mats)
-        if self._batch_mats is None or self._batch_mats[0] != sizes or self._batch_mats[1] != state:
-            # checked once for what these matrix sets hold, which stays alive with them
+        if self._batch_mats is None or self._batch_mats[0] != sizes or not _holds(self._batch_mats[1], mats):
+            # checked in full once for what these matrix sets hold
             args = _expert_q4_mats(mats, self.E, H, self.I, self.I_sh, d)
-            self._batch_mats = sizes, state, args, [_q4_parts(m) for m in mats]
+            self._batch_mats = sizes, [_held(m) for m in mats], args
         kept = self._batch_bufs.get((T, sizes))
         if kept is None:
             if d < 0:
