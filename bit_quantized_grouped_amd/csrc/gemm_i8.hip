@@ -521,8 +521,8 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
             int here = lane;   // nothing of this is computed before the product's loop, which needs the registers
             asm volatile("" : "+v"(here));
             const int tiles_in = min(BM / 16, (M - m0 + 15) / 16), cols_in = min(BN, N - n0);
-            const buf_rsrc_t ru = make_buf(lora.u + (size_t)(m0 / 16) * lora.steps * (WAVE * 8),
-                                           (uint32_t)(tiles_in * lora.steps) * 1024u);
+            const buf_rsrc_t ru = make_buf((const char*)lora.u + lora_u_at(m0 / 16, 0, lora.steps, 0),
+                                           (uint32_t)lora_u_bytes(tiles_in, lora.steps));
             unsigned long long left[QL];
             for (int base = 0; base < lora.steps; base += ST) {
 #pragma unroll
@@ -542,9 +542,9 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
                         for (int st = 0; st < ST; ++st)
                             for (int t = wave; t < BM / 16; t += WAVES)
-                                if (base + st < lora.steps)
-                                    buf_to_lds16(ru, s_a(st) + t * 1024, here * 16u,
-                                                 (uint32_t)(t * lora.steps + base + st) * 1024u);
+                                if (base + st < lora.steps)   // zeros for tiles behind the last row's
+                                    buf_to_lds16(ru, s_a(st) + t * 1024,
+                                                 (uint32_t)lora_u_at(t, base + st, lora.steps, here), 0);
                         first = false;
                     }
                     const buf_rsrc_t rl = make_buf(lora.b + ((size_t)j * N + n0) * lora.rank,

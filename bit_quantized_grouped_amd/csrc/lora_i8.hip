@@ -109,9 +109,9 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs& p, int j, int t0, 
                                         v[2 * i + 1] - __builtin_bit_cast(float, hi[i] & 0xFFFF0000u));
                 }
                 // ranks 4 fp .. + 3: half of what lane r % 16 + 16 (fp / 2) of the operand holds
-                uint16_t* o = p.u + (((size_t)(r / 16) * p.steps + t0 + t) * WAVE + r % 16 + fp / 2 * 16) * 8 + fp % 2 * 4;
+                char* o = (char*)p.u + lora_u_at(r / 16, t0 + t, p.steps, r % 16 + fp / 2 * 16) + fp % 2 * 8;
                 *(u32x2_t*)o = u32x2_t{hi[0], hi[1]};
-                *(u32x2_t*)(o + 32 * 8) = u32x2_t{lo[0], lo[1]};
+                *(u32x2_t*)(o + 32 * 16) = u32x2_t{lo[0], lo[1]};
             }
         }
     }
@@ -275,7 +275,7 @@ static LoraWs lora_ws(int M, int rank) {
         return at;
     };
     const size_t tiles = ((size_t)M + 15) / 16;
-    w.u = take(tiles * ((rank + 15) / 16) * 1024);
+    w.u = take(lora_u_bytes(tiles, (rank + 15) / 16));
     w.order = take((size_t)M * 4);
     w.of = take((size_t)M * 4);
     w.blocks = take(((size_t)M / kSgRows + (M < kGroupMax ? M : kGroupMax) + 1) * 16);

@@ -14,7 +14,8 @@ __device__ __forceinline__ buf_rsrc_t make_buf(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
 
-// 16 bytes per lane: lane l writes lds + 16 l (lds uniform over the wave).
+// 16 bytes per lane: lane l writes lds + 16 l (lds uniform over the wave).  The buffer's bound holds
+// for voff alone: where a load may pass the end, voff does so without soff.
 __device__ __forceinline__ void buf_to_lds16(buf_rsrc_t r, void* lds, uint32_t voff, uint32_t soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_dst_t)lds, 16, voff, soff, 0, 0);

@@ -13,9 +13,15 @@
 
 namespace moeq4 {
 
+// Bytes of u of a number of tiles of 16 rows, and the byte among them where 16 ranks of a tile lie.
+__host__ __device__ constexpr size_t lora_u_bytes(size_t tiles, int steps) { return tiles * steps * (WAVE * 16); }
+__host__ __device__ constexpr size_t lora_u_at(size_t m_tile, int step, int steps, int lane) {
+    return ((m_tile * steps + step) * WAVE + lane) * 16;
+}
+
 // 16 ranks of the rows of a tile of 16, as they lie.
 __device__ __forceinline__ u32x4_t lora_u(const LoraDev& l, int m_tile, int step, int lane) {
-    return *(const u32x4_t*)(l.u + (((size_t)m_tile * l.steps + step) * WAVE + lane) * 8);
+    return *(const u32x4_t*)((const char*)l.u + lora_u_at(m_tile, step, l.steps, lane));
 }
 
 __device__ __forceinline__ bf16x8_t lora_only(bool mine, const u32x4_t& u) {
