@@ -37,10 +37,8 @@ constexpr int kBdAhead = 2;
 // h as two bf16: the value and what its rounding left.
 __device__ __forceinline__ void split_bf16(float v, uint16_t* hi, uint16_t* lo) {
     const __bf16 h = (__bf16)v;
-    const uint16_t bits = __builtin_bit_cast(uint16_t, h);
-    const float rest = (bits & 0x7F80u) == 0x7F80u ? 0.f : v - (float)h;   // an infinity has no rest
-    *hi = bits;
-    *lo = __builtin_bit_cast(uint16_t, (__bf16)rest);
+    *hi = __builtin_bit_cast(uint16_t, h);
+    *lo = __builtin_bit_cast(uint16_t, (__bf16)bf16_rest(v, *hi));
 }
 
 template <int EPL>

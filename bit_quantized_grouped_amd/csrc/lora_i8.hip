@@ -105,8 +105,8 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs& p, int j, int t0, 
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                    lo[i] = pack_bf16x2(v[2 * i] - __builtin_bit_cast(float, hi[i] << 16),
-                                        v[2 * i + 1] - __builtin_bit_cast(float, hi[i] & 0xFFFF0000u));
+                    lo[i] = pack_bf16x2(bf16_rest(v[2 * i], (uint16_t)hi[i]),
+                                        bf16_rest(v[2 * i + 1], (uint16_t)(hi[i] >> 16)));
                 }
                 // ranks 4 fp .. + 3: half of what lane r % 16 + 16 (fp / 2) of the operand holds
                 char* o = (char*)p.u + lora_u_at(r / 16, t0 + t, p.steps, r % 16 + fp / 2 * 16) + fp % 2 * 8;

@@ -29,6 +29,11 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
     return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
+// What rounding v to the bf16 `h` left.  An infinity or NaN has no rest: v - h would be NaN for both.
+__device__ __forceinline__ float bf16_rest(float v, uint16_t h) {
+    return (h & 0x7F80u) == 0x7F80u ? 0.f : v - bf16_to_f32(h);
+}
+
 // A 4-bit code q held alone in a byte reads, as an fp8 e4m3 value, q times a
 // fixed power of two (the subnormal step equals the first binade's step, so
 // the 16 codes are evenly spaced).  fp8_unit() returns that power of two as
