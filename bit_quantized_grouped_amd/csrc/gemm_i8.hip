@@ -101,6 +101,17 @@ __device__ __forceinline__ void few_lora(const LoraDev& l, int M, int N, int m0,
                 b0[n] = lora_b(l, j0, N, n0 + n * 16, t0, lane);
                 b1[n] = lora_b(l, j1, N, n0 + n * 16, t1, lane);
             }
+            // lanes 32 .. 63 multiply what u's rounding left
+            uint32_t infinite = 0;
+#pragma unroll
+            for (int n = 0; n < NF; ++n) infinite |= lora_infinite(b0[n]) | lora_infinite(b1[n]);
+            if (__builtin_expect(lane >= 32 && infinite, 0)) {
+#pragma unroll
+                for (int n = 0; n < NF; ++n) {
+                    b0[n] = lora_without(b0[n], 0);
+                    b1[n] = lora_without(b1[n], 0);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NF; ++n) {
                 lora_add(b0[n], u0, of[m] == j0, v[m][n]);
@@ -515,6 +526,7 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
                 for (int i = 0; i < 4; ++i) v[i] = (float)acc[n][m][i] * as[m] * ws[n][i];
                 acc[n][m] = __builtin_bit_cast(i32x4_t, v);
             }
+        bool infinite = false;   // whether a b of this wave's columns has an infinity or NaN
         if constexpr (LORA) {
             // One adapter after another among the tile's rows, ST steps of ranks at a time: its
             // columns, and once the rows' u, go through LDS, where the product's stages were.
@@ -569,15 +581,13 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
 #pragma unroll
                         for (int m = 0; m < MF; ++m)
                             u[m] = *(const u32x4_t*)(s_a(st) + (wm * MF + m) * 1024 + here * 16);
-                        bool bad = false;
+                        uint32_t any = 0;
 #pragma unroll
-                        for (int n = 0; n < NF; ++n) bad |= !lora_finite(b[n]);
-                        // 0 times an infinity would reach other rows: such columns count as zeros, and u as NaN
-                        if (__ballot(bad)) {
+                        for (int n = 0; n < NF; ++n) any |= lora_infinite(b[n]);
+                        if (__builtin_expect(__ballot(any) != 0, 0)) {   // as 1 and -1 here, the rest behind the stores
+                            infinite = true;
 #pragma unroll
-                            for (int n = 0; n < NF; ++n) b[n] = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-                            for (int m = 0; m < MF; ++m) u[m][0] = 0x7FC07FC0u;
+                            for (int n = 0; n < NF; ++n) b[n] = lora_without(b[n], 0x3F80u);
                         }
 #pragma unroll
                         for (int m = 0; m < MF; ++m) {
@@ -628,6 +638,9 @@ __global__ __launch_bounds__(WM* WN* WAVE) void linear_tiles_kernel(
                 __builtin_amdgcn_wave_barrier();
             }
         }
+        if constexpr (LORA)
+            if (__builtin_expect(infinite, 0))
+                lora_add_infinite(lora, M, N, m0 + wm * MF * 16, MF * 16, n0 + wn * NF * 16, min(n0 + (wn + 1) * NF * 16, N), out);
         if (!more) break;
         m0 = m1;
         n0 = n1;

@@ -54,13 +54,50 @@ __device__ __forceinline__ int lora_of(const LoraDev& l, int r, int M) {
     return r < M && j >= 0 && j < l.n ? j : -1;
 }
 
-// No infinity or NaN among eight bf16.
-__device__ __forceinline__ bool lora_finite(const u32x4_t& v) {
-    bool ok = true;
+// Infinities and NaN in b reach their columns of their adapter's rows alone, as by the formula.
+// Two things stand against that: zeros in other rows' places (0 times an infinity is NaN), and
+// what u's rounding left, which may be 0 or of the other sign.
+
+// Bits 15 and 31 are set for the infinities and NaN among two bf16: an exponent of all ones carries.
+__device__ __forceinline__ uint32_t lora_infinite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+__device__ __forceinline__ uint32_t lora_infinite(const u32x4_t& v) {
+    return lora_infinite(v[0]) | lora_infinite(v[1]) | lora_infinite(v[2]) | lora_infinite(v[3]);
+}
+
+// b with `instead` and its sign for every such value.
+__device__ __forceinline__ u32x4_t lora_without(const u32x4_t& b, uint32_t instead) {
+    u32x4_t v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        ok = ok && (v[i] & 0x7F80u) != 0x7F80u && (v[i] & 0x7F800000u) != 0x7F800000u;
-    return ok;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t is = lora_infinite(b[i]), all = (is >> 15) * 0xFFFFu;
+        v[i] = (b[i] & ~all) | (all & ((b[i] & 0x80008000u) | instead * 0x10001u));
+    }
+    return v;
+}
+
+// What such values of their adapters' b add to rows at places r0 .. + rows and columns n0 .. n1 - 1 of
+// out, where they counted as finite values of their sign: infinities and NaN, after the rounding as
+// before it.  By one wave, which has stored these.  Slow, and rarely called.
+__device__ __forceinline__ void lora_add_infinite(const LoraDev& l, int M, int N, int r0, int rows, int n0, int n1,
+                                                  uint16_t* out) {
+    __threadfence();   // the values that other lanes stored
+    for (int r = r0 + __lane_id(); r < min(r0 + rows, M); r += WAVE) {
+        const int j = lora_of(l, r, M);
+        if (j < 0) continue;
+        uint16_t* o = out + (size_t)row_at<true>(l, r, M) * N;
+        const uint16_t* b = l.b + ((size_t)j * N + n0) * l.rank;
+        for (int c = n0; c < n1; ++c, b += l.rank) {
+            float sum = 0.f;
+            for (int k = 0; k < l.rank; k += 8) {
+                if (!lora_infinite(*(const u32x4_t*)(b + k))) continue;
+                const uint16_t* u = (const uint16_t*)((const char*)l.u + lora_u_at(r / 16, k / 16, l.steps, r % 16 + k / 8 % 2 * 16));
+                for (int i = 0; i < 8; ++i)
+                    if (lora_infinite(b[k + i])) sum += bf16_to_f32(b[k + i]) * bf16_to_f32(u[i]);
+            }
+            if (sum != 0.f) o[c] = (uint16_t)pack_bf16x2(bf16_to_f32(o[c]) + sum, 0.f);
+        }
+    }
 }
 
 // v += b u in the rows that are `mine`.

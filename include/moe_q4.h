@@ -615,8 +615,8 @@ typedef struct {
  *                    + scales[j] * sum_r b[j, n, r] * (sum_k a[j, r, k] * a[m, k])))
  * adapter int32 [M]; a row whose adapter lies outside 0 .. n - 1 has none, and moe_linear_i8's
  * values.  The adapters' sums are fp32, the first product's result counts to 16 bits, and out
- * has one rounding.  An adapter's values reach its own rows only, infinities and NaN too (of its b:
- * NaN in those rows then, also in other columns).
+ * has one rounding.  An adapter's values reach its own rows only, infinities and NaN too, and give there
+ * what the formula gives.
  *   ws: moe_linear_lora_i8_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned
  * Sizes as for moe_linear_i8.  Enqueues two kernels, three where the rows are put in order of their adapters first. */
 size_t moe_linear_lora_i8_workspace_bytes(int M, int N, int K, int rank);

@@ -70,3 +70,25 @@ def test_infinities_in_the_first_matrix(M, N, K):
     put = [("A", (1, 3, 7), np.inf), ("B", (1, 0, 3), 0.0), ("A", (2, 0, K - 1), -np.inf), ("A", (3, 5, 9), np.nan)]
     want = run(h, args, put, [1, 2, 3], f"lora, infinity in A, M={M} N={N} K={K}")
     assert np.isinf(want).any() and not np.isfinite(want).any()
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_infinities_in_the_second_matrix(M, N, K):
+    """They reach their column of their adapter's rows, and nothing else."""
+    require_gpu()
+    h, args = case(M, N, K)
+    put = [("B", (1, 0, 5), np.inf), ("B", (1, N // 2, 15), -np.inf), ("B", (2, N - 1, 0), -np.inf), ("B", (3, 7, 8), np.nan),
+           ("B", (3, 8, 2), np.inf), ("B", (3, 8, 3), np.inf)]
+    want = run(h, args, put, [1, 2, 3], f"lora, infinity in B, M={M} N={N} K={K}")
+    assert np.isinf(want).any() and np.isnan(want).any() and np.isfinite(want).mean() > 0.9
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_infinities_that_meet(M, N, K):
+    """An infinite u at the rank of an infinite b, and two infinite ranks in one column."""
+    require_gpu()
+    h, args = case(M, N, K)
+    put = [("A", (1, 3, 7), np.inf), ("B", (1, 2, 3), -np.inf), ("A", (2, 15, 1), -np.inf), ("A", (2, 0, 2), np.inf),
+           ("B", (2, N - 1, 15), np.inf), ("B", (0, 5, 0), np.inf), ("B", (0, 5, 9), -np.inf)]
+    want = run(h, args, put, [0, 1, 2], f"lora, infinities that meet, M={M} N={N} K={K}")
+    assert np.isinf(want).any() and np.isnan(want).any() and np.isfinite(want).any()
