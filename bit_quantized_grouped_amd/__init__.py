@@ -1300,7 +1300,8 @@ class MoeLayer:
         """1 to 64 tokens through one moe_decode_batch_q4 call.  Returns y (out when given), the
         selection topk_idx and topk_w, and the workspace ws.  These are this object's and the next
         call's for as many tokens too: calls on several streams at once need an object each.  The
-        first call for a T makes them; its stream then waits for the current one."""
+        first call for a T makes them; its stream then waits for the current one.  They are kept
+        until release."""
         shape = T, H = _few_tokens(x)
         d = x.get_device()
         if H != self.H:
@@ -1333,6 +1334,19 @@ class MoeLayer:
         _run(lib().moe_decode_batch_q4, "moe_decode_batch_q4", d, stream, *inputs, T, H, self.I,
              self.I_sh, self.E, self.k, *self._batch_mats[2], *outs, _arg(y, "y", BF16, shape, d), *ws)
         return dict(b, y=y)
+
+    def release(self, T: int | None = None):
+        """Gives the buffers for T tokens (None: for all), of decode_batch and of the other calls, back
+        to torch's allocator when the work on them has ended: the host waits for the device.  What
+        calls returned must not be read and a graph captured over them not be replayed afterwards; a
+        later call makes new ones."""
+        used = {sizes[0] for _, sizes in self._batch_bufs} - {-1}   # decode_batch's are where its x was
+        for device in used | ({self.device} if self.device.type == "cuda" else set()):
+            torch.cuda.synchronize(device)
+        for bufs in (self._bufs, self._batch_bufs):
+            for key in list(bufs):
+                if T is None or T == (key[0] if isinstance(key, tuple) else key):
+                    del bufs[key]
 
     def bf16_weights(self) -> dict:
         """Device buffers for the weights expanded to bf16 (allocated once, reused)."""

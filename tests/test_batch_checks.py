@@ -152,3 +152,14 @@ def test_binding_refusals():
         bq.moe_decode_batch_q4(X, LG, None, None, torch.zeros(4), 64, 0, 2, *m[:3], None, None, None, y, ws)
     with pytest.raises(ValueError, match="device tensors"):
         bq.moe_decode_batch_q4(X, LG, None, None, None, 64, 64, 2, *m, y, ws)
+
+
+def test_release_without_buffers():
+    m = layer()
+    m.release()
+    m.release(7)
+    m._batch_bufs[4, (-1,)], m._batch_bufs[5, (-1,)], m._bufs[4] = {}, {}, {}
+    m.release(4)
+    assert list(m._batch_bufs) == [(5, (-1,))] and not m._bufs
+    m.release()
+    assert not m._batch_bufs
