@@ -85,6 +85,21 @@ def test_an_adapter_sets_tensors_are_fixed():
         ad.a = bf(2, 16, 64)
 
 
+@pytest.mark.parametrize("part", ["a", "b", "scales"])
+def test_adapters_that_moved_are_refused(part):
+    """A tensor whose memory was exchanged in place: the call would read the old one."""
+    ad = bq.DeviceAdapters(bf(2, 16, 64), bf(2, 32, 16), torch.zeros(2))
+    args = dict(a=torch.zeros((3, 64), dtype=torch.int8), a_scale=torch.zeros(3),
+                w=bq.DeviceI8Mat(torch.zeros((1, 32, 64), dtype=torch.int8), torch.zeros((1, 32))), adapters=ad,
+                adapter=torch.zeros(3, dtype=torch.int32), out=bf(3, 32), ws=torch.zeros(1 << 12, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="device tensors"):
+        bq.moe_linear_lora_i8(**args)
+    t = getattr(ad, part)
+    t.set_(t.clone())
+    with pytest.raises(ValueError, match="lies elsewhere"):
+        bq.moe_linear_lora_i8(**args)
+
+
 @pytest.mark.parametrize("change,error", [
     (dict(a=torch.zeros((3, 64))), TypeError), (dict(a=torch.zeros((3, 128), dtype=torch.int8)), ValueError),
     (dict(a_scale=torch.zeros(4)), ValueError), (dict(w=None), TypeError), (dict(adapters=None), TypeError),
