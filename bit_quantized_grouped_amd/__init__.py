@@ -1300,8 +1300,9 @@ class MoeLayer:
     def decode_batch(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None,
                      rule: ScoreRule | None = None, score_bias=None, shared_gate=None,
                      stream=None) -> dict:
-        """1 to 64 tokens through one moe_decode_batch_q4 call.  Returns y (out when given), the
-        selection topk_idx and topk_w, and the workspace ws.  These are this object's and the next
+        """1 to 64 tokens through one moe_decode_batch_q4 call.  Without a rule or shared_gate, and
+        where its 16-bit h is not needed, forward is as fast or faster from 7 tokens of uniform
+        experts on (2048 wide; 4096: 4; 7168: 3).  Returns y (out when given), the selection topk_idx and topk_w, and the workspace ws.  These are this object's and the next
         call's for as many tokens too: calls on several streams at once need an object each.  The
         first call for a T makes them; its stream then waits for the current one.  They are kept
         until release."""

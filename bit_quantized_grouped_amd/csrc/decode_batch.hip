@@ -18,6 +18,8 @@
 //   1, 2, 4, 8 tokens 13.0 + 6.6, 15.4 + 8.2, 17.9 + 11.2 and 26.5 + 20.4 us, for weights that 6.2
 //   TB/s read in 2.6, 4.8, 9.2 and 16.5; in the form below 18.2 + 9.9 for 2, 18.1 + 10.9 for 4, 23.9 +
 //   16.6 for 8, each with 7 to 9 us of selection and join.
+//   Wider than 2048 (up to 4 tokens 4096) x does not fit the first launch's 32 KB, and every task fetches it
+//   in parts: 8 tokens 85 us in all 4096 wide and 143 7168 wide, where moe_layer_q4 takes 64 and 99.
 // More tokens, four launches: batch_select_kernel (4.7 us), batch_tiles_kernel for gate/up and for down,
 //   batch_join_kernel (4.6).  16 tokens 30.7 + 17.8 us (floor 14.5 + 7.2), 32 tokens 48.0 + 29.3 (31 +
 //   16), 64 tokens of skewed experts 29.4 + 18.1 (10 + 5).

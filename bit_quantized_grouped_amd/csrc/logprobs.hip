@@ -14,7 +14,8 @@
 //
 // Few rows are split over workgroups, whose results a second kernel joins.
 // Bound by vector instructions for bf16, about 14 a value with the exponential as four, which 2048
-// rows of 131072 need 90 us for where their bytes need 85: 132 us in all.  Few rows are bound by
+// rows of 131072 need 90 us for where their bytes need 85: 117 us in all back to back, 132 to 135 under
+// the tracer, where the figures below are from.  Few rows are bound by
 // latency: one of 131072 takes 8.9 us, 1.6 of them for its values, and 3.5 for the join.
 // The next pieces' loads before the present ones' sums, 1024 threads and 256 a workgroup were tried: 150, 191
 // and 135 us, 192 rows of 150001 in 21.1, 21.7 and 30.1 where 512 threads take 22.0.

@@ -251,7 +251,8 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(const int32_t
 // Bytes of A that workgroups of 16 rows may read at most, if their rows' adapters are mixed, before the
 // rows are put in order.  With the product, K = N = 4096, in order and as they come, 16 adapters of
 // rank 16: 1024 mixed rows (134 MB) 45 and 64 us, 1024 in runs 45 and 37; 512 rows 37 and 42, in runs 38
-// and 30; 256 rows 31 and 34, in runs 31 and 27.  6 adapters of rank 64, which the caches hold, 512 mixed
+// and 30; 256 rows 31 and 34, in runs 31 and 27.  Which of the two the rows are is on the device, so the
+// rule is for the mixed ones, which lose more (64) than runs do (45 for 37).  6 adapters of rank 64, which the caches hold, 512 mixed
 // rows (100 MB) 51 and 49, in runs 51 and 35.
 constexpr double kDirectBytes = 128e6;
 

@@ -586,6 +586,8 @@ int moe_layer_i8(const int8_t* x, const float* x_scale, const float* logits,
  * and y has one rounding, so y differs from the three-call path by that path's roundings of h
  * and of the experts' outputs.  A token's y depends on no other token but through the
  * order of its sums.  Deterministic: the same inputs give the same bits.
+ * Without a rule and gates moe_layer_q4 is as fast or faster from 7 tokens of uniform experts on for
+ * H 2048, from 4 for 4096 and 3 for 7168: x of all tokens fits LDS at once up to 2048 (T 5 .. 8) or 4096.
  *   ws: moe_decode_batch_workspace_bytes() bytes (0 on bad shapes), 256-byte aligned; need
  *   not be cleared.
  * Shapes and matrices as for moe_decode_q4, T <= 64, k <= 64, H < 2^24; for a rule also
