@@ -1131,6 +1131,8 @@ class DeviceAdapters(_Fixed):
             raise ValueError("a, b and scales: on different devices")
         self.a, self.b, self.scales = a, b, scales
         self.n, self.rank, self.K, self.N = n, rank, K, N
+        # the tensors' places, by bound methods: they are compared at every call
+        self.places = tuple((t.data_ptr, t.data_ptr()) for t in (a, b, scales))
         self.struct = MoeAdapters(a.data_ptr(), b.data_ptr(), scales.data_ptr(), n, rank)
 
 
@@ -1152,9 +1154,9 @@ def moe_linear_lora_i8(a: torch.Tensor, a_scale: torch.Tensor, w: DeviceI8Mat, a
         raise ValueError(f"adapters: for [{adapters.N}, {adapters.K}], the matrix is [{N}, {K}]")
     if adapters.a.get_device() != d:
         raise ValueError(f"adapters: on {adapters.a.device}, the call's first tensor is elsewhere")
-    s = adapters.struct
-    if (adapters.a.data_ptr(), adapters.b.data_ptr(), adapters.scales.data_ptr()) != (s.a, s.b, s.scales):
-        raise ValueError("adapters: a tensor lies elsewhere than when its DeviceAdapters was made")
+    for place, at in adapters.places:
+        if place() != at:
+            raise ValueError("adapters: a tensor lies elsewhere than when its DeviceAdapters was made")
     _run(lib().moe_linear_lora_i8, "moe_linear_lora_i8", d, stream, _arg(a, "a", I8, shape, d),
          _arg(a_scale, "a_scale", F32, (M,), d), M, K, _i8mat(w, "w", 1, N, K, d), N,
          ctypes.byref(adapters.struct), _arg(adapter, "adapter", I32, (M,), d),
